@@ -17,10 +17,12 @@ TGEMM_EPI_NONE, TGEMM_EPI_RELU, TGEMM_EPI_BIAS, TGEMM_EPI_BIAS_RELU = 0, 1, 2, 3
 TGEMM_EPI_GELU, TGEMM_EPI_BIAS_GELU = 4, 5
 STATUS = {0: "TGEMM_OK", 1: "TGEMM_ERR_INVALID_ARG", 2: "TGEMM_ERR_ALIGNMENT",
           3: "TGEMM_ERR_UNSUPPORTED_DEVICE", 4: "TGEMM_ERR_ALIAS", 5: "TGEMM_ERR_CUDA",
-          6: "TGEMM_ERR_TIMEOUT", 7: "TGEMM_ERR_SCRATCH_LIMIT", 8: "TGEMM_ERR_DEBUG_CHECK"}
+          6: "TGEMM_ERR_TIMEOUT", 7: "TGEMM_ERR_SCRATCH_LIMIT", 8: "TGEMM_ERR_DEBUG_CHECK",
+          9: "TGEMM_ERR_CACHE"}
 EXPORTED = ("tgemm_run", "tgemm_run_ex", "tgemm_run_host", "tgemm_status_string",
             "tgemm_last_device_status", "tgemm_version", "tgemm_run_noalloc", "tgemm_plan",
-            "tgemm_attention_fwd", "tgemm_debug_last_check")
+            "tgemm_attention_fwd", "tgemm_debug_last_check", "tgemm_kv_append", "tgemm_attention_decode",
+            "tgemm_attention_decode_workspace", "tgemm_kv_evict")
 PLAN_FIELDS = ("bn", "cg", "stages", "tiles", "groups", "split_k", "split_first", "narrow_first",
                "narrow_parts", "units")
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -28,6 +30,14 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 _lock = threading.Lock()
 _lib = None
 _debug_lib = None
+
+
+class KvCache(ctypes.Structure):
+    """tgemm_kv_cache."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+                + [(n, ctypes.c_int64) for n in ("pages", "page_stride", "slot_stride", "head_stride",
+                                                 "scale_page_stride", "scale_slot_stride", "scale_head_stride")]
+                + [(n, ctypes.c_int32) for n in ("page_size", "heads", "dim", "e4m3")])
 
 
 class TgemmError(RuntimeError):
@@ -61,6 +71,17 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.tgemm_plan.restype = i32
     lib.tgemm_attention_fwd.argtypes = [p, p, p, p, i64, i64, i64, i64, i32, i32, p]
     lib.tgemm_attention_fwd.restype = i32
+    f32 = ctypes.c_float
+    weights = [p, i64, i64, i64]
+    lib.tgemm_kv_append.argtypes = [p, p, p, i64, i64, i64, p, p, i64, i64, p, i64, *weights, i32, p]
+    lib.tgemm_kv_append.restype = i32
+    lib.tgemm_attention_decode.argtypes = [p, p, p, i64, i64, i64, i64, i64, i64, p, i64, i64, p, f32, f32, i64,
+                                           *weights, p, i64, i32, p]
+    lib.tgemm_attention_decode.restype = i32
+    lib.tgemm_attention_decode_workspace.argtypes = [i64, i64, i64, i64, i64, i32, p]
+    lib.tgemm_attention_decode_workspace.restype = i32
+    lib.tgemm_kv_evict.argtypes = [p, p, i64, i64, p, i64, *weights, p, p, i64, i64, i64, i64, p, p, *weights, p]
+    lib.tgemm_kv_evict.restype = i32
     return lib
 
 
@@ -159,3 +180,31 @@ def tgemm_plan(M: int, N: int, K: int, num_sms: int) -> dict:
 def tgemm_attention_fwd(Q: int, K: int, V: int, O: int, batch: int, seq: int, heads: int, dim: int,
                         causal: int, dtype: int, stream: int = 0) -> int:
     return int(load().tgemm_attention_fwd(Q, K, V, O, batch, seq, heads, dim, int(causal), dtype, stream))
+
+
+# The paged key-value cache.  `cache` is a ctypes reference to a KvCache; the
+# other arguments are those of include/tgemm.h in order, pointers as ints.
+def tgemm_kv_append(cache, *args) -> int:
+    lib = _lib if _lib is not None else load()
+    return lib.tgemm_kv_append(cache, *args)
+
+
+def tgemm_attention_decode(cache, *args) -> int:
+    lib = _lib if _lib is not None else load()
+    return lib.tgemm_attention_decode(cache, *args)
+
+
+def tgemm_attention_decode_workspace(batch: int, q_heads: int, kv_heads: int, dim: int, positions: int,
+                                     with_weights: bool) -> int:
+    """Bytes of workspace of tgemm_attention_decode (host logic, no GPU)."""
+    out = ctypes.c_int64()
+    st = load().tgemm_attention_decode_workspace(batch, q_heads, kv_heads, dim, positions, int(with_weights),
+                                                 ctypes.byref(out))
+    if st != 0:
+        raise TgemmError(st, "tgemm_attention_decode_workspace")
+    return int(out.value)
+
+
+def tgemm_kv_evict(cache, *args) -> int:
+    lib = _lib if _lib is not None else load()
+    return lib.tgemm_kv_evict(cache, *args)

@@ -31,8 +31,9 @@ enum DebugCheck : uint32_t {
     kChkRepack = 8,         // repack store outside the destination
 };
 
-// First check that failed since the host last read it (0: none).
-__device__ unsigned int g_debug_check;
+// First check that failed since the host last read it (0: none); one word per
+// translation unit.
+static __device__ unsigned int g_debug_check;
 
 // Records a kernel error in the device status word.  Debug builds keep the
 // first error since the host's last read (a copy skipped by a failed check
@@ -48,7 +49,7 @@ __device__ __forceinline__ void record_status(unsigned int *status, uint32_t cod
 }
 
 #ifdef TGEMM_DEBUG
-__device__ __noinline__ bool debug_fail(uint32_t id, unsigned int *status) {
+static __device__ __noinline__ bool debug_fail(uint32_t id, unsigned int *status) {
     atomicCAS(status, 0u, kStatusDebugCheck);
     atomicCAS(&g_debug_check, 0u, id);
     return false;

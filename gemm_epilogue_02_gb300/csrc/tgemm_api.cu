@@ -21,6 +21,7 @@
 #include "aux_kernels.cuh"
 #include "gemm_kernel.cuh"
 #include "attn_kernel.cuh"
+#include "runtime.h"
 
 namespace tgemm {
 namespace {
@@ -1192,6 +1193,25 @@ extern "C" tgemm_status tgemm_run_host(const void *A_host, const void *B_host,
     return st;
 }
 
+namespace tgemm {
+
+tgemm_status runtime_current(RuntimeInfo *out) {
+    DeviceInfo *d = nullptr;
+    const tgemm_status st = current_device(&d);
+    if (st != TGEMM_OK) return st;
+    if (cudaGetDevice(&out->device) != cudaSuccess) {
+        cudaGetLastError();
+        return TGEMM_ERR_CUDA;
+    }
+    out->num_sms = d->num_sms;
+    out->status = d->status;
+    return TGEMM_OK;
+}
+
+bool runtime_is_device_memory(const void *p, int device) { return is_device_memory(p, device); }
+
+}  // namespace tgemm
+
 extern "C" const char *tgemm_status_string(tgemm_status s) {
     switch (s) {
         case TGEMM_OK: return "TGEMM_OK";
@@ -1202,6 +1222,7 @@ extern "C" const char *tgemm_status_string(tgemm_status s) {
         case TGEMM_ERR_CUDA: return "TGEMM_ERR_CUDA: a CUDA call or launch failed";
         case TGEMM_ERR_TIMEOUT: return "TGEMM_ERR_TIMEOUT: a kernel gave up on a pipeline wait";
         case TGEMM_ERR_SCRATCH_LIMIT: return "TGEMM_ERR_SCRATCH_LIMIT: repacked operands exceed the fixed scratch of tgemm_run_noalloc";
+        case TGEMM_ERR_CACHE: return "TGEMM_ERR_CACHE: a page number, length or start outside the cache (its rows were left out)";
         case TGEMM_ERR_DEBUG_CHECK: return "TGEMM_ERR_DEBUG_CHECK: a device-side check of the debug build failed (access skipped)";
     }
     return "TGEMM_ERR_UNKNOWN";
@@ -1238,7 +1259,8 @@ extern "C" int tgemm_debug_last_check(void) {
         cudaGetLastError();
         return 0;
     }
-    return static_cast<int>(v);
+    const int kv = kv_debug_last_check();
+    return v ? static_cast<int>(v) : kv;
 #else
     return -1;
 #endif

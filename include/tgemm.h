@@ -61,8 +61,10 @@ typedef enum {
     TGEMM_ERR_CUDA = 5,               /* a CUDA runtime/driver call or a launch failed       */
     TGEMM_ERR_TIMEOUT = 6,            /* a kernel gave up on a pipeline wait (device status) */
     TGEMM_ERR_SCRATCH_LIMIT = 7,      /* tgemm_run_noalloc: repacked operands exceed its fixed scratch */
-    TGEMM_ERR_DEBUG_CHECK = 8         /* debug build: a device-side bounds / alignment check failed
+    TGEMM_ERR_DEBUG_CHECK = 8,        /* debug build: a device-side bounds / alignment check failed
                                          and the access was skipped (device status) */
+    TGEMM_ERR_CACHE = 9               /* a page number, length or start lies outside the cache; the
+                                         rows that it stands for were left out (device status) */
 } tgemm_status;
 
 /*
@@ -283,6 +285,133 @@ int tgemm_version(void);
 tgemm_status tgemm_attention_fwd(const void *Q, const void *K, const void *V, void *O,
                                  int64_t batch, int64_t seq, int64_t heads, int64_t dim,
                                  int causal, tgemm_dtype dtype, tgemm_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The paged key-value cache: what attention needs when tokens come one at a
+ * time.  (No counterpart on the pages, which stop at whole sequences.)
+ *
+ * Keys and values live in two pools of rows.  A row holds the `dim` elements of
+ * one head at one position; position pos of a sequence lies on page
+ * list[pos / page_size] of the pools, at slot pos % page_size, where list is the
+ * sequence's row of a page table:
+ *   row(page, slot, head) = base + page * page_stride + slot * slot_stride
+ *                                + head * head_stride            (elements)
+ * so that [page, slot, head, dim] and [page, head, slot, dim] pools, and pools
+ * that hold keys and values side by side, are all described by strides.  K and
+ * V share the strides.  Elements are fp16 or bf16 (the calls' dtype), or, with
+ * e4m3 = 1, e4m3 with one fp32 scale per row and pool: value = scale * element,
+ * scale > 0.
+ *
+ * Limits: dim a multiple of 8 (e4m3: 16), at most 256; page_size 1 .. 2^20;
+ * bases 16-byte aligned and strides multiples of 16 bytes; rows may not
+ * overlap.
+ */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;                                           /* e4m3 = 1 only */
+    int64_t pages;
+    int64_t page_stride, slot_stride, head_stride;                      /* elements      */
+    int64_t scale_page_stride, scale_slot_stride, scale_head_stride;    /* floats        */
+    int32_t page_size, heads, dim, e4m3;
+} tgemm_kv_cache;
+
+/*
+ * Common to the three calls below.
+ *   pages    int32 [batch, pages_stride], device: each sequence's page list, of
+ *            pages_width entries at most; entries past a sequence's length are
+ *            not read.
+ *   lengths  int32 [batch], device: positions each sequence holds.
+ *   weights  fp32 [batch, heads, weights_width] with strides: the attention
+ *            weights accumulated for each position (NULL where it is optional).
+ * Page numbers, lengths and starts are on the device, so the kernels check
+ * them: one that lies outside the pool or the table (a negative length too) is
+ * recorded as TGEMM_ERR_CACHE in the device status word
+ * (tgemm_last_device_status), and the rows that it stands for are left out;
+ * nothing outside the arrays is read or written.
+ *
+ * Errors that the host sees are returned before anything is enqueued:
+ * TGEMM_ERR_INVALID_ARG (sizes, strides, dtype, a NULL or host pointer),
+ * TGEMM_ERR_ALIGNMENT, TGEMM_ERR_ALIAS, TGEMM_ERR_UNSUPPORTED_DEVICE,
+ * TGEMM_ERR_CUDA.  batch is at most 65535.  Nothing is allocated and the host
+ * does not read device memory, so the calls can be captured into a graph, which
+ * then follows the lengths and pages that it finds at each replay.
+ */
+
+/*
+ * tgemm_kv_append — write the newest tokens' rows.  K and V are
+ * [tokens, heads, dim] (strides in elements, multiples of 8).  Sequence b
+ * brings the tokens starts[b] .. starts[b + 1] - 1 (starts: int32 [batch + 1],
+ * ascending, device); with starts = NULL each brings one (tokens = batch).
+ * lengths[b] counts them already: the last of them goes to position
+ * lengths[b] - 1.  Tokens outside starts[0] .. starts[batch] - 1 are left out.
+ * An e4m3 row's scale is max |x| / 448 (1 for a row of zeros) and its elements
+ * x / scale, rounded to nearest even.  With weights, those of the new positions
+ * are set to 0.
+ */
+tgemm_status tgemm_kv_append(const tgemm_kv_cache *cache, const void *K, const void *V, int64_t tokens,
+                             int64_t token_stride, int64_t head_stride, const int32_t *starts,
+                             const int32_t *pages, int64_t pages_width, int64_t pages_stride,
+                             const int32_t *lengths, int64_t batch, float *weights, int64_t weights_width,
+                             int64_t weights_batch_stride, int64_t weights_head_stride, tgemm_dtype dtype,
+                             tgemm_stream_t stream);
+
+/*
+ * tgemm_attention_decode — attention of one new token per sequence over its
+ * cache.  Q and O are [batch, q_heads, dim] with strides (multiples of 8
+ * elements); query head h reads the keys of head h / (q_heads / heads).
+ *
+ *   O[b, h] = sum_j p_j V[b, j],  p = softmax of s_j over max(0, n - window) <= j < n,  n = lengths[b],
+ *   s_j = scale * Q[b, h] . K[b, j], passed through cap * tanh(s / cap) when cap > 0;
+ *
+ * window = 0: all positions.  A sequence of length 0 gets zeros.  Rows past n,
+ * NaN and infinity among them, have no influence.  With weights,
+ * weights[b, g, j] grows by the sum of p_j over the query heads of group g.
+ *
+ * Arithmetic: products of 16-bit values (e4m3 elements are widened exactly)
+ * accumulated in fp32; softmax in fp32 with a running maximum; each output
+ * rounded once to dtype.
+ *
+ * workspace: device memory of tgemm_attention_decode_workspace() bytes,
+ * 16-byte aligned, that held zeros before its first use; the call leaves it fit
+ * for the next.  Calls that may overlap on the GPU need one each.
+ */
+tgemm_status tgemm_attention_decode(const tgemm_kv_cache *cache, const void *Q, void *O, int64_t batch,
+                                    int64_t q_heads, int64_t q_batch_stride, int64_t q_head_stride,
+                                    int64_t o_batch_stride, int64_t o_head_stride, const int32_t *pages,
+                                    int64_t pages_width, int64_t pages_stride, const int32_t *lengths, float scale,
+                                    float cap, int64_t window, float *weights, int64_t weights_width,
+                                    int64_t weights_batch_stride, int64_t weights_head_stride, void *workspace,
+                                    int64_t workspace_bytes, tgemm_dtype dtype, tgemm_stream_t stream);
+
+/*
+ * Bytes of workspace that tgemm_attention_decode needs for up to `batch`
+ * sequences of up to `positions` positions (pages_width * page_size).  Host
+ * logic only.
+ */
+tgemm_status tgemm_attention_decode_workspace(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim,
+                                              int64_t positions, int with_weights, int64_t *bytes);
+
+/*
+ * tgemm_kv_evict — bring sequences back to at most `keep` positions.  Of n =
+ * lengths[b] positions each head keeps k = min(n, keep): the last
+ * r = min(recent, k), and of the n - r before them the k - r of largest weight
+ * (ties to the lowest position, NaN below every number).  Their rows go, in
+ * order, to positions 0 .. k - 1 of the page lists to_pages of the cache `to`,
+ * with scales and weights.  `to` may describe the same pools as `from` as long
+ * as the pages written are not among those read (pages may be shared by
+ * sequences: nothing of `from` changes).  Outputs besides the rows:
+ *   kept        int32 [batch, heads, keep]: the positions kept, ascending, -1 from k on
+ *   to_lengths  int32 [batch]: k
+ *   to_weights  fp32 [batch, heads, to_weights_width >= keep]: the weights kept, 0 from k to keep - 1
+ */
+tgemm_status tgemm_kv_evict(const tgemm_kv_cache *from, const int32_t *pages, int64_t pages_width,
+                            int64_t pages_stride, const int32_t *lengths, int64_t batch, const float *weights,
+                            int64_t weights_width, int64_t weights_batch_stride, int64_t weights_head_stride,
+                            const tgemm_kv_cache *to, const int32_t *to_pages, int64_t to_pages_width,
+                            int64_t to_pages_stride, int64_t keep, int64_t recent, int32_t *kept,
+                            int32_t *to_lengths, float *to_weights, int64_t to_weights_width,
+                            int64_t to_weights_batch_stride, int64_t to_weights_head_stride, tgemm_stream_t stream);
 
 /*
  * tgemm_plan — the work plan tgemm_run (and tgemm_run_ex / tgemm_run_host per
