@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -97,7 +98,7 @@ tgemm_status check_cache(const tgemm_kv_cache *c, KvView *view, Extent *k, Exten
 // Checks the page lists and lengths of `batch` sequences.
 tgemm_status check_table(const int32_t *pages, int64_t width, int64_t stride, const int32_t *lengths, bool with_lengths,
                          int64_t batch, int page_size, KvTable *t) {
-    if (batch < 0 || batch > 65535 || width < 0 || width > INT32_MAX / page_size || stride < 0 ||
+    if (batch < 0 || batch > 65535 || width < 0 || width > (1 << 30) / page_size || stride < 0 ||
         (batch > 1 && stride < width) || stride > (int64_t(1) << 40))
         return TGEMM_ERR_INVALID_ARG;
     if (batch > 0 && ((width > 0 && !pages) || (with_lengths && !lengths))) return TGEMM_ERR_INVALID_ARG;
@@ -155,6 +156,75 @@ tgemm_status done(cudaError_t e) {
     if (e == cudaSuccess) return TGEMM_OK;
     cudaGetLastError();
     return TGEMM_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- attention
+int padded_dim(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+// Blocks of 8 query heads up to 8 heads on a key head, of 16 above (one read of
+// the keys instead of two); 256-wide rows leave registers for 8 only.
+int head_tiles(int64_t group, int64_t dim) { return group > 8 && dim <= 128 ? 2 : 1; }
+
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+// The workspace's parts; returns its bytes (-1: too many).
+int64_t attend_layout(int64_t batch, int64_t q_heads, int64_t group, int64_t dim, int64_t positions, bool weights,
+                      unsigned char *base, AttendSpace *out) {
+    const int64_t slots = 2 * kAttendMaxCtas, heads = 8 * head_tiles(group, dim);
+    int64_t at = 0, scores = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += align256(bytes);
+        return here;
+    };
+    const int64_t parts = take(slots * 4), groups = take(slots * 4);
+    const int64_t o = take(slots * heads * padded_dim(dim) * 4), ml = take(slots * heads * 8);
+    int64_t stats = 0, s = 0;
+    if (weights) {
+        if (__builtin_mul_overflow(batch * q_heads * 4, positions, &scores) || scores > kMost) return -1;
+        stats = take(batch * q_heads * 8);
+        s = take(scores);
+    }
+    if (out) {
+        out->parts = reinterpret_cast<unsigned *>(base + parts);
+        out->groups = reinterpret_cast<unsigned *>(base + groups);
+        out->out = reinterpret_cast<float *>(base + o);
+        out->ml = reinterpret_cast<float2 *>(base + ml);
+        out->stats = weights ? reinterpret_cast<float2 *>(base + stats) : nullptr;
+        out->scores = weights ? reinterpret_cast<float *>(base + s) : nullptr;
+    }
+    return at;
+}
+
+template <bool kBf16, bool kE4m3, int DP, int NT>
+cudaError_t launch_attend(const RuntimeInfo &rt, const AttendParams &p, cudaStream_t s) {
+    using Shape = AttendShape<kE4m3, DP, NT>;
+    auto kernel = kv_attend_kernel<kBf16, kE4m3, DP, NT>;
+    static std::atomic<uint64_t> ready{0};      // bit per device
+    const uint64_t bit = uint64_t(1) << rt.device;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    // One CTA per place on the GPU, fewer when there cannot be as many tiles.
+    const int64_t tiles = (p.positions + Shape::kTile - 1) / Shape::kTile;
+    const int64_t most = static_cast<int64_t>(p.table.batch) * p.cache.heads * p.blocks * std::max<int64_t>(1, tiles);
+    const int64_t places = std::min<int64_t>(kAttendMaxCtas, static_cast<int64_t>(rt.num_sms) * Shape::kCtas);
+    return launch(kernel, dim3(static_cast<unsigned>(std::min(most, places))), kAttendThreads, Shape::kBytes, s, p);
+}
+
+template <bool kBf16, bool kE4m3>
+cudaError_t launch_attend_dim(const RuntimeInfo &rt, const AttendParams &p, int tiles, cudaStream_t s) {
+    switch (padded_dim(p.cache.dim)) {
+        case 64:
+            return tiles == 2 ? launch_attend<kBf16, kE4m3, 64, 2>(rt, p, s) : launch_attend<kBf16, kE4m3, 64, 1>(rt, p, s);
+        case 128:
+            return tiles == 2 ? launch_attend<kBf16, kE4m3, 128, 2>(rt, p, s)
+                              : launch_attend<kBf16, kE4m3, 128, 1>(rt, p, s);
+        default:
+            return launch_attend<kBf16, kE4m3, 256, 1>(rt, p, s);
+    }
 }
 
 }  // namespace
@@ -228,9 +298,11 @@ extern "C" tgemm_status tgemm_kv_append(const tgemm_kv_cache *cache, const void 
 extern "C" tgemm_status tgemm_attention_decode_workspace(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim,
                                                          int64_t positions, int with_weights, int64_t *bytes) {
     if (!bytes || batch < 0 || batch > 65535 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || dim < 8 ||
-        dim > 256 || positions < 0 || (with_weights != 0 && with_weights != 1))
+        dim > 256 || q_heads > 65535 || positions < 0 || (with_weights != 0 && with_weights != 1))
         return TGEMM_ERR_INVALID_ARG;
-    *bytes = 256;
+    const int64_t need = attend_layout(batch, q_heads, q_heads / kv_heads, dim, positions, with_weights != 0, nullptr, nullptr);
+    if (need < 0) return TGEMM_ERR_INVALID_ARG;
+    *bytes = need;
     return TGEMM_OK;
 }
 
@@ -287,15 +359,28 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_kv_cache *cache, cons
     p.o_head_stride = o_head_stride * 2;
     p.group = static_cast<int>(q_heads / cache->heads);
     p.window = static_cast<int>(std::min<int64_t>(window, INT32_MAX));
-    p.scale = scale;
-    p.cap = cap;
+    constexpr double kLog2e = 1.4426950408889634;
+    p.capped = cap > 0.0f;
+    p.first = static_cast<float>(p.capped ? scale * 2.0 * kLog2e / cap : scale * kLog2e);
+    p.last = static_cast<float>(cap * kLog2e);
+    p.positions = pages_width * cache->page_size;
+    const int tiles = head_tiles(p.group, cache->dim);
+    p.blocks = (p.group + 8 * tiles - 1) / (8 * tiles);
+    attend_layout(batch, q_heads, p.group, cache->dim, p.positions, weights != nullptr,
+                  static_cast<unsigned char *>(workspace), &p.space);
     p.status = rt.status;
-    const dim3 grid(static_cast<unsigned>(cache->heads), static_cast<unsigned>(batch));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool bf16 = dtype == TGEMM_BF16;
-    auto kernel = bf16 ? (cache->e4m3 ? kv_attend_kernel<true, true> : kv_attend_kernel<true, false>)
-                       : (cache->e4m3 ? kv_attend_kernel<false, true> : kv_attend_kernel<false, false>);
-    return done(launch(kernel, grid, kAttendWarps * 32, 0, s, p));
+    cudaError_t e;
+    if (dtype == TGEMM_BF16)
+        e = cache->e4m3 ? launch_attend_dim<true, true>(rt, p, tiles, s) : launch_attend_dim<true, false>(rt, p, tiles, s);
+    else
+        e = cache->e4m3 ? launch_attend_dim<false, true>(rt, p, tiles, s) : launch_attend_dim<false, false>(rt, p, tiles, s);
+    if (e == cudaSuccess && weights) {
+        const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((p.positions + kSpreadThreads - 1) / kSpreadThreads, 64));
+        const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(cache->heads), static_cast<unsigned>(batch));
+        e = launch(kv_spread_kernel, grid, kSpreadThreads, 0, s, p);
+    }
+    return done(e);
 }
 
 extern "C" tgemm_status tgemm_kv_evict(const tgemm_kv_cache *from, const int32_t *pages, int64_t pages_width,

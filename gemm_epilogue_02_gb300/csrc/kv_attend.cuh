@@ -7,8 +7,47 @@
 // gives zeros.  With weights, weights[b, g, j] grows by the sum of p_j over the
 // group's heads.
 //
-// Simple form: one block per sequence and key head, one warp per key, the
-// running maximum, sum and output of a warp in registers, joined at the end.
+// Every key and value row is read once and used for `group` heads: 4 group
+// operations per 16-bit element pair, so the reading bounds it (6.8 TB/s), and
+// the design is about keeping enough bytes in flight on every SM whatever the
+// batch looks like.
+//
+// Work.  An item is one sequence, key head and block of up to 8 * NT query
+// heads; its positions come in tiles of kWarps * kKeys.  The tiles of all items
+// in a row are cut into equal runs, one per CTA (as many CTAs as fit the GPU at
+// once), so that a ragged batch, or a single long sequence, loads every SM
+// alike; each CTA finds its run from the lengths, which only the device knows.
+// A run that ends inside an item leaves (maximum, sum, output) of its part in
+// the workspace, and the CTA that arrives last joins the parts in order of
+// position (the result does not depend on the order of arrival).
+//
+// A CTA.  Each warp owns kKeys positions of a tile and a ring of kStages
+// stages in shared memory that it fills with its own asynchronous 16-byte
+// copies and drains alone: no barrier between warps until an item ends.  A row
+// is found through the page list, so any page size and layout will do; page
+// numbers are fetched one step before the copies that need them.
+//
+// Arithmetic.  Positions are the rows (M = 16) and heads the columns (N = 8) of
+// both products: S^T = K Q^T and O^T += V^T P^T with mma.sync m16n8k16, K as it
+// lies and V transposed by ldmatrix.  Eight heads fill a tile, where heads as
+// rows would leave half of sixteen empty, and P^T turns from accumulator to
+// operand by one 8 x 8 transpose per eight positions.  (tcgen05 needs 64 or 128
+// rows of one operand: with 8 heads at most 1/8 of it would be used, and P would
+// have to go through shared or tensor memory, to speed up what is not the bound.)
+// The softmax keeps a running reference m (at first the maximum; moved when
+// exceeded by a factor 2^8, so that the output is rarely rescaled) and the sum
+// of the unrounded weights in fp32; P is rounded to the 16-bit type of the
+// product (half a step of 2^-8 or 2^-11, averaged over the positions), as the
+// tensor core takes no wider operand at this rate.
+//
+// e4m3 rows are widened to fp16 exactly.  The row's key scale multiplies its
+// score; its value scale joins the exponent, w_j = 2^(t_j + log2 vs_j - m), and
+// comes off the sum again (w_j / vs_j), so P stays near 1 and in fp16's range
+// whatever the scales are.  bf16 queries enter that product as fp16 after a
+// power of two per head has been taken out.
+//
+// Weights.  p_j is known only when the item is joined, so the scores (fp32) go
+// to the workspace and a second kernel adds 2^(t_j - m) / sum over the group.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -18,127 +57,742 @@
 
 namespace tgemm {
 
-constexpr int kAttendWarps = 8;
-constexpr int kAttendMaxDim = 256;
+constexpr int kAttendWarps = 4;
+constexpr int kAttendThreads = 32 * kAttendWarps;
+constexpr int kAttendMaxCtas = 512;       // CTAs at most (workspace slots)
+constexpr int kAttendFanIn = 16;          // parts joined at once, and the least that a group's joiner has room for
+static_assert(kAttendMaxCtas / kAttendFanIn >= kAttendFanIn, "room for the parts and for the groups");
+constexpr int kAttendLeast = 4;           // tiles a CTA takes at least
+constexpr float kAttendGrow = 8.0f;       // log2 of the factor that moves the reference
+
+// The workspace: arrival counters (zero between calls), the parts' outputs
+// and their (m, l), then, with weights, each head's (m, l) and scores.
+struct AttendSpace {
+    unsigned *parts;        // [2 * kAttendMaxCtas]: arrivals at a group of parts, by its first part's slot
+    unsigned *groups;       // [2 * kAttendMaxCtas]: arrivals of an item's groups, by its first part's slot
+    float *out;             // [2 * kAttendMaxCtas][heads of a block][padded dim]
+    float2 *ml;             // [2 * kAttendMaxCtas][heads of a block]
+    float2 *stats;          // [batch, q_heads]
+    float *scores;          // [batch, q_heads, positions]
+};
 
 struct AttendParams {
     KvView cache;
     KvTable table;
     KvWeights weights;
+    AttendSpace space;
     const unsigned char *q;
     unsigned char *o;
     long long q_batch_stride, q_head_stride, o_batch_stride, o_head_stride;   // bytes
-    int group;
+    long long positions;                  // of a row of scores
+    int group, blocks;                    // query heads of a key head; blocks that they make
     int window;
-    float scale, cap;
+    // A score in log2 units is first * (q . k); capped, last * (1 - 2 / (1 + 2^(first * (q . k)))),
+    // which is last * tanh.
+    float first, last;
+    bool capped;
     unsigned int *status;
 };
 
+template <bool kE4m3, int DP, int NT>
+struct AttendShape {
+    static constexpr int kRow = DP * (kE4m3 ? 1 : 2);                     // bytes of a row in shared memory
+    static constexpr int kKeys = kRow >= 256 ? 16 : 16 * (256 / kRow);    // positions of a warp's step: 4 KiB of keys
+    static constexpr int kTile = kAttendWarps * kKeys;
+    static constexpr int kHeads = 8 * NT;
+    static constexpr int kStages = 3;
+    static constexpr int kScales = kE4m3 ? 2 * kKeys * 4 : 0;
+    static constexpr int kStage = 2 * kKeys * kRow + kScales + 16;        // keys, values, scales, mask
+    static constexpr int kRing = kAttendWarps * kStages * kStage;
+    static constexpr int kPitch = DP + 4;                                 // floats: heads 2t, dims g fall into different banks
+    static constexpr int kBytes = kRing + kHeads * kPitch * 4;
+    static constexpr int kCtas = kBytes + 4096 <= 115712 ? 2 : 1;         // per SM: 228 KiB, of which each CTA also takes 1 KiB and its statics
+    static_assert(kBytes + 4096 <= 232448, "a CTA's shared memory");
+};
+
+// ---------------------------------------------------------------- primitives
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
+    const int bytes = ok ? 16 : 0;          // 0: the destination is filled with zeros, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool ok) {
+    const int bytes = ok ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 template <bool kBf16>
-__device__ __forceinline__ float load16(const unsigned char *p, int i) {
-    if (kBf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
-    return __half2float(reinterpret_cast<const __half *>(p)[i]);
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (kBf16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <bool kBf16, bool kE4m3>
-__device__ __forceinline__ float load_row(const unsigned char *p, int i) {
-    if (kE4m3) {
-        const __nv_fp8_storage_t b = p[i];
-        return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
+// Two e4m3 values (the low 16 bits) as two fp16 ones.
+__device__ __forceinline__ uint32_t widen2(uint32_t x) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<unsigned short>(x)));
+    return y;
+}
+
+// 2^x, results below 2^-126 flushed to zero (relative error about 2^-22).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pair16(float lo, float hi) {
+    if (kBf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
     }
-    return load16<kBf16>(p, i);
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-template <bool kBf16, bool kE4m3>
-__global__ void __launch_bounds__(kAttendWarps * 32) kv_attend_kernel(const AttendParams p) {
-    constexpr int kPer = kAttendMaxDim / 32;
-    __shared__ float part_o[kAttendWarps][kAttendMaxDim];
-    __shared__ float part_m[kAttendWarps], part_l[kAttendWarps];
+// ---------------------------------------------------------------- the runs
+// Where a run is: the item (sequence b, head h of its heads * blocks) and the
+// tile in it.
+struct AttendCursor {
+    int b, h, tile, tiles, n, lo;
+};
+
+// Positions and tiles of a sequence; `pad`: tiles come in multiples of it.
+__host__ __device__ inline int attend_tiles(int n, int window, int tile, int pad, int *lo) {
+    *lo = window > 0 && n > window ? n - window : 0;
+    int t = (n - *lo + tile - 1) / tile;
+    if (t < 1) t = 1;                       // an empty sequence still has its zeros to write
+    return (t + pad - 1) / pad * pad;
+}
+
+// CTA c of `ctas` has the tiles [attend_first(c), attend_first(c + 1)) of `total`;
+// attend_owner() is the inverse.
+__host__ __device__ inline long long attend_first(long long c, long long ctas, long long total) {
+    return c * total / ctas;
+}
+__host__ __device__ inline int attend_owner(long long t, long long ctas, long long total) {
+    return static_cast<int>(((t + 1) * ctas - 1) / total);
+}
+
+// The slot of CTA c's part of an item whose first part is CTA `first`'s: a CTA
+// has at most one part that it begins and one that it continues.
+__host__ __device__ inline int attend_slot(int c, int first) { return 2 * c + (c == first ? 1 : 0); }
+
+__device__ __forceinline__ void cursor_load(AttendCursor &u, const AttendParams &p, int tile, int pad) {
+    bool bad = false;
+    u.n = kv_length(p.table.lengths[u.b], p.table.width, p.cache.page_size, &bad);
+    u.tiles = attend_tiles(u.n, p.window, tile, pad, &u.lo);
+}
+
+__device__ __forceinline__ void cursor_next(AttendCursor &u, const AttendParams &p, int tile, int pad) {
+    if (++u.tile < u.tiles) return;
+    u.tile = 0;
+    if (++u.h < p.cache.heads * p.blocks) return;
+    u.h = 0;
+    if (++u.b < p.table.batch) cursor_load(u, p, tile, pad);
+}
+
+template <bool kBf16, bool kE4m3, int DP, int NT>
+__global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kCtas)
+    kv_attend_kernel(const AttendParams p) {
+    using S = AttendShape<kE4m3, DP, NT>;
+    constexpr bool kMmaBf16 = kBf16 && !kE4m3;      // e4m3 is widened to fp16
+    constexpr int kChunks = S::kRow / 16;           // 16-byte pieces of a row
+    constexpr int kRowsPerCopy = 32 / kChunks;      // rows that a warp's copy instruction covers
+    constexpr int kLaneRows = (S::kKeys + 31) / 32; // rows whose place a lane looks up
+    constexpr int kBlocks = S::kKeys / 16;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long s_sum[2][kAttendWarps];
+    __shared__ int s_start[3];
+    __shared__ float s_m[kAttendWarps][S::kHeads], s_l[kAttendWarps][S::kHeads];
+    __shared__ float s_w[kAttendMaxCtas / kAttendFanIn][S::kHeads];
+    __shared__ float s_inv[S::kHeads], s_ref[S::kHeads];
+    __shared__ unsigned s_last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t4 = lane & 3;
+    float *merge = reinterpret_cast<float *>(smem + S::kRing);
+    const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kStage;
+    unsigned char *ring_ptr = smem + warp * S::kStages * S::kStage;
     griddep_wait();
     griddep_launch_dependents();
-    const int head = blockIdx.x, b = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    bool bad = false;
-    const int n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
-    if (bad && threadIdx.x == 0) record_status(p.status, kStatusCache);
-    const int lo = p.window > 0 && n > p.window ? n - p.window : 0;
-    const int *list = p.table.pages + b * p.table.stride;
-    float q[kPer];
-    auto score = [&](int j, float *ks_out, const unsigned char **vrow, float *vs) {
-        int page, slot;
-        if (!kv_row(list, j, p.cache.page_size, p.cache.pages, &page, &slot)) return false;
-        const unsigned char *krow = p.cache.k + kv_offset(p.cache, page, slot, head);
-        float s = 0.0f;
+
+    // ---- this CTA's run: all lengths summed, once as they are and once with
+    // runs of kAttendLeast tiles that end with their item
+    const int heads_all = p.cache.heads * p.blocks;
+    const int each = (p.table.batch + kAttendThreads - 1) / kAttendThreads;
+    const int b_lo = min(p.table.batch, static_cast<int>(threadIdx.x) * each), b_hi = min(p.table.batch, b_lo + each);
+    long long mine[2] = {0, 0};
+    for (int b = b_lo; b < b_hi; ++b) {
+        bool bad = false;
+        int lo;
+        const int n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
+        if (bad && blockIdx.x == 0) record_status(p.status, kStatusCache);
+        mine[0] += attend_tiles(n, p.window, S::kTile, 1, &lo);
+        mine[1] += attend_tiles(n, p.window, S::kTile, kAttendLeast, &lo);
+    }
+    long long upto[2] = {mine[0], mine[1]};
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (lane + 32 * i < p.cache.dim) s += q[i] * load_row<kBf16, kE4m3>(krow, lane + 32 * i);
+    for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (kE4m3) {
-            const long long at = kv_scale_offset(p.cache, page, slot, head);
-            s *= p.cache.k_scale[at];
-            *vs = p.cache.v_scale[at];
-        } else {
-            *vs = 1.0f;
+        for (int i = 0; i < 2; ++i) {
+            const long long u = __shfl_up_sync(0xffffffffu, upto[i], o);
+            if (lane >= o) upto[i] += u;
         }
-        s *= p.scale;
-        if (p.cap > 0.0f) s = p.cap * tanhf(s / p.cap);
-        *vrow = p.cache.v + kv_offset(p.cache, page, slot, head);
-        *ks_out = s;
-        return true;
+    if (lane == 31) {
+        s_sum[0][warp] = upto[0];
+        s_sum[1][warp] = upto[1];
+    }
+    __syncthreads();
+    long long total[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        for (int w = 0; w < kAttendWarps; ++w) {
+            if (w < warp) upto[i] += s_sum[i][w];
+            total[i] += s_sum[i][w];
+        }
+    const bool few = total[1] * heads_all <= static_cast<long long>(gridDim.x) * kAttendLeast;
+    const int pad = few ? kAttendLeast : 1;
+    const long long all = (few ? total[1] : total[0]) * heads_all;
+    const int ctas = static_cast<int>(few ? all / kAttendLeast : min(static_cast<long long>(gridDim.x), all));
+    const int cta = blockIdx.x;
+    if (cta >= ctas) return;
+    const long long first = attend_first(cta, ctas, all), last = attend_first(cta + 1, ctas, all);
+    {
+        const long long end = (few ? upto[1] : upto[0]) * heads_all;
+        long long at = end - (few ? mine[1] : mine[0]) * heads_all;
+        if (first >= at && first < end)
+            for (int b = b_lo; b < b_hi; ++b) {
+                bool bad = false;
+                int lo;
+                const int n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
+                const int tiles = attend_tiles(n, p.window, S::kTile, pad, &lo);
+                if (first < at + static_cast<long long>(tiles) * heads_all) {
+                    const long long in = first - at;
+                    s_start[0] = b;
+                    s_start[1] = static_cast<int>(in / tiles);
+                    s_start[2] = static_cast<int>(in % tiles);
+                    break;
+                }
+                at += static_cast<long long>(tiles) * heads_all;
+            }
+    }
+    __syncthreads();
+    const int steps = static_cast<int>(last - first);
+
+    // ---- loading: the places of the next step's rows are looked up, then copied
+    AttendCursor load;
+    load.b = s_start[0];
+    load.h = s_start[1];
+    load.tile = s_start[2];
+    cursor_load(load, p, S::kTile, pad);
+    AttendCursor use = load;
+    int page[kLaneRows], slot[kLaneRows], load_head = 0;
+    unsigned want[kLaneRows];
+    int looked = 0;
+    auto lookup = [&]() {
+        load_head = load.h / p.blocks;
+        const int pos0 = load.lo + load.tile * S::kTile + warp * S::kKeys;
+        const int *list = p.table.pages + load.b * p.table.stride;
+#pragma unroll
+        for (int r = 0; r < kLaneRows; ++r) {
+            const int row = lane + 32 * r, pos = pos0 + row;
+            const bool in = row < S::kKeys && pos < load.n && looked < steps;
+            const int i = in ? static_cast<int>(static_cast<unsigned>(pos) / static_cast<unsigned>(p.cache.page_size)) : 0;
+            slot[r] = pos - i * p.cache.page_size;
+            page[r] = in ? list[i] : -1;
+            want[r] = __ballot_sync(0xffffffffu, in);
+        }
+        if (++looked < steps) cursor_next(load, p, S::kTile, pad);
     };
-    for (int g = 0; g < p.group; ++g) {
-        const int qh = head * p.group + g;
-        const unsigned char *qrow = p.q + b * p.q_batch_stride + qh * p.q_head_stride;
+    const unsigned char *kpool = p.cache.k, *vpool = p.cache.v;
+    auto issue = [&](int stage) {
+        const uint32_t dst = ring + stage * S::kStage;
+        long long off[kLaneRows];
+        unsigned ok[kLaneRows];
+        unsigned some = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) q[i] = lane + 32 * i < p.cache.dim ? load16<kBf16>(qrow, lane + 32 * i) : 0.0f;
-        float m = -INFINITY, l = 0.0f, o[kPer] = {};
-        for (int j = lo + warp; j < n; j += kAttendWarps) {
-            float s, vs;
-            const unsigned char *vrow;
-            if (!score(j, &s, &vrow, &vs)) {
-                if (lane == 0) record_status(p.status, kStatusCache);
-                continue;
-            }
-            const float m_new = fmaxf(m, s);
-            const float a = expf(m - m_new), w = expf(s - m_new);
-            l = l * a + w;
-            m = m_new;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (lane + 32 * i < p.cache.dim)
-                    o[i] = o[i] * a + w * vs * load_row<kBf16, kE4m3>(vrow, lane + 32 * i);
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) part_o[warp][lane + 32 * i] = o[i];
-        if (lane == 0) {
-            part_m[warp] = m;
-            part_l[warp] = l;
-        }
-        __syncthreads();
-        float top = -INFINITY, sum = 0.0f;
-        for (int w = 0; w < kAttendWarps; ++w) top = fmaxf(top, part_m[w]);
-        const float ref = top == -INFINITY ? 0.0f : top;
-        for (int w = 0; w < kAttendWarps; ++w) sum += part_l[w] * expf(part_m[w] - ref);
-        for (int d = threadIdx.x; d < p.cache.dim; d += kAttendWarps * 32) {
-            float v = 0.0f;
-            for (int w = 0; w < kAttendWarps; ++w) v += part_o[w][d] * expf(part_m[w] - ref);
-            v = sum != 0.0f ? v / sum : 0.0f;
-            unsigned char *orow = p.o + b * p.o_batch_stride + qh * p.o_head_stride;
-            if (kBf16) reinterpret_cast<__nv_bfloat16 *>(orow)[d] = __float2bfloat16_rn(v);
-            else reinterpret_cast<__half *>(orow)[d] = __float2half_rn(v);
-        }
-        if (p.weights.base) {
-            float *w = p.weights.base + b * p.weights.batch_stride + head * p.weights.head_stride;
-            for (int j = lo + warp; j < n; j += kAttendWarps) {
-                float s, vs;
-                const unsigned char *vrow;
-                if (!score(j, &s, &vrow, &vs) || lane != 0) continue;
-                if (j < p.weights.width) w[j] += expf(s - ref) / sum;
-                else record_status(p.status, kStatusCache);
+        for (int r = 0; r < kLaneRows; ++r) {
+            const bool in = page[r] >= 0 && page[r] < p.cache.pages;
+            ok[r] = __ballot_sync(0xffffffffu, in);
+            some |= want[r];
+            if (ok[r] != want[r] && lane == 0) record_status(p.status, kStatusCache);
+            off[r] = in ? kv_offset(p.cache, page[r], slot[r], load_head) : 0;
+            if (kE4m3 && want[r]) {
+                const int row = lane + 32 * r;
+                const long long so = in ? kv_scale_offset(p.cache, page[r], slot[r], load_head) : 0;
+                if (row < S::kKeys) {
+                    cp_async4(dst + 2 * S::kKeys * S::kRow + 4 * row, p.cache.k_scale + so, in);
+                    cp_async4(dst + 2 * S::kKeys * S::kRow + 4 * (S::kKeys + row), p.cache.v_scale + so, in);
+                }
             }
         }
-        __syncthreads();
+        if (some) {
+            const int chunk = lane % kChunks;
+            const bool inside = chunk * 16 < p.cache.row_bytes;     // past dim: zeros
+#pragma unroll
+            for (int i = 0; i < S::kKeys / kRowsPerCopy; ++i) {
+                const int row = i * kRowsPerCopy + lane / kChunks;
+                const long long o = __shfl_sync(0xffffffffu, off[(i * kRowsPerCopy) / 32], row & 31);
+                const bool good = inside && ((ok[(i * kRowsPerCopy) / 32] >> (row & 31)) & 1u);
+                const int sw = kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1));
+                const uint32_t to = dst + row * S::kRow + ((chunk ^ sw) << 4);
+                cp_async16(to, kpool + o + chunk * 16 * (good ? 1 : 0), good);
+                cp_async16(to + S::kKeys * S::kRow, vpool + o + chunk * 16 * (good ? 1 : 0), good);
+            }
+        }
+        if (lane < kLaneRows)
+            *reinterpret_cast<unsigned *>(ring_ptr + stage * S::kStage + 2 * S::kKeys * S::kRow + S::kScales + 4 * lane) =
+                kLaneRows == 1 || lane == 0 ? ok[0] : ok[kLaneRows - 1];
+        cp_async_commit();
+    };
+
+    lookup();
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) {
+        issue(s);
+        lookup();
+    }
+
+    // ---- the item at hand
+    uint32_t qf[NT][DP / 16][2];
+    float qscale[NT][2];                   // to log2 units, for heads 2 t4 and 2 t4 + 1
+    float o[NT][DP / 16][4], m[NT][2], l[NT][2];
+    bool fresh = true;
+    int begun = use.tile;                  // first tile of this CTA's part
+    int stage = 0;
+    for (int step = 0; step < steps; ++step) {
+        const int head = use.h / p.blocks, block = use.h - head * p.blocks;
+        const int h0 = block * S::kHeads, hn = min(S::kHeads, p.group - h0);    // heads of the group in this block
+        if (fresh) {
+            fresh = false;
+            begun = use.tile;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int qh = h0 + 8 * nt + g;
+                const bool is = 8 * nt + g < hn;
+                const unsigned char *row = p.q + use.b * p.q_batch_stride +
+                                           (static_cast<long long>(head) * p.group + (is ? qh : h0)) * p.q_head_stride;
+                float top = 0.0f;
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int d = kE4m3 ? 16 * kk + 4 * t4 + 2 * i : 16 * kk + 2 * t4 + 8 * i;
+                        const uint32_t x = is && d < p.cache.dim ? *reinterpret_cast<const uint32_t *>(row + 2 * d) : 0u;
+                        qf[nt][kk][i] = x;
+                        if (kE4m3 && kBf16)
+                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x << 16)), fabsf(__uint_as_float(x & 0xFFFF0000u))));
+                    }
+                float unit = 1.0f;
+                if (kE4m3 && kBf16) {
+                    // Largest element to [2^14, 2^15): fp16 then keeps bf16's eight bits down to
+                    // 2^-29 of it.
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;      // -127 for zero
+                    const int shift = min(max(14 - e, -126), 126);
+                    const float up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+                    unit = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+#pragma unroll
+                    for (int kk = 0; kk < DP / 16; ++kk)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t x = qf[nt][kk][i];
+                            qf[nt][kk][i] = pair16<false>(__uint_as_float(x << 16) * up,
+                                                          __uint_as_float(x & 0xFFFF0000u) * up);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    qscale[nt][i] = p.first * __shfl_sync(0xffffffffu, unit, (2 * t4 + i) * 4);
+                    m[nt][i] = -INFINITY;
+                    l[nt][i] = 0.0f;
+                }
+#pragma unroll
+                for (int mt = 0; mt < DP / 16; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.0f;
+            }
+        }
+        cp_async_wait<S::kStages - 2>();
+        __syncwarp();
+        // the stage that the previous step has read takes the step that comes kStages - 1 after this one
+        issue(stage == 0 ? S::kStages - 1 : stage - 1);
+        lookup();
+        const uint32_t src = ring + stage * S::kStage;
+        const unsigned char *src_ptr = ring_ptr + stage * S::kStage;
+        const unsigned *mask_ptr = reinterpret_cast<const unsigned *>(src_ptr + 2 * S::kKeys * S::kRow + S::kScales);
+        unsigned some = mask_ptr[0];
+        if (kLaneRows > 1) some |= mask_ptr[1];
+        if (some) {
+            // S^T = K Q^T
+            float s[NT][kBlocks][4];
+#pragma unroll
+            for (int kb = 0; kb < kBlocks; ++kb) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[nt][kb][i] = 0.0f;
+                // 16-bit: matrices (rows 0-7 | 8-15) x (chunk 0 | 1), one k step; e4m3: the same bytes are two k steps.
+                const int row = 16 * kb + (lane & 7) + ((lane >> 3) & 1) * 8, half = lane >> 4;
+                const int sw = kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1));
+#pragma unroll
+                for (int c = 0; c < kChunks / 2; ++c) {
+                    uint32_t a[4];
+                    ldmatrix4(a, src + row * S::kRow + (((2 * c + half) ^ sw) << 4));
+                    if (!kE4m3) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816<kMmaBf16>(s[nt][kb], a, qf[nt][c][0], qf[nt][c][1]);
+                    } else {
+                        // a[0] / a[1]: rows g / g + 8 of dims 32 c + 4 t4 .. + 3; a[2] / a[3]: of the next 16 dims
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t w[4] = {widen2(a[2 * i]), widen2(a[2 * i + 1]), widen2(a[2 * i] >> 16),
+                                                   widen2(a[2 * i + 1] >> 16)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<false>(s[nt][kb], w, qf[nt][2 * c + i][0], qf[nt][2 * c + i][1]);
+                        }
+                    }
+                }
+            }
+            // scores in log2 units, masked; the value scales join the exponent
+            float lv[kBlocks][2], inv[kBlocks][2];
+            const float *scales = reinterpret_cast<const float *>(src_ptr + 2 * S::kKeys * S::kRow);
+            const int pos0 = use.lo + use.tile * S::kTile + warp * S::kKeys;
+#pragma unroll
+            for (int kb = 0; kb < kBlocks; ++kb)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = 16 * kb + g + 8 * r;
+                    const bool in = (mask_ptr[kLaneRows > 1 ? row >> 5 : 0] >> (row & 31)) & 1u;
+                    float ks = 1.0f;
+                    if (kE4m3) {
+                        ks = scales[row];
+                        const float vs = in ? scales[S::kKeys + row] : 1.0f;
+                        lv[kb][r] = __log2f(vs);
+                        inv[kb][r] = __fdividef(1.0f, vs);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float x = s[nt][kb][2 * r + i] * qscale[nt][i];
+                            if (kE4m3) x *= ks;
+                            if (p.capped) x = p.last * (1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x)));
+                            if (p.space.scores) {
+                                const int h = 8 * nt + 2 * t4 + i;
+                                if (in && h < hn)
+                                    p.space.scores[(static_cast<long long>(use.b) * p.cache.heads * p.group +
+                                                    head * p.group + h0 + h) * p.positions + pos0 + row] = x;
+                            }
+                            if (kE4m3) x += lv[kb][r];
+                            s[nt][kb][2 * r + i] = in ? x : -INFINITY;
+                        }
+                }
+            // the reference moves when some score exceeds it by more than 2^kAttendGrow
+            bool grow = false;
+            float top[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x = -INFINITY;
+#pragma unroll
+                    for (int kb = 0; kb < kBlocks; ++kb) x = fmaxf(x, fmaxf(s[nt][kb][i], s[nt][kb][2 + i]));
+                    top[nt][i] = x;
+                    grow |= x > m[nt][i] + kAttendGrow;
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float a[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float x = top[nt][i];
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        const float next = fmaxf(m[nt][i], x);
+                        a[i] = next == -INFINITY ? 1.0f : exp2_fast(m[nt][i] - next);
+                        m[nt][i] = next;
+                        l[nt][i] *= a[i];
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < DP / 16; ++mt) {
+                        o[nt][mt][0] *= a[0];
+                        o[nt][mt][1] *= a[1];
+                        o[nt][mt][2] *= a[0];
+                        o[nt][mt][3] *= a[1];
+                    }
+                }
+            }
+            // weights, their sum, and O^T += V^T P^T
+#pragma unroll
+            for (int kb = 0; kb < kBlocks; ++kb) {
+                uint32_t pf[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float w[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float ref = m[nt][i] == -INFINITY ? 0.0f : m[nt][i];
+                            w[i] = exp2_fast(s[nt][kb][2 * r + i] - ref);
+                            l[nt][i] += kE4m3 ? w[i] * inv[kb][r] : w[i];
+                        }
+                        pf[nt][r] = movmatrix_trans(pair16<kMmaBf16>(w[0], w[1]));
+                    }
+                }
+                const int vrow = 16 * kb + (lane & 7), sel = lane >> 3;
+                if (!kE4m3) {
+                    // matrices: (positions 0-7 | 8-15: sel >> 1) x (dims 0-7 | 8-15: sel & 1)
+                    const int row = vrow + (sel >> 1) * 8;
+                    const int sw = kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1));
+#pragma unroll
+                    for (int mt = 0; mt < DP / 16; ++mt) {
+                        uint32_t a[4];
+                        ldmatrix4_trans(a, src + (S::kKeys + row) * S::kRow + (((2 * mt + (sel & 1)) ^ sw) << 4));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816<kMmaBf16>(o[nt][mt], a, pf[nt][0], pf[nt][1]);
+                    }
+                } else {
+                    // matrices of byte pairs: (positions 0-7 | 8-15: sel & 1) x (dims 0-15 | 16-31: sel >> 1);
+                    // a register holds two positions of dims 2 g and 2 g + 1, which become rows g and g + 8
+                    const int row = vrow + (sel & 1) * 8;
+                    const int sw = kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1));
+#pragma unroll
+                    for (int c = 0; c < DP / 32; ++c) {
+                        uint32_t a[4];
+                        ldmatrix4_trans(a, src + (S::kKeys + row) * S::kRow + (((2 * c + (sel >> 1)) ^ sw) << 4));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t x = __byte_perm(a[2 * i], 0, 0x3120), y = __byte_perm(a[2 * i + 1], 0, 0x3120);
+                            const uint32_t w[4] = {widen2(x), widen2(x >> 16), widen2(y), widen2(y >> 16)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * c + i], w, pf[nt][0], pf[nt][1]);
+                        }
+                    }
+                }
+            }
+        }
+        stage = stage + 1 == S::kStages ? 0 : stage + 1;
+
+        const bool ends = use.tile + 1 == use.tiles;
+        if (ends || step + 1 == steps) {
+            // ---- join the warps: one reference, then the outputs one warp after the other
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
+                    if (g == 0) {
+                        s_m[warp][8 * nt + 2 * t4 + i] = m[nt][i];
+                        s_l[warp][8 * nt + 2 * t4 + i] = l[nt][i];
+                    }
+                }
+            __syncthreads();
+            float a[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int h = 8 * nt + 2 * t4 + i;
+                    float ref = s_m[0][h], sum = 0.0f;
+#pragma unroll
+                    for (int w = 1; w < kAttendWarps; ++w) ref = fmaxf(ref, s_m[w][h]);
+                    const float base = ref == -INFINITY ? 0.0f : ref;
+#pragma unroll
+                    for (int w = 0; w < kAttendWarps; ++w) sum += s_l[w][h] * exp2_fast(s_m[w][h] - base);
+                    a[nt][i] = exp2_fast(m[nt][i] - base);
+                    if (warp == 0 && g == 0) {
+                        s_ref[h] = ref;
+                        s_inv[h] = sum;
+                    }
+                }
+            for (int w = 0; w < kAttendWarps; ++w) {
+                if (warp == w) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int mt = 0; mt < DP / 16; ++mt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int d = 16 * mt + (kE4m3 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
+                                float *at = merge + (8 * nt + 2 * t4 + (i & 1)) * S::kPitch + d;
+                                const float x = o[nt][mt][i] * a[nt][i & 1];
+                                *at = w == 0 ? x : *at + x;
+                            }
+                }
+                __syncthreads();
+            }
+            // ---- whole: the answer; a part: to the workspace, and the last to arrive joins
+            const long long item = first + step - use.tile;      // the item's first tile among all
+            const long long item_end = item + use.tiles;
+            const bool whole = begun == 0 && ends;
+            bool answer = whole;
+            if (!whole) {
+                const int c0 = attend_owner(item, ctas, all), c1 = attend_owner(item_end - 1, ctas, all);
+                const int parts = c1 - c0 + 1, mine_at = cta - c0;
+                const int group = mine_at / kAttendFanIn, groups = (parts + kAttendFanIn - 1) / kAttendFanIn;
+                auto slot_of = [&](int part) { return attend_slot(c0 + part, c0); };
+                auto put = [&](int to) {
+                    float *dst = p.space.out + static_cast<long long>(to) * S::kHeads * DP;
+                    for (int i = threadIdx.x; i < S::kHeads * DP / 4; i += kAttendThreads) {
+                        const int h = i / (DP / 4), d = i % (DP / 4) * 4;
+                        __stcg(reinterpret_cast<float4 *>(dst) + i, *reinterpret_cast<const float4 *>(merge + h * S::kPitch + d));
+                    }
+                    if (threadIdx.x < S::kHeads)
+                        __stcg(p.space.ml + to * S::kHeads + threadIdx.x, make_float2(s_ref[threadIdx.x], s_inv[threadIdx.x]));
+                };
+                // Whether this CTA is the last of `n` to count at `counter` (which then is 0 again).
+                auto arrive = [&](unsigned *counter, int n) {
+                    __threadfence();
+                    __syncthreads();
+                    if (threadIdx.x == 0) s_last = atomicInc(counter, static_cast<unsigned>(n - 1)) == static_cast<unsigned>(n - 1);
+                    __syncthreads();
+                    __threadfence();
+                    return s_last != 0u;
+                };
+                // Joins `n` parts (the first at part0, `stride` apart) into merge, s_ref and s_inv.
+                auto join = [&](int part0, int stride, int n) {
+                    for (int i = threadIdx.x; i < n * S::kHeads; i += kAttendThreads) {
+                        const int e = i / S::kHeads, h = i % S::kHeads;
+                        s_w[e][h] = __ldcg(&p.space.ml[slot_of(part0 + e * stride) * S::kHeads + h].x);
+                    }
+                    __syncthreads();
+                    if (threadIdx.x < S::kHeads) {
+                        const int h = threadIdx.x;
+                        float ref = -INFINITY, sum = 0.0f;
+                        for (int e = 0; e < n; ++e) ref = fmaxf(ref, s_w[e][h]);
+                        const float base = ref == -INFINITY ? 0.0f : ref;
+                        for (int e = 0; e < n; ++e) {
+                            const float w = exp2_fast(s_w[e][h] - base);
+                            s_w[e][h] = w;
+                            sum += w * __ldcg(&p.space.ml[slot_of(part0 + e * stride) * S::kHeads + h].y);
+                        }
+                        s_ref[h] = ref;
+                        s_inv[h] = sum;
+                    }
+                    __syncthreads();
+                    for (int i = threadIdx.x; i < S::kHeads * DP / 4; i += kAttendThreads) {
+                        const int h = i / (DP / 4), d = i % (DP / 4) * 4;
+                        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                        for (int e = 0; e < n; ++e) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(
+                                p.space.out + static_cast<long long>(slot_of(part0 + e * stride)) * S::kHeads * DP) + i);
+                            const float w = s_w[e][h];
+                            sum.x += w * x.x;
+                            sum.y += w * x.y;
+                            sum.z += w * x.z;
+                            sum.w += w * x.w;
+                        }
+                        *reinterpret_cast<float4 *>(merge + h * S::kPitch + d) = sum;
+                    }
+                    __syncthreads();
+                };
+                put(slot_of(mine_at));
+                const int part0 = group * kAttendFanIn, count = min(kAttendFanIn, parts - part0);
+                bool here = arrive(p.space.parts + slot_of(part0), count);
+                if (here) {
+                    join(part0, 1, count);
+                    if (groups > 1) {
+                        put(slot_of(part0));
+                        here = arrive(p.space.groups + slot_of(0), groups);
+                        if (here) join(0, kAttendFanIn, groups);
+                    }
+                }
+                answer = here;
+            }
+            if (answer) {
+                const int h_all = p.cache.heads * p.group;
+                if (threadIdx.x < hn && p.space.scores)
+                    p.space.stats[static_cast<long long>(use.b) * h_all + head * p.group + h0 + threadIdx.x] =
+                        make_float2(s_ref[threadIdx.x], s_inv[threadIdx.x]);
+                for (int i = threadIdx.x; i < hn * (DP / 8); i += kAttendThreads) {
+                    const int h = i / (DP / 8), d = i % (DP / 8) * 8;
+                    if (d >= p.cache.dim) continue;
+                    const float sum = s_inv[h];
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = sum == 0.0f ? 0.0f : merge[h * S::kPitch + d + e] / sum;
+                    const uint4 v = make_uint4(pair16<kBf16>(x[0], x[1]), pair16<kBf16>(x[2], x[3]),
+                                               pair16<kBf16>(x[4], x[5]), pair16<kBf16>(x[6], x[7]));
+                    *reinterpret_cast<uint4 *>(p.o + use.b * p.o_batch_stride +
+                                               (static_cast<long long>(head) * p.group + h0 + h) * p.o_head_stride +
+                                               2 * d) = v;
+                }
+            }
+            __syncthreads();               // merge and the statistics are free again
+            fresh = true;
+        }
+        if (step + 1 < steps) cursor_next(use, p, S::kTile, pad);
+    }
+    cp_async_wait<0>();
+}
+
+// weights[b, head, j] += sum over the group of 2^(t_j - m) / l; one thread per position.
+constexpr int kSpreadThreads = 256;
+
+__global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int head = blockIdx.y, b = blockIdx.z;
+    bool bad = false;
+    int n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
+    int lo;
+    attend_tiles(n, p.window, 1, 1, &lo);
+    if (n > p.weights.width) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kStatusCache);
+        n = p.weights.width;
+    }
+    const int *list = p.table.pages + b * p.table.stride;
+    float *w = p.weights.base + b * p.weights.batch_stride + head * p.weights.head_stride;
+    const long long row0 = static_cast<long long>(b) * p.cache.heads * p.group + head * p.group;
+    for (int j = lo + blockIdx.x * kSpreadThreads + threadIdx.x; j < n; j += gridDim.x * kSpreadThreads) {
+        int page, slot;
+        if (!kv_row(list, j, p.cache.page_size, p.cache.pages, &page, &slot)) continue;   // it has no score
+        float sum = 0.0f;
+        for (int h = 0; h < p.group; ++h) {
+            const float2 ml = p.space.stats[row0 + h];
+            sum += exp2_fast(p.space.scores[(row0 + h) * p.positions + j] - ml.x) / ml.y;
+        }
+        w[j] += sum;
     }
 }
 

@@ -1,6 +1,7 @@
 // The host side of the functions that guard the paged cache's addresses, for
 // tests on a machine without a GPU.
 #include "../gemm_epilogue_02_gb300/csrc/kv_append.cuh"
+#include "../gemm_epilogue_02_gb300/csrc/kv_attend.cuh"
 #include "../gemm_epilogue_02_gb300/csrc/kv_cache.cuh"
 #include "../gemm_epilogue_02_gb300/csrc/kv_evict.cuh"
 
@@ -19,3 +20,21 @@ extern "C" int check_sequence(const int *starts, int batch, long long t) {
 }
 
 extern "C" unsigned check_key(unsigned bits) { return tgemm::kv_weight_key(bits); }
+
+extern "C" int check_tiles(int n, int window, int tile, int pad, int *lo) {
+    return tgemm::attend_tiles(n, window, tile, pad, lo);
+}
+
+extern "C" long long check_first(long long c, long long ctas, long long total) {
+    return tgemm::attend_first(c, ctas, total);
+}
+
+extern "C" int check_owner(long long t, long long ctas, long long total) { return tgemm::attend_owner(t, ctas, total); }
+
+extern "C" int check_slot(int c, int first) { return tgemm::attend_slot(c, first); }
+
+extern "C" void check_limits(int *out) {
+    out[0] = tgemm::kAttendMaxCtas;
+    out[1] = tgemm::kAttendFanIn;
+    out[2] = tgemm::kAttendLeast;
+}

@@ -196,6 +196,10 @@ def host(tmp_path_factory):
     h = ctypes.CDLL(lib)
     h.check_row.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_void_p]
     h.check_sequence.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong]
+    h.check_tiles.argtypes = [ctypes.c_int] * 4 + [ctypes.c_void_p]
+    for f in (h.check_first, h.check_owner):
+        f.argtypes = [ctypes.c_longlong] * 3
+    h.check_first.restype = ctypes.c_longlong
     h.check_key.argtypes, h.check_key.restype = [ctypes.c_uint], ctypes.c_uint
     return h
 
@@ -237,6 +241,74 @@ def test_keys_order_weights_as_numbers(host):
     assert keys == sorted(keys) and len(set(keys)) == len(keys)
     assert key(-0.0) == key(0.0)
     assert key(math.nan) < keys[0] and host.check_key(0xFFC00000) < keys[0]
+
+
+def runs(host, lengths, window, tile, heads, places):
+    """The runs of attention_decode's CTAs: [(first, end)], and each item's [first, end) tiles."""
+    lo = ctypes.c_int()
+    out = (ctypes.c_int * 3)()
+    host.check_limits(out)
+    least = out[2]
+    tiles = [[host.check_tiles(n, window, tile, pad, ctypes.byref(lo)) for n in lengths] for pad in (1, least)]
+    few = sum(tiles[1]) * heads <= places * least
+    counts = tiles[1] if few else tiles[0]
+    total = sum(counts) * heads
+    ctas = total // least if few else min(places, total)
+    items, at = [], 0
+    for c in counts:
+        for _ in range(heads):
+            items.append((at, at + c))
+            at += c
+    return [(host.check_first(c, ctas, total), host.check_first(c + 1, ctas, total)) for c in range(ctas)], items, total
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_runs_cover_every_tile_once_and_parts_have_slots_of_their_own(host, seed):
+    rng = np.random.default_rng(seed)
+    places = int(rng.choice([1, 2, 7, 152, 304, 512]))
+    batch = int(rng.choice([1, 2, 5, 40, 300]))
+    most = int(rng.choice([1, 64, 300, 5000, 200000]))
+    lengths = rng.integers(0, most + 1, batch).tolist()
+    window = int(rng.choice([0, 0, 1, 100]))
+    tile = int(rng.choice([64, 128, 256]))
+    cta_runs, items, total = runs(host, lengths, window, tile, int(rng.choice([1, 2, 8])), places)
+    assert len(cta_runs) <= places
+    assert cta_runs[0][0] == 0 and cta_runs[-1][1] == total
+    assert all(a < b for a, b in cta_runs) and all(x[1] == y[0] for x, y in zip(cta_runs, cta_runs[1:]))
+    limits = (ctypes.c_int * 3)()
+    host.check_limits(limits)
+    slots, counters, tops = set(), set(), set()
+    for first, end in items:
+        c0, c1 = (host.check_owner(t, len(cta_runs), total) for t in (first, end - 1))
+        assert cta_runs[c0][0] <= first < cta_runs[c0][1] and cta_runs[c1][0] < end <= cta_runs[c1][1]
+        if c0 == c1:
+            continue
+        parts = [host.check_slot(c, c0) for c in range(c0, c1 + 1)]
+        assert not slots & set(parts) and len(set(parts)) == len(parts)
+        assert max(parts) < 2 * limits[0]
+        slots |= set(parts)
+        groups = -(-len(parts) // limits[1])
+        assert groups <= limits[0] // limits[1]
+        heads = set(parts[::limits[1]])
+        assert not counters & heads
+        counters |= heads
+        assert parts[0] not in tops
+        tops.add(parts[0])
+
+
+def test_few_tiles_make_runs_that_end_with_their_item(host):
+    cta_runs, items, _ = runs(host, [77, 300, 0, 5000], 0, 64, 2, 304)
+    starts = {a for a, _ in items}
+    assert all(any(a <= r[0] and r[1] <= b for a, b in items) for r in cta_runs)
+    assert starts <= {r[0] for r in cta_runs}
+
+
+def test_tiles_of_lengths_and_windows(host):
+    lo = ctypes.c_int()
+    for n, window, tile, pad, want, want_lo in ((0, 0, 64, 1, 1, 0), (0, 5, 64, 4, 4, 0), (1, 0, 64, 1, 1, 0), (64, 0, 64, 1, 1, 0),
+                                                (65, 0, 64, 1, 2, 0), (65, 0, 64, 4, 4, 0), (65, 64, 64, 1, 1, 1),
+                                                (1000, 130, 64, 1, 3, 870), (1 << 30, 0, 64, 4, 1 << 24, 0)):
+        assert host.check_tiles(n, window, tile, pad, ctypes.byref(lo)) == want and lo.value == want_lo
 
 
 # ---------------------------------------------------------------- the tests' own definitions
