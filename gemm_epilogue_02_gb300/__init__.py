@@ -12,7 +12,7 @@ from ._binding import (  # noqa: F401
     TGEMM_BF16, TGEMM_EPI_BIAS, TGEMM_EPI_BIAS_GELU, TGEMM_EPI_BIAS_RELU, TGEMM_EPI_GELU,
     TGEMM_EPI_NONE, TGEMM_EPI_RELU, TGEMM_F16,
     EXPORTED, NOALLOC_SCRATCH_BYTES, PLAN_FIELDS, STATUS, TgemmError, library_path, load, load_debug,
-    KvCache, tgemm_attention_decode, tgemm_attention_decode_workspace, tgemm_attention_fwd,
+    ATTENTION_DECODE_ARGS, KV_APPEND_ARGS, KV_EVICT_ARGS, KvCache, tgemm_attention_decode, tgemm_attention_decode_workspace, tgemm_attention_fwd,
     tgemm_debug_last_check, tgemm_kv_append, tgemm_kv_evict, tgemm_last_device_status, tgemm_plan, tgemm_run,
     tgemm_run_ex, tgemm_run_host, tgemm_run_noalloc,
     tgemm_status_string, tgemm_version,

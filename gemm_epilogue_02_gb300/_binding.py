@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -38,6 +39,15 @@ class KvCache(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in ("pages", "page_stride", "slot_stride", "head_stride",
                                                  "scale_page_stride", "scale_slot_stride", "scale_head_stride")]
                 + [(n, ctypes.c_int32) for n in ("page_size", "heads", "dim", "e4m3")])
+
+
+# The argument structures of the paged-cache calls, as struct.pack formats (every
+# field takes 8 bytes): pointers and sizes Q / q, real numbers d.
+_SEQUENCES = "QQqqq"          # pages, lengths, pages_width, pages_stride, batch
+_WEIGHTS = "Qqqq"             # data, width, batch_stride, head_stride
+KV_APPEND_ARGS = struct.Struct("=Q" + _SEQUENCES + _WEIGHTS + "QQQqqqq")
+ATTENTION_DECODE_ARGS = struct.Struct("=Q" + _SEQUENCES + _WEIGHTS + "QQqqqqqqddQqq")
+KV_EVICT_ARGS = struct.Struct("=Q" + _SEQUENCES + _WEIGHTS + "Q" + _SEQUENCES + _WEIGHTS + "QQqq")
 
 
 class TgemmError(RuntimeError):
@@ -71,17 +81,12 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.tgemm_plan.restype = i32
     lib.tgemm_attention_fwd.argtypes = [p, p, p, p, i64, i64, i64, i64, i32, i32, p]
     lib.tgemm_attention_fwd.restype = i32
-    f32 = ctypes.c_float
-    weights = [p, i64, i64, i64]
-    lib.tgemm_kv_append.argtypes = [p, p, p, i64, i64, i64, p, p, i64, i64, p, i64, *weights, i32, p]
-    lib.tgemm_kv_append.restype = i32
-    lib.tgemm_attention_decode.argtypes = [p, p, p, i64, i64, i64, i64, i64, i64, p, i64, i64, p, f32, f32, i64,
-                                           *weights, p, i64, i32, p]
-    lib.tgemm_attention_decode.restype = i32
+    for name in ("tgemm_kv_append", "tgemm_attention_decode", "tgemm_kv_evict"):
+        f = getattr(lib, name)
+        f.argtypes = [p, p]
+        f.restype = i32
     lib.tgemm_attention_decode_workspace.argtypes = [i64, i64, i64, i64, i64, i32, p]
     lib.tgemm_attention_decode_workspace.restype = i32
-    lib.tgemm_kv_evict.argtypes = [p, p, i64, i64, p, i64, *weights, p, p, i64, i64, i64, i64, p, p, *weights, p]
-    lib.tgemm_kv_evict.restype = i32
     return lib
 
 
@@ -182,16 +187,19 @@ def tgemm_attention_fwd(Q: int, K: int, V: int, O: int, batch: int, seq: int, he
     return int(load().tgemm_attention_fwd(Q, K, V, O, batch, seq, heads, dim, int(causal), dtype, stream))
 
 
-# The paged key-value cache.  `cache` is a ctypes reference to a KvCache; the
-# other arguments are those of include/tgemm.h in order, pointers as ints.
-def tgemm_kv_append(cache, *args) -> int:
-    lib = _lib if _lib is not None else load()
-    return lib.tgemm_kv_append(cache, *args)
+# The paged key-value cache: `args` are the bytes of the call's argument
+# structure (KV_APPEND_ARGS.pack(...) and so on: the fields of include/tgemm.h
+# in order, pointers as ints).
+def tgemm_kv_append(args: bytes, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_kv_append(args, stream)
 
 
-def tgemm_attention_decode(cache, *args) -> int:
-    lib = _lib if _lib is not None else load()
-    return lib.tgemm_attention_decode(cache, *args)
+def tgemm_attention_decode(args: bytes, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_attention_decode(args, stream)
+
+
+def tgemm_kv_evict(args: bytes, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_kv_evict(args, stream)
 
 
 def tgemm_attention_decode_workspace(batch: int, q_heads: int, kv_heads: int, dim: int, positions: int,
@@ -203,8 +211,3 @@ def tgemm_attention_decode_workspace(batch: int, q_heads: int, kv_heads: int, di
     if st != 0:
         raise TgemmError(st, "tgemm_attention_decode_workspace")
     return int(out.value)
-
-
-def tgemm_kv_evict(cache, *args) -> int:
-    lib = _lib if _lib is not None else load()
-    return lib.tgemm_kv_evict(cache, *args)

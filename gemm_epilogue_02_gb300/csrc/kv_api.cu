@@ -95,38 +95,39 @@ tgemm_status check_cache(const tgemm_kv_cache *c, KvView *view, Extent *k, Exten
     return TGEMM_OK;
 }
 
-// Checks the page lists and lengths of `batch` sequences.
-tgemm_status check_table(const int32_t *pages, int64_t width, int64_t stride, const int32_t *lengths, bool with_lengths,
-                         int64_t batch, int page_size, KvTable *t) {
-    if (batch < 0 || batch > 65535 || width < 0 || width > (1 << 30) / page_size || stride < 0 ||
-        (batch > 1 && stride < width) || stride > (int64_t(1) << 40))
+// Checks the page lists and lengths of a batch.
+tgemm_status check_sequences(const tgemm_kv_sequences &q, bool with_lengths, int page_size, KvTable *t) {
+    if (q.batch < 0 || q.batch > 65535 || q.pages_width < 0 || q.pages_width > (1 << 30) / page_size ||
+        q.pages_stride < 0 || (q.batch > 1 && q.pages_stride < q.pages_width) || q.pages_stride > (int64_t(1) << 40))
         return TGEMM_ERR_INVALID_ARG;
-    if (batch > 0 && ((width > 0 && !pages) || (with_lengths && !lengths))) return TGEMM_ERR_INVALID_ARG;
-    if (!aligned4(pages) || !aligned4(lengths)) return TGEMM_ERR_ALIGNMENT;
-    t->pages = pages;
-    t->lengths = lengths;
-    t->stride = stride;
-    t->width = static_cast<int>(width);
-    t->batch = static_cast<int>(batch);
+    if (q.batch > 0 && ((q.pages_width > 0 && !q.pages) || (with_lengths && !q.lengths))) return TGEMM_ERR_INVALID_ARG;
+    if (!aligned4(q.pages) || !aligned4(q.lengths)) return TGEMM_ERR_ALIGNMENT;
+    t->pages = q.pages;
+    t->lengths = q.lengths;
+    t->stride = q.pages_stride;
+    t->width = static_cast<int>(q.pages_width);
+    t->batch = static_cast<int>(q.batch);
     return TGEMM_OK;
 }
 
-tgemm_status check_weights(const float *base, int64_t width, int64_t batch_stride, int64_t head_stride, int64_t batch,
-                           int64_t heads, KvWeights *w) {
-    w->base = const_cast<float *>(base);
-    w->width = 0;
-    w->batch_stride = w->head_stride = 0;
-    if (!base) return TGEMM_OK;
-    const int64_t size[2] = {batch, heads}, stride[2] = {batch_stride, head_stride};
+tgemm_status check_weights(const tgemm_kv_weights &a, int64_t batch, int64_t heads, KvWeights *w, Extent *e) {
+    std::memset(w, 0, sizeof(*w));
+    *e = Extent();
+    if (!a.data) return TGEMM_OK;
+    const int64_t size[2] = {batch, heads}, stride[2] = {a.batch_stride, a.head_stride};
     int64_t bytes = 0;
-    if (width < 0 || width > INT32_MAX || !extent(size, stride, 2, width, 4, true, &bytes))
+    if (a.width < 0 || a.width > INT32_MAX || !extent(size, stride, 2, a.width, 4, true, &bytes))
         return TGEMM_ERR_INVALID_ARG;
-    if (!aligned4(base)) return TGEMM_ERR_ALIGNMENT;
-    w->width = static_cast<int>(width);
-    w->batch_stride = batch_stride;
-    w->head_stride = head_stride;
+    if (!aligned4(a.data)) return TGEMM_ERR_ALIGNMENT;
+    w->base = a.data;
+    w->width = static_cast<int>(a.width);
+    w->batch_stride = a.batch_stride;
+    w->head_stride = a.head_stride;
+    *e = {a.data, bytes};
     return TGEMM_OK;
 }
+
+bool valid_dtype(int64_t d) { return d == TGEMM_F16 || d == TGEMM_BF16; }
 
 bool all_device(int device, std::initializer_list<const void *> ps) {
     for (const void *p : ps)
@@ -136,19 +137,23 @@ bool all_device(int device, std::initializer_list<const void *> ps) {
 
 // A programmatic dependent of the stream's previous kernel: every kernel here
 // waits for it (griddepcontrol.wait) before it touches global memory.
+// cluster: blocks along x that form a cluster (1: none).
 template <typename P>
-cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P &p) {
+cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P &p, int cluster = 1) {
     cudaLaunchConfig_t lc;
     std::memset(&lc, 0, sizeof(lc));
-    cudaLaunchAttribute la[1];
+    cudaLaunchAttribute la[2];
     la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     la[0].val.programmaticStreamSerializationAllowed = 1;
+    la[1].id = cudaLaunchAttributeClusterDimension;
+    la[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    la[1].val.clusterDim.y = la[1].val.clusterDim.z = 1;
     lc.gridDim = grid;
     lc.blockDim = dim3(static_cast<unsigned>(threads));
     lc.dynamicSmemBytes = smem;
     lc.stream = s;
     lc.attrs = la;
-    lc.numAttrs = 1;
+    lc.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&lc, kernel, p);
 }
 
@@ -156,6 +161,46 @@ tgemm_status done(cudaError_t e) {
     if (e == cudaSuccess) return TGEMM_OK;
     cudaGetLastError();
     return TGEMM_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- rows
+// Lanes that hold a row of `bytes` in 16-byte pieces: the power of two at or above, 8 to 32.
+int row_lanes(int bytes) { return bytes <= 128 ? 8 : bytes <= 256 ? 16 : 32; }
+
+template <bool kBf16, bool kE4m3, int kLanes>
+cudaError_t launch_append_lanes(const RuntimeInfo &rt, const AppendParams &p, cudaStream_t s) {
+    constexpr int kPass = kRowThreads / kLanes;
+    const int64_t passes = (p.tokens * p.cache.heads + kPass - 1) / kPass;
+    if (passes <= 2 * rt.num_sms)
+        return launch(kv_append_kernel<kBf16, kE4m3, kLanes, 1>, dim3(static_cast<unsigned>(passes)), kRowThreads, 0, s, p);
+    const int64_t chunks = std::min<int64_t>((passes + 3) / 4, INT32_MAX);
+    return launch(kv_append_kernel<kBf16, kE4m3, kLanes, 4>, dim3(static_cast<unsigned>(chunks)), kRowThreads, 0, s, p);
+}
+
+template <bool kBf16, bool kE4m3>
+cudaError_t launch_append(const RuntimeInfo &rt, const AppendParams &p, cudaStream_t s) {
+    switch (row_lanes(p.cache.dim * 2)) {
+        case 8: return launch_append_lanes<kBf16, kE4m3, 8>(rt, p, s);
+        case 16: return launch_append_lanes<kBf16, kE4m3, 16>(rt, p, s);
+        default: return launch_append_lanes<kBf16, kE4m3, 32>(rt, p, s);
+    }
+}
+
+template <bool kE4m3, int kLanes>
+cudaError_t launch_gather_lanes(const EvictParams &p, int64_t most, int heads, int batch, cudaStream_t s) {
+    constexpr int kUnroll = 4, kRows = kGatherThreads / kLanes * kUnroll;
+    const int64_t chunks = std::max<int64_t>(1, (most + kRows - 1) / kRows);
+    const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(heads), static_cast<unsigned>(batch));
+    return launch(kv_gather_kernel<kE4m3, kLanes, kUnroll>, grid, kGatherThreads, 0, s, p);
+}
+
+template <bool kE4m3>
+cudaError_t launch_gather(const EvictParams &p, int64_t most, int heads, int batch, cudaStream_t s) {
+    switch (row_lanes(p.from.row_bytes)) {
+        case 8: return launch_gather_lanes<kE4m3, 8>(p, most, heads, batch, s);
+        case 16: return launch_gather_lanes<kE4m3, 16>(p, most, heads, batch, s);
+        default: return launch_gather_lanes<kE4m3, 32>(p, most, heads, batch, s);
+    }
 }
 
 // ---------------------------------------------------------------- attention
@@ -245,54 +290,48 @@ int kv_debug_last_check() {
 
 using namespace tgemm;
 
-extern "C" tgemm_status tgemm_kv_append(const tgemm_kv_cache *cache, const void *K, const void *V, int64_t tokens,
-                                        int64_t token_stride, int64_t head_stride, const int32_t *starts,
-                                        const int32_t *pages, int64_t pages_width, int64_t pages_stride,
-                                        const int32_t *lengths, int64_t batch, float *weights, int64_t weights_width,
-                                        int64_t weights_batch_stride, int64_t weights_head_stride, tgemm_dtype dtype,
-                                        tgemm_stream_t stream) {
+extern "C" tgemm_status tgemm_kv_append(const tgemm_kv_append_args *a, tgemm_stream_t stream) {
     AppendParams p;
     std::memset(&p, 0, sizeof(p));
-    Extent ck, cv;
+    Extent ck, cv, ew;
+    if (!a) return TGEMM_ERR_INVALID_ARG;
+    const tgemm_kv_cache *cache = a->cache;
     tgemm_status st = check_cache(cache, &p.cache, &ck, &cv);
     if (st != TGEMM_OK) return st;
-    if ((dtype != TGEMM_F16 && dtype != TGEMM_BF16) || tokens < 0 || tokens > INT32_MAX || (!starts && tokens != batch))
+    const int64_t tokens = a->tokens, batch = a->seq.batch;
+    if (!valid_dtype(a->dtype) || tokens < 0 || tokens > INT32_MAX || (!a->starts && tokens != batch))
         return TGEMM_ERR_INVALID_ARG;
-    st = check_table(pages, pages_width, pages_stride, lengths, true, batch, cache->page_size, &p.table);
+    st = check_sequences(a->seq, true, cache->page_size, &p.table);
     if (st != TGEMM_OK) return st;
-    st = check_weights(weights, weights_width, weights_batch_stride, weights_head_stride, batch, cache->heads,
-                       &p.weights);
+    st = check_weights(a->weights, batch, cache->heads, &p.weights, &ew);
     if (st != TGEMM_OK) return st;
-    const int64_t size[2] = {tokens, cache->heads}, stride[2] = {token_stride, head_stride};
+    const int64_t size[2] = {tokens, cache->heads}, stride[2] = {a->token_stride, a->head_stride};
     int64_t bytes = 0;
     if (!extent(size, stride, 2, cache->dim, 2, false, &bytes)) return TGEMM_ERR_INVALID_ARG;
     if (tokens == 0 || batch == 0) return TGEMM_OK;
-    if (!K || !V) return TGEMM_ERR_INVALID_ARG;
-    if (!aligned16(K) || !aligned16(V) || !aligned4(starts) || (tokens > 1 && token_stride % 8 != 0) ||
-        (cache->heads > 1 && head_stride % 8 != 0))
+    if (!a->K || !a->V) return TGEMM_ERR_INVALID_ARG;
+    if (!aligned16(a->K) || !aligned16(a->V) || !aligned4(a->starts) || (tokens > 1 && a->token_stride % 8 != 0) ||
+        (cache->heads > 1 && a->head_stride % 8 != 0))
         return TGEMM_ERR_ALIGNMENT;
-    const Extent nk = {K, bytes}, nv = {V, bytes};
+    const Extent nk = {a->K, bytes}, nv = {a->V, bytes};
     if (overlaps(nk, ck) || overlaps(nk, cv) || overlaps(nv, ck) || overlaps(nv, cv) || cache->k == cache->v)
         return TGEMM_ERR_ALIAS;
     RuntimeInfo rt;
     st = runtime_current(&rt);
     if (st != TGEMM_OK) return st;
-    if (!all_device(rt.device, {K, V, starts, pages, lengths, weights, cache->k, cache->v,
+    if (!all_device(rt.device, {a->K, a->V, a->starts, a->seq.pages, a->seq.lengths, a->weights.data, cache->k, cache->v,
                                 cache->e4m3 ? cache->k_scale : nullptr, cache->e4m3 ? cache->v_scale : nullptr}))
         return TGEMM_ERR_INVALID_ARG;
-    p.k = static_cast<const unsigned char *>(K);
-    p.v = static_cast<const unsigned char *>(V);
-    p.token_stride = token_stride * 2;
-    p.head_stride = head_stride * 2;
-    p.starts = starts;
+    p.k = static_cast<const unsigned char *>(a->K);
+    p.v = static_cast<const unsigned char *>(a->V);
+    p.token_stride = a->token_stride * 2;
+    p.head_stride = a->head_stride * 2;
+    p.starts = a->starts;
     p.tokens = tokens;
     p.status = rt.status;
-    const int64_t rows = tokens * cache->heads, per = kAppendThreads / 32;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((rows + per - 1) / per, rt.num_sms * 8)));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (!cache->e4m3) return done(launch(kv_append_kernel<false, false>, grid, kAppendThreads, 0, s, p));
-    if (dtype == TGEMM_BF16) return done(launch(kv_append_kernel<true, true>, grid, kAppendThreads, 0, s, p));
-    return done(launch(kv_append_kernel<false, true>, grid, kAppendThreads, 0, s, p));
+    if (!cache->e4m3) return done(launch_append<false, false>(rt, p, s));
+    return done(a->dtype == TGEMM_BF16 ? launch_append<true, true>(rt, p, s) : launch_append<false, true>(rt, p, s));
 }
 
 extern "C" tgemm_status tgemm_attention_decode_workspace(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim,
@@ -306,76 +345,69 @@ extern "C" tgemm_status tgemm_attention_decode_workspace(int64_t batch, int64_t 
     return TGEMM_OK;
 }
 
-extern "C" tgemm_status tgemm_attention_decode(const tgemm_kv_cache *cache, const void *Q, void *O, int64_t batch,
-                                               int64_t q_heads, int64_t q_batch_stride, int64_t q_head_stride,
-                                               int64_t o_batch_stride, int64_t o_head_stride, const int32_t *pages,
-                                               int64_t pages_width, int64_t pages_stride, const int32_t *lengths,
-                                               float scale, float cap, int64_t window, float *weights,
-                                               int64_t weights_width, int64_t weights_batch_stride,
-                                               int64_t weights_head_stride, void *workspace, int64_t workspace_bytes,
-                                               tgemm_dtype dtype, tgemm_stream_t stream) {
+extern "C" tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args *a, tgemm_stream_t stream) {
     AttendParams p;
     std::memset(&p, 0, sizeof(p));
-    Extent ck, cv;
+    Extent ck, cv, ex;
+    if (!a) return TGEMM_ERR_INVALID_ARG;
+    const tgemm_kv_cache *cache = a->cache;
     tgemm_status st = check_cache(cache, &p.cache, &ck, &cv);
     if (st != TGEMM_OK) return st;
-    if ((dtype != TGEMM_F16 && dtype != TGEMM_BF16) || q_heads < 1 || q_heads > 65535 || q_heads % cache->heads != 0 ||
-        !std::isfinite(scale) || !std::isfinite(cap) || cap < 0.0f || window < 0)
+    const int64_t batch = a->seq.batch, q_heads = a->q_heads;
+    if (!valid_dtype(a->dtype) || q_heads < 1 || q_heads > 65535 || q_heads % cache->heads != 0 ||
+        !std::isfinite(a->scale) || !std::isfinite(a->cap) || a->cap < 0.0 || a->window < 0)
         return TGEMM_ERR_INVALID_ARG;
-    st = check_table(pages, pages_width, pages_stride, lengths, true, batch, cache->page_size, &p.table);
+    st = check_sequences(a->seq, true, cache->page_size, &p.table);
     if (st != TGEMM_OK) return st;
-    st = check_weights(weights, weights_width, weights_batch_stride, weights_head_stride, batch, cache->heads,
-                       &p.weights);
+    st = check_weights(a->weights, batch, cache->heads, &p.weights, &ex);
     if (st != TGEMM_OK) return st;
     const int64_t size[2] = {batch, q_heads};
-    const int64_t qs[2] = {q_batch_stride, q_head_stride}, os[2] = {o_batch_stride, o_head_stride};
+    const int64_t qs[2] = {a->q_batch_stride, a->q_head_stride}, os[2] = {a->o_batch_stride, a->o_head_stride};
     int64_t qbytes = 0, obytes = 0;
     if (!extent(size, qs, 2, cache->dim, 2, false, &qbytes) || !extent(size, os, 2, cache->dim, 2, true, &obytes))
         return TGEMM_ERR_INVALID_ARG;
-    int64_t need = 0;
-    st = tgemm_attention_decode_workspace(batch, q_heads, cache->heads, cache->dim, pages_width * cache->page_size,
-                                          weights ? 1 : 0, &need);
-    if (st != TGEMM_OK) return st;
+    p.group = static_cast<int>(q_heads / cache->heads);
+    p.positions = a->seq.pages_width * cache->page_size;
+    const int64_t need = attend_layout(batch, q_heads, p.group, cache->dim, p.positions, a->weights.data != nullptr,
+                                       static_cast<unsigned char *>(a->workspace), &p.space);
+    if (need < 0) return TGEMM_ERR_INVALID_ARG;
     if (batch == 0) return TGEMM_OK;
-    if (!Q || !O || !workspace || workspace_bytes < need) return TGEMM_ERR_INVALID_ARG;
-    if (!aligned16(Q) || !aligned16(O) || !aligned16(workspace) || (batch > 1 && (q_batch_stride | o_batch_stride) % 8) ||
-        (q_heads > 1 && (q_head_stride | o_head_stride) % 8))
+    if (!a->Q || !a->O || !a->workspace || a->workspace_bytes < need) return TGEMM_ERR_INVALID_ARG;
+    if (!aligned16(a->Q) || !aligned16(a->O) || !aligned16(a->workspace) ||
+        (batch > 1 && (a->q_batch_stride | a->o_batch_stride) % 8) ||
+        (q_heads > 1 && (a->q_head_stride | a->o_head_stride) % 8))
         return TGEMM_ERR_ALIGNMENT;
-    const Extent eo = {O, obytes}, ew = {workspace, need};
-    if (overlaps(eo, {Q, qbytes}) || overlaps(eo, ck) || overlaps(eo, cv) || overlaps(ew, eo) ||
-        overlaps(ew, {Q, qbytes}) || overlaps(ew, ck) || overlaps(ew, cv))
+    const Extent eo = {a->O, obytes}, eq = {a->Q, qbytes}, ew = {a->workspace, need};
+    if (overlaps(eo, eq) || overlaps(eo, ck) || overlaps(eo, cv) || overlaps(eo, ex) || overlaps(ew, eo) ||
+        overlaps(ew, eq) || overlaps(ew, ck) || overlaps(ew, cv) || overlaps(ew, ex))
         return TGEMM_ERR_ALIAS;
     RuntimeInfo rt;
     st = runtime_current(&rt);
     if (st != TGEMM_OK) return st;
-    if (!all_device(rt.device, {Q, O, pages, lengths, weights, workspace, cache->k, cache->v,
+    if (!all_device(rt.device, {a->Q, a->O, a->seq.pages, a->seq.lengths, a->weights.data, a->workspace, cache->k, cache->v,
                                 cache->e4m3 ? cache->k_scale : nullptr, cache->e4m3 ? cache->v_scale : nullptr}))
         return TGEMM_ERR_INVALID_ARG;
-    p.q = static_cast<const unsigned char *>(Q);
-    p.o = static_cast<unsigned char *>(O);
-    p.q_batch_stride = q_batch_stride * 2;
-    p.q_head_stride = q_head_stride * 2;
-    p.o_batch_stride = o_batch_stride * 2;
-    p.o_head_stride = o_head_stride * 2;
-    p.group = static_cast<int>(q_heads / cache->heads);
-    p.window = static_cast<int>(std::min<int64_t>(window, INT32_MAX));
+    p.q = static_cast<const unsigned char *>(a->Q);
+    p.o = static_cast<unsigned char *>(a->O);
+    p.q_batch_stride = a->q_batch_stride * 2;
+    p.q_head_stride = a->q_head_stride * 2;
+    p.o_batch_stride = a->o_batch_stride * 2;
+    p.o_head_stride = a->o_head_stride * 2;
+    p.window = static_cast<int>(std::min<int64_t>(a->window, INT32_MAX));
     constexpr double kLog2e = 1.4426950408889634;
-    p.capped = cap > 0.0f;
-    p.first = static_cast<float>(p.capped ? scale * 2.0 * kLog2e / cap : scale * kLog2e);
-    p.last = static_cast<float>(cap * kLog2e);
-    p.positions = pages_width * cache->page_size;
+    p.capped = a->cap > 0.0;
+    p.first = static_cast<float>(p.capped ? a->scale * 2.0 * kLog2e / a->cap : a->scale * kLog2e);
+    p.last = static_cast<float>(a->cap * kLog2e);
     const int tiles = head_tiles(p.group, cache->dim);
     p.blocks = (p.group + 8 * tiles - 1) / (8 * tiles);
-    attend_layout(batch, q_heads, p.group, cache->dim, p.positions, weights != nullptr,
-                  static_cast<unsigned char *>(workspace), &p.space);
     p.status = rt.status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (dtype == TGEMM_BF16)
+    if (a->dtype == TGEMM_BF16)
         e = cache->e4m3 ? launch_attend_dim<true, true>(rt, p, tiles, s) : launch_attend_dim<true, false>(rt, p, tiles, s);
     else
         e = cache->e4m3 ? launch_attend_dim<false, true>(rt, p, tiles, s) : launch_attend_dim<false, false>(rt, p, tiles, s);
-    if (e == cudaSuccess && weights) {
+    if (e == cudaSuccess && p.weights.base) {
         const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((p.positions + kSpreadThreads - 1) / kSpreadThreads, 64));
         const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(cache->heads), static_cast<unsigned>(batch));
         e = launch(kv_spread_kernel, grid, kSpreadThreads, 0, s, p);
@@ -383,70 +415,59 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_kv_cache *cache, cons
     return done(e);
 }
 
-extern "C" tgemm_status tgemm_kv_evict(const tgemm_kv_cache *from, const int32_t *pages, int64_t pages_width,
-                                       int64_t pages_stride, const int32_t *lengths, int64_t batch,
-                                       const float *weights, int64_t weights_width, int64_t weights_batch_stride,
-                                       int64_t weights_head_stride, const tgemm_kv_cache *to, const int32_t *to_pages,
-                                       int64_t to_pages_width, int64_t to_pages_stride, int64_t keep, int64_t recent,
-                                       int32_t *kept, int32_t *to_lengths, float *to_weights, int64_t to_weights_width,
-                                       int64_t to_weights_batch_stride, int64_t to_weights_head_stride,
-                                       tgemm_stream_t stream) {
+extern "C" tgemm_status tgemm_kv_evict(const tgemm_kv_evict_args *a, tgemm_stream_t stream) {
     EvictParams p;
     std::memset(&p, 0, sizeof(p));
-    Extent fk, fv, tk, tv;
+    Extent fk, fv, tk, tv, ew, et;
+    if (!a) return TGEMM_ERR_INVALID_ARG;
+    const tgemm_kv_cache *from = a->from, *to = a->to;
     tgemm_status st = check_cache(from, &p.from, &fk, &fv);
     if (st != TGEMM_OK) return st;
     st = check_cache(to, &p.to, &tk, &tv);
     if (st != TGEMM_OK) return st;
-    if (from->heads != to->heads || from->dim != to->dim || from->e4m3 != to->e4m3 || keep < 1 || keep > INT32_MAX ||
-        recent < 0)
+    const int64_t batch = a->seq.batch, heads = from->heads, keep = a->keep;
+    if (to->heads != heads || from->dim != to->dim || from->e4m3 != to->e4m3 || a->to_seq.batch != batch || keep < 1 ||
+        keep > (1 << 30) || a->recent < 0 || batch > 65535 || heads * batch > INT32_MAX)
         return TGEMM_ERR_INVALID_ARG;
-    st = check_table(pages, pages_width, pages_stride, lengths, true, batch, from->page_size, &p.table);
+    st = check_sequences(a->seq, true, from->page_size, &p.table);
     if (st != TGEMM_OK) return st;
-    st = check_table(to_pages, to_pages_width, to_pages_stride, nullptr, false, batch, to->page_size, &p.to_table);
+    st = check_sequences(a->to_seq, false, to->page_size, &p.to_table);
     if (st != TGEMM_OK) return st;
-    st = check_weights(weights, weights_width, weights_batch_stride, weights_head_stride, batch, from->heads,
-                       &p.weights);
+    st = check_weights(a->weights, batch, heads, &p.weights, &ew);
     if (st != TGEMM_OK) return st;
-    st = check_weights(to_weights, to_weights_width, to_weights_batch_stride, to_weights_head_stride, batch,
-                       from->heads, &p.to_weights);
+    st = check_weights(a->to_weights, batch, heads, &p.to_weights, &et);
     if (st != TGEMM_OK) return st;
     if (batch == 0) return TGEMM_OK;
-    if (!weights || !kept || !to_lengths || !to_weights || to_weights_width < keep) return TGEMM_ERR_INVALID_ARG;
-    if (!aligned4(kept) || !aligned4(to_lengths)) return TGEMM_ERR_ALIGNMENT;
-    const int64_t heads = from->heads;
-    int64_t wb = 0, twb = 0;
-    const int64_t size[2] = {batch, heads};
-    const int64_t ws[2] = {weights_batch_stride, weights_head_stride};
-    const int64_t ts[2] = {to_weights_batch_stride, to_weights_head_stride};
-    extent(size, ws, 2, weights_width, 4, true, &wb);
-    extent(size, ts, 2, to_weights_width, 4, true, &twb);
-    const Extent ew = {weights, wb}, et = {to_weights, twb}, ek = {kept, batch * heads * keep * 4},
-                 el = {lengths, batch * 4}, en = {to_lengths, batch * 4};
-    if (overlaps(et, ew) || overlaps(ek, ew) || overlaps(ek, et) || overlaps(en, el) || overlaps(en, ek) ||
-        overlaps(en, et) || overlaps(en, ew))
+    if (!a->weights.data || !a->kept || !a->to_lengths || !a->to_weights.data || a->to_weights.width < keep)
+        return TGEMM_ERR_INVALID_ARG;
+    if (!aligned4(a->kept) || !aligned4(a->to_lengths)) return TGEMM_ERR_ALIGNMENT;
+    const Extent ek = {a->kept, batch * heads * keep * 4}, el = {a->seq.lengths, batch * 4}, en = {a->to_lengths, batch * 4};
+    if (overlaps(et, ew) || overlaps(ek, ew) || overlaps(ek, et) || overlaps(en, el) || overlaps(ek, el) ||
+        overlaps(et, el) || overlaps(en, ek) || overlaps(en, et) || overlaps(en, ew))
         return TGEMM_ERR_ALIAS;
     RuntimeInfo rt;
     st = runtime_current(&rt);
     if (st != TGEMM_OK) return st;
     if (!all_device(rt.device,
-                    {pages, lengths, weights, to_pages, kept, to_lengths, to_weights, from->k, from->v, to->k, to->v,
-                     from->e4m3 ? from->k_scale : nullptr, from->e4m3 ? from->v_scale : nullptr,
-                     to->e4m3 ? to->k_scale : nullptr, to->e4m3 ? to->v_scale : nullptr}))
+                    {a->seq.pages, a->seq.lengths, a->weights.data, a->to_seq.pages, a->kept, a->to_lengths,
+                     a->to_weights.data, from->k, from->v, to->k, to->v, from->e4m3 ? from->k_scale : nullptr,
+                     from->e4m3 ? from->v_scale : nullptr, to->e4m3 ? to->k_scale : nullptr,
+                     to->e4m3 ? to->v_scale : nullptr}))
         return TGEMM_ERR_INVALID_ARG;
-    p.kept = kept;
-    p.to_lengths = to_lengths;
+    p.kept = a->kept;
+    p.to_lengths = a->to_lengths;
     p.keep = static_cast<int>(keep);
-    p.recent = static_cast<int>(std::min<int64_t>(recent, INT32_MAX));
+    p.recent = static_cast<int>(std::min<int64_t>(a->recent, INT32_MAX));
     p.status = rt.status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    st = done(launch(kv_select_kernel, dim3(static_cast<unsigned>(heads), static_cast<unsigned>(batch)),
-                     kSelectThreads, 0, s, p));
+    // Blocks that share a sequence and head: one per 8192 positions that there can be.
+    const int64_t positions = std::min<int64_t>(a->seq.pages_width * from->page_size, a->weights.width);
+    int cluster = 1;
+    while (cluster < 8 && cluster * 8192 < positions) cluster *= 2;
+    st = done(launch(kv_select_kernel, dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(heads), static_cast<unsigned>(batch)),
+                     kSelectThreads, 0, s, p, cluster));
     if (st != TGEMM_OK) return st;
-    const int64_t items = heads * batch, most = std::min<int64_t>(keep, pages_width * from->page_size);
-    const int64_t per = kGatherThreads / 32;
-    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((most + per - 1) / per, 16));
-    if (items > 65535) return TGEMM_ERR_INVALID_ARG;
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(items));
-    return done(launch(from->e4m3 ? kv_gather_kernel<true> : kv_gather_kernel<false>, grid, kGatherThreads, 0, s, p));
+    const int64_t most = std::min<int64_t>(keep, positions);
+    return done(from->e4m3 ? launch_gather<true>(p, most, from->heads, static_cast<int>(batch), s)
+                           : launch_gather<false>(p, most, from->heads, static_cast<int>(batch), s));
 }

@@ -4,9 +4,13 @@
 //
 // (without starts, one token per sequence), as it is (16-bit cache) or in e4m3
 // with a scale per row: scale = max |x| / 448 (1 for a row of zeros), element =
-// x / scale rounded to nearest even.  448 is e4m3's largest value.  The
-// quotient is a true division: a product with the reciprocal would move some
-// elements by a whole e4m3 step.
+// x / scale rounded to nearest even.  448 is e4m3's largest value.
+//
+// Reading and writing each row once bounds it.  Where a row goes takes a chain
+// of dependent loads (starts, lengths, page list), so a block first finds the
+// places of a whole chunk of rows, one thread each, and then streams the chunk:
+// as many lanes as a row has 16-byte pieces, every piece of the chunk (keys and
+// values) requested before the first is used.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -15,8 +19,6 @@
 #include "kv_cache.cuh"
 
 namespace tgemm {
-
-constexpr int kAppendThreads = 256;
 
 struct AppendParams {
     KvView cache;
@@ -58,73 +60,126 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
     }
 }
 
-// One warp per row pair (token, head): its key row, then its value row; a lane
-// holds eight elements.
-template <bool kBf16, bool kE4m3>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
+// x[i] / scale, each rounded as a division is (a product with the reciprocal
+// would move some elements by a whole e4m3 step), from one division per row:
+// with r the rounded reciprocal and q = x r, q + (x - q scale) r, whose
+// parenthesis is exact, is the rounded quotient (Markstein 1990, "Computation
+// of elementary functions on the IBM RISC System/6000 processor").  That
+// holds while nothing leaves fp32's normal range, where it matters: a quotient
+// below 2^-60 is rounded to zero in e4m3 either way.  Scales outside 2^+-60
+// take the division.
+__device__ __forceinline__ void divide8(float (&x)[8], float scale) {
+    if (scale > 0x1p-60f && scale < 0x1p60f) {
+        const float r = 1.0f / scale;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q = x[i] * r;
+            x[i] = fmaf(fmaf(-q, scale, x[i]), r, q);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] / scale;
+    }
+}
+
+// Eight floats as e4m3.
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8]) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE,
+                                                                    __NV_E4M3))
+                     << (16 * (i & 1));
+    return make_uint2(w[0], w[1]);
+}
+
+// Blocks take chunks of kRows rows, a row being the keys and values of one
+// (token, head), kUnroll passes of kRowThreads / kLanes rows.
+constexpr int kRowThreads = 256;
+
+template <bool kBf16, bool kE4m3, int kLanes, int kUnroll>
+__global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const AppendParams p) {
+    constexpr int kPass = kRowThreads / kLanes, kRows = kPass * kUnroll;
+    __shared__ long long s_src[kRows], s_dst[kRows], s_scale[kRows];
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
     const long long rows = p.tokens * p.cache.heads;
-    const long long warps = static_cast<long long>(gridDim.x) * (kAppendThreads / 32);
-    for (long long r = static_cast<long long>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5); r < rows;
-         r += warps) {
-        const long long t = r / p.cache.heads;
-        const int head = static_cast<int>(r - t * p.cache.heads);
-        int b, count, index;
-        if (p.starts) {
-            b = kv_sequence_of(p.starts, p.table.batch, t);
-            if (b < 0) continue;
-            count = p.starts[b + 1] - p.starts[b];
-            index = static_cast<int>(t - p.starts[b]);
-        } else {
-            b = static_cast<int>(t);
-            count = 1;
-            index = 0;
-        }
-        const int length = p.table.lengths[b];
-        const long long pos = static_cast<long long>(length) - count + index;
-        int page = 0, slot = 0;
-        if (pos < 0 || pos >= static_cast<long long>(p.table.width) * p.cache.page_size ||
-            !kv_row(p.table.pages + b * p.table.stride, static_cast<int>(pos), p.cache.page_size, p.cache.pages,
-                    &page, &slot)) {
-            if (lane == 0) record_status(p.status, kStatusCache);
-            continue;
-        }
-        if (p.weights.base && lane == 0) {
-            if (pos < p.weights.width)
-                p.weights.base[b * p.weights.batch_stride + head * p.weights.head_stride + pos] = 0.0f;
-            else
-                record_status(p.status, kStatusCache);
-        }
-        const bool has = lane * 8 < p.cache.dim;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const unsigned char *src = (which ? p.v : p.k) + t * p.token_stride + head * p.head_stride;
-            unsigned char *dst = (which ? p.cache.v : p.cache.k) + kv_offset(p.cache, page, slot, head);
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (has) u = *reinterpret_cast<const uint4 *>(src + lane * 16);
-            if (!kE4m3) {
-                if (has) *reinterpret_cast<uint4 *>(dst + lane * 16) = u;
-                continue;
+    const int piece = threadIdx.x % kLanes, in_pass = threadIdx.x / kLanes;
+    const bool inside = piece * 8 < p.cache.dim;
+    for (long long r0 = static_cast<long long>(blockIdx.x) * kRows; r0 < rows;
+         r0 += static_cast<long long>(gridDim.x) * kRows) {
+        if (threadIdx.x < kRows) {
+            const long long r = r0 + threadIdx.x;
+            long long src = 0, dst = -1, scale = 0;
+            if (r < rows) {
+                const long long t = r / p.cache.heads;
+                const int head = static_cast<int>(r - t * p.cache.heads);
+                int b = static_cast<int>(t);
+                long long back = 1;                 // positions from the sequence's end
+                if (p.starts) {
+                    b = kv_sequence_of(p.starts, p.table.batch, t);
+                    if (b >= 0) back = p.starts[b + 1] - t;
+                }
+                if (b >= 0) {
+                    const long long pos = p.table.lengths[b] - back;
+                    int page, slot;
+                    if (pos < 0 || pos >= static_cast<long long>(p.table.width) * p.cache.page_size ||
+                        !kv_row(p.table.pages + b * p.table.stride, static_cast<int>(pos), p.cache.page_size,
+                                p.cache.pages, &page, &slot)) {
+                        record_status(p.status, kStatusCache);
+                    } else {
+                        src = t * p.token_stride + head * p.head_stride;
+                        dst = kv_offset(p.cache, page, slot, head);
+                        if (kE4m3) scale = kv_scale_offset(p.cache, page, slot, head);
+                        if (p.weights.base) {
+                            if (pos < p.weights.width)
+                                p.weights.base[b * p.weights.batch_stride + head * p.weights.head_stride + pos] = 0.0f;
+                            else
+                                record_status(p.status, kStatusCache);
+                        }
+                    }
+                }
             }
-            float x[8];
-            unpack8<kBf16>(u, x);
-            float top = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float scale = top > 0.0f ? top / 448.0f : 1.0f;
-            uint32_t packed[2] = {0, 0};
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                packed[i >> 2] |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(x[i] / scale, __NV_SATFINITE, __NV_E4M3))
-                                  << (8 * (i & 3));
-            if (has) *reinterpret_cast<uint2 *>(dst + lane * 8) = make_uint2(packed[0], packed[1]);
-            if (lane == 0)
-                (which ? p.cache.v_scale : p.cache.k_scale)[kv_scale_offset(p.cache, page, slot, head)] = scale;
+            s_src[threadIdx.x] = src;
+            s_dst[threadIdx.x] = dst;
+            s_scale[threadIdx.x] = scale;
         }
+        __syncthreads();
+        uint4 x[kUnroll][2];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = u * kPass + in_pass;
+            x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+            if (s_dst[i] >= 0 && inside) {
+                x[u][0] = __ldcs(reinterpret_cast<const uint4 *>(p.k + s_src[i]) + piece);
+                x[u][1] = __ldcs(reinterpret_cast<const uint4 *>(p.v + s_src[i]) + piece);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = u * kPass + in_pass;
+            const long long dst = s_dst[i];
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                unsigned char *pool = which ? p.cache.v : p.cache.k;
+                if (!kE4m3) {
+                    if (dst >= 0 && inside) *(reinterpret_cast<uint4 *>(pool + dst) + piece) = x[u][which];
+                    continue;
+                }
+                float f[8];
+                unpack8<kBf16>(x[u][which], f);
+                float top = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float scale = top > 0.0f ? top / 448.0f : 1.0f;
+                divide8(f, scale);
+                if (dst >= 0 && inside) *(reinterpret_cast<uint2 *>(pool + dst) + piece) = pack8_e4m3(f);
+                if (dst >= 0 && piece == 0) (which ? p.cache.v_scale : p.cache.k_scale)[s_scale[i]] = scale;
+            }
+        }
+        __syncthreads();
     }
 }
 

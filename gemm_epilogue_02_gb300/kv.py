@@ -2,7 +2,10 @@
 per sequence, and eviction by accumulated attention weight.
 
 The computation lives in the CUDA library (csrc/kv_*.cuh, C ABI in
-include/tgemm.h); this module checks and marshals torch tensors.
+include/tgemm.h); this module checks torch tensors and packs their addresses
+and sizes into the calls' argument structures.  A call costs the host a few
+microseconds, so every tensor attribute is read once and by its cheapest name
+(get_device() rather than device).
 """
 from __future__ import annotations
 
@@ -12,8 +15,10 @@ import torch
 
 from . import _binding as _b
 
-_DT = {torch.float16: _b.TGEMM_F16, torch.bfloat16: _b.TGEMM_BF16}
-_E4M3 = torch.float8_e4m3fn
+_F16, _BF16, _E4M3 = torch.float16, torch.bfloat16, torch.float8_e4m3fn
+_DT = {_F16: _b.TGEMM_F16, _BF16: _b.TGEMM_BF16}
+_NO_WEIGHTS = (0, 0, 0, 0)
+_append, _decode, _evict = _b.KV_APPEND_ARGS.pack, _b.ATTENTION_DECODE_ARGS.pack, _b.KV_EVICT_ARGS.pack
 
 
 class PagedCache:
@@ -57,57 +62,49 @@ class PagedCache:
             c.k_scale, c.v_scale = k_scale.data_ptr() or None, v_scale.data_ptr() or None
             c.scale_page_stride, c.scale_slot_stride, c.scale_head_stride = k_scale.stride()
         self._struct = c
-        self._ref = ctypes.byref(c)
+        self._address = ctypes.addressof(c)
+        self._index = k.get_device()          # -1: not on a GPU
+        self._dtypes = (_F16, _BF16) if e4m3 else (k.dtype,)
 
 
-def _table(page_table, lengths, cache, need_lengths=True):
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+def _table(page_table, index):
+    """(pages, width, stride, batch) of a page table."""
+    shape, stride = page_table.shape, page_table.stride()
+    if len(shape) != 2 or page_table.dtype is not torch.int32 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError("the page table must be int32 [batch, pages] with unit stride of pages")
-    batch, width = page_table.shape
-    if page_table.device != cache.device:
+    if page_table.get_device() != index:
         raise ValueError("the page table must be on the cache's device")
-    if need_lengths:
-        _vector("lengths", lengths, batch, cache)
-    return batch, width, page_table.stride(0)
+    return page_table.data_ptr(), shape[1], stride[0], shape[0]
 
 
-def _vector(name, t, n, cache):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.device != cache.device:
+def _vector(name, t, n, index):
+    """The address of a contiguous int32 [n] tensor."""
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
         raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on the cache's device")
+    return t.data_ptr()
 
 
-def _weights(name, w, batch, cache):
-    """(pointer, width, batch stride, head stride) of accumulated weights, or zeros for None."""
-    if w is None:
-        return 0, 0, 0, 0
-    if w.dim() != 3 or w.dtype != torch.float32 or w.device != cache.device or tuple(w.shape[:2]) != (batch, cache.heads) or (
-            w.shape[2] > 1 and w.stride(2) != 1):
+def _weights(name, w, batch, heads, index):
+    """(address, width, batch stride, head stride) of accumulated weights."""
+    shape, stride = w.shape, w.stride()
+    if (len(shape) != 3 or w.dtype is not torch.float32 or shape[0] != batch or shape[1] != heads
+            or (stride[2] != 1 and shape[2] > 1) or w.get_device() != index):
         raise ValueError(f"{name} must be float32 [batch, heads, positions] on the cache's device with unit stride of positions")
-    return w.data_ptr(), w.shape[2], w.stride(0), w.stride(1)
+    return w.data_ptr(), shape[2], stride[0], stride[1]
 
 
-def _launch(cache, stream, where, call):
-    """call(stream handle) with the cache's device current; raises on a status."""
-    dev = cache.device
-    if dev.type != "cuda":
+def _launch(index, stream, fn, args):
+    """fn(args, stream) with the cache's device current; raises on a status."""
+    if index < 0:
         raise ValueError("the cache must be on a CUDA device")
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    if dev.index == torch.cuda.current_device():
-        st = call(s.cuda_stream)
+    s = (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream
+    if index == torch.cuda.current_device():
+        st = fn(args, s)
     else:
-        with torch.cuda.device(dev):
-            st = call(s.cuda_stream)
+        with torch.cuda.device(index):
+            st = fn(args, s)
     if st != 0:
-        raise _b.TgemmError(st, where)
-
-
-def _call_dtype(name, t, cache):
-    code = _DT.get(t.dtype)
-    if code is None or (not cache.e4m3 and t.dtype != cache.dtype):
-        raise ValueError(f"{name} must be float16 or bfloat16, and the cache's dtype unless that is e4m3")
-    if t.device != cache.device:
-        raise ValueError(f"{name} must be on the cache's device")
-    return code
+        raise _b.TgemmError(st, fn.__name__)
 
 
 def kv_append(cache: PagedCache, K: torch.Tensor, V: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -117,24 +114,28 @@ def kv_append(cache: PagedCache, K: torch.Tensor, V: torch.Tensor, page_table: t
     int32 [batch + 1]; None: one token each), which lengths[b] counts already:
     its last token goes to position lengths[b] - 1.  weights (float32 [batch,
     heads, positions]) are set to zero there."""
-    batch, width, stride = _table(page_table, lengths, cache)
-    if K.dim() != 3 or K.shape != V.shape or tuple(K.shape[1:]) != (cache.heads, cache.dim):
+    index = cache._index
+    pages, width, stride, batch = _table(page_table, index)
+    length = _vector("lengths", lengths, batch, index)
+    shape, sk, dtype = K.shape, K.stride(), K.dtype
+    if len(shape) != 3 or V.shape != shape or shape[1] != cache.heads or shape[2] != cache.dim:
         raise ValueError("K and V must be [tokens, heads, dim] of the cache's heads and dim")
-    sk = K.stride()
-    if sk != V.stride() or sk[2] != 1:
+    if sk[2] != 1 or V.stride() != sk:
         raise ValueError("K and V must share strides, with unit stride of dim")
-    if K.dtype != V.dtype or K.device != V.device:
-        raise ValueError("K and V must share dtype and device")
-    code = _call_dtype("K", K, cache)
+    if dtype not in cache._dtypes or V.dtype is not dtype:
+        raise ValueError("K and V must be float16 or bfloat16, and the cache's dtype unless that is e4m3")
+    if K.get_device() != index or V.get_device() != index:
+        raise ValueError("K and V must be on the cache's device")
     if starts is not None:
-        _vector("starts", starts, batch + 1, cache)
-    elif K.shape[0] != batch:
+        start = _vector("starts", starts, batch + 1, index)
+    elif shape[0] == batch:
+        start = 0
+    else:
         raise ValueError("without starts every sequence brings one token")
-    w = _weights("weights", weights, batch, cache)
-    args = (cache._ref, K.data_ptr(), V.data_ptr(), K.shape[0], sk[0], sk[1],
-            starts.data_ptr() if starts is not None else 0, page_table.data_ptr(), width, stride, lengths.data_ptr(),
-            batch, *w, code)
-    _launch(cache, stream, "tgemm_kv_append", lambda s: _b.tgemm_kv_append(*args, s))
+    w = _NO_WEIGHTS if weights is None else _weights("weights", weights, batch, cache.heads, index)
+    _launch(index, stream, _b.tgemm_kv_append,
+            _append(cache._address, pages, length, width, stride, batch, *w, K.data_ptr(), V.data_ptr(), start,
+                    shape[0], sk[0], sk[1], _DT[dtype]))
 
 
 def attention_decode_workspace(Q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor,
@@ -157,27 +158,30 @@ def attention_decode(Q: torch.Tensor, cache: PagedCache, page_table: torch.Tenso
     scores through cap * tanh(s / cap).  weights (float32 [batch, heads,
     positions]) grow by each group's summed attention.  Without a workspace one
     is allocated and zeroed for the call."""
-    batch, width, stride = _table(page_table, lengths, cache)
-    if Q.dim() != 3 or Q.shape != O.shape or Q.shape[0] != batch or Q.shape[2] != cache.dim or Q.shape[1] % cache.heads:
+    index = cache._index
+    pages, width, stride, batch = _table(page_table, index)
+    length = _vector("lengths", lengths, batch, index)
+    shape, sq, so, dtype = Q.shape, Q.stride(), O.stride(), Q.dtype
+    if len(shape) != 3 or O.shape != shape or shape[0] != batch or shape[2] != cache.dim or shape[1] % cache.heads:
         raise ValueError("Q and O must be [batch, q_heads, dim], q_heads a multiple of the cache's heads")
-    sq, so = Q.stride(), O.stride()
     if sq[2] != 1 or so[2] != 1:
         raise ValueError("Q and O need unit stride of dim")
-    if O.dtype != Q.dtype or O.device != Q.device:
-        raise ValueError("Q and O must share dtype and device")
-    code = _call_dtype("Q", Q, cache)
-    if scale is None:
-        scale = cache.dim ** -0.5
-    w = _weights("weights", weights, batch, cache)
+    if dtype not in cache._dtypes or O.dtype is not dtype:
+        raise ValueError("Q and O must be float16 or bfloat16, and the cache's dtype unless that is e4m3")
+    if Q.get_device() != index or O.get_device() != index:
+        raise ValueError("Q and O must be on the cache's device")
+    w = _NO_WEIGHTS if weights is None else _weights("weights", weights, batch, cache.heads, index)
+    if index < 0:
+        raise ValueError("the cache must be on a CUDA device")
     if workspace is None:
         with torch.cuda.stream(stream):   # the zeros belong to the stream that uses them
             workspace = attention_decode_workspace(Q, cache, page_table, weights is not None)
-    elif workspace.device != cache.device or not workspace.is_contiguous():
+    elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the cache's device")
-    args = (cache._ref, Q.data_ptr(), O.data_ptr(), batch, Q.shape[1], sq[0], sq[1], so[0], so[1],
-            page_table.data_ptr(), width, stride, lengths.data_ptr(), scale, cap, window, *w, workspace.data_ptr(),
-            workspace.nbytes, code)
-    _launch(cache, stream, "tgemm_attention_decode", lambda s: _b.tgemm_attention_decode(*args, s))
+    _launch(index, stream, _b.tgemm_attention_decode,
+            _decode(cache._address, pages, length, width, stride, batch, *w, Q.data_ptr(), O.data_ptr(), shape[1],
+                    sq[0], sq[1], so[0], so[1], window, cache.dim ** -0.5 if scale is None else scale, cap,
+                    workspace.data_ptr(), workspace.nbytes, _DT[dtype]))
     return O
 
 
@@ -191,19 +195,22 @@ def kv_evict(cache: PagedCache, page_table: torch.Tensor, lengths: torch.Tensor,
     pages written must not be among those read).  Written besides: kept (int32
     [batch, heads, keep], -1 where a sequence has fewer), to_lengths (int32
     [batch]) and to_weights (float32 [batch, heads, at least keep])."""
-    batch, width, stride = _table(page_table, lengths, cache)
-    to_batch, to_width, to_stride = _table(to_page_table, None, to_cache, need_lengths=False)
-    if to_batch != batch or to_cache.device != cache.device or (to_cache.dtype, to_cache.heads, to_cache.dim) != (
-            cache.dtype, cache.heads, cache.dim):
+    index, heads = cache._index, cache.heads
+    pages, width, stride, batch = _table(page_table, index)
+    length = _vector("lengths", lengths, batch, index)
+    to_pages, to_width, to_stride, to_batch = _table(to_page_table, index)
+    if to_batch != batch or to_cache._index != index or to_cache.dtype is not cache.dtype or to_cache.heads != heads or (
+            to_cache.dim != cache.dim):
         raise ValueError("both caches must share dtype, heads, dim and device, both page tables the batch")
-    if kept.dim() != 3 or kept.dtype != torch.int32 or not kept.is_contiguous() or kept.device != cache.device or tuple(
-            kept.shape[:2]) != (batch, cache.heads):
+    shape = kept.shape
+    if len(shape) != 3 or shape[0] != batch or shape[1] != heads or kept.dtype is not torch.int32 or (
+            not kept.is_contiguous()) or kept.get_device() != index:
         raise ValueError("kept must be a contiguous int32 [batch, heads, keep] tensor on the cache's device")
-    _vector("to_lengths", to_lengths, batch, cache)
-    keep = kept.shape[2]
-    if to_weights.dim() != 3 or to_weights.shape[2] < keep:
+    to_length = _vector("to_lengths", to_lengths, batch, index)
+    w = _weights("weights", weights, batch, heads, index)
+    to_w = _weights("to_weights", to_weights, batch, heads, index)
+    if to_w[1] < shape[2]:
         raise ValueError("to_weights must hold at least keep positions")
-    args = (cache._ref, page_table.data_ptr(), width, stride, lengths.data_ptr(), batch,
-            *_weights("weights", weights, batch, cache), to_cache._ref, to_page_table.data_ptr(), to_width, to_stride,
-            keep, recent, kept.data_ptr(), to_lengths.data_ptr(), *_weights("to_weights", to_weights, batch, cache))
-    _launch(cache, stream, "tgemm_kv_evict", lambda s: _b.tgemm_kv_evict(*args, s))
+    _launch(index, stream, _b.tgemm_kv_evict,
+            _evict(cache._address, pages, length, width, stride, batch, *w, to_cache._address, to_pages, 0, to_width,
+                   to_stride, batch, *to_w, kept.data_ptr(), to_length, shape[2], recent))

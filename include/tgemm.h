@@ -317,13 +317,28 @@ typedef struct {
 } tgemm_kv_cache;
 
 /*
- * Common to the three calls below.
+ * Sequences that share a cache.
  *   pages    int32 [batch, pages_stride], device: each sequence's page list, of
  *            pages_width entries at most; entries past a sequence's length are
- *            not read.
+ *            not read.  pages_width * page_size is at most 2^30.
  *   lengths  int32 [batch], device: positions each sequence holds.
- *   weights  fp32 [batch, heads, weights_width] with strides: the attention
- *            weights accumulated for each position (NULL where it is optional).
+ * batch is at most 65535.
+ */
+typedef struct {
+    const int32_t *pages;
+    const int32_t *lengths;
+    int64_t pages_width, pages_stride, batch;
+} tgemm_kv_sequences;
+
+/* Accumulated attention weights, fp32 [batch, heads, width], device (data NULL: none). */
+typedef struct {
+    float *data;
+    int64_t width, batch_stride, head_stride;
+} tgemm_kv_weights;
+
+/*
+ * Common to the three calls below.
+ *
  * Page numbers, lengths and starts are on the device, so the kernels check
  * them: one that lies outside the pool or the table (a negative length too) is
  * recorded as TGEMM_ERR_CACHE in the device status word
@@ -333,9 +348,10 @@ typedef struct {
  * Errors that the host sees are returned before anything is enqueued:
  * TGEMM_ERR_INVALID_ARG (sizes, strides, dtype, a NULL or host pointer),
  * TGEMM_ERR_ALIGNMENT, TGEMM_ERR_ALIAS, TGEMM_ERR_UNSUPPORTED_DEVICE,
- * TGEMM_ERR_CUDA.  batch is at most 65535.  Nothing is allocated and the host
- * does not read device memory, so the calls can be captured into a graph, which
- * then follows the lengths and pages that it finds at each replay.
+ * TGEMM_ERR_CUDA.  The argument structures are read during the call only.
+ * Nothing is allocated and the host does not read device memory, so the calls
+ * can be captured into a graph, which then follows the lengths and pages that
+ * it finds at each replay.
  */
 
 /*
@@ -349,12 +365,16 @@ typedef struct {
  * x / scale, rounded to nearest even.  With weights, those of the new positions
  * are set to 0.
  */
-tgemm_status tgemm_kv_append(const tgemm_kv_cache *cache, const void *K, const void *V, int64_t tokens,
-                             int64_t token_stride, int64_t head_stride, const int32_t *starts,
-                             const int32_t *pages, int64_t pages_width, int64_t pages_stride,
-                             const int32_t *lengths, int64_t batch, float *weights, int64_t weights_width,
-                             int64_t weights_batch_stride, int64_t weights_head_stride, tgemm_dtype dtype,
-                             tgemm_stream_t stream);
+typedef struct {
+    const tgemm_kv_cache *cache;
+    tgemm_kv_sequences seq;
+    tgemm_kv_weights weights;
+    const void *K, *V;
+    const int32_t *starts;
+    int64_t tokens, token_stride, head_stride;
+    int64_t dtype;                                  /* tgemm_dtype of K and V */
+} tgemm_kv_append_args;
+tgemm_status tgemm_kv_append(const tgemm_kv_append_args *args, tgemm_stream_t stream);
 
 /*
  * tgemm_attention_decode — attention of one new token per sequence over its
@@ -369,20 +389,28 @@ tgemm_status tgemm_kv_append(const tgemm_kv_cache *cache, const void *K, const v
  * weights[b, g, j] grows by the sum of p_j over the query heads of group g.
  *
  * Arithmetic: products of 16-bit values (e4m3 elements are widened exactly)
- * accumulated in fp32; softmax in fp32 with a running maximum; each output
- * rounded once to dtype.
+ * accumulated in fp32; softmax in fp32 with a running maximum, its weights
+ * rounded to the 16-bit type (fp16 for an e4m3 cache) before they multiply V;
+ * each output rounded once to dtype.
  *
  * workspace: device memory of tgemm_attention_decode_workspace() bytes,
  * 16-byte aligned, that held zeros before its first use; the call leaves it fit
  * for the next.  Calls that may overlap on the GPU need one each.
  */
-tgemm_status tgemm_attention_decode(const tgemm_kv_cache *cache, const void *Q, void *O, int64_t batch,
-                                    int64_t q_heads, int64_t q_batch_stride, int64_t q_head_stride,
-                                    int64_t o_batch_stride, int64_t o_head_stride, const int32_t *pages,
-                                    int64_t pages_width, int64_t pages_stride, const int32_t *lengths, float scale,
-                                    float cap, int64_t window, float *weights, int64_t weights_width,
-                                    int64_t weights_batch_stride, int64_t weights_head_stride, void *workspace,
-                                    int64_t workspace_bytes, tgemm_dtype dtype, tgemm_stream_t stream);
+typedef struct {
+    const tgemm_kv_cache *cache;
+    tgemm_kv_sequences seq;
+    tgemm_kv_weights weights;
+    const void *Q;
+    void *O;
+    int64_t q_heads, q_batch_stride, q_head_stride, o_batch_stride, o_head_stride;
+    int64_t window;
+    double scale, cap;
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t dtype;                                  /* tgemm_dtype of Q and O */
+} tgemm_attention_decode_args;
+tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args *args, tgemm_stream_t stream);
 
 /*
  * Bytes of workspace that tgemm_attention_decode needs for up to `batch`
@@ -397,21 +425,27 @@ tgemm_status tgemm_attention_decode_workspace(int64_t batch, int64_t q_heads, in
  * lengths[b] positions each head keeps k = min(n, keep): the last
  * r = min(recent, k), and of the n - r before them the k - r of largest weight
  * (ties to the lowest position, NaN below every number).  Their rows go, in
- * order, to positions 0 .. k - 1 of the page lists to_pages of the cache `to`,
- * with scales and weights.  `to` may describe the same pools as `from` as long
- * as the pages written are not among those read (pages may be shared by
- * sequences: nothing of `from` changes).  Outputs besides the rows:
+ * order, to positions 0 .. k - 1 of the page lists of `to_seq` in the cache
+ * `to`, with scales and weights.  `to` may describe the same pools as `from` as
+ * long as the pages written are not among those read (pages may be shared by
+ * sequences: nothing of `from` changes).  to_seq.lengths is not used.  Outputs
+ * besides the rows:
  *   kept        int32 [batch, heads, keep]: the positions kept, ascending, -1 from k on
  *   to_lengths  int32 [batch]: k
- *   to_weights  fp32 [batch, heads, to_weights_width >= keep]: the weights kept, 0 from k to keep - 1
+ *   to_weights  fp32 [batch, heads, width >= keep]: the weights kept, 0 from k to keep - 1
  */
-tgemm_status tgemm_kv_evict(const tgemm_kv_cache *from, const int32_t *pages, int64_t pages_width,
-                            int64_t pages_stride, const int32_t *lengths, int64_t batch, const float *weights,
-                            int64_t weights_width, int64_t weights_batch_stride, int64_t weights_head_stride,
-                            const tgemm_kv_cache *to, const int32_t *to_pages, int64_t to_pages_width,
-                            int64_t to_pages_stride, int64_t keep, int64_t recent, int32_t *kept,
-                            int32_t *to_lengths, float *to_weights, int64_t to_weights_width,
-                            int64_t to_weights_batch_stride, int64_t to_weights_head_stride, tgemm_stream_t stream);
+typedef struct {
+    const tgemm_kv_cache *from;
+    tgemm_kv_sequences seq;
+    tgemm_kv_weights weights;
+    const tgemm_kv_cache *to;
+    tgemm_kv_sequences to_seq;
+    tgemm_kv_weights to_weights;
+    int32_t *kept;
+    int32_t *to_lengths;
+    int64_t keep, recent;
+} tgemm_kv_evict_args;
+tgemm_status tgemm_kv_evict(const tgemm_kv_evict_args *args, tgemm_stream_t stream);
 
 /*
  * tgemm_plan — the work plan tgemm_run (and tgemm_run_ex / tgemm_run_host per

@@ -48,28 +48,33 @@ BAD_CACHES = [
 ]
 
 
+def call(fn, fmt, fields, **kw):
+    """fn on the packed fields, a dict in the structure's order; cache structures by address."""
+    unknown = set(kw) - set(fields)
+    assert not unknown, unknown
+    fields.update(kw)
+    keep = [f for f in fields.values() if isinstance(f, tg.KvCache)]
+    return fn(fmt.pack(*[ctypes.addressof(f) if isinstance(f, tg.KvCache) else f for f in fields.values()]), 0), keep
+
+
 def append(c=None, **kw):
-    a = dict(K=AT["K"], V=AT["V"], tokens=8, ts=256, hs=64, starts=0, table=AT["table"], width=8, stride=8,
-             lengths=AT["lengths"], batch=8, w=0, ww=0, wb=0, wh=0, dtype=0)
-    a.update(kw)
-    return tg.tgemm_kv_append(ctypes.byref(c or cache()), *a.values(), 0)
+    return call(tg.tgemm_kv_append, tg.KV_APPEND_ARGS, dict(
+        cache=c or cache(), table=AT["table"], lengths=AT["lengths"], width=8, stride=8, batch=8, w=0, ww=0, wb=0, wh=0,
+        K=AT["K"], V=AT["V"], starts=0, tokens=8, ts=256, hs=64, dtype=0), **kw)[0]
 
 
 def attend(c=None, **kw):
-    a = dict(Q=AT["Q"], O=AT["O"], batch=8, heads=16, qb=1024, qh=64, ob=1024, oh=64, table=AT["table"], width=8, stride=8,
-             lengths=AT["lengths"], scale=0.125, cap=0.0, window=0, w=0, ww=0, wb=0, wh=0, ws=AT["workspace"], wsb=60 * MB,
-             dtype=0)
-    a.update(kw)
-    return tg.tgemm_attention_decode(ctypes.byref(c or cache()), *a.values(), 0)
+    return call(tg.tgemm_attention_decode, tg.ATTENTION_DECODE_ARGS, dict(
+        cache=c or cache(), table=AT["table"], lengths=AT["lengths"], width=8, stride=8, batch=8, w=0, ww=0, wb=0, wh=0,
+        Q=AT["Q"], O=AT["O"], heads=16, qb=1024, qh=64, ob=1024, oh=64, window=0, scale=0.125, cap=0.0, ws=AT["workspace"],
+        wsb=60 * MB, dtype=0), **kw)[0]
 
 
 def evict(c=None, to=None, **kw):
-    a = dict(table=AT["table"], width=8, stride=8, lengths=AT["lengths"], batch=8, w=AT["weights"], ww=128, wb=512, wh=128,
-             to=None, to_table=AT["to_table"], tw=4, tstride=4, keep=64, recent=8, kept=AT["kept"], tl=AT["to_lengths"],
-             tow=AT["to_weights"], toww=64, towb=256, towh=64)
-    a.update(kw)
-    a["to"] = ctypes.byref(to or cache("t"))
-    return tg.tgemm_kv_evict(ctypes.byref(c or cache()), *a.values(), 0)
+    return call(tg.tgemm_kv_evict, tg.KV_EVICT_ARGS, dict(
+        cache=c or cache(), table=AT["table"], lengths=AT["lengths"], width=8, stride=8, batch=8, w=AT["weights"], ww=128,
+        wb=512, wh=128, to=to or cache("t"), to_table=AT["to_table"], unused=0, tw=4, tstride=4, to_batch=8,
+        tow=AT["to_weights"], toww=64, towb=256, towh=64, kept=AT["kept"], tl=AT["to_lengths"], keep=64, recent=8), **kw)[0]
 
 
 def test_valid_calls():
@@ -80,7 +85,7 @@ def test_valid_calls():
     assert attend(w=AT["weights"], ww=128, wb=512, wh=128) in VALID
     assert append(batch=0, tokens=0, K=0, V=0, table=0, lengths=0) == OK
     assert attend(batch=0, Q=0, O=0, table=0, lengths=0) == OK
-    assert evict(batch=0, table=0, lengths=0, to_table=0, w=0, kept=0, tl=0, tow=0) == OK
+    assert evict(batch=0, to_batch=0, table=0, lengths=0, to_table=0, w=0, kept=0, tl=0, tow=0) == OK
 
 
 @pytest.mark.parametrize("kw,code", BAD_CACHES)
@@ -115,7 +120,7 @@ def test_attention_decode_refusals(kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(keep=0), INVALID), (dict(recent=-1), INVALID), (dict(w=0), INVALID), (dict(kept=0), INVALID), (dict(tl=0), INVALID),
+    (dict(keep=0), INVALID), (dict(recent=-1), INVALID), (dict(to_batch=7), INVALID), (dict(w=0), INVALID), (dict(kept=0), INVALID), (dict(tl=0), INVALID),
     (dict(tow=0), INVALID), (dict(toww=63), INVALID), (dict(kept=AT["kept"] + 2), ALIGN), (dict(tl=AT["lengths"] + 8), ALIAS),
     (dict(tow=AT["weights"] + 128), ALIAS), (dict(kept=AT["to_weights"]), ALIAS), (dict(to_table=0), INVALID), (dict(wh=100), INVALID),
 ])
@@ -127,6 +132,12 @@ def test_evict_refuses_caches_that_do_not_match():
     assert evict(to=cache("t", dim=128, page_stride=16 * 4 * 128, slot_stride=512, head_stride=128)) == INVALID
     assert evict(to=cache("t", heads=2)) == INVALID
     assert evict(to=cache("t", e4m3=1)) == INVALID
+
+
+def test_null_arguments():
+    for fn in (tg.load().tgemm_kv_append, tg.load().tgemm_attention_decode, tg.load().tgemm_kv_evict):
+        assert fn(None, None) == INVALID
+    assert attend(cache=0) == INVALID and append(cache=0) == INVALID and evict(cache=0) == INVALID and evict(to=None, **{"to_table": 0}) == INVALID
 
 
 def test_workspace_sizes():
