@@ -398,6 +398,9 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args
     p.capped = a->cap > 0.0;
     p.first = static_cast<float>(p.capped ? a->scale * 2.0 * kLog2e / a->cap : a->scale * kLog2e);
     p.last = static_cast<float>(a->cap * kLog2e);
+    p.page_shift = -1;
+    for (int i = 0; i <= 20; ++i)
+        if (cache->page_size == 1 << i) p.page_shift = i;
     const int tiles = head_tiles(p.group, cache->dim);
     p.blocks = (p.group + 8 * tiles - 1) / (8 * tiles);
     p.status = rt.status;
@@ -408,7 +411,8 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args
     else
         e = cache->e4m3 ? launch_attend_dim<false, true>(rt, p, tiles, s) : launch_attend_dim<false, false>(rt, p, tiles, s);
     if (e == cudaSuccess && p.weights.base) {
-        const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((p.positions + kSpreadThreads - 1) / kSpreadThreads, 64));
+        constexpr int64_t kPer = kSpreadThreads * kSpreadEach;
+        const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((p.positions + kPer - 1) / kPer, 1024));
         const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(cache->heads), static_cast<unsigned>(batch));
         e = launch(kv_spread_kernel, grid, kSpreadThreads, 0, s, p);
     }

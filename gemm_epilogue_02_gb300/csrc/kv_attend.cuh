@@ -59,7 +59,7 @@ namespace tgemm {
 
 constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
-constexpr int kAttendMaxCtas = 512;       // CTAs at most (workspace slots)
+constexpr int kAttendMaxCtas = 320;       // CTAs at most (workspace slots)
 constexpr int kAttendFanIn = 16;          // parts joined at once, and the least that a group's joiner has room for
 static_assert(kAttendMaxCtas / kAttendFanIn >= kAttendFanIn, "room for the parts and for the groups");
 constexpr int kAttendLeast = 4;           // tiles a CTA takes at least
@@ -87,6 +87,7 @@ struct AttendParams {
     long long positions;                  // of a row of scores
     int group, blocks;                    // query heads of a key head; blocks that they make
     int window;
+    int page_shift;                       // log2 of the page size, -1: not a power of two
     // A score in log2 units is first * (q . k); capped, last * (1 - 2 / (1 + 2^(first * (q . k)))),
     // which is last * tanh.
     float first, last;
@@ -101,13 +102,16 @@ struct AttendShape {
     static constexpr int kTile = kAttendWarps * kKeys;
     static constexpr int kHeads = 8 * NT;
     static constexpr int kStages = 3;
-    static constexpr int kScales = kE4m3 ? 2 * kKeys * 4 : 0;
-    static constexpr int kStage = 2 * kKeys * kRow + kScales + 16;        // keys, values, scales, mask
-    static constexpr int kRing = kAttendWarps * kStages * kStage;
+    static constexpr int kStage = 2 * kKeys * kRow;                       // keys, values
+    static constexpr int kSide = kE4m3 ? 2 * kKeys * 4 + 16 : 16;         // a stage's scales and mask
+    static constexpr int kSides = kAttendWarps * kStages * kStage;        // where the sides begin
+    static constexpr int kOffsets = kSides + kAttendWarps * kStages * kSide;      // a step's rows in the pools
+    static constexpr int kMerge = kOffsets + kAttendWarps * kKeys * 8;
     static constexpr int kPitch = DP + 4;                                 // floats: heads 2t, dims g fall into different banks
-    static constexpr int kBytes = kRing + kHeads * kPitch * 4;
+    static constexpr int kBytes = kMerge + kHeads * kPitch * 4;
     static constexpr int kCtas = kBytes + 4096 <= 115712 ? 2 : 1;         // per SM: 228 KiB, of which each CTA also takes 1 KiB and its statics
     static_assert(kBytes + 4096 <= 232448, "a CTA's shared memory");
+    static_assert(kStage % 128 == 0 && kOffsets % 16 == 0 && kMerge % 16 == 0, "alignment");
 };
 
 // ---------------------------------------------------------------- primitives
@@ -166,6 +170,15 @@ __device__ __forceinline__ uint32_t widen2(uint32_t x) {
     return y;
 }
 
+// Counts up to `last` and from there back to 0; returns the count before.  The
+// block's writes before it (through a barrier) are visible to the blocks that
+// count after it, and theirs before to this one.
+__device__ __forceinline__ unsigned count_acq_rel(unsigned *counter, unsigned last) {
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(last) : "memory");
+    return old;
+}
+
 // 2^x, results below 2^-126 flushed to zero (relative error about 2^-22).
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -184,10 +197,10 @@ __device__ __forceinline__ uint32_t pair16(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------- the runs
-// Where a run is: the item (sequence b, head h of its heads * blocks) and the
+// Where a run is: the item (sequence b, key head, block of query heads) and the
 // tile in it.
 struct AttendCursor {
-    int b, h, tile, tiles, n, lo;
+    int b, head, block, tile, tiles, n, lo;
 };
 
 // Positions and tiles of a sequence; `pad`: tiles come in multiples of it.
@@ -220,8 +233,10 @@ __device__ __forceinline__ void cursor_load(AttendCursor &u, const AttendParams 
 __device__ __forceinline__ void cursor_next(AttendCursor &u, const AttendParams &p, int tile, int pad) {
     if (++u.tile < u.tiles) return;
     u.tile = 0;
-    if (++u.h < p.cache.heads * p.blocks) return;
-    u.h = 0;
+    if (++u.block < p.blocks) return;
+    u.block = 0;
+    if (++u.head < p.cache.heads) return;
+    u.head = 0;
     if (++u.b < p.table.batch) cursor_load(u, p, tile, pad);
 }
 
@@ -243,9 +258,10 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     __shared__ unsigned s_last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t4 = lane & 3;
-    float *merge = reinterpret_cast<float *>(smem + S::kRing);
+    float *merge = reinterpret_cast<float *>(smem + S::kMerge);
     const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kStage;
-    unsigned char *ring_ptr = smem + warp * S::kStages * S::kStage;
+    unsigned char *const sides = smem + S::kSides + warp * S::kStages * S::kSide;
+    long long *const offsets = reinterpret_cast<long long *>(smem + S::kOffsets) + warp * S::kKeys;
     griddep_wait();
     griddep_launch_dependents();
 
@@ -315,7 +331,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     // ---- loading: the places of the next step's rows are looked up, then copied
     AttendCursor load;
     load.b = s_start[0];
-    load.h = s_start[1];
+    load.head = s_start[1] / p.blocks;
+    load.block = s_start[1] - load.head * p.blocks;
     load.tile = s_start[2];
     cursor_load(load, p, S::kTile, pad);
     AttendCursor use = load;
@@ -323,59 +340,69 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     unsigned want[kLaneRows];
     int looked = 0;
     auto lookup = [&]() {
-        load_head = load.h / p.blocks;
+        load_head = load.head;
         const int pos0 = load.lo + load.tile * S::kTile + warp * S::kKeys;
         const int *list = p.table.pages + load.b * p.table.stride;
 #pragma unroll
         for (int r = 0; r < kLaneRows; ++r) {
             const int row = lane + 32 * r, pos = pos0 + row;
             const bool in = row < S::kKeys && pos < load.n && looked < steps;
-            const int i = in ? static_cast<int>(static_cast<unsigned>(pos) / static_cast<unsigned>(p.cache.page_size)) : 0;
+            int i = 0;
+            if (in)
+                i = p.page_shift >= 0 ? pos >> p.page_shift
+                                      : static_cast<int>(static_cast<unsigned>(pos) / static_cast<unsigned>(p.cache.page_size));
             slot[r] = pos - i * p.cache.page_size;
             page[r] = in ? list[i] : -1;
             want[r] = __ballot_sync(0xffffffffu, in);
         }
         if (++looked < steps) cursor_next(load, p, S::kTile, pad);
     };
-    const unsigned char *kpool = p.cache.k, *vpool = p.cache.v;
+    // A lane copies piece `piece` of rows in_copy, in_copy + kRowsPerCopy, ...; the pieces of a row are
+    // exchanged by its low bits (xor), so that ldmatrix finds eight rows in different banks.
+    const int piece = lane % kChunks, in_copy = lane / kChunks;
+    const bool inside = piece * 16 < p.cache.row_bytes;         // past dim: zeros
+    const unsigned char *const kpool = p.cache.k + (inside ? piece * 16 : 0);
+    const unsigned char *const vpool = p.cache.v + (inside ? piece * 16 : 0);
+    auto swizzle = [](int row) { return kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1)); };
+    const uint32_t copy_to = in_copy * S::kRow + ((piece ^ swizzle(in_copy)) << 4);
     auto issue = [&](int stage) {
         const uint32_t dst = ring + stage * S::kStage;
-        long long off[kLaneRows];
-        unsigned ok[kLaneRows];
-        unsigned some = 0;
+        unsigned char *const side = sides + stage * S::kSide;
+        unsigned ok[kLaneRows], some = 0;
+        bool full = inside;
 #pragma unroll
         for (int r = 0; r < kLaneRows; ++r) {
             const bool in = page[r] >= 0 && page[r] < p.cache.pages;
             ok[r] = __ballot_sync(0xffffffffu, in);
             some |= want[r];
+            full = full && ok[r] == (S::kKeys >= 32 ? 0xffffffffu : (1u << (S::kKeys & 31)) - 1u);
             if (ok[r] != want[r] && lane == 0) record_status(p.status, kStatusCache);
-            off[r] = in ? kv_offset(p.cache, page[r], slot[r], load_head) : 0;
-            if (kE4m3 && want[r]) {
-                const int row = lane + 32 * r;
-                const long long so = in ? kv_scale_offset(p.cache, page[r], slot[r], load_head) : 0;
-                if (row < S::kKeys) {
-                    cp_async4(dst + 2 * S::kKeys * S::kRow + 4 * row, p.cache.k_scale + so, in);
-                    cp_async4(dst + 2 * S::kKeys * S::kRow + 4 * (S::kKeys + row), p.cache.v_scale + so, in);
+            const int row = lane + 32 * r;
+            if (row < S::kKeys) {
+                offsets[row] = in ? kv_offset(p.cache, page[r], slot[r], load_head) : -1;
+                if (kE4m3) {
+                    const long long so = in ? kv_scale_offset(p.cache, page[r], slot[r], load_head) : 0;
+                    cp_async4(smem_u32(side) + 16 + 4 * row, p.cache.k_scale + so, in);
+                    cp_async4(smem_u32(side) + 16 + 4 * (S::kKeys + row), p.cache.v_scale + so, in);
                 }
             }
         }
+        if (lane == 0) {
+#pragma unroll
+            for (int r = 0; r < kLaneRows; ++r) reinterpret_cast<unsigned *>(side)[r] = ok[r];
+        }
+        __syncwarp();
         if (some) {
-            const int chunk = lane % kChunks;
-            const bool inside = chunk * 16 < p.cache.row_bytes;     // past dim: zeros
 #pragma unroll
             for (int i = 0; i < S::kKeys / kRowsPerCopy; ++i) {
-                const int row = i * kRowsPerCopy + lane / kChunks;
-                const long long o = __shfl_sync(0xffffffffu, off[(i * kRowsPerCopy) / 32], row & 31);
-                const bool good = inside && ((ok[(i * kRowsPerCopy) / 32] >> (row & 31)) & 1u);
-                const int sw = kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1));
-                const uint32_t to = dst + row * S::kRow + ((chunk ^ sw) << 4);
-                cp_async16(to, kpool + o + chunk * 16 * (good ? 1 : 0), good);
-                cp_async16(to + S::kKeys * S::kRow, vpool + o + chunk * 16 * (good ? 1 : 0), good);
+                const long long o = offsets[i * kRowsPerCopy + in_copy];
+                // swizzle(row) of row i * kRowsPerCopy + in_copy is swizzle(in_copy) ^ swizzle(i * kRowsPerCopy)
+                const uint32_t to = dst + i * kRowsPerCopy * S::kRow + (copy_to ^ (swizzle(i * kRowsPerCopy) << 4));
+                const bool good = full || (inside && o >= 0);
+                cp_async16(to, kpool + (good ? o : 0), good);
+                cp_async16(to + S::kKeys * S::kRow, vpool + (good ? o : 0), good);
             }
         }
-        if (lane < kLaneRows)
-            *reinterpret_cast<unsigned *>(ring_ptr + stage * S::kStage + 2 * S::kKeys * S::kRow + S::kScales + 4 * lane) =
-                kLaneRows == 1 || lane == 0 ? ok[0] : ok[kLaneRows - 1];
         cp_async_commit();
     };
 
@@ -383,6 +410,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
 #pragma unroll
     for (int s = 0; s < S::kStages - 1; ++s) {
         issue(s);
+        __syncwarp();
         lookup();
     }
 
@@ -394,8 +422,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     int begun = use.tile;                  // first tile of this CTA's part
     int stage = 0;
     for (int step = 0; step < steps; ++step) {
-        const int head = use.h / p.blocks, block = use.h - head * p.blocks;
-        const int h0 = block * S::kHeads, hn = min(S::kHeads, p.group - h0);    // heads of the group in this block
+        const int head = use.head, h0 = use.block * S::kHeads, hn = min(S::kHeads, p.group - h0);    // the block's heads
         if (fresh) {
             fresh = false;
             begun = use.tile;
@@ -453,26 +480,29 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
         issue(stage == 0 ? S::kStages - 1 : stage - 1);
         lookup();
         const uint32_t src = ring + stage * S::kStage;
-        const unsigned char *src_ptr = ring_ptr + stage * S::kStage;
-        const unsigned *mask_ptr = reinterpret_cast<const unsigned *>(src_ptr + 2 * S::kKeys * S::kRow + S::kScales);
-        unsigned some = mask_ptr[0];
-        if (kLaneRows > 1) some |= mask_ptr[1];
+        const unsigned char *const side = sides + stage * S::kSide;
+        unsigned mask[kLaneRows], some = 0;
+#pragma unroll
+        for (int r = 0; r < kLaneRows; ++r) {
+            mask[r] = reinterpret_cast<const unsigned *>(side)[r];
+            some |= mask[r];
+        }
         if (some) {
-            // S^T = K Q^T
+            // S^T = K Q^T.  16-bit: matrices (rows 0-7 | 8-15) x (pieces 2c | 2c + 1), one k step; e4m3: the
+            // same bytes are two.
             float s[NT][kBlocks][4];
+            const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;
+            const uint32_t ka = src + krow * S::kRow, kx = ((lane >> 4) ^ swizzle(krow)) << 4;
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[nt][kb][i] = 0.0f;
-                // 16-bit: matrices (rows 0-7 | 8-15) x (chunk 0 | 1), one k step; e4m3: the same bytes are two k steps.
-                const int row = 16 * kb + (lane & 7) + ((lane >> 3) & 1) * 8, half = lane >> 4;
-                const int sw = kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1));
 #pragma unroll
                 for (int c = 0; c < kChunks / 2; ++c) {
                     uint32_t a[4];
-                    ldmatrix4(a, src + row * S::kRow + (((2 * c + half) ^ sw) << 4));
+                    ldmatrix4(a, ka + (kx ^ (c << 5)) + kb * 16 * S::kRow);
                     if (!kE4m3) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma16816<kMmaBf16>(s[nt][kb], a, qf[nt][c][0], qf[nt][c][1]);
@@ -491,14 +521,16 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
             }
             // scores in log2 units, masked; the value scales join the exponent
             float lv[kBlocks][2], inv[kBlocks][2];
-            const float *scales = reinterpret_cast<const float *>(src_ptr + 2 * S::kKeys * S::kRow);
-            const int pos0 = use.lo + use.tile * S::kTile + warp * S::kKeys;
+            const float *scales = reinterpret_cast<const float *>(side + 16);
+            float *const scores = p.space.scores + (static_cast<long long>(use.b) * p.cache.heads * p.group +
+                                                    head * p.group + h0) * p.positions +
+                                  use.lo + use.tile * S::kTile + warp * S::kKeys;
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int row = 16 * kb + g + 8 * r;
-                    const bool in = (mask_ptr[kLaneRows > 1 ? row >> 5 : 0] >> (row & 31)) & 1u;
+                    const bool in = (mask[kb / 2 < kLaneRows ? kb / 2 : 0] >> (row & 31)) & 1u;
                     float ks = 1.0f;
                     if (kE4m3) {
                         ks = scales[row];
@@ -515,9 +547,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                             if (p.capped) x = p.last * (1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x)));
                             if (p.space.scores) {
                                 const int h = 8 * nt + 2 * t4 + i;
-                                if (in && h < hn)
-                                    p.space.scores[(static_cast<long long>(use.b) * p.cache.heads * p.group +
-                                                    head * p.group + h0 + h) * p.positions + pos0 + row] = x;
+                                if (in && h < hn) scores[h * p.positions + row] = x;
                             }
                             if (kE4m3) x += lv[kb][r];
                             s[nt][kb][2 * r + i] = in ? x : -INFINITY;
@@ -577,27 +607,26 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                         pf[nt][r] = movmatrix_trans(pair16<kMmaBf16>(w[0], w[1]));
                     }
                 }
-                const int vrow = 16 * kb + (lane & 7), sel = lane >> 3;
                 if (!kE4m3) {
-                    // matrices: (positions 0-7 | 8-15: sel >> 1) x (dims 0-7 | 8-15: sel & 1)
-                    const int row = vrow + (sel >> 1) * 8;
-                    const int sw = kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1));
+                    // matrices: (positions 0-7 | 8-15: bit 4 of the lane) x (dims 0-7 | 8-15: bit 3)
+                    const int row = (lane & 7) + (lane >> 4) * 8;
+                    const uint32_t va = src + (S::kKeys + 16 * kb + row) * S::kRow, vx = (((lane >> 3) & 1) ^ swizzle(row)) << 4;
 #pragma unroll
                     for (int mt = 0; mt < DP / 16; ++mt) {
                         uint32_t a[4];
-                        ldmatrix4_trans(a, src + (S::kKeys + row) * S::kRow + (((2 * mt + (sel & 1)) ^ sw) << 4));
+                        ldmatrix4_trans(a, va + (vx ^ (mt << 5)));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma16816<kMmaBf16>(o[nt][mt], a, pf[nt][0], pf[nt][1]);
                     }
                 } else {
-                    // matrices of byte pairs: (positions 0-7 | 8-15: sel & 1) x (dims 0-15 | 16-31: sel >> 1);
-                    // a register holds two positions of dims 2 g and 2 g + 1, which become rows g and g + 8
-                    const int row = vrow + (sel & 1) * 8;
-                    const int sw = kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1));
+                    // matrices of byte pairs: (positions 0-7 | 8-15: bit 3) x (dims 0-15 | 16-31: bit 4); a
+                    // register holds two positions of dims 2 g and 2 g + 1, which become rows g and g + 8
+                    const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
+                    const uint32_t va = src + (S::kKeys + 16 * kb + row) * S::kRow, vx = ((lane >> 4) ^ swizzle(row)) << 4;
 #pragma unroll
                     for (int c = 0; c < DP / 32; ++c) {
                         uint32_t a[4];
-                        ldmatrix4_trans(a, src + (S::kKeys + row) * S::kRow + (((2 * c + (sel >> 1)) ^ sw) << 4));
+                        ldmatrix4_trans(a, va + (vx ^ (c << 5)));
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t x = __byte_perm(a[2 * i], 0, 0x3120), y = __byte_perm(a[2 * i + 1], 0, 0x3120);
@@ -681,11 +710,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                 };
                 // Whether this CTA is the last of `n` to count at `counter` (which then is 0 again).
                 auto arrive = [&](unsigned *counter, int n) {
-                    __threadfence();
                     __syncthreads();
-                    if (threadIdx.x == 0) s_last = atomicInc(counter, static_cast<unsigned>(n - 1)) == static_cast<unsigned>(n - 1);
+                    if (threadIdx.x == 0) s_last = count_acq_rel(counter, static_cast<unsigned>(n - 1)) == static_cast<unsigned>(n - 1);
                     __syncthreads();
-                    __threadfence();
                     return s_last != 0u;
                 };
                 // Joins `n` parts (the first at part0, `stride` apart) into merge, s_ref and s_inv.
@@ -712,7 +739,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                     for (int i = threadIdx.x; i < S::kHeads * DP / 4; i += kAttendThreads) {
                         const int h = i / (DP / 4), d = i % (DP / 4) * 4;
                         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
+#pragma unroll 16
                         for (int e = 0; e < n; ++e) {
                             const float4 x = __ldcg(reinterpret_cast<const float4 *>(
                                 p.space.out + static_cast<long long>(slot_of(part0 + e * stride)) * S::kHeads * DP) + i);
@@ -766,8 +793,10 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     cp_async_wait<0>();
 }
 
-// weights[b, head, j] += sum over the group of 2^(t_j - m) / l; one thread per position.
-constexpr int kSpreadThreads = 256;
+// weights[b, head, j] += sum over the group of 2^(t_j - m) / l.  A thread adds
+// for kSpreadEach positions, kSpreadThreads apart, so that their scores are
+// requested together.
+constexpr int kSpreadThreads = 128, kSpreadEach = 4;
 
 __global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendParams p) {
     griddep_wait();
@@ -784,15 +813,35 @@ __global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendP
     const int *list = p.table.pages + b * p.table.stride;
     float *w = p.weights.base + b * p.weights.batch_stride + head * p.weights.head_stride;
     const long long row0 = static_cast<long long>(b) * p.cache.heads * p.group + head * p.group;
-    for (int j = lo + blockIdx.x * kSpreadThreads + threadIdx.x; j < n; j += gridDim.x * kSpreadThreads) {
-        int page, slot;
-        if (!kv_row(list, j, p.cache.page_size, p.cache.pages, &page, &slot)) continue;   // it has no score
-        float sum = 0.0f;
+    const float *const scores = p.space.scores + row0 * p.positions;
+    for (long long base = lo + static_cast<long long>(blockIdx.x) * kSpreadThreads * kSpreadEach; base < n;
+         base += static_cast<long long>(gridDim.x) * kSpreadThreads * kSpreadEach) {
+        int at[kSpreadEach];
+        bool is[kSpreadEach];
+        float sum[kSpreadEach], old[kSpreadEach];
+#pragma unroll
+        for (int e = 0; e < kSpreadEach; ++e) {
+            const long long j = base + e * kSpreadThreads + threadIdx.x;
+            is[e] = j < n;
+            at[e] = is[e] ? static_cast<int>(j) : lo;
+            int page, slot;
+            is[e] = is[e] && kv_row(list, at[e], p.cache.page_size, p.cache.pages, &page, &slot);   // else it has no score
+            old[e] = is[e] ? w[at[e]] : 0.0f;
+            sum[e] = 0.0f;
+        }
+#pragma unroll 4
         for (int h = 0; h < p.group; ++h) {
             const float2 ml = p.space.stats[row0 + h];
-            sum += exp2_fast(p.space.scores[(row0 + h) * p.positions + j] - ml.x) / ml.y;
+            const float inv = 1.0f / ml.y;
+#pragma unroll
+            for (int e = 0; e < kSpreadEach; ++e) {
+                const float t = is[e] ? scores[h * p.positions + at[e]] : -INFINITY;
+                sum[e] += exp2_fast(t - ml.x) * inv;
+            }
         }
-        w[j] += sum;
+#pragma unroll
+        for (int e = 0; e < kSpreadEach; ++e)
+            if (is[e]) w[at[e]] = old[e] + sum[e];
     }
 }
 
