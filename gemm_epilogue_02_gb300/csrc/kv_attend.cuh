@@ -60,8 +60,9 @@ namespace tgemm {
 constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kAttendMaxCtas = 320;       // CTAs at most (workspace slots)
-constexpr int kAttendFanIn = 16;          // parts joined at once, and the least that a group's joiner has room for
-static_assert(kAttendMaxCtas / kAttendFanIn >= kAttendFanIn, "room for the parts and for the groups");
+constexpr int kAttendFanIn = 32;          // parts joined at once (more: in two levels)
+constexpr int kAttendBatch = 16;          // parts whose outputs a thread requests together
+static_assert(kAttendMaxCtas <= kAttendFanIn * kAttendFanIn, "two levels join every CTA's part");
 constexpr int kAttendLeast = 4;           // tiles a CTA takes at least
 constexpr float kAttendGrow = 8.0f;       // log2 of the factor that moves the reference
 
@@ -213,11 +214,15 @@ __host__ __device__ inline int attend_tiles(int n, int window, int tile, int pad
 
 // CTA c of `ctas` has the tiles [attend_first(c), attend_first(c + 1)) of `total`;
 // attend_owner() is the inverse.
+__host__ __device__ inline long long attend_div(long long a, long long b) {     // a >= 0, b > 0
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
 __host__ __device__ inline long long attend_first(long long c, long long ctas, long long total) {
-    return c * total / ctas;
+    return attend_div(c * total, ctas);
 }
 __host__ __device__ inline int attend_owner(long long t, long long ctas, long long total) {
-    return static_cast<int>(((t + 1) * ctas - 1) / total);
+    return static_cast<int>(attend_div((t + 1) * ctas - 1, total));
 }
 
 // The slot of CTA c's part of an item whose first part is CTA `first`'s: a CTA
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     __shared__ long long s_sum[2][kAttendWarps];
     __shared__ int s_start[3];
     __shared__ float s_m[kAttendWarps][S::kHeads], s_l[kAttendWarps][S::kHeads];
-    __shared__ float s_w[kAttendMaxCtas / kAttendFanIn][S::kHeads];
+    __shared__ float s_w[kAttendFanIn][S::kHeads];
     __shared__ float s_inv[S::kHeads], s_ref[S::kHeads];
     __shared__ unsigned s_last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -318,8 +323,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                 if (first < at + static_cast<long long>(tiles) * heads_all) {
                     const long long in = first - at;
                     s_start[0] = b;
-                    s_start[1] = static_cast<int>(in / tiles);
-                    s_start[2] = static_cast<int>(in % tiles);
+                    s_start[1] = static_cast<int>(attend_div(in, tiles));
+                    s_start[2] = static_cast<int>(in - static_cast<long long>(s_start[1]) * tiles);
                     break;
                 }
                 at += static_cast<long long>(tiles) * heads_all;
@@ -365,7 +370,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     const unsigned char *const vpool = p.cache.v + (inside ? piece * 16 : 0);
     auto swizzle = [](int row) { return kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1)); };
     const uint32_t copy_to = in_copy * S::kRow + ((piece ^ swizzle(in_copy)) << 4);
-    auto issue = [&](int stage) {
+    // Starts the copies of the rows that lookup() found (page, slot, want, head).
+    auto issue = [&](int stage, const int (&page)[kLaneRows], const int (&slot)[kLaneRows],
+                     const unsigned (&want)[kLaneRows], int load_head) {
         const uint32_t dst = ring + stage * S::kStage;
         unsigned char *const side = sides + stage * S::kSide;
         unsigned ok[kLaneRows], some = 0;
@@ -406,11 +413,23 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
         cp_async_commit();
     };
 
-    lookup();
+    {
+        // The first two steps' pages are requested together.
+        static_assert(S::kStages == 3, "two steps ahead");
+        lookup();
+        int page0[kLaneRows], slot0[kLaneRows];
+        unsigned want0[kLaneRows];
+        const int head0 = load_head;
 #pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) {
-        issue(s);
+        for (int r = 0; r < kLaneRows; ++r) {
+            page0[r] = page[r];
+            slot0[r] = slot[r];
+            want0[r] = want[r];
+        }
+        lookup();
+        issue(0, page0, slot0, want0, head0);
         __syncwarp();
+        issue(1, page, slot, want, load_head);
         lookup();
     }
 
@@ -418,66 +437,74 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     uint32_t qf[NT][DP / 16][2];
     float qscale[NT][2];                   // to log2 units, for heads 2 t4 and 2 t4 + 1
     float o[NT][DP / 16][4], m[NT][2], l[NT][2];
-    bool fresh = true;
     int begun = use.tile;                  // first tile of this CTA's part
-    int stage = 0;
-    for (int step = 0; step < steps; ++step) {
-        const int head = use.head, h0 = use.block * S::kHeads, hn = min(S::kHeads, p.group - h0);    // the block's heads
-        if (fresh) {
-            fresh = false;
-            begun = use.tile;
+    // The item's queries are requested (request_q) as soon as the previous item's last product is done,
+    // and made ready (begin) after it is joined.
+    auto request_q = [&](const AttendCursor &u) {
+        const int h0 = u.block * S::kHeads, hn = min(S::kHeads, p.group - h0);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int qh = h0 + 8 * nt + g;
-                const bool is = 8 * nt + g < hn;
-                const unsigned char *row = p.q + use.b * p.q_batch_stride +
-                                           (static_cast<long long>(head) * p.group + (is ? qh : h0)) * p.q_head_stride;
+        for (int nt = 0; nt < NT; ++nt) {
+            const bool is = 8 * nt + g < hn;
+            const unsigned char *row = p.q + u.b * p.q_batch_stride +
+                                       (static_cast<long long>(u.head) * p.group + h0 + (is ? 8 * nt + g : 0)) * p.q_head_stride;
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int d = kE4m3 ? 16 * kk + 4 * t4 + 2 * i : 16 * kk + 2 * t4 + 8 * i;
+                    qf[nt][kk][i] = is && d < p.cache.dim ? *reinterpret_cast<const uint32_t *>(row + 2 * d) : 0u;
+                }
+        }
+    };
+    auto begin = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float unit = 1.0f;
+            if (kE4m3 && kBf16) {
+                // Largest element to [2^14, 2^15): fp16 then keeps bf16's eight bits down to 2^-29 of it.
                 float top = 0.0f;
 #pragma unroll
                 for (int kk = 0; kk < DP / 16; ++kk)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int d = kE4m3 ? 16 * kk + 4 * t4 + 2 * i : 16 * kk + 2 * t4 + 8 * i;
-                        const uint32_t x = is && d < p.cache.dim ? *reinterpret_cast<const uint32_t *>(row + 2 * d) : 0u;
-                        qf[nt][kk][i] = x;
-                        if (kE4m3 && kBf16)
-                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x << 16)), fabsf(__uint_as_float(x & 0xFFFF0000u))));
+                        const uint32_t x = qf[nt][kk][i];
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x << 16)), fabsf(__uint_as_float(x & 0xFFFF0000u))));
                     }
-                float unit = 1.0f;
-                if (kE4m3 && kBf16) {
-                    // Largest element to [2^14, 2^15): fp16 then keeps bf16's eight bits down to
-                    // 2^-29 of it.
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;      // -127 for zero
-                    const int shift = min(max(14 - e, -126), 126);
-                    const float up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
-                    unit = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;      // -127 for zero
+                const int shift = min(max(14 - e, -126), 126);
+                const float up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+                unit = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
 #pragma unroll
-                    for (int kk = 0; kk < DP / 16; ++kk)
+                for (int kk = 0; kk < DP / 16; ++kk)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t x = qf[nt][kk][i];
-                            qf[nt][kk][i] = pair16<false>(__uint_as_float(x << 16) * up,
-                                                          __uint_as_float(x & 0xFFFF0000u) * up);
-                        }
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    qscale[nt][i] = p.first * __shfl_sync(0xffffffffu, unit, (2 * t4 + i) * 4);
-                    m[nt][i] = -INFINITY;
-                    l[nt][i] = 0.0f;
-                }
-#pragma unroll
-                for (int mt = 0; mt < DP / 16; ++mt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.0f;
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t x = qf[nt][kk][i];
+                        qf[nt][kk][i] = pair16<false>(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xFFFF0000u) * up);
+                    }
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                qscale[nt][i] = p.first * __shfl_sync(0xffffffffu, unit, (2 * t4 + i) * 4);
+                m[nt][i] = -INFINITY;
+                l[nt][i] = 0.0f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < DP / 16; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.0f;
         }
+    };
+    request_q(use);
+    begin();
+    int stage = 0;
+    for (int step = 0; step < steps; ++step) {
+        const int head = use.head, h0 = use.block * S::kHeads, hn = min(S::kHeads, p.group - h0);    // the block's heads
         cp_async_wait<S::kStages - 2>();
         __syncwarp();
         // the stage that the previous step has read takes the step that comes kStages - 1 after this one
-        issue(stage == 0 ? S::kStages - 1 : stage - 1);
+        issue(stage == 0 ? S::kStages - 1 : stage - 1, page, slot, want, load_head);
         lookup();
         const uint32_t src = ring + stage * S::kStage;
         const unsigned char *const side = sides + stage * S::kSide;
@@ -640,8 +667,21 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
         }
         stage = stage + 1 == S::kStages ? 0 : stage + 1;
 
-        const bool ends = use.tile + 1 == use.tiles;
-        if (ends || step + 1 == steps) {
+        const bool ends = use.tile + 1 == use.tiles, more = step + 1 < steps;
+        if (!ends && more) {
+            ++use.tile;
+            continue;
+        }
+        {
+            const int b = use.b;
+            const long long item = first + step - use.tile;      // the item's first tile among all
+            const long long item_end = item + use.tiles;
+            const bool whole = begun == 0 && ends;
+            if (more) {
+                cursor_next(use, p, S::kTile, pad);
+                request_q(use);
+                begun = use.tile;
+            }
             // ---- join the warps: one reference, then the outputs one warp after the other
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -673,26 +713,29 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                         s_inv[h] = sum;
                     }
                 }
-            for (int w = 0; w < kAttendWarps; ++w) {
-                if (warp == w) {
+            // Each round every warp adds a quarter of the dims of its own, so that all work at once and every
+            // quarter meets the warps in a fixed order.
+            static_assert(kAttendWarps == 4 && DP % 64 == 0, "quarters of whole 16-row tiles");
+#pragma unroll 1
+            for (int round = 0; round < kAttendWarps; ++round) {
+                const int quarter = (warp + round) & 3;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                for (int mt = 0; mt < DP / 16; ++mt) {
+                    if (mt / (DP / 64) == quarter) {
 #pragma unroll
-                        for (int mt = 0; mt < DP / 16; ++mt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const int d = 16 * mt + (kE4m3 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
                                 float *at = merge + (8 * nt + 2 * t4 + (i & 1)) * S::kPitch + d;
                                 const float x = o[nt][mt][i] * a[nt][i & 1];
-                                *at = w == 0 ? x : *at + x;
+                                *at = round == 0 ? x : *at + x;
                             }
+                    }
                 }
                 __syncthreads();
             }
             // ---- whole: the answer; a part: to the workspace, and the last to arrive joins
-            const long long item = first + step - use.tile;      // the item's first tile among all
-            const long long item_end = item + use.tiles;
-            const bool whole = begun == 0 && ends;
             bool answer = whole;
             if (!whole) {
                 const int c0 = attend_owner(item, ctas, all), c1 = attend_owner(item_end - 1, ctas, all);
@@ -701,7 +744,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                 auto slot_of = [&](int part) { return attend_slot(c0 + part, c0); };
                 auto put = [&](int to) {
                     float *dst = p.space.out + static_cast<long long>(to) * S::kHeads * DP;
-                    for (int i = threadIdx.x; i < S::kHeads * DP / 4; i += kAttendThreads) {
+                    for (int i = threadIdx.x; i < hn * DP / 4; i += kAttendThreads) {
                         const int h = i / (DP / 4), d = i % (DP / 4) * 4;
                         __stcg(reinterpret_cast<float4 *>(dst) + i, *reinterpret_cast<const float4 *>(merge + h * S::kPitch + d));
                     }
@@ -719,7 +762,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                 auto join = [&](int part0, int stride, int n) {
                     for (int i = threadIdx.x; i < n * S::kHeads; i += kAttendThreads) {
                         const int e = i / S::kHeads, h = i % S::kHeads;
-                        s_w[e][h] = __ldcg(&p.space.ml[slot_of(part0 + e * stride) * S::kHeads + h].x);
+                        const float2 ml = __ldcg(p.space.ml + slot_of(part0 + e * stride) * S::kHeads + h);
+                        s_w[e][h] = ml.x;
+                        merge[i] = ml.y;
                     }
                     __syncthreads();
                     if (threadIdx.x < S::kHeads) {
@@ -730,24 +775,34 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                         for (int e = 0; e < n; ++e) {
                             const float w = exp2_fast(s_w[e][h] - base);
                             s_w[e][h] = w;
-                            sum += w * __ldcg(&p.space.ml[slot_of(part0 + e * stride) * S::kHeads + h].y);
+                            sum += w * merge[e * S::kHeads + h];
                         }
                         s_ref[h] = ref;
                         s_inv[h] = sum;
                     }
                     __syncthreads();
-                    for (int i = threadIdx.x; i < S::kHeads * DP / 4; i += kAttendThreads) {
+#pragma unroll 1
+                    for (int i = threadIdx.x; i < hn * DP / 4; i += kAttendThreads) {
                         const int h = i / (DP / 4), d = i % (DP / 4) * 4;
                         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 16
-                        for (int e = 0; e < n; ++e) {
-                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(
-                                p.space.out + static_cast<long long>(slot_of(part0 + e * stride)) * S::kHeads * DP) + i);
-                            const float w = s_w[e][h];
-                            sum.x += w * x.x;
-                            sum.y += w * x.y;
-                            sum.z += w * x.z;
-                            sum.w += w * x.w;
+#pragma unroll 1
+                        for (int e0 = 0; e0 < n; e0 += kAttendBatch) {
+                            float4 x[kAttendBatch];
+#pragma unroll
+                            for (int e = 0; e < kAttendBatch; ++e)
+                                x[e] = e0 + e < n ? __ldcg(reinterpret_cast<const float4 *>(
+                                                               p.space.out + static_cast<long long>(slot_of(part0 + (e0 + e) * stride)) *
+                                                                                 S::kHeads * DP) + i)
+                                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                            for (int e = 0; e < kAttendBatch; ++e) {
+                                if (e0 + e >= n) break;
+                                const float w = s_w[e0 + e][h];
+                                sum.x += w * x[e].x;
+                                sum.y += w * x[e].y;
+                                sum.z += w * x[e].z;
+                                sum.w += w * x[e].w;
+                            }
                         }
                         *reinterpret_cast<float4 *>(merge + h * S::kPitch + d) = sum;
                     }
@@ -769,7 +824,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
             if (answer) {
                 const int h_all = p.cache.heads * p.group;
                 if (threadIdx.x < hn && p.space.scores)
-                    p.space.stats[static_cast<long long>(use.b) * h_all + head * p.group + h0 + threadIdx.x] =
+                    p.space.stats[static_cast<long long>(b) * h_all + head * p.group + h0 + threadIdx.x] =
                         make_float2(s_ref[threadIdx.x], s_inv[threadIdx.x]);
                 for (int i = threadIdx.x; i < hn * (DP / 8); i += kAttendThreads) {
                     const int h = i / (DP / 8), d = i % (DP / 8) * 8;
@@ -780,15 +835,14 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                     for (int e = 0; e < 8; ++e) x[e] = sum == 0.0f ? 0.0f : merge[h * S::kPitch + d + e] / sum;
                     const uint4 v = make_uint4(pair16<kBf16>(x[0], x[1]), pair16<kBf16>(x[2], x[3]),
                                                pair16<kBf16>(x[4], x[5]), pair16<kBf16>(x[6], x[7]));
-                    *reinterpret_cast<uint4 *>(p.o + use.b * p.o_batch_stride +
+                    *reinterpret_cast<uint4 *>(p.o + b * p.o_batch_stride +
                                                (static_cast<long long>(head) * p.group + h0 + h) * p.o_head_stride +
                                                2 * d) = v;
                 }
             }
             __syncthreads();               // merge and the statistics are free again
-            fresh = true;
+            if (more) begin();
         }
-        if (step + 1 < steps) cursor_next(use, p, S::kTile, pad);
     }
     cp_async_wait<0>();
 }
