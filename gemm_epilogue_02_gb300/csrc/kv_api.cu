@@ -173,7 +173,7 @@ cudaError_t launch_append_lanes(const RuntimeInfo &rt, const AppendParams &p, cu
     const int64_t passes = (p.tokens * p.cache.heads + kPass - 1) / kPass;
     if (passes <= 2 * rt.num_sms)
         return launch(kv_append_kernel<kBf16, kE4m3, kLanes, 1>, dim3(static_cast<unsigned>(passes)), kRowThreads, 0, s, p);
-    const int64_t chunks = std::min<int64_t>((passes + 3) / 4, INT32_MAX);
+    const int64_t chunks = std::min<int64_t>((passes + 3) / 4, static_cast<int64_t>(rt.num_sms) * kAppendCtas);
     return launch(kv_append_kernel<kBf16, kE4m3, kLanes, 4>, dim3(static_cast<unsigned>(chunks)), kRowThreads, 0, s, p);
 }
 
@@ -184,6 +184,31 @@ cudaError_t launch_append(const RuntimeInfo &rt, const AppendParams &p, cudaStre
         case 16: return launch_append_lanes<kBf16, kE4m3, 16>(rt, p, s);
         default: return launch_append_lanes<kBf16, kE4m3, 32>(rt, p, s);
     }
+}
+
+template <int kThreads>
+cudaError_t launch_select_threads(const RuntimeInfo &rt, EvictParams &p, int64_t positions, int cluster, cudaStream_t s) {
+    auto kernel = kv_select_kernel<kThreads>;
+    const int64_t slice = (positions + cluster - 1) / cluster;
+    p.cached = slice <= kSelectMaxCached ? static_cast<int>(slice) : 0;
+    static std::atomic<uint64_t> ready{0};      // bit per device
+    const uint64_t bit = uint64_t(1) << rt.device;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectMaxCached * 4);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    const dim3 grid(static_cast<unsigned>(cluster), static_cast<unsigned>(p.from.heads), static_cast<unsigned>(p.table.batch));
+    return launch(kernel, grid, kThreads, static_cast<size_t>(p.cached) * 4, s, p, cluster);
+}
+
+// positions: what a sequence can have at most.  Up to 4096 one block of 256
+// threads takes them; beyond, blocks of 1024 take 8192 each, up to eight blocks.
+cudaError_t launch_select(const RuntimeInfo &rt, EvictParams &p, int64_t positions, cudaStream_t s) {
+    if (positions <= 4096) return launch_select_threads<256>(rt, p, positions, 1, s);
+    int cluster = 1;
+    while (cluster < 8 && cluster * 8192 < positions) cluster *= 2;
+    return launch_select_threads<1024>(rt, p, positions, cluster, s);
 }
 
 template <bool kE4m3, int kLanes>
@@ -226,7 +251,8 @@ int64_t attend_layout(int64_t batch, int64_t q_heads, int64_t group, int64_t dim
     const int64_t o = take(slots * heads * padded_dim(dim) * 4), ml = take(slots * heads * 8);
     int64_t stats = 0, s = 0;
     if (weights) {
-        if (__builtin_mul_overflow(batch * q_heads * 4, positions, &scores) || scores > kMost) return -1;
+        const int64_t scored = batch * (q_heads / group) * ((group + 1) / 2 * 2);
+        if (__builtin_mul_overflow(scored * 4, positions, &scores) || scores > kMost) return -1;
         stats = take(batch * q_heads * 8);
         s = take(scores);
     }
@@ -367,6 +393,7 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args
     if (!extent(size, qs, 2, cache->dim, 2, false, &qbytes) || !extent(size, os, 2, cache->dim, 2, true, &obytes))
         return TGEMM_ERR_INVALID_ARG;
     p.group = static_cast<int>(q_heads / cache->heads);
+    p.scored = (p.group + 1) / 2 * 2;
     p.positions = a->seq.pages_width * cache->page_size;
     const int64_t need = attend_layout(batch, q_heads, p.group, cache->dim, p.positions, a->weights.data != nullptr,
                                        static_cast<unsigned char *>(a->workspace), &p.space);
@@ -464,12 +491,8 @@ extern "C" tgemm_status tgemm_kv_evict(const tgemm_kv_evict_args *a, tgemm_strea
     p.recent = static_cast<int>(std::min<int64_t>(a->recent, INT32_MAX));
     p.status = rt.status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // Blocks that share a sequence and head: one per 8192 positions that there can be.
     const int64_t positions = std::min<int64_t>(a->seq.pages_width * from->page_size, a->weights.width);
-    int cluster = 1;
-    while (cluster < 8 && cluster * 8192 < positions) cluster *= 2;
-    st = done(launch(kv_select_kernel, dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(heads), static_cast<unsigned>(batch)),
-                     kSelectThreads, 0, s, p, cluster));
+    st = done(launch_select(rt, p, positions, s));
     if (st != TGEMM_OK) return st;
     const int64_t most = std::min<int64_t>(keep, positions);
     return done(from->e4m3 ? launch_gather<true>(p, most, from->heads, static_cast<int>(batch), s)

@@ -10,7 +10,8 @@
 // of dependent loads (starts, lengths, page list), so a block first finds the
 // places of a whole chunk of rows, one thread each, and then streams the chunk:
 // as many lanes as a row has 16-byte pieces, every piece of the chunk (keys and
-// values) requested before the first is used.
+// values) requested before the first is used, and the next chunk's places found
+// while they are on their way.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -95,70 +96,74 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8]) {
 
 // Blocks take chunks of kRows rows, a row being the keys and values of one
 // (token, head), kUnroll passes of kRowThreads / kLanes rows.
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256, kAppendCtas = 4;     // per SM
 
 template <bool kBf16, bool kE4m3, int kLanes, int kUnroll>
-__global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kRowThreads, kAppendCtas) kv_append_kernel(const AppendParams p) {
     constexpr int kPass = kRowThreads / kLanes, kRows = kPass * kUnroll;
-    __shared__ long long s_src[kRows], s_dst[kRows], s_scale[kRows];
+    __shared__ long long s_src[2][kRows], s_dst[2][kRows], s_scale[2][kRows];
     griddep_wait();
     griddep_launch_dependents();
-    const long long rows = p.tokens * p.cache.heads;
+    const long long rows = p.tokens * p.cache.heads, step = static_cast<long long>(gridDim.x) * kRows;
     const int piece = threadIdx.x % kLanes, in_pass = threadIdx.x / kLanes;
     const bool inside = piece * 8 < p.cache.dim;
-    for (long long r0 = static_cast<long long>(blockIdx.x) * kRows; r0 < rows;
-         r0 += static_cast<long long>(gridDim.x) * kRows) {
-        if (threadIdx.x < kRows) {
-            const long long r = r0 + threadIdx.x;
-            long long src = 0, dst = -1, scale = 0;
-            if (r < rows) {
-                const long long t = r / p.cache.heads;
-                const int head = static_cast<int>(r - t * p.cache.heads);
-                int b = static_cast<int>(t);
-                long long back = 1;                 // positions from the sequence's end
-                if (p.starts) {
-                    b = kv_sequence_of(p.starts, p.table.batch, t);
-                    if (b >= 0) back = p.starts[b + 1] - t;
-                }
-                if (b >= 0) {
-                    const long long pos = p.table.lengths[b] - back;
-                    int page, slot;
-                    if (pos < 0 || pos >= static_cast<long long>(p.table.width) * p.cache.page_size ||
-                        !kv_row(p.table.pages + b * p.table.stride, static_cast<int>(pos), p.cache.page_size,
-                                p.cache.pages, &page, &slot)) {
-                        record_status(p.status, kStatusCache);
-                    } else {
-                        src = t * p.token_stride + head * p.head_stride;
-                        dst = kv_offset(p.cache, page, slot, head);
-                        if (kE4m3) scale = kv_scale_offset(p.cache, page, slot, head);
-                        if (p.weights.base) {
-                            if (pos < p.weights.width)
-                                p.weights.base[b * p.weights.batch_stride + head * p.weights.head_stride + pos] = 0.0f;
-                            else
-                                record_status(p.status, kStatusCache);
-                        }
+    // Thread i < kRows finds the place of row r0 + i.
+    auto place = [&](long long r0, int to) {
+        if (threadIdx.x >= kRows) return;
+        const long long r = r0 + threadIdx.x;
+        long long src = 0, dst = -1, scale = 0;
+        if (r < rows) {
+            const long long t = r / p.cache.heads;
+            const int head = static_cast<int>(r - t * p.cache.heads);
+            int b = static_cast<int>(t);
+            long long back = 1;                 // positions from the sequence's end
+            if (p.starts) {
+                b = kv_sequence_of(p.starts, p.table.batch, t);
+                if (b >= 0) back = p.starts[b + 1] - t;
+            }
+            if (b >= 0) {
+                const long long pos = p.table.lengths[b] - back;
+                int page, slot;
+                if (pos < 0 || pos >= static_cast<long long>(p.table.width) * p.cache.page_size ||
+                    !kv_row(p.table.pages + b * p.table.stride, static_cast<int>(pos), p.cache.page_size,
+                            p.cache.pages, &page, &slot)) {
+                    record_status(p.status, kStatusCache);
+                } else {
+                    src = t * p.token_stride + head * p.head_stride;
+                    dst = kv_offset(p.cache, page, slot, head);
+                    if (kE4m3) scale = kv_scale_offset(p.cache, page, slot, head);
+                    if (p.weights.base) {
+                        if (pos < p.weights.width)
+                            p.weights.base[b * p.weights.batch_stride + head * p.weights.head_stride + pos] = 0.0f;
+                        else
+                            record_status(p.status, kStatusCache);
                     }
                 }
             }
-            s_src[threadIdx.x] = src;
-            s_dst[threadIdx.x] = dst;
-            s_scale[threadIdx.x] = scale;
         }
-        __syncthreads();
+        s_src[to][threadIdx.x] = src;
+        s_dst[to][threadIdx.x] = dst;
+        s_scale[to][threadIdx.x] = scale;
+    };
+    long long r0 = static_cast<long long>(blockIdx.x) * kRows;
+    place(r0, 0);
+    __syncthreads();
+    for (int at = 0; r0 < rows; r0 += step, at ^= 1) {
         uint4 x[kUnroll][2];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int i = u * kPass + in_pass;
             x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-            if (s_dst[i] >= 0 && inside) {
-                x[u][0] = __ldcs(reinterpret_cast<const uint4 *>(p.k + s_src[i]) + piece);
-                x[u][1] = __ldcs(reinterpret_cast<const uint4 *>(p.v + s_src[i]) + piece);
+            if (s_dst[at][i] >= 0 && inside) {
+                x[u][0] = __ldcs(reinterpret_cast<const uint4 *>(p.k + s_src[at][i]) + piece);
+                x[u][1] = __ldcs(reinterpret_cast<const uint4 *>(p.v + s_src[at][i]) + piece);
             }
         }
+        if (r0 + step < rows) place(r0 + step, at ^ 1);      // while the rows are on their way
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int i = u * kPass + in_pass;
-            const long long dst = s_dst[i];
+            const long long dst = s_dst[at][i];
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 unsigned char *pool = which ? p.cache.v : p.cache.k;
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const AppendPara
                 const float scale = top > 0.0f ? top / 448.0f : 1.0f;
                 divide8(f, scale);
                 if (dst >= 0 && inside) *(reinterpret_cast<uint2 *>(pool + dst) + piece) = pack8_e4m3(f);
-                if (dst >= 0 && piece == 0) (which ? p.cache.v_scale : p.cache.k_scale)[s_scale[i]] = scale;
+                if (dst >= 0 && piece == 0) (which ? p.cache.v_scale : p.cache.k_scale)[s_scale[at][i]] = scale;
             }
         }
         __syncthreads();

@@ -61,7 +61,6 @@ constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kAttendMaxCtas = 320;       // CTAs at most (workspace slots)
 constexpr int kAttendFanIn = 32;          // parts joined at once (more: in two levels)
-constexpr int kAttendBatch = 16;          // parts whose outputs a thread requests together
 static_assert(kAttendMaxCtas <= kAttendFanIn * kAttendFanIn, "two levels join every CTA's part");
 constexpr int kAttendLeast = 4;           // tiles a CTA takes at least
 constexpr float kAttendGrow = 8.0f;       // log2 of the factor that moves the reference
@@ -74,7 +73,7 @@ struct AttendSpace {
     float *out;             // [2 * kAttendMaxCtas][heads of a block][padded dim]
     float2 *ml;             // [2 * kAttendMaxCtas][heads of a block]
     float2 *stats;          // [batch, q_heads]
-    float *scores;          // [batch, q_heads, positions]
+    float *scores;          // [batch, heads, positions, scored]: in log2 units, before the reference is taken off
 };
 
 struct AttendParams {
@@ -85,7 +84,8 @@ struct AttendParams {
     const unsigned char *q;
     unsigned char *o;
     long long q_batch_stride, q_head_stride, o_batch_stride, o_head_stride;   // bytes
-    long long positions;                  // of a row of scores
+    long long positions;                  // what the page lists can hold
+    int scored;                           // query heads of a key head, rounded up to an even number
     int group, blocks;                    // query heads of a key head; blocks that they make
     int window;
     int page_shift;                       // log2 of the page size, -1: not a power of two
@@ -103,6 +103,7 @@ struct AttendShape {
     static constexpr int kTile = kAttendWarps * kKeys;
     static constexpr int kHeads = 8 * NT;
     static constexpr int kStages = 3;
+    static constexpr int kBatch = NT == 2 || DP == 256 ? 10 : 16;              // parts joined per request (what registers hold)
     static constexpr int kStage = 2 * kKeys * kRow;                       // keys, values
     static constexpr int kSide = kE4m3 ? 2 * kKeys * 4 + 16 : 16;         // a stage's scales and mask
     static constexpr int kSides = kAttendWarps * kStages * kStage;        // where the sides begin
@@ -549,9 +550,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
             // scores in log2 units, masked; the value scales join the exponent
             float lv[kBlocks][2], inv[kBlocks][2];
             const float *scales = reinterpret_cast<const float *>(side + 16);
-            float *const scores = p.space.scores + (static_cast<long long>(use.b) * p.cache.heads * p.group +
-                                                    head * p.group + h0) * p.positions +
-                                  use.lo + use.tile * S::kTile + warp * S::kKeys;
+            float *const scores = p.space.scores +
+                                  ((static_cast<long long>(use.b) * p.cache.heads + head) * p.positions + use.lo +
+                                   use.tile * S::kTile + warp * S::kKeys) * p.scored + h0 + 2 * t4;
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb)
 #pragma unroll
@@ -566,19 +567,22 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                         inv[kb][r] = __fdividef(1.0f, vs);
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float x[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float x = s[nt][kb][2 * r + i] * qscale[nt][i];
-                            if (kE4m3) x *= ks;
-                            if (p.capped) x = p.last * (1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x)));
-                            if (p.space.scores) {
-                                const int h = 8 * nt + 2 * t4 + i;
-                                if (in && h < hn) scores[h * p.positions + row] = x;
-                            }
-                            if (kE4m3) x += lv[kb][r];
-                            s[nt][kb][2 * r + i] = in ? x : -INFINITY;
+                            x[i] = s[nt][kb][2 * r + i] * qscale[nt][i];
+                            if (kE4m3) x[i] *= ks;
+                            if (p.capped) x[i] = p.last * (1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x[i])));
                         }
+                        if (p.space.scores && in && 8 * nt + 2 * t4 < hn)
+                            *reinterpret_cast<float2 *>(scores + row * p.scored + 8 * nt) = make_float2(x[0], x[1]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (kE4m3) x[i] += lv[kb][r];
+                            s[nt][kb][2 * r + i] = in ? x[i] : -INFINITY;
+                        }
+                    }
                 }
             // the reference moves when some score exceeds it by more than 2^kAttendGrow
             bool grow = false;
@@ -781,30 +785,42 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                         s_inv[h] = sum;
                     }
                     __syncthreads();
+                    // Two outputs of a thread at a time, kBatch parts of each requested together.
+                    const int outputs = hn * DP / 4;
 #pragma unroll 1
-                    for (int i = threadIdx.x; i < hn * DP / 4; i += kAttendThreads) {
-                        const int h = i / (DP / 4), d = i % (DP / 4) * 4;
-                        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int i0 = threadIdx.x; i0 < outputs; i0 += 2 * kAttendThreads) {
+                        float4 sum[2] = {};
 #pragma unroll 1
-                        for (int e0 = 0; e0 < n; e0 += kAttendBatch) {
-                            float4 x[kAttendBatch];
+                        for (int e0 = 0; e0 < n; e0 += S::kBatch) {
+                            float4 x[2][S::kBatch];
 #pragma unroll
-                            for (int e = 0; e < kAttendBatch; ++e)
-                                x[e] = e0 + e < n ? __ldcg(reinterpret_cast<const float4 *>(
-                                                               p.space.out + static_cast<long long>(slot_of(part0 + (e0 + e) * stride)) *
-                                                                                 S::kHeads * DP) + i)
-                                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            for (int e = 0; e < S::kBatch; ++e) {
+                                const float4 *from = reinterpret_cast<const float4 *>(
+                                    p.space.out + static_cast<long long>(slot_of(part0 + (e0 + e) * stride)) * S::kHeads * DP);
 #pragma unroll
-                            for (int e = 0; e < kAttendBatch; ++e) {
+                                for (int y = 0; y < 2; ++y) {
+                                    const int i = i0 + y * kAttendThreads;
+                                    x[y][e] = e0 + e < n && i < outputs ? __ldcg(from + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < S::kBatch; ++e) {
                                 if (e0 + e >= n) break;
-                                const float w = s_w[e0 + e][h];
-                                sum.x += w * x[e].x;
-                                sum.y += w * x[e].y;
-                                sum.z += w * x[e].z;
-                                sum.w += w * x[e].w;
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    const float w = s_w[e0 + e][min(i0 + y * kAttendThreads, outputs - 1) / (DP / 4)];
+                                    sum[y].x += w * x[y][e].x;
+                                    sum[y].y += w * x[y][e].y;
+                                    sum[y].z += w * x[y][e].z;
+                                    sum[y].w += w * x[y][e].w;
+                                }
                             }
                         }
-                        *reinterpret_cast<float4 *>(merge + h * S::kPitch + d) = sum;
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int i = i0 + y * kAttendThreads;
+                            if (i < outputs) *reinterpret_cast<float4 *>(merge + i / (DP / 4) * S::kPitch + i % (DP / 4) * 4) = sum[y];
+                        }
                     }
                     __syncthreads();
                 };
@@ -847,12 +863,13 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     cp_async_wait<0>();
 }
 
-// weights[b, head, j] += sum over the group of 2^(t_j - m) / l.  A thread adds
-// for kSpreadEach positions, kSpreadThreads apart, so that their scores are
-// requested together.
-constexpr int kSpreadThreads = 128, kSpreadEach = 4;
+// weights[b, head, j] += sum over the group of 2^(t_j - m) / l.  A position's
+// scores lie together; a thread adds for kSpreadEach positions, kSpreadThreads
+// apart, whose first eight heads it requests together.
+constexpr int kSpreadThreads = 256, kSpreadEach = 4;
 
 __global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendParams p) {
+    constexpr int kPairs = 4;             // of heads, per request
     griddep_wait();
     griddep_launch_dependents();
     const int head = blockIdx.y, b = blockIdx.z;
@@ -866,36 +883,46 @@ __global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendP
     }
     const int *list = p.table.pages + b * p.table.stride;
     float *w = p.weights.base + b * p.weights.batch_stride + head * p.weights.head_stride;
-    const long long row0 = static_cast<long long>(b) * p.cache.heads * p.group + head * p.group;
-    const float *const scores = p.space.scores + row0 * p.positions;
+    const long long row0 = static_cast<long long>(b) * p.cache.heads + head;
+    const float *const scores = p.space.scores + row0 * p.positions * p.scored;
+    const float2 *const stats = p.space.stats + row0 * p.group;
     for (long long base = lo + static_cast<long long>(blockIdx.x) * kSpreadThreads * kSpreadEach; base < n;
          base += static_cast<long long>(gridDim.x) * kSpreadThreads * kSpreadEach) {
         int at[kSpreadEach];
         bool is[kSpreadEach];
-        float sum[kSpreadEach], old[kSpreadEach];
+        float old[kSpreadEach], sum[kSpreadEach];
 #pragma unroll
         for (int e = 0; e < kSpreadEach; ++e) {
             const long long j = base + e * kSpreadThreads + threadIdx.x;
             is[e] = j < n;
             at[e] = is[e] ? static_cast<int>(j) : lo;
-            int page, slot;
-            is[e] = is[e] && kv_row(list, at[e], p.cache.page_size, p.cache.pages, &page, &slot);   // else it has no score
-            old[e] = is[e] ? w[at[e]] : 0.0f;
+            old[e] = w[at[e]];
             sum[e] = 0.0f;
         }
-#pragma unroll 4
-        for (int h = 0; h < p.group; ++h) {
-            const float2 ml = p.space.stats[row0 + h];
-            const float inv = 1.0f / ml.y;
+        for (int h0 = 0; h0 < p.group; h0 += 2 * kPairs) {
+            float2 t[kSpreadEach][kPairs];
 #pragma unroll
-            for (int e = 0; e < kSpreadEach; ++e) {
-                const float t = is[e] ? scores[h * p.positions + at[e]] : -INFINITY;
-                sum[e] += exp2_fast(t - ml.x) * inv;
+            for (int e = 0; e < kSpreadEach; ++e)
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i)
+                    t[e][i] = *reinterpret_cast<const float2 *>(scores + static_cast<long long>(at[e]) * p.scored +
+                                                                min(h0 + 2 * i, p.scored - 2));
+#pragma unroll
+            for (int i = 0; i < 2 * kPairs; ++i) {
+                if (h0 + i >= p.group) break;
+                const float2 ml = stats[h0 + i];
+                const float inv = __fdividef(1.0f, ml.y);
+#pragma unroll
+                for (int e = 0; e < kSpreadEach; ++e)
+                    sum[e] += exp2_fast((i & 1 ? t[e][i / 2].y : t[e][i / 2].x) - ml.x) * inv;
             }
         }
 #pragma unroll
-        for (int e = 0; e < kSpreadEach; ++e)
-            if (is[e]) w[at[e]] = old[e] + sum[e];
+        for (int e = 0; e < kSpreadEach; ++e) {
+            int page, slot;
+            if (is[e] && kv_row(list, at[e], p.cache.page_size, p.cache.pages, &page, &slot))   // else it has no score
+                w[at[e]] = old[e] + sum[e];
+        }
     }
 }
 

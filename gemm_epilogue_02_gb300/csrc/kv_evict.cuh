@@ -10,11 +10,12 @@
 //
 // Selection reads 4 bytes a position and is bound by latency: a cluster of
 // blocks shares one sequence and head, each block a slice of its positions.  A
-// weight becomes a 32-bit key of the same order; the key of rank k - r is found
-// 11 bits at a time (11 + 11 + 10) from histograms of the keys that share the
-// bits found so far, which the blocks add up through distributed shared memory;
-// then every larger key is kept, and of the equal ones the first few in order of
-// position.  A slice stays in the block's L1 between its five passes.
+// weight becomes a 32-bit key of the same order, which stays in shared memory;
+// the key of rank k - r is found 11 bits at a time (11 + 11 + 10) from
+// histograms of the keys that share the bits found so far, added up through
+// distributed shared memory: one warp of each block reads the sums of 32 bins,
+// finds the group, then reads its bins.  Then every larger key is kept, and of
+// the equal ones the first few in order of position.
 #pragma once
 #include <cooperative_groups.h>
 
@@ -22,9 +23,10 @@
 
 namespace tgemm {
 
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectBins = 2048;
+constexpr int kSelectGroups = kSelectBins / 32;
+constexpr int kSelectMaxCached = 48 * 1024;           // keys of a slice in shared memory (192 KiB); of longer ones none
+static_assert(kSelectGroups == 64, "two groups a lane");
 
 struct EvictParams {
     KvView from, to;
@@ -33,6 +35,7 @@ struct EvictParams {
     int *kept;                     // [batch, heads, keep]
     int *to_lengths;
     int keep, recent;
+    int cached;                    // keys that the selection's blocks have room for
     unsigned int *status;
 };
 
@@ -44,19 +47,34 @@ __host__ __device__ inline uint32_t kv_weight_key(uint32_t bits) {
     return (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;
 }
 
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ int warp_scan(int v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
 // Grid: (cluster size, heads, batch), a cluster along x.
-__global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const EvictParams p) {
-    __shared__ int hist[kSelectBins];
-    __shared__ int warp_sums[2][kSelectWarps];
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParams p) {
+    constexpr int kWarps = kThreads / 32;
+    extern __shared__ uint32_t keys[];
+    __shared__ int hist[3][kSelectBins], groups[3][kSelectGroups];
+    __shared__ int warp_sums[2][kWarps];
     __shared__ int s_counts[2];                  // this block's larger and equal keys
     __shared__ int s_digit, s_need;
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
     const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-    griddep_wait();
-    griddep_launch_dependents();
     const int head = blockIdx.y, b = blockIdx.z;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < 3 * kSelectBins; i += kThreads) (&hist[0][0])[i] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
     bool bad = false;
     int n = kv_length(p.table.lengths[b], p.table.width, p.from.page_size, &bad);
     if (n > p.weights.width) {
@@ -70,74 +88,100 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const EvictPa
     int *kept = p.kept + (static_cast<long long>(b) * p.from.heads + head) * p.keep;
     if (head == 0 && rank == 0 && threadIdx.x == 0) p.to_lengths[b] = k;
     const int first = n - r, best = k - r;       // of the first `first` positions, `best` stay
-    // What follows them: the recent ones, and -1 past k.
-    for (int i = best + rank * kSelectThreads + threadIdx.x; i < p.keep; i += blocks * kSelectThreads) {
+    const int slice = (first + blocks - 1) / blocks, lo = min(first, rank * slice), size = min(first, lo + slice) - lo;
+    const float *const mine = w + lo;
+    const bool cached = size <= p.cached;
+    auto key_at = [&](int i) { return cached ? keys[i] : kv_weight_key(__float_as_uint(mine[i])); };
+    const bool some = best > 0 && best < first;  // the same for every block of the cluster
+    if (some && cached) {
+#pragma unroll 8
+        for (int i = threadIdx.x; i < size; i += kThreads) keys[i] = kv_weight_key(__float_as_uint(mine[i]));
+    }
+    // What follows the best: the recent ones, and -1 past k.
+    for (int i = best + rank * kThreads + threadIdx.x; i < p.keep; i += blocks * kThreads) {
         const int j = first + i - best;
         kept[i] = i < k ? j : -1;
         to_w[i] = i < k ? w[j] : 0.0f;
     }
-    if (best == first) {                         // nothing is evicted
-        for (int j = rank * kSelectThreads + threadIdx.x; j < first; j += blocks * kSelectThreads) {
-            kept[j] = j;
-            to_w[j] = w[j];
-        }
-        return;                                  // every block of the cluster
+    if (!some) {
+        if (best > 0)                            // nothing is evicted
+            for (int j = rank * kThreads + threadIdx.x; j < first; j += blocks * kThreads) {
+                kept[j] = j;
+                to_w[j] = w[j];
+            }
+        return;
     }
-    if (best == 0) return;
-    const int slice = (first + blocks - 1) / blocks, lo = min(first, rank * slice), hi = min(first, lo + slice);
+    __syncthreads();                             // the histograms are zero, the keys there
 
     uint32_t prefix = 0;
     int need = best;                             // rank of the limit among the keys with this prefix
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, digit_mask = pass == 2 ? 1023 : 2047;
         const uint32_t mask = pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10);
-        for (int i = threadIdx.x; i < kSelectBins; i += kSelectThreads) hist[i] = 0;
-        __syncthreads();
 #pragma unroll 4
-        for (int j = lo + threadIdx.x; j < hi; j += kSelectThreads) {
-            const uint32_t key = kv_weight_key(__float_as_uint(w[j]));
-            if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
+        for (int i = threadIdx.x; i < size; i += kThreads) {
+            const uint32_t key = key_at(i);
+            if ((key & mask) == prefix) atomicAdd(&hist[pass][(key >> shift) & digit_mask], 1);
         }
-        cluster.sync();
-        // Thread i: bins bins-1-2i and bins-2-2i of all blocks; the first whose running sum from the top
-        // reaches `need` holds the limit.
-        int c[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int bin = bins - 1 - 2 * static_cast<int>(threadIdx.x) - e;
-            if (bin >= 0)
-                for (int q = 0; q < blocks; ++q) c[e] += cluster.map_shared_rank(hist, q)[bin];
-        }
-        int sum = c[0] + c[1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += u;
-        }
-        if (lane == 31) warp_sums[0][warp] = sum;
         __syncthreads();
-        int before = 0;
-        for (int q = 0; q < warp; ++q) before += warp_sums[0][q];
-        sum += before;
-        const int above = sum - c[0] - c[1];
-        if (above < need && sum >= need) {       // one thread
-            const bool second = above + c[0] < need;
-            s_digit = bins - 1 - 2 * static_cast<int>(threadIdx.x) - (second ? 1 : 0);
-            s_need = need - above - (second ? c[0] : 0);
+#pragma unroll 2
+        for (int i = warp; i < kSelectGroups; i += kWarps) {
+            const int sum = __reduce_add_sync(0xffffffffu, hist[pass][i * 32 + lane]);
+            if (lane == 0) groups[pass][i] = sum;
         }
-        cluster.sync();                          // every block has read the histograms
+        if (blocks > 1) cluster.sync();
+        else __syncthreads();
+        if (warp == 0) {
+            // Sums over the blocks, from the top: lane l has groups 63 - 2 l and 62 - 2 l, then bin 31 - l of the
+            // group in which the running sum reaches `need`.
+            int c0 = 0, c1 = 0, c = 0;
+            if (blocks == 1) {
+                c0 = groups[pass][63 - 2 * lane];
+                c1 = groups[pass][62 - 2 * lane];
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int *other = cluster.map_shared_rank(groups[pass], q < blocks ? q : rank);
+                    const int x0 = other[63 - 2 * lane], x1 = other[62 - 2 * lane];
+                    c0 += q < blocks ? x0 : 0;
+                    c1 += q < blocks ? x1 : 0;
+                }
+            }
+            const int above = warp_scan(c0 + c1) - c0 - c1;
+            const unsigned found = __ballot_sync(0xffffffffu, above < need && above + c0 + c1 >= need);
+            const int owner = __ffs(found) - 1;
+            const bool second = above + c0 < need;
+            const int group = __shfl_sync(0xffffffffu, 63 - 2 * lane - (second ? 1 : 0), owner);
+            const int left = need - __shfl_sync(0xffffffffu, above + (second ? c0 : 0), owner);
+            if (blocks == 1) {
+                c = hist[pass][group * 32 + 31 - lane];
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int x = cluster.map_shared_rank(hist[pass], q < blocks ? q : rank)[group * 32 + 31 - lane];
+                    c += q < blocks ? x : 0;
+                }
+            }
+            const int over = warp_scan(c) - c;
+            if (over < left && over + c >= left) {
+                s_digit = group * 32 + 31 - lane;
+                s_need = left - over;
+            }
+        }
+        __syncthreads();
         prefix |= static_cast<uint32_t>(s_digit) << shift;
         need = s_need;
     }
 
-    // Each warp takes a contiguous part of the slice: counted, then written.
-    const int part = ((hi - lo + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-    const int from = min(hi, lo + warp * part), to = min(hi, from + part);
+    // Each warp has a contiguous part of the slice: its larger and equal keys are counted, then written after
+    // those of the warps and blocks before.
+    const int part = ((size + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int from = min(size, warp * part), to = min(size, from + part);
     int larger = 0, equal = 0;
 #pragma unroll 4
-    for (int j = from + lane; j < to; j += 32) {
-        const uint32_t key = kv_weight_key(__float_as_uint(w[j]));
+    for (int i = from + lane; i < to; i += 32) {
+        const uint32_t key = key_at(i);
         larger += key > prefix;
         equal += key == prefix;
     }
@@ -148,38 +192,40 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const EvictPa
         warp_sums[1][warp] = equal;
     }
     __syncthreads();
-    if (warp < 2) {
-        const int total = __reduce_add_sync(0xffffffffu, warp_sums[warp][lane]);
-        if (lane == 0) s_counts[warp] = total;
-    }
-    cluster.sync();
-    int larger_before = 0, equal_before = 0;
-    for (int q = 0; q < rank; ++q) {
-        const int *other = cluster.map_shared_rank(s_counts, q);
-        larger_before += other[0];
-        equal_before += other[1];
-    }
-    for (int q = 0; q < warp; ++q) {
-        larger_before += warp_sums[0][q];
-        equal_before += warp_sums[1][q];
-    }
-    cluster.sync();                              // no block leaves while its counts are read
-    const unsigned below = (1u << lane) - 1u;
-#pragma unroll 4
-    for (int j0 = from; j0 < to; j0 += 32) {
-        const int j = j0 + lane;
-        const float x = j < to ? w[j] : 0.0f;
-        const uint32_t key = j < to ? kv_weight_key(__float_as_uint(x)) : 0u;
-        const bool is_larger = j < to && key > prefix, is_equal = j < to && key == prefix;
-        const unsigned ml = __ballot_sync(0xffffffffu, is_larger), me = __ballot_sync(0xffffffffu, is_equal);
-        const int ties = equal_before + __popc(me & below);
-        const int at = larger_before + __popc(ml & below) + min(ties, need);
-        if (is_larger || (is_equal && ties < need)) {
-            kept[at] = j;
-            to_w[at] = x;
+    const int a = lane < kWarps ? warp_sums[0][lane] : 0, e = lane < kWarps ? warp_sums[1][lane] : 0;
+    int at_larger = __reduce_add_sync(0xffffffffu, lane < warp ? a : 0);
+    int at_equal = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0);
+    if (blocks > 1) {
+        if (warp == 0) {
+            const int x = __reduce_add_sync(0xffffffffu, a), y = __reduce_add_sync(0xffffffffu, e);
+            if (lane == 0) {
+                s_counts[0] = x;
+                s_counts[1] = y;
+            }
         }
-        larger_before += __popc(ml);
-        equal_before += __popc(me);
+        cluster.sync();
+        for (int q = 0; q < rank; ++q) {
+            const int *other = cluster.map_shared_rank(s_counts, q);
+            at_larger += other[0];
+            at_equal += other[1];
+        }
+        cluster.sync();                          // no block leaves while its counts are read
+    }
+    const unsigned below = (1u << lane) - 1u;
+#pragma unroll 2
+    for (int i0 = from; i0 < to; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t key = i < to ? key_at(i) : 0u;
+        const bool is_larger = i < to && key > prefix, is_equal = i < to && key == prefix;
+        const unsigned ml = __ballot_sync(0xffffffffu, is_larger), me = __ballot_sync(0xffffffffu, is_equal);
+        const int ties = at_equal + __popc(me & below);
+        if (is_larger || (is_equal && ties < need)) {
+            const int at = at_larger + __popc(ml & below) + min(ties, need);
+            kept[at] = lo + i;
+            to_w[at] = mine[i];
+        }
+        at_larger += __popc(ml);
+        at_equal += __popc(me);
     }
 }
 
