@@ -61,26 +61,49 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
     }
 }
 
-// x[i] / scale, each rounded as a division is (a product with the reciprocal
-// would move some elements by a whole e4m3 step), from one division per row:
-// with r the rounded reciprocal and q = x r, q + (x - q scale) r, whose
-// parenthesis is exact, is the rounded quotient (Markstein 1990, "Computation
-// of elementary functions on the IBM RISC System/6000 processor").  That
-// holds while nothing leaves fp32's normal range, where it matters: a quotient
-// below 2^-60 is rounded to zero in e4m3 either way.  Scales outside 2^+-60
-// take the division.
-__device__ __forceinline__ void divide8(float (&x)[8], float scale) {
-    if (scale > 0x1p-60f && scale < 0x1p60f) {
-        const float r = 1.0f / scale;
+// a / b rounded as a division is, from r = 1 / b rounded: with q = a r rounded,
+// q + (a - q b) r is the rounded quotient, the parenthesis being exact
+// (Markstein 1990, "Computation of elementary functions on the IBM RISC
+// System/6000 processor").  That holds while nothing leaves fp32's normal range.
+__device__ __forceinline__ float divide_by(float a, float b, float r) {
+    const float q = a * r;
+    return fmaf(fmaf(-q, b, a), r, q);
+}
+
+// A row's scale from its largest magnitude, and its elements x[i] / scale in
+// place (a product with the reciprocal would move some by a whole e4m3 step):
+// one division a row.  Scales outside 2^+-60, where intermediate results might
+// leave the normal range, take divisions; within, an element whose quotient is
+// that small is zero in e4m3 either way.
+__device__ __forceinline__ float scale_row(float (&x)[8], float top) {
+    constexpr float kInv = 1.0f / 448.0f;
+    if (top > 448 * 0x1p-60f && top < 448 * 0x1p60f) {
+        const float scale = divide_by(top, 448.0f, kInv), r = 1.0f / scale;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q = x[i] * r;
-            x[i] = fmaf(fmaf(-q, scale, x[i]), r, q);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] / scale;
+        for (int i = 0; i < 8; ++i) x[i] = divide_by(x[i], scale, r);
+        return scale;
     }
+    const float scale = top > 0.0f ? top / 448.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] / scale;
+    return scale;
+}
+
+// Largest magnitude of eight 16-bit elements, in both halves' larger one.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+    if (kBf16) {
+        const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&m);
+    }
+    const __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t top8(const uint4 &u) {       // both halves count
+    constexpr uint32_t kMagnitude = 0x7FFF7FFFu;
+    return max_pair<kBf16>(max_pair<kBf16>(u.x & kMagnitude, u.y & kMagnitude),
+                           max_pair<kBf16>(u.z & kMagnitude, u.w & kMagnitude));
 }
 
 // Eight floats as e4m3.
@@ -164,6 +187,13 @@ __global__ void __launch_bounds__(kRowThreads, kAppendCtas) kv_append_kernel(con
         for (int u = 0; u < kUnroll; ++u) {
             const int i = u * kPass + in_pass;
             const long long dst = s_dst[at][i];
+            uint32_t top = 0;                    // keys' largest magnitude below, values' above
+            if (kE4m3) {
+                const uint32_t a = top8<kBf16>(x[u][0]), b = top8<kBf16>(x[u][1]);
+                top = max_pair<kBf16>(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) top = max_pair<kBf16>(top, __shfl_xor_sync(0xffffffffu, top, o));
+            }
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 unsigned char *pool = which ? p.cache.v : p.cache.k;
@@ -173,13 +203,9 @@ __global__ void __launch_bounds__(kRowThreads, kAppendCtas) kv_append_kernel(con
                 }
                 float f[8];
                 unpack8<kBf16>(x[u][which], f);
-                float top = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-#pragma unroll
-                for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float scale = top > 0.0f ? top / 448.0f : 1.0f;
-                divide8(f, scale);
+                const uint32_t half = which ? top >> 16 : top & 0xFFFFu;
+                const float scale = scale_row(f, kBf16 ? __uint_as_float(half << 16)
+                                                       : __half2float(__ushort_as_half(static_cast<unsigned short>(half))));
                 if (dst >= 0 && inside) *(reinterpret_cast<uint2 *>(pool + dst) + piece) = pack8_e4m3(f);
                 if (dst >= 0 && piece == 0) (which ? p.cache.v_scale : p.cache.k_scale)[s_scale[at][i]] = scale;
             }

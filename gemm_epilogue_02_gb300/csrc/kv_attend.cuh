@@ -866,7 +866,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
 // weights[b, head, j] += sum over the group of 2^(t_j - m) / l.  A position's
 // scores lie together; a thread adds for kSpreadEach positions, kSpreadThreads
 // apart, whose first eight heads it requests together.
-constexpr int kSpreadThreads = 256, kSpreadEach = 4;
+constexpr int kSpreadThreads = 256, kSpreadEach = 2;
 
 __global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendParams p) {
     constexpr int kPairs = 4;             // of heads, per request
@@ -898,31 +898,42 @@ __global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendP
             at[e] = is[e] ? static_cast<int>(j) : lo;
             old[e] = w[at[e]];
             sum[e] = 0.0f;
+            int page, slot;
+            is[e] = kv_row(list, at[e], p.cache.page_size, p.cache.pages, &page, &slot) && is[e];   // else it has no score
         }
         for (int h0 = 0; h0 < p.group; h0 += 2 * kPairs) {
-            float2 t[kSpreadEach][kPairs];
+            float2 t[kSpreadEach][kPairs], ml[2 * kPairs];
 #pragma unroll
-            for (int e = 0; e < kSpreadEach; ++e)
+            for (int i = 0; i < 2 * kPairs; ++i) ml[i] = stats[min(h0 + i, p.group - 1)];
 #pragma unroll
-                for (int i = 0; i < kPairs; ++i)
-                    t[e][i] = *reinterpret_cast<const float2 *>(scores + static_cast<long long>(at[e]) * p.scored +
-                                                                min(h0 + 2 * i, p.scored - 2));
+            for (int e = 0; e < kSpreadEach; ++e) {
+                const float *const row = scores + static_cast<long long>(at[e]) * p.scored + h0;
+                if (p.scored % 8 == 0) {
+#pragma unroll
+                    for (int i = 0; i < kPairs; i += 2) {
+                        const float4 x = *reinterpret_cast<const float4 *>(row + 2 * i);
+                        t[e][i] = make_float2(x.x, x.y);
+                        t[e][i + 1] = make_float2(x.z, x.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i)
+                        t[e][i] = *reinterpret_cast<const float2 *>(row + min(2 * i, p.scored - 2 - h0));
+                }
+            }
 #pragma unroll
             for (int i = 0; i < 2 * kPairs; ++i) {
-                if (h0 + i >= p.group) break;
-                const float2 ml = stats[h0 + i];
-                const float inv = __fdividef(1.0f, ml.y);
+                const float inv = h0 + i < p.group ? __fdividef(1.0f, ml[i].y) : 0.0f;
 #pragma unroll
-                for (int e = 0; e < kSpreadEach; ++e)
-                    sum[e] += exp2_fast((i & 1 ? t[e][i / 2].y : t[e][i / 2].x) - ml.x) * inv;
+                for (int e = 0; e < kSpreadEach; ++e) {
+                    const float x = i & 1 ? t[e][i / 2].y : t[e][i / 2].x;
+                    sum[e] += h0 + i < p.group ? exp2_fast(x - ml[i].x) * inv : 0.0f;
+                }
             }
         }
 #pragma unroll
-        for (int e = 0; e < kSpreadEach; ++e) {
-            int page, slot;
-            if (is[e] && kv_row(list, at[e], p.cache.page_size, p.cache.pages, &page, &slot))   // else it has no score
-                w[at[e]] = old[e] + sum[e];
-        }
+        for (int e = 0; e < kSpreadEach; ++e)
+            if (is[e]) w[at[e]] = old[e] + sum[e];
     }
 }
 
