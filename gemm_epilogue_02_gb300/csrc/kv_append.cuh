@@ -61,31 +61,53 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
     }
 }
 
-// a / b rounded as a division is, from r = 1 / b rounded: with q = a r rounded,
-// q + (a - q b) r is the rounded quotient, the parenthesis being exact
-// (Markstein 1990, "Computation of elementary functions on the IBM RISC
-// System/6000 processor").  That holds while nothing leaves fp32's normal range.
-__device__ __forceinline__ float divide_by(float a, float b, float r) {
-    const float q = a * r;
-    return fmaf(fmaf(-q, b, a), r, q);
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
 
-// A row's scale from its largest magnitude, and its elements x[i] / scale in
-// place (a product with the reciprocal would move some by a whole e4m3 step):
-// one division a row.  Scales outside 2^+-60, where intermediate results might
-// leave the normal range, take divisions; within, an element whose quotient is
-// that small is zero in e4m3 either way.
+// A row's scale from its largest magnitude, and -x[i] / scale in place of its
+// elements (with the minus, zeros keep their signs).  A product with the reciprocal would move some elements by a whole
+// e4m3 step, and eight divisions cost more than the row's traffic; but with r =
+// 1 / b and q = a r rounded, q + (a - q b) r is the rounded quotient, the
+// parenthesis being exact (Markstein 1990, "Computation of elementary functions
+// on the IBM RISC System/6000 processor").  For 1 / 448 r is the rounded
+// reciprocal, as the theorem asks; for the elements it is an approximation with
+// one Newton step, which leaves the quotient off its rounding only within
+// 2^-23 of a unit in the last place of a midpoint.  While nothing leaves fp32's
+// normal range that holds; scales outside 2^+-60 take divisions, and within, an
+// element so small that it might is zero in e4m3 either way.
 __device__ __forceinline__ float scale_row(float (&x)[8], float top) {
-    constexpr float kInv = 1.0f / 448.0f;
-    if (top > 448 * 0x1p-60f && top < 448 * 0x1p60f) {
-        const float scale = divide_by(top, 448.0f, kInv), r = 1.0f / scale;
+    if (!(top > 448 * 0x1p-60f && top < 448 * 0x1p60f)) {
+        const float scale = top > 0.0f ? top / 448.0f : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = divide_by(x[i], scale, r);
+        for (int i = 0; i < 8; ++i) x[i] = x[i] / -scale;
         return scale;
     }
-    const float scale = top > 0.0f ? top / 448.0f : 1.0f;
+    constexpr float kInv = 1.0f / 448.0f;
+    const float q = top * kInv, scale = fmaf(fmaf(-q, 448.0f, top), kInv, q);
+    float r = __fdividef(1.0f, scale);
+    r = fmaf(fmaf(-r, scale, 1.0f), r, r);
+    const float2 rr = make_float2(-r, -r), ss = make_float2(scale, scale);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] / scale;
+    for (int i = 0; i < 8; i += 2) {
+        const float2 a = make_float2(x[i], x[i + 1]), q2 = mul2(a, rr), y = fma2(fma2(q2, ss, a), rr, q2);
+        x[i] = y.x;
+        x[i + 1] = y.y;
+    }
     return scale;
 }
 
@@ -106,15 +128,15 @@ __device__ __forceinline__ uint32_t top8(const uint4 &u) {       // both halves 
                            max_pair<kBf16>(u.z & kMagnitude, u.w & kMagnitude));
 }
 
-// Eight floats as e4m3.
-__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8]) {
+// Eight floats' negatives as e4m3.
+__device__ __forceinline__ uint2 pack8_negated(const float (&x)[8]) {
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         w[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE,
                                                                     __NV_E4M3))
                      << (16 * (i & 1));
-    return make_uint2(w[0], w[1]);
+    return make_uint2(w[0] ^ 0x80808080u, w[1] ^ 0x80808080u);
 }
 
 // Blocks take chunks of kRows rows, a row being the keys and values of one
@@ -206,7 +228,7 @@ __global__ void __launch_bounds__(kRowThreads, kAppendCtas) kv_append_kernel(con
                 const uint32_t half = which ? top >> 16 : top & 0xFFFFu;
                 const float scale = scale_row(f, kBf16 ? __uint_as_float(half << 16)
                                                        : __half2float(__ushort_as_half(static_cast<unsigned short>(half))));
-                if (dst >= 0 && inside) *(reinterpret_cast<uint2 *>(pool + dst) + piece) = pack8_e4m3(f);
+                if (dst >= 0 && inside) *(reinterpret_cast<uint2 *>(pool + dst) + piece) = pack8_negated(f);
                 if (dst >= 0 && piece == 0) (which ? p.cache.v_scale : p.cache.k_scale)[s_scale[at][i]] = scale;
             }
         }

@@ -18,6 +18,10 @@ from . import _binding as _b
 _F16, _BF16, _E4M3 = torch.float16, torch.bfloat16, torch.float8_e4m3fn
 _DT = {_F16: _b.TGEMM_F16, _BF16: _b.TGEMM_BF16}
 _NO_WEIGHTS = (0, 0, 0, 0)
+# The current stream's handle and the current device, without building the
+# objects that torch.cuda's functions return (about a microsecond a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _append, _decode, _evict = _b.KV_APPEND_ARGS.pack, _b.ATTENTION_DECODE_ARGS.pack, _b.KV_EVICT_ARGS.pack
 
 
@@ -97,8 +101,8 @@ def _launch(index, stream, fn, args):
     """fn(args, stream) with the cache's device current; raises on a status."""
     if index < 0:
         raise ValueError("the cache must be on a CUDA device")
-    s = (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream
-    if index == torch.cuda.current_device():
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == _current_device():
         st = fn(args, s)
     else:
         with torch.cuda.device(index):

@@ -85,6 +85,33 @@ def test_append_many_tokens(cuda_lib):
     run_append(cuda_lib, [3, 0, 1], [1500, 1, 700], 2, 128, 32, "fp16", "e4m3", "phsd", seed=4)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_append_e4m3_quotients_of_every_magnitude(cuda_lib, dtype):
+    """Rows whose largest element runs over the type's whole range, subnormals among them, with elements from it
+    down: scales and elements are those of the definition, bit for bit."""
+    tg = cuda_lib
+    heads, dim, page, n = 4, 256, 16, 700
+    g = torch.Generator().manual_seed(21)
+    lo, hi = (-24, 15) if dtype == "fp16" else (-133, 127)
+    top = torch.exp2(lo + (hi - lo) * torch.rand(n, heads, 1, generator=g, dtype=torch.float64))
+    x = top * torch.exp2(-12 * torch.rand(n, heads, dim, generator=g, dtype=torch.float64))
+    x *= torch.randint(0, 2, x.shape, generator=g) * 2 - 1
+    x[:, :, 7] = top[:, :, 0]
+    x = x.to(TDT[dtype])
+    x = torch.where(torch.isfinite(x), x, torch.zeros_like(x))
+    k, v = make_pool(n // page + 1, page, heads, dim, E4M3, "pshd", "cuda")
+    ks, vs = (torch.full((n // page + 1, page, heads), float("nan"), device="cuda") for _ in range(2))
+    table = torch.arange(n // page + 1, dtype=torch.int32).view(1, -1).cuda()
+    tg.kv_append(tg.PagedCache(k, v, ks, vs), x.cuda(), -x.flip(0).cuda(), table,
+                 torch.tensor([n], dtype=torch.int32).cuda(), starts=torch.tensor([0, n], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    for pool, scale, rows in ((k, ks, x), (v, vs, -x.flip(0))):
+        e, s = split_e4m3(rows)
+        assert torch.equal(scale.view(-1, heads)[:n].cpu().view(torch.int32), s.view(torch.int32))
+        assert torch.equal(pool.view(torch.uint8).view(-1, heads, dim)[:n].cpu(), e.view(torch.uint8))
+    assert tg.tgemm_last_device_status() == 0
+
+
 @pytest.mark.parametrize("cache", ["16", "e4m3"])
 def test_append_bad_pages_and_lengths_are_left_out(cuda_lib, cache):
     """A page outside the pool, a length that does not reach back to position 0, and one past the page list: their
