@@ -5,8 +5,8 @@
 // access whose address the kernels compute: the innermost coordinate of each
 // tensor-memory-access copy (it must start on a 16-byte boundary), and the
 // element offset of each plain store of C, of each split-K partial and
-// arrival counter, of the attention output and of the repacked operands,
-// against bounds the host computes from the allocation sizes.  A failed check
+// arrival counter, of the attention output, of the repacked operands and of the
+// paged cache's rows, outputs and workspace, against bounds the host computes from the allocation sizes.  A failed check
 // records TGEMM_ERR_DEBUG_CHECK in the device status word (unless another
 // error is already there) and its check id in g_debug_check, and the access
 // is skipped: nothing traps, and a skipped copy leaves its ring slot
@@ -29,6 +29,9 @@ enum DebugCheck : uint32_t {
     kChkCounter = 6,        // arrival counter outside the counter buffer
     kChkAttnStore = 7,      // attention output store outside O's elements
     kChkRepack = 8,         // repack store outside the destination
+    kChkKvRow = 9,          // paged cache: a row written outside its pool
+    kChkKvOutput = 10,      // paged cache: an output of attention or eviction outside its array
+    kChkKvSpace = 11,       // paged cache: a part or score outside the workspace
 };
 
 // First check that failed since the host last read it (0: none); one word per

@@ -90,6 +90,7 @@ tgemm_status check_cache(const tgemm_kv_cache *c, KvView *view, Extent *k, Exten
     view->heads = c->heads;
     view->dim = c->dim;
     view->row_bytes = c->dim * esize;
+    view->dbg_bytes = bytes;
     *k = {c->k, bytes};
     *v = {c->v, bytes};
     return TGEMM_OK;
@@ -428,6 +429,8 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args
     p.page_shift = -1;
     for (int i = 0; i <= 20; ++i)
         if (cache->page_size == 1 << i) p.page_shift = i;
+    p.dbg_o_bytes = obytes;
+    p.dbg_scores = batch * cache->heads * p.positions * p.scored;
     const int tiles = head_tiles(p.group, cache->dim);
     p.blocks = (p.group + 8 * tiles - 1) / (8 * tiles);
     p.status = rt.status;

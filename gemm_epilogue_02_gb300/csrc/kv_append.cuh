@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kRowThreads, kAppendCtas) kv_append_kernel(con
                 } else {
                     src = t * p.token_stride + head * p.head_stride;
                     dst = kv_offset(p.cache, page, slot, head);
+                    if (!TGEMM_CHECK(dst + p.cache.row_bytes <= p.cache.dbg_bytes, kChkKvRow, p.status)) dst = -1;
                     if (kE4m3) scale = kv_scale_offset(p.cache, page, slot, head);
                     if (p.weights.base) {
                         if (pos < p.weights.width)

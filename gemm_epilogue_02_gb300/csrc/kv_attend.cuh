@@ -94,6 +94,7 @@ struct AttendParams {
     float first, last;
     bool capped;
     unsigned int *status;
+    long long dbg_o_bytes, dbg_scores;    // debug builds: O's bytes, the workspace's scores
 };
 
 template <bool kE4m3, int DP, int NT>
@@ -223,7 +224,9 @@ __host__ __device__ inline long long attend_first(long long c, long long ctas, l
     return attend_div(c * total, ctas);
 }
 __host__ __device__ inline int attend_owner(long long t, long long ctas, long long total) {
-    return static_cast<int>(attend_div((t + 1) * ctas - 1, total));
+    // The bounds hold by themselves; lengths that another stream changes meanwhile must not lead out of the slots.
+    const long long c = t < 0 ? 0 : attend_div((t + 1) * ctas - 1, total);
+    return static_cast<int>(c < ctas ? c : ctas - 1);
 }
 
 // The slot of CTA c's part of an item whose first part is CTA `first`'s: a CTA
@@ -243,7 +246,10 @@ __device__ __forceinline__ void cursor_next(AttendCursor &u, const AttendParams 
     u.block = 0;
     if (++u.head < p.cache.heads) return;
     u.head = 0;
-    if (++u.b < p.table.batch) cursor_load(u, p, tile, pad);
+    if (u.b + 1 < p.table.batch) {
+        ++u.b;
+        cursor_load(u, p, tile, pad);
+    }
 }
 
 template <bool kBf16, bool kE4m3, int DP, int NT>
@@ -264,6 +270,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     __shared__ unsigned s_last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t4 = lane & 3;
+    if (threadIdx.x < 3) s_start[threadIdx.x] = 0;
     float *merge = reinterpret_cast<float *>(smem + S::kMerge);
     const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kStage;
     unsigned char *const sides = smem + S::kSides + warp * S::kStages * S::kSide;
@@ -562,7 +569,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                     float ks = 1.0f;
                     if (kE4m3) {
                         ks = scales[row];
-                        const float vs = in ? scales[S::kKeys + row] : 1.0f;
+                        // (a scale of 0 stands for values of 0, whatever their weight)
+                        float vs = in ? scales[S::kKeys + row] : 1.0f;
+                        vs = vs < 0x1p-100f ? 0x1p-100f : vs;
                         lv[kb][r] = __log2f(vs);
                         inv[kb][r] = __fdividef(1.0f, vs);
                     }
@@ -575,7 +584,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                             if (kE4m3) x[i] *= ks;
                             if (p.capped) x[i] = p.last * (1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x[i])));
                         }
-                        if (p.space.scores && in && 8 * nt + 2 * t4 < hn)
+                        if (p.space.scores && in && 8 * nt + 2 * t4 < hn &&
+                            TGEMM_CHECK(scores - p.space.scores + row * p.scored + 8 * nt + 2 <= p.dbg_scores, kChkKvSpace, p.status))
                             *reinterpret_cast<float2 *>(scores + row * p.scored + 8 * nt) = make_float2(x[0], x[1]);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -743,10 +753,11 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
             bool answer = whole;
             if (!whole) {
                 const int c0 = attend_owner(item, ctas, all), c1 = attend_owner(item_end - 1, ctas, all);
-                const int parts = c1 - c0 + 1, mine_at = cta - c0;
+                const int parts = max(c1 - c0 + 1, 1), mine_at = min(max(cta - c0, 0), parts - 1);
                 const int group = mine_at / kAttendFanIn, groups = (parts + kAttendFanIn - 1) / kAttendFanIn;
                 auto slot_of = [&](int part) { return attend_slot(c0 + part, c0); };
                 auto put = [&](int to) {
+                    if (!TGEMM_CHECK(to >= 0 && to < 2 * kAttendMaxCtas, kChkKvSpace, p.status)) return;
                     float *dst = p.space.out + static_cast<long long>(to) * S::kHeads * DP;
                     for (int i = threadIdx.x; i < hn * DP / 4; i += kAttendThreads) {
                         const int h = i / (DP / 4), d = i % (DP / 4) * 4;
@@ -851,9 +862,10 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                     for (int e = 0; e < 8; ++e) x[e] = sum == 0.0f ? 0.0f : merge[h * S::kPitch + d + e] / sum;
                     const uint4 v = make_uint4(pair16<kBf16>(x[0], x[1]), pair16<kBf16>(x[2], x[3]),
                                                pair16<kBf16>(x[4], x[5]), pair16<kBf16>(x[6], x[7]));
-                    *reinterpret_cast<uint4 *>(p.o + b * p.o_batch_stride +
-                                               (static_cast<long long>(head) * p.group + h0 + h) * p.o_head_stride +
-                                               2 * d) = v;
+                    const long long at = b * p.o_batch_stride +
+                                         (static_cast<long long>(head) * p.group + h0 + h) * p.o_head_stride + 2 * d;
+                    if (TGEMM_CHECK(at >= 0 && at + 16 <= p.dbg_o_bytes, kChkKvOutput, p.status))
+                        *reinterpret_cast<uint4 *>(p.o + at) = v;
                 }
             }
             __syncthreads();               // merge and the statistics are free again

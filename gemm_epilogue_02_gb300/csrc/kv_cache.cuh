@@ -32,6 +32,7 @@ struct KvView {
     long long scale_page_stride, scale_slot_stride, scale_head_stride;   // floats
     int page_size, heads, dim;
     int row_bytes;                                                 // dim elements
+    long long dbg_bytes;                                           // debug builds: a pool's bytes
 };
 
 // The sequences' page lists and lengths.

@@ -221,8 +221,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
         const int ties = at_equal + __popc(me & below);
         if (is_larger || (is_equal && ties < need)) {
             const int at = at_larger + __popc(ml & below) + min(ties, need);
-            kept[at] = lo + i;
-            to_w[at] = mine[i];
+            if (TGEMM_CHECK(at >= 0 && at < p.keep, kChkKvOutput, p.status)) {
+                kept[at] = lo + i;
+                to_w[at] = mine[i];
+            }
         }
         at_larger += __popc(ml);
         at_equal += __popc(me);
@@ -260,6 +262,7 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(const EvictPa
                 } else {
                     src = kv_offset(p.from, page, slot, head);
                     dst = kv_offset(p.to, to_page, to_slot, head);
+                    if (!TGEMM_CHECK(dst + p.to.row_bytes <= p.to.dbg_bytes, kChkKvRow, p.status)) dst = -1;
                     if (kE4m3) {
                         const long long s = kv_scale_offset(p.from, page, slot, head);
                         const long long d = kv_scale_offset(p.to, to_page, to_slot, head);

@@ -244,7 +244,9 @@ tgemm_status tgemm_last_device_status(void);
  * store of C outside its (M - 1) * ldc + N elements, 5 a split-K partial
  * outside its scratch, 6 an arrival counter outside its buffer, 7 an
  * attention output store outside O, 8 a repack store outside its
- * destination.  The failing access is skipped (nothing traps); a skipped
+ * destination, 9 a row of the paged cache written outside its pool, 10 an
+ * output of tgemm_attention_decode or tgemm_kv_evict outside its array, 11 a
+ * part or score outside the workspace.  The failing access is skipped (nothing traps); a skipped
  * copy leaves its pipeline slot incomplete, which the bounded waits end.
  * Synchronises the device.  Returns -1 in the release build, which compiles
  * no checks.  Testing only: TGEMM_DEBUG_PLANT=c_store makes the debug build's
@@ -301,7 +303,7 @@ tgemm_status tgemm_attention_fwd(const void *Q, const void *K, const void *V, vo
  * that hold keys and values side by side, are all described by strides.  K and
  * V share the strides.  Elements are fp16 or bf16 (the calls' dtype), or, with
  * e4m3 = 1, e4m3 with one fp32 scale per row and pool: value = scale * element,
- * scale > 0.
+ * scale >= 0.
  *
  * Limits: dim a multiple of 8 (e4m3: 16), at most 256; page_size 1 .. 2^20;
  * bases 16-byte aligned and strides multiples of 16 bytes; rows may not
