@@ -279,11 +279,16 @@ cudaError_t launch_attend(const RuntimeInfo &rt, const AttendParams &p, cudaStre
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    // One CTA per place on the GPU, fewer when there cannot be as many tiles.
-    const int64_t tiles = (p.positions + Shape::kTile - 1) / Shape::kTile;
-    const int64_t most = static_cast<int64_t>(p.table.batch) * p.cache.heads * p.blocks * std::max<int64_t>(1, tiles);
+    // One CTA per place on the GPU, fewer when there cannot be as many tiles.  A run is shared by the heads where
+    // that leaves at most a ninth of the places empty.
+    const int64_t heads = static_cast<int64_t>(p.cache.heads) * p.blocks;
     const int64_t places = std::min<int64_t>(kAttendMaxCtas, static_cast<int64_t>(rt.num_sms) * Shape::kCtas);
-    return launch(kernel, dim3(static_cast<unsigned>(std::min(most, places))), kAttendThreads, Shape::kBytes, s, p);
+    AttendParams q = p;
+    q.lanes = places >= 8 * heads ? static_cast<int>(heads) : 1;
+    const int64_t tiles = std::max<int64_t>(1, (p.positions + Shape::kTile - 1) / Shape::kTile);
+    const int64_t most = p.table.batch * (q.lanes > 1 ? 1 : heads) * tiles;
+    const int64_t grid = std::min(most, places / q.lanes) * q.lanes;
+    return launch(kernel, dim3(static_cast<unsigned>(grid)), Shape::kThreads, Shape::kBytes, s, q);
 }
 
 template <bool kBf16, bool kE4m3>

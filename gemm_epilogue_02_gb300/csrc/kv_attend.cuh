@@ -13,10 +13,15 @@
 // batch looks like.
 //
 // Work.  An item is one sequence, key head and block of up to 8 * NT query
-// heads; its positions come in tiles of kWarps * kKeys.  The tiles of all items
-// in a row are cut into equal runs, one per CTA (as many CTAs as fit the GPU at
-// once), so that a ragged batch, or a single long sequence, loads every SM
-// alike; each CTA finds its run from the lengths, which only the device knows.
+// heads; its positions come in tiles of kWarps * kKeys.  The tiles of all
+// sequences in a row are cut into equal runs, and each run is given to one CTA
+// per (key head, block), as many as fit the GPU at once: a ragged batch, or a
+// single long sequence, loads every SM alike, and the heads of a position are
+// read at about the same time, which is what DRAM wants where they lie side by
+// side (with every CTA on its own, 64-byte rows of 8 heads came at 2.8 TB/s
+// instead of 5.7, and blocks of one head read its rows twice).  Each CTA finds
+// its run from the lengths, which only the device knows.  With so many heads
+// that a run each would leave places empty, runs go through the heads instead.
 // A run that ends inside an item leaves (maximum, sum, output) of its part in
 // the workspace, and the CTA that arrives last joins the parts in order of
 // position (the result does not depend on the order of arrival).
@@ -57,8 +62,6 @@
 
 namespace tgemm {
 
-constexpr int kAttendWarps = 4;
-constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kAttendMaxCtas = 320;       // CTAs at most (workspace slots)
 constexpr int kAttendFanIn = 32;          // parts joined at once (more: in two levels)
 static_assert(kAttendMaxCtas <= kAttendFanIn * kAttendFanIn, "two levels join every CTA's part");
@@ -87,6 +90,7 @@ struct AttendParams {
     long long positions;                  // what the page lists can hold
     int scored;                           // query heads of a key head, rounded up to an even number
     int group, blocks;                    // query heads of a key head; blocks that they make
+    int lanes;                            // CTAs that share a run: heads * blocks, or 1
     int window;
     int page_shift;                       // log2 of the page size, -1: not a power of two
     // A score in log2 units is first * (q . k); capped, last * (1 - 2 / (1 + 2^(first * (q . k)))),
@@ -97,19 +101,26 @@ struct AttendParams {
     long long dbg_o_bytes, dbg_scores;    // debug builds: O's bytes, the workspace's scores
 };
 
+// Shapes.  What limits a step is the latency of its chain (copy, product,
+// softmax, product), so many warps with short steps do better than few with
+// long ones, down to a step's fixed cost: steps of 16 positions, 32 for 64-byte
+// rows, and as many warps as registers allow beside about 96 KiB of ring per
+// CTA.
 template <bool kE4m3, int DP, int NT>
 struct AttendShape {
     static constexpr int kRow = DP * (kE4m3 ? 1 : 2);                     // bytes of a row in shared memory
-    static constexpr int kKeys = kRow >= 256 ? 16 : 16 * (256 / kRow);    // positions of a warp's step: 4 KiB of keys
-    static constexpr int kTile = kAttendWarps * kKeys;
+    static constexpr int kKeys = kRow >= 256 ? 16 : 32;                   // positions of a warp's step
+    static constexpr int kWarps = DP * NT == 256 && kRow < 512 ? 4 : 6;        // 255 registers a thread, or 168
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kStages = kWarps == 4 ? 3 : kKeys * kRow >= 4096 ? 2 : 4;
+    static constexpr int kTile = kWarps * kKeys;
     static constexpr int kHeads = 8 * NT;
-    static constexpr int kStages = 3;
-    static constexpr int kBatch = NT == 2 || DP == 256 ? 10 : 16;              // parts joined per request (what registers hold)
+    static constexpr int kBatch = kThreads == 128 ? 16 : 8;               // parts joined per request (what registers hold)
     static constexpr int kStage = 2 * kKeys * kRow;                       // keys, values
     static constexpr int kSide = kE4m3 ? 2 * kKeys * 4 + 16 : 16;         // a stage's scales and mask
-    static constexpr int kSides = kAttendWarps * kStages * kStage;        // where the sides begin
-    static constexpr int kOffsets = kSides + kAttendWarps * kStages * kSide;      // a step's rows in the pools
-    static constexpr int kMerge = kOffsets + kAttendWarps * kKeys * 8;
+    static constexpr int kSides = kWarps * kStages * kStage;              // where the sides begin
+    static constexpr int kOffsets = kSides + kWarps * kStages * kSide;    // a step's rows in the pools
+    static constexpr int kMerge = kOffsets + kWarps * kKeys * 8;
     static constexpr int kPitch = DP + 4;                                 // floats: heads 2t, dims g fall into different banks
     static constexpr int kBytes = kMerge + kHeads * kPitch * 4;
     static constexpr int kCtas = kBytes + 4096 <= 115712 ? 2 : 1;         // per SM: 228 KiB, of which each CTA also takes 1 KiB and its statics
@@ -214,7 +225,7 @@ __host__ __device__ inline int attend_tiles(int n, int window, int tile, int pad
     return (t + pad - 1) / pad * pad;
 }
 
-// CTA c of `ctas` has the tiles [attend_first(c), attend_first(c + 1)) of `total`;
+// Run c of `ctas` has the tiles [attend_first(c), attend_first(c + 1)) of `total`;
 // attend_owner() is the inverse.
 __host__ __device__ inline long long attend_div(long long a, long long b) {     // a >= 0, b > 0
     if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
@@ -229,9 +240,12 @@ __host__ __device__ inline int attend_owner(long long t, long long ctas, long lo
     return static_cast<int>(c < ctas ? c : ctas - 1);
 }
 
-// The slot of CTA c's part of an item whose first part is CTA `first`'s: a CTA
-// has at most one part that it begins and one that it continues.
-__host__ __device__ inline int attend_slot(int c, int first) { return 2 * c + (c == first ? 1 : 0); }
+// The slot of run c's part of an item whose first part is run `first`'s, for the
+// run's CTA `lane` of `lanes`: a CTA has at most one part that it begins and one
+// that it continues.
+__host__ __device__ inline int attend_slot(int c, int first, int lane, int lanes) {
+    return 2 * (c * lanes + lane) + (c == first ? 1 : 0);
+}
 
 __device__ __forceinline__ void cursor_load(AttendCursor &u, const AttendParams &p, int tile, int pad) {
     bool bad = false;
@@ -242,10 +256,12 @@ __device__ __forceinline__ void cursor_load(AttendCursor &u, const AttendParams 
 __device__ __forceinline__ void cursor_next(AttendCursor &u, const AttendParams &p, int tile, int pad) {
     if (++u.tile < u.tiles) return;
     u.tile = 0;
-    if (++u.block < p.blocks) return;
-    u.block = 0;
-    if (++u.head < p.cache.heads) return;
-    u.head = 0;
+    if (p.lanes == 1) {
+        if (++u.block < p.blocks) return;
+        u.block = 0;
+        if (++u.head < p.cache.heads) return;
+        u.head = 0;
+    }
     if (u.b + 1 < p.table.batch) {
         ++u.b;
         cursor_load(u, p, tile, pad);
@@ -253,18 +269,17 @@ __device__ __forceinline__ void cursor_next(AttendCursor &u, const AttendParams 
 }
 
 template <bool kBf16, bool kE4m3, int DP, int NT>
-__global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kCtas)
+__global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendShape<kE4m3, DP, NT>::kCtas)
     kv_attend_kernel(const AttendParams p) {
     using S = AttendShape<kE4m3, DP, NT>;
     constexpr bool kMmaBf16 = kBf16 && !kE4m3;      // e4m3 is widened to fp16
     constexpr int kChunks = S::kRow / 16;           // 16-byte pieces of a row
     constexpr int kRowsPerCopy = 32 / kChunks;      // rows that a warp's copy instruction covers
-    constexpr int kLaneRows = (S::kKeys + 31) / 32; // rows whose place a lane looks up
     constexpr int kBlocks = S::kKeys / 16;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long s_sum[2][kAttendWarps];
+    __shared__ long long s_sum[2][S::kWarps];
     __shared__ int s_start[3];
-    __shared__ float s_m[kAttendWarps][S::kHeads], s_l[kAttendWarps][S::kHeads];
+    __shared__ float s_m[S::kWarps][S::kHeads], s_l[S::kWarps][S::kHeads];
     __shared__ float s_w[kAttendFanIn][S::kHeads];
     __shared__ float s_inv[S::kHeads], s_ref[S::kHeads];
     __shared__ unsigned s_last;
@@ -280,8 +295,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
 
     // ---- this CTA's run: all lengths summed, once as they are and once with
     // runs of kAttendLeast tiles that end with their item
-    const int heads_all = p.cache.heads * p.blocks;
-    const int each = (p.table.batch + kAttendThreads - 1) / kAttendThreads;
+    const int heads_all = p.lanes > 1 ? 1 : p.cache.heads * p.blocks;    // that a run goes through
+    const int runs = static_cast<int>(gridDim.x) / p.lanes, lane_cta = static_cast<int>(blockIdx.x) % p.lanes;
+    const int each = (p.table.batch + S::kThreads - 1) / S::kThreads;
     const int b_lo = min(p.table.batch, static_cast<int>(threadIdx.x) * each), b_hi = min(p.table.batch, b_lo + each);
     long long mine[2] = {0, 0};
     for (int b = b_lo; b < b_hi; ++b) {
@@ -308,15 +324,15 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     long long total[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        for (int w = 0; w < kAttendWarps; ++w) {
+        for (int w = 0; w < S::kWarps; ++w) {
             if (w < warp) upto[i] += s_sum[i][w];
             total[i] += s_sum[i][w];
         }
-    const bool few = total[1] * heads_all <= static_cast<long long>(gridDim.x) * kAttendLeast;
+    const bool few = total[1] * heads_all <= static_cast<long long>(runs) * kAttendLeast;
     const int pad = few ? kAttendLeast : 1;
     const long long all = (few ? total[1] : total[0]) * heads_all;
-    const int ctas = static_cast<int>(few ? all / kAttendLeast : min(static_cast<long long>(gridDim.x), all));
-    const int cta = blockIdx.x;
+    const int ctas = static_cast<int>(few ? all / kAttendLeast : min(static_cast<long long>(runs), all));
+    const int cta = static_cast<int>(blockIdx.x) / p.lanes;
     if (cta >= ctas) return;
     const long long first = attend_first(cta, ctas, all), last = attend_first(cta + 1, ctas, all);
     {
@@ -344,30 +360,26 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     // ---- loading: the places of the next step's rows are looked up, then copied
     AttendCursor load;
     load.b = s_start[0];
-    load.head = s_start[1] / p.blocks;
-    load.block = s_start[1] - load.head * p.blocks;
+    const int h_first = p.lanes > 1 ? lane_cta : s_start[1];
+    load.head = h_first / p.blocks;
+    load.block = h_first - load.head * p.blocks;
     load.tile = s_start[2];
     cursor_load(load, p, S::kTile, pad);
     AttendCursor use = load;
-    int page[kLaneRows], slot[kLaneRows], load_head = 0;
-    unsigned want[kLaneRows];
+    int page = -1, slot = 0, load_head = 0;    // lane i: of the step's position i
+    unsigned want = 0;                         // positions that there are
     int looked = 0;
     auto lookup = [&]() {
         load_head = load.head;
-        const int pos0 = load.lo + load.tile * S::kTile + warp * S::kKeys;
-        const int *list = p.table.pages + load.b * p.table.stride;
-#pragma unroll
-        for (int r = 0; r < kLaneRows; ++r) {
-            const int row = lane + 32 * r, pos = pos0 + row;
-            const bool in = row < S::kKeys && pos < load.n && looked < steps;
-            int i = 0;
-            if (in)
-                i = p.page_shift >= 0 ? pos >> p.page_shift
-                                      : static_cast<int>(static_cast<unsigned>(pos) / static_cast<unsigned>(p.cache.page_size));
-            slot[r] = pos - i * p.cache.page_size;
-            page[r] = in ? list[i] : -1;
-            want[r] = __ballot_sync(0xffffffffu, in);
-        }
+        const int pos = load.lo + load.tile * S::kTile + warp * S::kKeys + lane;
+        const bool in = lane < S::kKeys && pos < load.n && looked < steps;
+        int i = 0;
+        if (in)
+            i = p.page_shift >= 0 ? pos >> p.page_shift
+                                  : static_cast<int>(static_cast<unsigned>(pos) / static_cast<unsigned>(p.cache.page_size));
+        slot = pos - i * p.cache.page_size;
+        page = in ? p.table.pages[load.b * p.table.stride + i] : -1;
+        want = __ballot_sync(0xffffffffu, in);
         if (++looked < steps) cursor_next(load, p, S::kTile, pad);
     };
     // A lane copies piece `piece` of rows in_copy, in_copy + kRowsPerCopy, ...; the pieces of a row are
@@ -378,36 +390,26 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
     const unsigned char *const vpool = p.cache.v + (inside ? piece * 16 : 0);
     auto swizzle = [](int row) { return kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1)); };
     const uint32_t copy_to = in_copy * S::kRow + ((piece ^ swizzle(in_copy)) << 4);
-    // Starts the copies of the rows that lookup() found (page, slot, want, head).
-    auto issue = [&](int stage, const int (&page)[kLaneRows], const int (&slot)[kLaneRows],
-                     const unsigned (&want)[kLaneRows], int load_head) {
+    constexpr unsigned kAll = S::kKeys == 32 ? 0xffffffffu : (1u << (S::kKeys & 31)) - 1u;
+    // Starts the copies of the rows that lookup() found.
+    auto issue = [&](int stage, int page, int slot, unsigned want, int load_head) {
         const uint32_t dst = ring + stage * S::kStage;
         unsigned char *const side = sides + stage * S::kSide;
-        unsigned ok[kLaneRows], some = 0;
-        bool full = inside;
-#pragma unroll
-        for (int r = 0; r < kLaneRows; ++r) {
-            const bool in = page[r] >= 0 && page[r] < p.cache.pages;
-            ok[r] = __ballot_sync(0xffffffffu, in);
-            some |= want[r];
-            full = full && ok[r] == (S::kKeys >= 32 ? 0xffffffffu : (1u << (S::kKeys & 31)) - 1u);
-            if (ok[r] != want[r] && lane == 0) record_status(p.status, kStatusCache);
-            const int row = lane + 32 * r;
-            if (row < S::kKeys) {
-                offsets[row] = in ? kv_offset(p.cache, page[r], slot[r], load_head) : -1;
-                if (kE4m3) {
-                    const long long so = in ? kv_scale_offset(p.cache, page[r], slot[r], load_head) : 0;
-                    cp_async4(smem_u32(side) + 16 + 4 * row, p.cache.k_scale + so, in);
-                    cp_async4(smem_u32(side) + 16 + 4 * (S::kKeys + row), p.cache.v_scale + so, in);
-                }
+        const bool in = page >= 0 && page < p.cache.pages;
+        const unsigned ok = __ballot_sync(0xffffffffu, in);
+        if (ok != want && lane == 0) record_status(p.status, kStatusCache);
+        if (lane < S::kKeys) {
+            offsets[lane] = in ? kv_offset(p.cache, page, slot, load_head) : -1;
+            if (kE4m3) {
+                const long long so = in ? kv_scale_offset(p.cache, page, slot, load_head) : 0;
+                cp_async4(smem_u32(side) + 16 + 4 * lane, p.cache.k_scale + so, in);
+                cp_async4(smem_u32(side) + 16 + 4 * (S::kKeys + lane), p.cache.v_scale + so, in);
             }
         }
-        if (lane == 0) {
-#pragma unroll
-            for (int r = 0; r < kLaneRows; ++r) reinterpret_cast<unsigned *>(side)[r] = ok[r];
-        }
+        if (lane == 0) *reinterpret_cast<unsigned *>(side) = ok;
         __syncwarp();
-        if (some) {
+        if (want) {
+            const bool full = inside && ok == kAll;
 #pragma unroll
             for (int i = 0; i < S::kKeys / kRowsPerCopy; ++i) {
                 const long long o = offsets[i * kRowsPerCopy + in_copy];
@@ -423,22 +425,17 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
 
     {
         // The first two steps' pages are requested together.
-        static_assert(S::kStages == 3, "two steps ahead");
         lookup();
-        int page0[kLaneRows], slot0[kLaneRows];
-        unsigned want0[kLaneRows];
-        const int head0 = load_head;
-#pragma unroll
-        for (int r = 0; r < kLaneRows; ++r) {
-            page0[r] = page[r];
-            slot0[r] = slot[r];
-            want0[r] = want[r];
-        }
+        const int page0 = page, slot0 = slot, head0 = load_head;
+        const unsigned want0 = want;
         lookup();
         issue(0, page0, slot0, want0, head0);
-        __syncwarp();
-        issue(1, page, slot, want, load_head);
-        lookup();
+#pragma unroll
+        for (int s = 1; s < S::kStages - 1; ++s) {
+            __syncwarp();
+            issue(s, page, slot, want, load_head);
+            lookup();
+        }
     }
 
     // ---- the item at hand
@@ -516,31 +513,25 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
         lookup();
         const uint32_t src = ring + stage * S::kStage;
         const unsigned char *const side = sides + stage * S::kSide;
-        unsigned mask[kLaneRows], some = 0;
-#pragma unroll
-        for (int r = 0; r < kLaneRows; ++r) {
-            mask[r] = reinterpret_cast<const unsigned *>(side)[r];
-            some |= mask[r];
-        }
-        if (some) {
+        const unsigned mask = *reinterpret_cast<const unsigned *>(side);
+        if (mask) {
             // S^T = K Q^T.  16-bit: matrices (rows 0-7 | 8-15) x (pieces 2c | 2c + 1), one k step; e4m3: the
-            // same bytes are two.
+            // same bytes are two.  A lone block's k steps go to two accumulators in turn: half the chain.
+            constexpr int kChains = NT * kBlocks == 1 ? 2 : 1;
             float s[NT][kBlocks][4];
             const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;
             const uint32_t ka = src + krow * S::kRow, kx = ((lane >> 4) ^ swizzle(krow)) << 4;
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[nt][kb][i] = 0.0f;
+                float acc[kChains][NT][4] = {};
 #pragma unroll
                 for (int c = 0; c < kChunks / 2; ++c) {
                     uint32_t a[4];
                     ldmatrix4(a, ka + (kx ^ (c << 5)) + kb * 16 * S::kRow);
                     if (!kE4m3) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816<kMmaBf16>(s[nt][kb], a, qf[nt][c][0], qf[nt][c][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<kMmaBf16>(acc[c % kChains][nt], a, qf[nt][c][0], qf[nt][c][1]);
                     } else {
                         // a[0] / a[1]: rows g / g + 8 of dims 32 c + 4 t4 .. + 3; a[2] / a[3]: of the next 16 dims
 #pragma unroll
@@ -549,51 +540,76 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                                                    widen2(a[2 * i + 1] >> 16)};
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma16816<false>(s[nt][kb], w, qf[nt][2 * c + i][0], qf[nt][2 * c + i][1]);
+                                mma16816<false>(acc[i % kChains][nt], w, qf[nt][2 * c + i][0], qf[nt][2 * c + i][1]);
                         }
                     }
                 }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[nt][kb][i] = kChains == 2 ? acc[0][nt][i] + acc[kChains - 1][nt][i] : acc[0][nt][i];
             }
-            // scores in log2 units, masked; the value scales join the exponent
+            // scores in log2 units; the value scales join the exponent
             float lv[kBlocks][2], inv[kBlocks][2];
             const float *scales = reinterpret_cast<const float *>(side + 16);
-            float *const scores = p.space.scores +
-                                  ((static_cast<long long>(use.b) * p.cache.heads + head) * p.positions + use.lo +
-                                   use.tile * S::kTile + warp * S::kKeys) * p.scored + h0 + 2 * t4;
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int row = 16 * kb + g + 8 * r;
-                    const bool in = (mask[kb / 2 < kLaneRows ? kb / 2 : 0] >> (row & 31)) & 1u;
                     float ks = 1.0f;
                     if (kE4m3) {
-                        ks = scales[row];
-                        // (a scale of 0 stands for values of 0, whatever their weight)
-                        float vs = in ? scales[S::kKeys + row] : 1.0f;
+                        // (a scale of 0 stands for values of 0, whatever their weight; rows left out have it too)
+                        ks = scales[16 * kb + g + 8 * r];
+                        float vs = scales[S::kKeys + 16 * kb + g + 8 * r];
                         vs = vs < 0x1p-100f ? 0x1p-100f : vs;
                         lv[kb][r] = __log2f(vs);
                         inv[kb][r] = __fdividef(1.0f, vs);
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float x[2];
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            x[i] = s[nt][kb][2 * r + i] * qscale[nt][i];
-                            if (kE4m3) x[i] *= ks;
-                            if (p.capped) x[i] = p.last * (1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x[i])));
+                            float &x = s[nt][kb][2 * r + i];
+                            x *= kE4m3 ? qscale[nt][i] * ks : qscale[nt][i];
+                            if (p.capped) x = p.last * (1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x)));
                         }
-                        if (p.space.scores && in && 8 * nt + 2 * t4 < hn &&
-                            TGEMM_CHECK(scores - p.space.scores + row * p.scored + 8 * nt + 2 <= p.dbg_scores, kChkKvSpace, p.status))
-                            *reinterpret_cast<float2 *>(scores + row * p.scored + 8 * nt) = make_float2(x[0], x[1]);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (kE4m3) x[i] += lv[kb][r];
-                            s[nt][kb][2 * r + i] = in ? x[i] : -INFINITY;
-                        }
-                    }
                 }
+            if (p.space.scores) {
+                float *const scores = p.space.scores +
+                                      ((static_cast<long long>(use.b) * p.cache.heads + head) * p.positions + use.lo +
+                                       use.tile * S::kTile + warp * S::kKeys) * p.scored + h0 + 2 * t4;
+#pragma unroll
+                for (int kb = 0; kb < kBlocks; ++kb)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int row = 16 * kb + g + 8 * r;
+                            if (((mask >> row) & 1u) && 8 * nt + 2 * t4 < hn &&
+                                TGEMM_CHECK(scores - p.space.scores + row * p.scored + 8 * nt + 2 <= p.dbg_scores, kChkKvSpace, p.status))
+                                *reinterpret_cast<float2 *>(scores + row * p.scored + 8 * nt) =
+                                    make_float2(s[nt][kb][2 * r], s[nt][kb][2 * r + 1]);
+                        }
+            }
+            if (kE4m3) {
+#pragma unroll
+                for (int kb = 0; kb < kBlocks; ++kb)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[nt][kb][i] += lv[kb][i >> 1];
+            }
+            if (mask != kAll) {
+#pragma unroll
+                for (int kb = 0; kb < kBlocks; ++kb)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (!((mask >> (16 * kb + g + 8 * r)) & 1u)) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) s[nt][kb][2 * r] = s[nt][kb][2 * r + 1] = -INFINITY;
+                        }
+            }
             // the reference moves when some score exceeds it by more than 2^kAttendGrow
             bool grow = false;
             float top[NT][2];
@@ -631,6 +647,11 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                 }
             }
             // weights, their sum, and O^T += V^T P^T
+            float ref[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) ref[nt][i] = m[nt][i] == -INFINITY ? 0.0f : m[nt][i];
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb) {
                 uint32_t pf[NT][2];
@@ -641,8 +662,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                         float w[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float ref = m[nt][i] == -INFINITY ? 0.0f : m[nt][i];
-                            w[i] = exp2_fast(s[nt][kb][2 * r + i] - ref);
+                            w[i] = exp2_fast(s[nt][kb][2 * r + i] - ref[nt][i]);
                             l[nt][i] += kE4m3 ? w[i] * inv[kb][r] : w[i];
                         }
                         pf[nt][r] = movmatrix_trans(pair16<kMmaBf16>(w[0], w[1]));
@@ -717,25 +737,24 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                     const int h = 8 * nt + 2 * t4 + i;
                     float ref = s_m[0][h], sum = 0.0f;
 #pragma unroll
-                    for (int w = 1; w < kAttendWarps; ++w) ref = fmaxf(ref, s_m[w][h]);
+                    for (int w = 1; w < S::kWarps; ++w) ref = fmaxf(ref, s_m[w][h]);
                     const float base = ref == -INFINITY ? 0.0f : ref;
 #pragma unroll
-                    for (int w = 0; w < kAttendWarps; ++w) sum += s_l[w][h] * exp2_fast(s_m[w][h] - base);
+                    for (int w = 0; w < S::kWarps; ++w) sum += s_l[w][h] * exp2_fast(s_m[w][h] - base);
                     a[nt][i] = exp2_fast(m[nt][i] - base);
                     if (warp == 0 && g == 0) {
                         s_ref[h] = ref;
                         s_inv[h] = sum;
                     }
                 }
-            // Each round every warp adds a quarter of the dims of its own, so that all work at once and every
-            // quarter meets the warps in a fixed order.
-            static_assert(kAttendWarps == 4 && DP % 64 == 0, "quarters of whole 16-row tiles");
+            // Each round every warp adds a part of the dims of its own, so that all work at once and every part
+            // meets the warps in a fixed order.
 #pragma unroll 1
-            for (int round = 0; round < kAttendWarps; ++round) {
-                const int quarter = (warp + round) & 3;
+            for (int round = 0; round < S::kWarps; ++round) {
+                const int part = warp + round < S::kWarps ? warp + round : warp + round - S::kWarps;
 #pragma unroll
                 for (int mt = 0; mt < DP / 16; ++mt) {
-                    if (mt / (DP / 64) == quarter) {
+                    if (mt * S::kWarps / (DP / 16) == part) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -755,11 +774,11 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                 const int c0 = attend_owner(item, ctas, all), c1 = attend_owner(item_end - 1, ctas, all);
                 const int parts = max(c1 - c0 + 1, 1), mine_at = min(max(cta - c0, 0), parts - 1);
                 const int group = mine_at / kAttendFanIn, groups = (parts + kAttendFanIn - 1) / kAttendFanIn;
-                auto slot_of = [&](int part) { return attend_slot(c0 + part, c0); };
+                auto slot_of = [&](int part) { return attend_slot(c0 + part, c0, lane_cta, p.lanes); };
                 auto put = [&](int to) {
                     if (!TGEMM_CHECK(to >= 0 && to < 2 * kAttendMaxCtas, kChkKvSpace, p.status)) return;
                     float *dst = p.space.out + static_cast<long long>(to) * S::kHeads * DP;
-                    for (int i = threadIdx.x; i < hn * DP / 4; i += kAttendThreads) {
+                    for (int i = threadIdx.x; i < hn * DP / 4; i += S::kThreads) {
                         const int h = i / (DP / 4), d = i % (DP / 4) * 4;
                         __stcg(reinterpret_cast<float4 *>(dst) + i, *reinterpret_cast<const float4 *>(merge + h * S::kPitch + d));
                     }
@@ -775,7 +794,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                 };
                 // Joins `n` parts (the first at part0, `stride` apart) into merge, s_ref and s_inv.
                 auto join = [&](int part0, int stride, int n) {
-                    for (int i = threadIdx.x; i < n * S::kHeads; i += kAttendThreads) {
+                    for (int i = threadIdx.x; i < n * S::kHeads; i += S::kThreads) {
                         const int e = i / S::kHeads, h = i % S::kHeads;
                         const float2 ml = __ldcg(p.space.ml + slot_of(part0 + e * stride) * S::kHeads + h);
                         s_w[e][h] = ml.x;
@@ -796,42 +815,31 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                         s_inv[h] = sum;
                     }
                     __syncthreads();
-                    // Two outputs of a thread at a time, kBatch parts of each requested together.
-                    const int outputs = hn * DP / 4;
+                    // kBatch parts of a thread's output requested together.
 #pragma unroll 1
-                    for (int i0 = threadIdx.x; i0 < outputs; i0 += 2 * kAttendThreads) {
-                        float4 sum[2] = {};
+                    for (int i = threadIdx.x; i < hn * DP / 4; i += S::kThreads) {
+                        const int h = i / (DP / 4);
+                        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
                         for (int e0 = 0; e0 < n; e0 += S::kBatch) {
-                            float4 x[2][S::kBatch];
+                            float4 x[S::kBatch];
 #pragma unroll
-                            for (int e = 0; e < S::kBatch; ++e) {
-                                const float4 *from = reinterpret_cast<const float4 *>(
-                                    p.space.out + static_cast<long long>(slot_of(part0 + (e0 + e) * stride)) * S::kHeads * DP);
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    const int i = i0 + y * kAttendThreads;
-                                    x[y][e] = e0 + e < n && i < outputs ? __ldcg(from + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                                }
-                            }
+                            for (int e = 0; e < S::kBatch; ++e)
+                                x[e] = e0 + e < n ? __ldcg(reinterpret_cast<const float4 *>(
+                                                               p.space.out + static_cast<long long>(slot_of(part0 + (e0 + e) * stride)) *
+                                                                                 S::kHeads * DP) + i)
+                                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                             for (int e = 0; e < S::kBatch; ++e) {
                                 if (e0 + e >= n) break;
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    const float w = s_w[e0 + e][min(i0 + y * kAttendThreads, outputs - 1) / (DP / 4)];
-                                    sum[y].x += w * x[y][e].x;
-                                    sum[y].y += w * x[y][e].y;
-                                    sum[y].z += w * x[y][e].z;
-                                    sum[y].w += w * x[y][e].w;
-                                }
+                                const float w = s_w[e0 + e][h];
+                                sum.x += w * x[e].x;
+                                sum.y += w * x[e].y;
+                                sum.z += w * x[e].z;
+                                sum.w += w * x[e].w;
                             }
                         }
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const int i = i0 + y * kAttendThreads;
-                            if (i < outputs) *reinterpret_cast<float4 *>(merge + i / (DP / 4) * S::kPitch + i % (DP / 4) * 4) = sum[y];
-                        }
+                        *reinterpret_cast<float4 *>(merge + h * S::kPitch + i % (DP / 4) * 4) = sum;
                     }
                     __syncthreads();
                 };
@@ -853,7 +861,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<kE4m3, DP, NT>::kC
                 if (threadIdx.x < hn && p.space.scores)
                     p.space.stats[static_cast<long long>(b) * h_all + head * p.group + h0 + threadIdx.x] =
                         make_float2(s_ref[threadIdx.x], s_inv[threadIdx.x]);
-                for (int i = threadIdx.x; i < hn * (DP / 8); i += kAttendThreads) {
+                for (int i = threadIdx.x; i < hn * (DP / 8); i += S::kThreads) {
                     const int h = i / (DP / 8), d = i % (DP / 8) * 8;
                     if (d >= p.cache.dim) continue;
                     const float sum = s_inv[h];

@@ -31,7 +31,9 @@ extern "C" long long check_first(long long c, long long ctas, long long total) {
 
 extern "C" int check_owner(long long t, long long ctas, long long total) { return tgemm::attend_owner(t, ctas, total); }
 
-extern "C" int check_slot(int c, int first) { return tgemm::attend_slot(c, first); }
+extern "C" int check_slot(int c, int first, int lane, int lanes) {
+    return tgemm::attend_slot(c, first, lane, lanes);
+}
 
 extern "C" void check_limits(int *out) {
     out[0] = tgemm::kAttendMaxCtas;

@@ -255,22 +255,25 @@ def test_keys_order_weights_as_numbers(host):
 
 
 def runs(host, lengths, window, tile, heads, places):
-    """The runs of attention_decode's CTAs: [(first, end)], and each item's [first, end) tiles."""
+    """The runs of attention_decode, [(first, end)], each item's [first, end) tiles in them, the CTAs that share a
+    run and the heads that a run goes through."""
     lo = ctypes.c_int()
     out = (ctypes.c_int * 3)()
     host.check_limits(out)
     least = out[2]
+    lanes = heads if places >= 8 * heads else 1
+    through, most = heads // lanes, places // lanes
     tiles = [[host.check_tiles(n, window, tile, pad, ctypes.byref(lo)) for n in lengths] for pad in (1, least)]
-    few = sum(tiles[1]) * heads <= places * least
+    few = sum(tiles[1]) * through <= most * least
     counts = tiles[1] if few else tiles[0]
-    total = sum(counts) * heads
-    ctas = total // least if few else min(places, total)
+    total = sum(counts) * through
+    ctas = total // least if few else min(most, total)
     items, at = [], 0
     for c in counts:
-        for _ in range(heads):
+        for _ in range(through):
             items.append((at, at + c))
             at += c
-    return [(host.check_first(c, ctas, total), host.check_first(c + 1, ctas, total)) for c in range(ctas)], items, total
+    return [(host.check_first(c, ctas, total), host.check_first(c + 1, ctas, total)) for c in range(ctas)], items, total, lanes
 
 
 @pytest.mark.parametrize("seed", range(60))
@@ -281,9 +284,9 @@ def test_runs_cover_every_tile_once_and_parts_have_slots_of_their_own(host, seed
     most = int(rng.choice([1, 64, 300, 5000, 200000]))
     lengths = rng.integers(0, most + 1, batch).tolist()
     window = int(rng.choice([0, 0, 1, 100]))
-    tile = int(rng.choice([64, 128, 256]))
-    cta_runs, items, total = runs(host, lengths, window, tile, int(rng.choice([1, 2, 8])), places)
-    assert len(cta_runs) <= places
+    tile = int(rng.choice([64, 96, 192]))
+    cta_runs, items, total, lanes = runs(host, lengths, window, tile, int(rng.choice([1, 2, 3, 8, 24, 64])), places)
+    assert len(cta_runs) * lanes <= places
     assert cta_runs[0][0] == 0 and cta_runs[-1][1] == total
     assert all(a < b for a, b in cta_runs) and all(x[1] == y[0] for x, y in zip(cta_runs, cta_runs[1:]))
     limits = (ctypes.c_int * 3)()
@@ -294,24 +297,32 @@ def test_runs_cover_every_tile_once_and_parts_have_slots_of_their_own(host, seed
         assert cta_runs[c0][0] <= first < cta_runs[c0][1] and cta_runs[c1][0] < end <= cta_runs[c1][1]
         if c0 == c1:
             continue
-        parts = [host.check_slot(c, c0) for c in range(c0, c1 + 1)]
-        assert not slots & set(parts) and len(set(parts)) == len(parts)
-        assert max(parts) < 2 * limits[0]
-        slots |= set(parts)
-        groups = -(-len(parts) // limits[1])
-        assert groups <= limits[0] // limits[1]
-        heads = set(parts[::limits[1]])
-        assert not counters & heads
-        counters |= heads
-        assert parts[0] not in tops
-        tops.add(parts[0])
+        for lane in range(lanes):
+            parts = [host.check_slot(c, c0, lane, lanes) for c in range(c0, c1 + 1)]
+            assert not slots & set(parts) and len(set(parts)) == len(parts)
+            assert max(parts) < 2 * limits[0]
+            slots |= set(parts)
+            groups = -(-len(parts) // limits[1])
+            assert groups <= limits[1]
+            heads = set(parts[::limits[1]])
+            assert not counters & heads
+            counters |= heads
+            assert parts[0] not in tops
+            tops.add(parts[0])
 
 
 def test_few_tiles_make_runs_that_end_with_their_item(host):
-    cta_runs, items, _ = runs(host, [77, 300, 0, 5000], 0, 64, 2, 304)
-    starts = {a for a, _ in items}
-    assert all(any(a <= r[0] and r[1] <= b for a, b in items) for r in cta_runs)
-    assert starts <= {r[0] for r in cta_runs}
+    for heads in (2, 64):
+        cta_runs, items, _, _ = runs(host, [77, 300, 0, 2000], 0, 64, heads, 304)
+        if heads == 2:
+            assert all(any(a <= r[0] and r[1] <= b for a, b in items) for r in cta_runs)
+            assert {a for a, _ in items} <= {r[0] for r in cta_runs}
+
+
+def test_owners_of_tiles_outside_stay_inside(host):
+    """What inconsistent lengths could ask for must not lead out of the runs."""
+    for t in (-5, -1, 100, 10 ** 12):
+        assert 0 <= host.check_owner(t, 7, 100) < 7
 
 
 def test_tiles_of_lengths_and_windows(host):
