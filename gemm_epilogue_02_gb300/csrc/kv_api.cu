@@ -232,16 +232,25 @@ cudaError_t launch_gather(const EvictParams &p, int64_t most, int heads, int bat
 // ---------------------------------------------------------------- attention
 int padded_dim(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-// Blocks of 8 query heads up to 8 heads on a key head, of 16 above (one read of
-// the keys instead of two); 256-wide rows leave registers for 8 only.
-int head_tiles(int64_t group, int64_t dim) { return group > 8 && dim <= 128 ? 2 : 1; }
+// Eights of query heads that a block takes.  Every block copies the rows for
+// itself, so the fewest blocks read fastest (24 heads over 1.2 GB of 16-bit
+// rows: three eights at once 231 us, 16 + 8 302 us), but a block's parts take
+// longer to join the more heads it has (24 heads, 7 windows of 8192: 34 us
+// against 26): three only where a run has 16 tiles of 64 or more.  256-wide rows leave
+// registers for one eight, and widening e4m3 rows leaves no gain for three.
+int head_tiles(int64_t group, int64_t dim, bool e4m3, int64_t batch, int64_t heads, int64_t positions, int num_sms) {
+    if (group <= 8 || dim > 128) return 1;
+    if (e4m3 || group <= 16 || batch * heads * (positions / 64) < int64_t(16) * 2 * num_sms) return 2;
+    const int64_t eights = (group + 7) / 8;
+    return (eights + 2) / 3 < (eights + 1) / 2 ? 3 : 2;
+}
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
 // The workspace's parts; returns its bytes (-1: too many).
 int64_t attend_layout(int64_t batch, int64_t q_heads, int64_t group, int64_t dim, int64_t positions, bool weights,
                       unsigned char *base, AttendSpace *out) {
-    const int64_t slots = 2 * kAttendMaxCtas, heads = 8 * head_tiles(group, dim);
+    const int64_t slots = 2 * kAttendMaxCtas, heads = group <= 8 || dim > 128 ? 8 : group <= 16 ? 16 : 24;   // of a block, at most
     int64_t at = 0, scores = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -295,10 +304,15 @@ template <bool kBf16, bool kE4m3>
 cudaError_t launch_attend_dim(const RuntimeInfo &rt, const AttendParams &p, int tiles, cudaStream_t s) {
     switch (padded_dim(p.cache.dim)) {
         case 64:
-            return tiles == 2 ? launch_attend<kBf16, kE4m3, 64, 2>(rt, p, s) : launch_attend<kBf16, kE4m3, 64, 1>(rt, p, s);
+            if constexpr (!kE4m3)
+                if (tiles == 3) return launch_attend<kBf16, kE4m3, 64, 3>(rt, p, s);
+            return tiles == 2 ? launch_attend<kBf16, kE4m3, 64, 2>(rt, p, s)
+                                : launch_attend<kBf16, kE4m3, 64, 1>(rt, p, s);
         case 128:
+            if constexpr (!kE4m3)
+                if (tiles == 3) return launch_attend<kBf16, kE4m3, 128, 3>(rt, p, s);
             return tiles == 2 ? launch_attend<kBf16, kE4m3, 128, 2>(rt, p, s)
-                              : launch_attend<kBf16, kE4m3, 128, 1>(rt, p, s);
+                                : launch_attend<kBf16, kE4m3, 128, 1>(rt, p, s);
         default:
             return launch_attend<kBf16, kE4m3, 256, 1>(rt, p, s);
     }
@@ -436,7 +450,8 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args
         if (cache->page_size == 1 << i) p.page_shift = i;
     p.dbg_o_bytes = obytes;
     p.dbg_scores = batch * cache->heads * p.positions * p.scored;
-    const int tiles = head_tiles(p.group, cache->dim);
+    const int64_t most = a->window > 0 ? std::min<int64_t>(p.positions, a->window) : p.positions;
+    const int tiles = head_tiles(p.group, cache->dim, cache->e4m3 != 0, batch, cache->heads, most, rt.num_sms);
     p.blocks = (p.group + 8 * tiles - 1) / (8 * tiles);
     p.status = rt.status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

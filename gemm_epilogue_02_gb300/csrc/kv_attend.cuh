@@ -65,7 +65,6 @@ namespace tgemm {
 constexpr int kAttendMaxCtas = 320;       // CTAs at most (workspace slots)
 constexpr int kAttendFanIn = 32;          // parts joined at once (more: in two levels)
 static_assert(kAttendMaxCtas <= kAttendFanIn * kAttendFanIn, "two levels join every CTA's part");
-constexpr int kAttendLeast = 4;           // tiles a CTA takes at least
 constexpr float kAttendGrow = 8.0f;       // log2 of the factor that moves the reference
 
 // The workspace: arrival counters (zero between calls), the parts' outputs
@@ -110,9 +109,9 @@ template <bool kE4m3, int DP, int NT>
 struct AttendShape {
     static constexpr int kRow = DP * (kE4m3 ? 1 : 2);                     // bytes of a row in shared memory
     static constexpr int kKeys = kRow >= 256 ? 16 : 32;                   // positions of a warp's step
-    static constexpr int kWarps = DP * NT == 256 && kRow < 512 ? 4 : 6;        // 255 registers a thread, or 168
+    static constexpr int kWarps = DP * NT >= 256 && kRow < 512 ? 4 : 6;        // 255 registers a thread, or 168
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kStages = kWarps == 4 ? 3 : kKeys * kRow >= 4096 ? 2 : 4;
+    static constexpr int kStages = kWarps == 4 && NT < 3 ? 3 : kKeys * kRow >= 4096 ? 2 : 4;
     static constexpr int kTile = kWarps * kKeys;
     static constexpr int kHeads = 8 * NT;
     static constexpr int kBatch = kThreads == 128 ? 16 : 8;               // parts joined per request (what registers hold)
@@ -225,6 +224,22 @@ __host__ __device__ inline int attend_tiles(int n, int window, int tile, int pad
     return (t + pad - 1) / pad * pad;
 }
 
+// With up to 32 sequences and few tiles, runs of one length that end with their item (its
+// tiles padded to a multiple) join faster than equal ones that begin and end
+// anywhere.  The shortest of these lengths is taken that makes at most `runs`
+// of them, unless that would cost more than four tiles over an equal share.
+// units[k]: runs of length attend_length(k) that the items make; 0: equal runs.
+constexpr int kAttendLengths = 8;
+__host__ __device__ inline int attend_length(int k) {
+    constexpr int kLength[kAttendLengths] = {1, 2, 3, 4, 6, 8, 12, 16};
+    return kLength[k];
+}
+__host__ __device__ inline int attend_pad(const long long *units, long long total, int runs) {
+    for (int k = 0; k < kAttendLengths; ++k)
+        if (units[k] <= runs && static_cast<long long>(attend_length(k)) * runs <= total + 4ll * runs) return attend_length(k);
+    return 0;
+}
+
 // Run c of `ctas` has the tiles [attend_first(c), attend_first(c + 1)) of `total`;
 // attend_owner() is the inverse.
 __host__ __device__ inline long long attend_div(long long a, long long b) {     // a >= 0, b > 0
@@ -277,7 +292,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
     constexpr int kRowsPerCopy = 32 / kChunks;      // rows that a warp's copy instruction covers
     constexpr int kBlocks = S::kKeys / 16;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long s_sum[2][S::kWarps];
+    __shared__ long long s_sum[S::kWarps];
     __shared__ int s_start[3];
     __shared__ float s_m[S::kWarps][S::kHeads], s_l[S::kWarps][S::kHeads];
     __shared__ float s_w[kAttendFanIn][S::kHeads];
@@ -285,7 +300,6 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
     __shared__ unsigned s_last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t4 = lane & 3;
-    if (threadIdx.x < 3) s_start[threadIdx.x] = 0;
     float *merge = reinterpret_cast<float *>(smem + S::kMerge);
     const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kStage;
     unsigned char *const sides = smem + S::kSides + warp * S::kStages * S::kSide;
@@ -293,57 +307,87 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
     griddep_wait();
     griddep_launch_dependents();
 
-    // ---- this CTA's run: all lengths summed, once as they are and once with
-    // runs of kAttendLeast tiles that end with their item
+    // ---- this CTA's run, from all lengths
     const int heads_all = p.lanes > 1 ? 1 : p.cache.heads * p.blocks;    // that a run goes through
     const int runs = static_cast<int>(gridDim.x) / p.lanes, lane_cta = static_cast<int>(blockIdx.x) % p.lanes;
-    const int each = (p.table.batch + S::kThreads - 1) / S::kThreads;
-    const int b_lo = min(p.table.batch, static_cast<int>(threadIdx.x) * each), b_hi = min(p.table.batch, b_lo + each);
-    long long mine[2] = {0, 0};
-    for (int b = b_lo; b < b_hi; ++b) {
-        bool bad = false;
-        int lo;
-        const int n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
-        if (bad && blockIdx.x == 0) record_status(p.status, kStatusCache);
-        mine[0] += attend_tiles(n, p.window, S::kTile, 1, &lo);
-        mine[1] += attend_tiles(n, p.window, S::kTile, kAttendLeast, &lo);
-    }
-    long long upto[2] = {mine[0], mine[1]};
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const long long u = __shfl_up_sync(0xffffffffu, upto[i], o);
-            if (lane >= o) upto[i] += u;
-        }
-    if (lane == 31) {
-        s_sum[0][warp] = upto[0];
-        s_sum[1][warp] = upto[1];
-    }
-    __syncthreads();
-    long long total[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        for (int w = 0; w < S::kWarps; ++w) {
-            if (w < warp) upto[i] += s_sum[i][w];
-            total[i] += s_sum[i][w];
-        }
-    const bool few = total[1] * heads_all <= static_cast<long long>(runs) * kAttendLeast;
-    const int pad = few ? kAttendLeast : 1;
-    const long long all = (few ? total[1] : total[0]) * heads_all;
-    const int ctas = static_cast<int>(few ? all / kAttendLeast : min(static_cast<long long>(runs), all));
     const int cta = static_cast<int>(blockIdx.x) / p.lanes;
-    if (cta >= ctas) return;
-    const long long first = attend_first(cta, ctas, all), last = attend_first(cta + 1, ctas, all);
-    {
-        const long long end = (few ? upto[1] : upto[0]) * heads_all;
-        long long at = end - (few ? mine[1] : mine[0]) * heads_all;
-        if (first >= at && first < end)
+    int pad = 1, start_b = 0, start_h = 0, start_tile = 0, ctas;
+    long long all, first, last;
+    if (p.table.batch <= 32) {
+        // One sequence a lane, in every warp for itself.
+        bool bad = false;
+        int lo, tiles = 0;
+        if (lane < p.table.batch) {
+            const int n = kv_length(p.table.lengths[lane], p.table.width, p.cache.page_size, &bad);
+            if (bad && threadIdx.x < 32 && blockIdx.x == 0) record_status(p.status, kStatusCache);
+            tiles = attend_tiles(n, p.window, S::kTile, 1, &lo);
+        }
+        int length = 0;
+        if (static_cast<long long>(p.table.batch) * heads_all <= runs) {
+            long long units[kAttendLengths];
+#pragma unroll
+            for (int k = 0; k < kAttendLengths; ++k)
+                units[k] = static_cast<long long>(__reduce_add_sync(0xffffffffu, (tiles + attend_length(k) - 1) / attend_length(k))) * heads_all;
+            length = attend_pad(units, static_cast<long long>(__reduce_add_sync(0xffffffffu, tiles)) * heads_all, runs);
+            pad = max(length, 1);
+            tiles = (tiles + pad - 1) / pad * pad;
+        }
+        int upto = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += u;
+        }
+        all = static_cast<long long>(__shfl_sync(0xffffffffu, upto, 31)) * heads_all;
+        ctas = static_cast<int>(length > 0 ? attend_div(all, length) : min(static_cast<long long>(runs), all));
+        if (cta >= ctas) return;
+        first = attend_first(cta, ctas, all);
+        last = attend_first(cta + 1, ctas, all);
+        const long long at = static_cast<long long>(upto - tiles) * heads_all;
+        const unsigned found = __ballot_sync(0xffffffffu, first >= at && first < at + static_cast<long long>(tiles) * heads_all);
+        start_b = max(__ffs(found) - 1, 0);
+        const int its = max(__shfl_sync(0xffffffffu, tiles, start_b), 1);
+        const long long in = first - static_cast<long long>(__shfl_sync(0xffffffffu, upto, start_b) - its) * heads_all;
+        start_h = static_cast<int>(attend_div(in, its));
+        start_tile = static_cast<int>(in - static_cast<long long>(start_h) * its);
+    } else {
+        const int each = (p.table.batch + S::kThreads - 1) / S::kThreads;
+        const int b_lo = min(p.table.batch, static_cast<int>(threadIdx.x) * each), b_hi = min(p.table.batch, b_lo + each);
+        long long mine = 0;
+        for (int b = b_lo; b < b_hi; ++b) {
+            bool bad = false;
+            int lo;
+            const int n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
+            if (bad && blockIdx.x == 0) record_status(p.status, kStatusCache);
+            mine += attend_tiles(n, p.window, S::kTile, 1, &lo);
+        }
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += u;
+        }
+        if (lane == 31) s_sum[warp] = upto;
+        if (threadIdx.x < 3) s_start[threadIdx.x] = 0;
+        __syncthreads();
+        all = 0;
+#pragma unroll
+        for (int w = 0; w < S::kWarps; ++w) {
+            if (w < warp) upto += s_sum[w];
+            all += s_sum[w];
+        }
+        all *= heads_all;
+        ctas = static_cast<int>(min(static_cast<long long>(runs), all));
+        if (cta >= ctas) return;
+        first = attend_first(cta, ctas, all);
+        last = attend_first(cta + 1, ctas, all);
+        long long at = (upto - mine) * heads_all;
+        if (first >= at && first < upto * heads_all)
             for (int b = b_lo; b < b_hi; ++b) {
                 bool bad = false;
                 int lo;
                 const int n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
-                const int tiles = attend_tiles(n, p.window, S::kTile, pad, &lo);
+                const int tiles = attend_tiles(n, p.window, S::kTile, 1, &lo);
                 if (first < at + static_cast<long long>(tiles) * heads_all) {
                     const long long in = first - at;
                     s_start[0] = b;
@@ -353,17 +397,20 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                 }
                 at += static_cast<long long>(tiles) * heads_all;
             }
+        __syncthreads();
+        start_b = s_start[0];
+        start_h = s_start[1];
+        start_tile = s_start[2];
     }
-    __syncthreads();
     const int steps = static_cast<int>(last - first);
 
     // ---- loading: the places of the next step's rows are looked up, then copied
     AttendCursor load;
-    load.b = s_start[0];
-    const int h_first = p.lanes > 1 ? lane_cta : s_start[1];
+    load.b = start_b;
+    const int h_first = p.lanes > 1 ? lane_cta : start_h;
     load.head = h_first / p.blocks;
     load.block = h_first - load.head * p.blocks;
-    load.tile = s_start[2];
+    load.tile = start_tile;
     cursor_load(load, p, S::kTile, pad);
     AttendCursor use = load;
     int page = -1, slot = 0, load_head = 0;    // lane i: of the step's position i

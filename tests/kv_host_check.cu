@@ -38,5 +38,9 @@ extern "C" int check_slot(int c, int first, int lane, int lanes) {
 extern "C" void check_limits(int *out) {
     out[0] = tgemm::kAttendMaxCtas;
     out[1] = tgemm::kAttendFanIn;
-    out[2] = tgemm::kAttendLeast;
+    out[2] = tgemm::kAttendLengths;
 }
+
+extern "C" int check_length_of(int k) { return tgemm::attend_length(k); }
+
+extern "C" int check_pad(const long long *units, long long total, int runs) { return tgemm::attend_pad(units, total, runs); }

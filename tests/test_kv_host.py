@@ -210,6 +210,7 @@ def host(tmp_path_factory):
     h.check_tiles.argtypes = [ctypes.c_int] * 4 + [ctypes.c_void_p]
     for f in (h.check_first, h.check_owner):
         f.argtypes = [ctypes.c_longlong] * 3
+    h.check_pad.argtypes = [ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int]
     h.check_first.restype = ctypes.c_longlong
     h.check_key.argtypes, h.check_key.restype = [ctypes.c_uint], ctypes.c_uint
     return h
@@ -260,14 +261,18 @@ def runs(host, lengths, window, tile, heads, places):
     lo = ctypes.c_int()
     out = (ctypes.c_int * 3)()
     host.check_limits(out)
-    least = out[2]
+    lengths_of = [host.check_length_of(k) for k in range(out[2])]
     lanes = heads if places >= 8 * heads else 1
     through, most = heads // lanes, places // lanes
-    tiles = [[host.check_tiles(n, window, tile, pad, ctypes.byref(lo)) for n in lengths] for pad in (1, least)]
-    few = sum(tiles[1]) * through <= most * least
-    counts = tiles[1] if few else tiles[0]
+    counts = [host.check_tiles(n, window, tile, 1, ctypes.byref(lo)) for n in lengths]
+    pad = 0
+    if len(lengths) <= 32 and len(lengths) * through <= most:
+        units = (ctypes.c_longlong * out[2])(*[sum(-(-c // u) for c in counts) * through for u in lengths_of])
+        pad = host.check_pad(units, sum(counts) * through, most)
+    if pad > 1:
+        counts = [host.check_tiles(n, window, tile, pad, ctypes.byref(lo)) for n in lengths]
     total = sum(counts) * through
-    ctas = total // least if few else min(most, total)
+    ctas = total // pad if pad else min(most, total)
     items, at = [], 0
     for c in counts:
         for _ in range(through):
@@ -311,12 +316,18 @@ def test_runs_cover_every_tile_once_and_parts_have_slots_of_their_own(host, seed
             tops.add(parts[0])
 
 
-def test_few_tiles_make_runs_that_end_with_their_item(host):
-    for heads in (2, 64):
-        cta_runs, items, _, _ = runs(host, [77, 300, 0, 2000], 0, 64, heads, 304)
-        if heads == 2:
-            assert all(any(a <= r[0] and r[1] <= b for a, b in items) for r in cta_runs)
-            assert {a for a, _ in items} <= {r[0] for r in cta_runs}
+@pytest.mark.parametrize("lengths,heads", [([77, 300, 0, 2000], 2), ([4096], 8), ([2000] * 4, 8), ([100, 300] * 8, 8), ([30], 100)])
+def test_few_tiles_make_runs_that_end_with_their_item(host, lengths, heads):
+    cta_runs, items, _, _ = runs(host, lengths, 0, 96, heads, 304)
+    assert all(any(a <= r[0] and r[1] <= b for a, b in items) for r in cta_runs)
+    assert {a for a, _ in items} <= {r[0] for r in cta_runs}
+
+
+def test_many_tiles_make_equal_runs(host):
+    for lengths in ([100000, 3, 70000], [1000] * 60):
+        cta_runs, _, total, lanes = runs(host, lengths, 0, 96, 8, 304)
+        sizes = [b - a for a, b in cta_runs]
+        assert len(cta_runs) == 304 // lanes and max(sizes) - min(sizes) <= 1
 
 
 def test_owners_of_tiles_outside_stay_inside(host):
