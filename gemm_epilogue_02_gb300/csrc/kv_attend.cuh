@@ -65,6 +65,7 @@ namespace tgemm {
 constexpr int kAttendMaxCtas = 320;       // CTAs at most (workspace slots)
 constexpr int kAttendFanIn = 32;          // parts joined at once (more: in two levels)
 static_assert(kAttendMaxCtas <= kAttendFanIn * kAttendFanIn, "two levels join every CTA's part");
+constexpr int kAttendDirect = 8;          // parts that threads join on their own
 constexpr float kAttendGrow = 8.0f;       // log2 of the factor that moves the reference
 
 // The workspace: arrival counters (zero between calls), the parts' outputs
@@ -114,7 +115,6 @@ struct AttendShape {
     static constexpr int kStages = kWarps == 4 && NT < 3 ? 3 : kKeys * kRow >= 4096 ? 2 : 4;
     static constexpr int kTile = kWarps * kKeys;
     static constexpr int kHeads = 8 * NT;
-    static constexpr int kBatch = kThreads == 128 ? 16 : 8;               // parts joined per request (what registers hold)
     static constexpr int kStage = 2 * kKeys * kRow;                       // keys, values
     static constexpr int kSide = kE4m3 ? 2 * kKeys * 4 + 16 : 16;         // a stage's scales and mask
     static constexpr int kSides = kWarps * kStages * kStage;              // where the sides begin
@@ -862,31 +862,88 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                         s_inv[h] = sum;
                     }
                     __syncthreads();
-                    // kBatch parts of a thread's output requested together.
+                    if (n <= kAttendDirect) {
+                        // Few parts: a thread's outputs one after the other, all parts requested together.
 #pragma unroll 1
-                    for (int i = threadIdx.x; i < hn * DP / 4; i += S::kThreads) {
-                        const int h = i / (DP / 4);
-                        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-                        for (int e0 = 0; e0 < n; e0 += S::kBatch) {
-                            float4 x[S::kBatch];
+                        for (int i = threadIdx.x; i < hn * DP / 4; i += S::kThreads) {
+                            const int h = i / (DP / 4);
+                            float4 x[kAttendDirect], sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                            for (int e = 0; e < S::kBatch; ++e)
-                                x[e] = e0 + e < n ? __ldcg(reinterpret_cast<const float4 *>(
-                                                               p.space.out + static_cast<long long>(slot_of(part0 + (e0 + e) * stride)) *
-                                                                                 S::kHeads * DP) + i)
-                                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            for (int e = 0; e < kAttendDirect; ++e)
+                                x[e] = e < n ? __ldcg(reinterpret_cast<const float4 *>(p.space.out) +
+                                                      static_cast<long long>(slot_of(part0 + e * stride)) * (S::kHeads * DP / 4) + i)
+                                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                            for (int e = 0; e < S::kBatch; ++e) {
-                                if (e0 + e >= n) break;
-                                const float w = s_w[e0 + e][h];
+                            for (int e = 0; e < kAttendDirect; ++e) {
+                                if (e >= n) break;
+                                const float w = s_w[e][h];
                                 sum.x += w * x[e].x;
                                 sum.y += w * x[e].y;
                                 sum.z += w * x[e].z;
                                 sum.w += w * x[e].w;
                             }
+                            *reinterpret_cast<float4 *>(merge + h * S::kPitch + i % (DP / 4) * 4) = sum;
                         }
-                        *reinterpret_cast<float4 *>(merge + h * S::kPitch + i % (DP / 4) * 4) = sum;
+                        __syncthreads();
+                        return;
+                    }
+                    // Each warp sums every kWarps-th part, two parts' loads in flight, then the warps' sums are
+                    // added in a fixed order as above; up to eight float4s of a lane at a time.
+                    constexpr int kAllOfLane = S::kHeads * DP / 4 / 32, kEach = kAllOfLane < 8 ? kAllOfLane : 8;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kAllOfLane && c0 * 128 < hn * DP; c0 += kEach) {
+                        float4 sum[kEach] = {};
+#pragma unroll 1
+                        for (int e = warp; e < n; e += 2 * S::kWarps) {
+                            const int e2 = e + S::kWarps < n ? e + S::kWarps : e;
+                            const float4 *const from = reinterpret_cast<const float4 *>(p.space.out) + c0 * 32 + lane;
+                            const float4 *const a = from + static_cast<long long>(slot_of(part0 + e * stride)) * (S::kHeads * DP / 4);
+                            const float4 *const b = from + static_cast<long long>(slot_of(part0 + e2 * stride)) * (S::kHeads * DP / 4);
+                            float4 x[kEach], y[kEach];
+#pragma unroll
+                            for (int c = 0; c < kEach; ++c) x[c] = __ldcg(a + c * 32);
+#pragma unroll
+                            for (int c = 0; c < kEach; ++c) y[c] = __ldcg(b + c * 32);
+#pragma unroll
+                            for (int c = 0; c < kEach; ++c) {
+                                const int h = ((c0 + c) * 32 + lane) / (DP / 4);
+                                const float w = s_w[e][h];
+                                sum[c].x += w * x[c].x;
+                                sum[c].y += w * x[c].y;
+                                sum[c].z += w * x[c].z;
+                                sum[c].w += w * x[c].w;
+                            }
+                            if (e2 == e) break;
+#pragma unroll
+                            for (int c = 0; c < kEach; ++c) {
+                                const int h = ((c0 + c) * 32 + lane) / (DP / 4);
+                                const float w = s_w[e2][h];
+                                sum[c].x += w * y[c].x;
+                                sum[c].y += w * y[c].y;
+                                sum[c].z += w * y[c].z;
+                                sum[c].w += w * y[c].w;
+                            }
+                        }
+#pragma unroll 1
+                        for (int round = 0; round < S::kWarps; ++round) {
+                            const int part = warp + round < S::kWarps ? warp + round : warp + round - S::kWarps;
+#pragma unroll
+                            for (int c = 0; c < kEach; ++c)
+                                if (c * S::kWarps / kEach == part) {
+                                    const int i = (c0 + c) * 32 + lane;
+                                    float4 *const at = reinterpret_cast<float4 *>(merge + i / (DP / 4) * S::kPitch + i % (DP / 4) * 4);
+                                    float4 v = sum[c];
+                                    if (round > 0) {
+                                        const float4 old = *at;
+                                        v.x += old.x;
+                                        v.y += old.y;
+                                        v.z += old.z;
+                                        v.w += old.w;
+                                    }
+                                    *at = v;
+                                }
+                            if (round + 1 < S::kWarps) __syncthreads();
+                        }
                     }
                     __syncthreads();
                 };
