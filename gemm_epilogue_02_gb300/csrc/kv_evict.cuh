@@ -12,10 +12,12 @@
 // blocks shares one sequence and head, each block a slice of its positions.  A
 // weight becomes a 32-bit key of the same order, which stays in shared memory;
 // the key of rank k - r is found 11 bits at a time (11 + 11 + 10) from
-// histograms of the keys that share the bits found so far, added up through
-// distributed shared memory: one warp of each block reads the sums of 32 bins,
-// finds the group, then reads its bins.  Then every larger key is kept, and of
-// the equal ones the first few in order of position.
+// histograms of the keys that share the bits found so far.  A block alone scans
+// its bins; the blocks of a cluster add theirs up through distributed shared
+// memory, whose reads are slow, so one warp of each reads the sums of 32 bins,
+// finds the group and then reads its bins (131072 positions: 28 us; every block
+// reading every bin 34 us).  Then every larger key is kept, and of the equal
+// ones the first few in order of position.
 #pragma once
 #include <cooperative_groups.h>
 
@@ -24,8 +26,9 @@
 namespace tgemm {
 
 constexpr int kSelectBins = 2048;
-constexpr int kSelectGroups = kSelectBins / 32;
 constexpr int kSelectMaxCached = 48 * 1024;           // keys of a slice in shared memory (192 KiB); of longer ones none
+constexpr int kSelectMaxBlocks = 8;                   // of a cluster
+constexpr int kSelectGroups = kSelectBins / 32;
 static_assert(kSelectGroups == 64, "two groups a lane");
 
 struct EvictParams {
@@ -63,9 +66,10 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParams p) {
     constexpr int kWarps = kThreads / 32;
     extern __shared__ uint32_t keys[];
-    __shared__ int hist[3][kSelectBins], groups[3][kSelectGroups];
+    __shared__ __align__(16) int hist[3][kSelectBins];
+    __shared__ int groups[3][kSelectGroups];     // sums of 32 bins
     __shared__ int warp_sums[2][kWarps];
-    __shared__ int s_counts[2];                  // this block's larger and equal keys
+    __shared__ int s_counts[2], s_before[2];     // larger and equal keys: this block's, those of the blocks before
     __shared__ int s_digit, s_need;
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
@@ -125,48 +129,67 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
             if ((key & mask) == prefix) atomicAdd(&hist[pass][(key >> shift) & digit_mask], 1);
         }
         __syncthreads();
-#pragma unroll 2
-        for (int i = warp; i < kSelectGroups; i += kWarps) {
-            const int sum = __reduce_add_sync(0xffffffffu, hist[pass][i * 32 + lane]);
-            if (lane == 0) groups[pass][i] = sum;
-        }
-        if (blocks > 1) cluster.sync();
-        else __syncthreads();
-        if (warp == 0) {
-            // Sums over the blocks, from the top: lane l has groups 63 - 2 l and 62 - 2 l, then bin 31 - l of the
-            // group in which the running sum reaches `need`.
-            int c0 = 0, c1 = 0, c = 0;
-            if (blocks == 1) {
-                c0 = groups[pass][63 - 2 * lane];
-                c1 = groups[pass][62 - 2 * lane];
-            } else {
+        if (blocks == 1) {
+            // Thread t has the bins from kSelectBins - 1 - t * kPer down; the one in which the running sum from the
+            // top reaches `need` has the limit's digit.  (The last pass leaves the upper bins empty.)
+            constexpr int kPer = kSelectBins / kThreads;
+            const int low = kSelectBins - kPer - static_cast<int>(threadIdx.x) * kPer;
+            int c[kPer], sum = 0;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int *other = cluster.map_shared_rank(groups[pass], q < blocks ? q : rank);
+            for (int i = 0; i < kPer; i += 2) {
+                const int2 x = *reinterpret_cast<const int2 *>(&hist[pass][low + i]);
+                c[i] = x.x;
+                c[i + 1] = x.y;
+                sum += x.x + x.y;
+            }
+            const int upto = warp_scan(sum);
+            if (lane == 31) warp_sums[0][warp] = upto;
+            __syncthreads();
+            int above = upto - sum + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[0][lane] : 0);
+            if (above < need && above + sum >= need) {
+#pragma unroll
+                for (int i = kPer - 1; i >= 0; --i) {
+                    if (above < need && above + c[i] >= need) {
+                        s_digit = low + i;
+                        s_need = need - above;
+                    }
+                    above += c[i];
+                }
+            }
+        } else {
+#pragma unroll 2
+            for (int i = warp; i < kSelectGroups; i += kWarps) {
+                const int sum = __reduce_add_sync(0xffffffffu, hist[pass][i * 32 + lane]);
+                if (lane == 0) groups[pass][i] = sum;
+            }
+            cluster.sync();
+            if (warp == 0) {
+                // Sums over the blocks, from the top: lane l has groups 63 - 2 l and 62 - 2 l, then bin 31 - l of
+                // the group in which the running sum reaches `need`.
+                int c0 = 0, c1 = 0, c = 0;
+#pragma unroll
+                for (int q = 0; q < kSelectMaxBlocks; ++q) {
+                    const int *const other = cluster.map_shared_rank(groups[pass], q < blocks ? q : rank);
                     const int x0 = other[63 - 2 * lane], x1 = other[62 - 2 * lane];
                     c0 += q < blocks ? x0 : 0;
                     c1 += q < blocks ? x1 : 0;
                 }
-            }
-            const int above = warp_scan(c0 + c1) - c0 - c1;
-            const unsigned found = __ballot_sync(0xffffffffu, above < need && above + c0 + c1 >= need);
-            const int owner = __ffs(found) - 1;
-            const bool second = above + c0 < need;
-            const int group = __shfl_sync(0xffffffffu, 63 - 2 * lane - (second ? 1 : 0), owner);
-            const int left = need - __shfl_sync(0xffffffffu, above + (second ? c0 : 0), owner);
-            if (blocks == 1) {
-                c = hist[pass][group * 32 + 31 - lane];
-            } else {
+                const int above = warp_scan(c0 + c1) - c0 - c1;
+                const unsigned found = __ballot_sync(0xffffffffu, above < need && above + c0 + c1 >= need);
+                const int owner = __ffs(found) - 1;
+                const bool second = above + c0 < need;
+                const int group = __shfl_sync(0xffffffffu, 63 - 2 * lane - (second ? 1 : 0), owner);
+                const int left = need - __shfl_sync(0xffffffffu, above + (second ? c0 : 0), owner);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < kSelectMaxBlocks; ++q) {
                     const int x = cluster.map_shared_rank(hist[pass], q < blocks ? q : rank)[group * 32 + 31 - lane];
                     c += q < blocks ? x : 0;
                 }
-            }
-            const int over = warp_scan(c) - c;
-            if (over < left && over + c >= left) {
-                s_digit = group * 32 + 31 - lane;
-                s_need = left - over;
+                const int over = warp_scan(c) - c;
+                if (over < left && over + c >= left) {
+                    s_digit = group * 32 + 31 - lane;
+                    s_need = left - over;
+                }
             }
         }
         __syncthreads();
@@ -204,15 +227,21 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
             }
         }
         cluster.sync();
-        for (int q = 0; q < rank; ++q) {
-            const int *other = cluster.map_shared_rank(s_counts, q);
-            at_larger += other[0];
-            at_equal += other[1];
+        if (warp == 0) {
+            const int *const other = cluster.map_shared_rank(s_counts, min(lane, rank));
+            const int x = lane < rank ? other[0] : 0, y = lane < rank ? other[1] : 0;
+            const int larger_before = __reduce_add_sync(0xffffffffu, x), equal_before = __reduce_add_sync(0xffffffffu, y);
+            if (lane == 0) {
+                s_before[0] = larger_before;
+                s_before[1] = equal_before;
+            }
         }
         cluster.sync();                          // no block leaves while its counts are read
+        at_larger += s_before[0];
+        at_equal += s_before[1];
     }
     const unsigned below = (1u << lane) - 1u;
-#pragma unroll 2
+#pragma unroll 4
     for (int i0 = from; i0 < to; i0 += 32) {
         const int i = i0 + lane;
         const uint32_t key = i < to ? key_at(i) : 0u;
