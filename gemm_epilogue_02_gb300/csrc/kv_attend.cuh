@@ -990,7 +990,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
 // weights[b, head, j] += sum over the group of 2^(t_j - m) / l.  A position's
 // scores lie together; a thread adds for kSpreadEach positions, kSpreadThreads
 // apart, whose first eight heads it requests together.
-constexpr int kSpreadThreads = 256, kSpreadEach = 2;
+constexpr int kSpreadThreads = 128, kSpreadEach = 4;
 
 __global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendParams p) {
     constexpr int kPairs = 4;             // of heads, per request
