@@ -168,22 +168,25 @@ tgemm_status done(cudaError_t e) {
 // Lanes that hold a row of `bytes` in 16-byte pieces: the power of two at or above, 8 to 32.
 int row_lanes(int bytes) { return bytes <= 128 ? 8 : bytes <= 256 ? 16 : 32; }
 
+// Few rows: one pass a block, so that they reach all SMs; from two blocks an SM
+// on, chunks of 64 to 128 rows (256 tokens of 8 heads: one pass 4.6 us on the
+// GPU; 52042 tokens to e4m3: one pass 80 us, chunks 59 us).
 template <bool kBf16, bool kE4m3, int kLanes>
 cudaError_t launch_append_lanes(const RuntimeInfo &rt, const AppendParams &p, cudaStream_t s) {
-    constexpr int kPass = kRowThreads / kLanes;
+    constexpr int kPass = kRowThreads / kLanes, kPieces = kE4m3 ? 2 : 1, kUnroll = kE4m3 ? 2 : 4;
     const int64_t passes = (p.tokens * p.cache.heads + kPass - 1) / kPass;
     if (passes <= 2 * rt.num_sms)
-        return launch(kv_append_kernel<kBf16, kE4m3, kLanes, 1>, dim3(static_cast<unsigned>(passes)), kRowThreads, 0, s, p);
-    const int64_t chunks = std::min<int64_t>((passes + 3) / 4, static_cast<int64_t>(rt.num_sms) * kAppendCtas);
-    return launch(kv_append_kernel<kBf16, kE4m3, kLanes, 4>, dim3(static_cast<unsigned>(chunks)), kRowThreads, 0, s, p);
+        return launch(kv_append_kernel<kBf16, kE4m3, kLanes, kPieces, 1>, dim3(static_cast<unsigned>(passes)), kRowThreads, 0, s, p);
+    const int64_t chunks = std::min<int64_t>((passes + kUnroll - 1) / kUnroll, static_cast<int64_t>(rt.num_sms) * kAppendCtas);
+    return launch(kv_append_kernel<kBf16, kE4m3, kLanes, kPieces, kUnroll>, dim3(static_cast<unsigned>(chunks)), kRowThreads, 0, s, p);
 }
 
 template <bool kBf16, bool kE4m3>
 cudaError_t launch_append(const RuntimeInfo &rt, const AppendParams &p, cudaStream_t s) {
     switch (row_lanes(p.cache.dim * 2)) {
-        case 8: return launch_append_lanes<kBf16, kE4m3, 8>(rt, p, s);
-        case 16: return launch_append_lanes<kBf16, kE4m3, 16>(rt, p, s);
-        default: return launch_append_lanes<kBf16, kE4m3, 32>(rt, p, s);
+        case 8: return launch_append_lanes<kBf16, kE4m3, kE4m3 ? 4 : 8>(rt, p, s);
+        case 16: return launch_append_lanes<kBf16, kE4m3, kE4m3 ? 8 : 16>(rt, p, s);
+        default: return launch_append_lanes<kBf16, kE4m3, kE4m3 ? 16 : 32>(rt, p, s);
     }
 }
 

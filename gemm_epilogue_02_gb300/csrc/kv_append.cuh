@@ -46,7 +46,7 @@ __host__ __device__ inline int kv_sequence_of(const int *starts, int batch, long
 
 // Eight 16-bit elements as floats.
 template <bool kBf16>
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(const uint4 &u, float *x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -90,11 +90,12 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // 2^-23 of a unit in the last place of a midpoint.  While nothing leaves fp32's
 // normal range that holds; scales outside 2^+-60 take divisions, and within, an
 // element so small that it might is zero in e4m3 either way.
-__device__ __forceinline__ float scale_row(float (&x)[8], float top) {
+template <int N>
+__device__ __forceinline__ float scale_row(float (&x)[N], float top) {
     if (!(top > 448 * 0x1p-60f && top < 448 * 0x1p60f)) {
         const float scale = top > 0.0f ? top / 448.0f : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] / -scale;
+        for (int i = 0; i < N; ++i) x[i] = x[i] / -scale;
         return scale;
     }
     constexpr float kInv = 1.0f / 448.0f;
@@ -103,7 +104,7 @@ __device__ __forceinline__ float scale_row(float (&x)[8], float top) {
     r = fmaf(fmaf(-r, scale, 1.0f), r, r);
     const float2 rr = make_float2(-r, -r), ss = make_float2(scale, scale);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
+    for (int i = 0; i < N; i += 2) {
         const float2 a = make_float2(x[i], x[i + 1]), q2 = mul2(a, rr), y = fma2(fma2(q2, ss, a), rr, q2);
         x[i] = y.x;
         x[i + 1] = y.y;
@@ -129,7 +130,7 @@ __device__ __forceinline__ uint32_t top8(const uint4 &u) {       // both halves 
 }
 
 // Eight floats' negatives as e4m3.
-__device__ __forceinline__ uint2 pack8_negated(const float (&x)[8]) {
+__device__ __forceinline__ uint2 pack8_negated(const float *x) {
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -140,10 +141,12 @@ __device__ __forceinline__ uint2 pack8_negated(const float (&x)[8]) {
 }
 
 // Blocks take chunks of kRows rows, a row being the keys and values of one
-// (token, head), kUnroll passes of kRowThreads / kLanes rows.
+// (token, head), kUnroll passes of kRowThreads / kLanes rows; a lane has kPieces
+// 16-byte pieces of a row, kLanes apart (two where a row's maximum and scale
+// cost more than its copy: a lane's share of them halves).
 constexpr int kRowThreads = 256, kAppendCtas = 4;     // per SM
 
-template <bool kBf16, bool kE4m3, int kLanes, int kUnroll>
+template <bool kBf16, bool kE4m3, int kLanes, int kPieces, int kUnroll>
 __global__ void __launch_bounds__(kRowThreads, kAppendCtas) kv_append_kernel(const AppendParams p) {
     constexpr int kPass = kRowThreads / kLanes, kRows = kPass * kUnroll;
     __shared__ long long s_src[2][kRows], s_dst[2][kRows], s_scale[2][kRows];
@@ -151,7 +154,9 @@ __global__ void __launch_bounds__(kRowThreads, kAppendCtas) kv_append_kernel(con
     griddep_launch_dependents();
     const long long rows = p.tokens * p.cache.heads, step = static_cast<long long>(gridDim.x) * kRows;
     const int piece = threadIdx.x % kLanes, in_pass = threadIdx.x / kLanes;
-    const bool inside = piece * 8 < p.cache.dim;
+    bool inside[kPieces];
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) inside[c] = (piece + c * kLanes) * 8 < p.cache.dim;
     // Thread i < kRows finds the place of row r0 + i.
     auto place = [&](long long r0, int to) {
         if (threadIdx.x >= kRows) return;
@@ -195,14 +200,17 @@ __global__ void __launch_bounds__(kRowThreads, kAppendCtas) kv_append_kernel(con
     place(r0, 0);
     __syncthreads();
     for (int at = 0; r0 < rows; r0 += step, at ^= 1) {
-        uint4 x[kUnroll][2];
+        uint4 x[kUnroll][2][kPieces];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int i = u * kPass + in_pass;
-            x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-            if (s_dst[at][i] >= 0 && inside) {
-                x[u][0] = __ldcs(reinterpret_cast<const uint4 *>(p.k + s_src[at][i]) + piece);
-                x[u][1] = __ldcs(reinterpret_cast<const uint4 *>(p.v + s_src[at][i]) + piece);
+#pragma unroll
+            for (int c = 0; c < kPieces; ++c) {
+                x[u][0][c] = x[u][1][c] = make_uint4(0, 0, 0, 0);
+                if (s_dst[at][i] >= 0 && inside[c]) {
+                    x[u][0][c] = __ldcs(reinterpret_cast<const uint4 *>(p.k + s_src[at][i]) + piece + c * kLanes);
+                    x[u][1][c] = __ldcs(reinterpret_cast<const uint4 *>(p.v + s_src[at][i]) + piece + c * kLanes);
+                }
             }
         }
         if (r0 + step < rows) place(r0 + step, at ^ 1);      // while the rows are on their way
@@ -212,7 +220,12 @@ __global__ void __launch_bounds__(kRowThreads, kAppendCtas) kv_append_kernel(con
             const long long dst = s_dst[at][i];
             uint32_t top = 0;                    // keys' largest magnitude below, values' above
             if (kE4m3) {
-                const uint32_t a = top8<kBf16>(x[u][0]), b = top8<kBf16>(x[u][1]);
+                uint32_t a = top8<kBf16>(x[u][0][0]), b = top8<kBf16>(x[u][1][0]);
+#pragma unroll
+                for (int c = 1; c < kPieces; ++c) {
+                    a = max_pair<kBf16>(a, top8<kBf16>(x[u][0][c]));
+                    b = max_pair<kBf16>(b, top8<kBf16>(x[u][1][c]));
+                }
                 top = max_pair<kBf16>(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
 #pragma unroll
                 for (int o = kLanes / 2; o > 0; o >>= 1) top = max_pair<kBf16>(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -220,17 +233,23 @@ __global__ void __launch_bounds__(kRowThreads, kAppendCtas) kv_append_kernel(con
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 unsigned char *pool = which ? p.cache.v : p.cache.k;
-                if (!kE4m3) {
-                    if (dst >= 0 && inside) *(reinterpret_cast<uint4 *>(pool + dst) + piece) = x[u][which];
-                    continue;
+                if constexpr (!kE4m3) {
+#pragma unroll
+                    for (int c = 0; c < kPieces; ++c)
+                        if (dst >= 0 && inside[c]) *(reinterpret_cast<uint4 *>(pool + dst) + piece + c * kLanes) = x[u][which][c];
+                } else {
+                    float f[8 * kPieces];
+#pragma unroll
+                    for (int c = 0; c < kPieces; ++c) unpack8<kBf16>(x[u][which][c], f + 8 * c);
+                    const uint32_t half = which ? top >> 16 : top & 0xFFFFu;
+                    const float scale = scale_row(f, kBf16 ? __uint_as_float(half << 16)
+                                                           : __half2float(__ushort_as_half(static_cast<unsigned short>(half))));
+#pragma unroll
+                    for (int c = 0; c < kPieces; ++c)
+                        if (dst >= 0 && inside[c])
+                            *(reinterpret_cast<uint2 *>(pool + dst) + piece + c * kLanes) = pack8_negated(f + 8 * c);
+                    if (dst >= 0 && piece == 0) (which ? p.cache.v_scale : p.cache.k_scale)[s_scale[at][i]] = scale;
                 }
-                float f[8];
-                unpack8<kBf16>(x[u][which], f);
-                const uint32_t half = which ? top >> 16 : top & 0xFFFFu;
-                const float scale = scale_row(f, kBf16 ? __uint_as_float(half << 16)
-                                                       : __half2float(__ushort_as_half(static_cast<unsigned short>(half))));
-                if (dst >= 0 && inside) *(reinterpret_cast<uint2 *>(pool + dst) + piece) = pack8_negated(f);
-                if (dst >= 0 && piece == 0) (which ? p.cache.v_scale : p.cache.k_scale)[s_scale[at][i]] = scale;
             }
         }
         __syncthreads();
