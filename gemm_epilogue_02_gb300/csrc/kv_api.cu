@@ -420,7 +420,7 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args
     p.positions = a->seq.pages_width * cache->page_size;
     const int64_t need = attend_layout(batch, q_heads, p.group, cache->dim, p.positions, a->weights.data != nullptr,
                                        static_cast<unsigned char *>(a->workspace), &p.space);
-    if (need < 0) return TGEMM_ERR_INVALID_ARG;
+    if (need < 0 || batch * q_heads > (int64_t(1) << 42) / std::max<int64_t>(1, p.positions)) return TGEMM_ERR_INVALID_ARG;
     if (batch == 0) return TGEMM_OK;
     if (!a->Q || !a->O || !a->workspace || a->workspace_bytes < need) return TGEMM_ERR_INVALID_ARG;
     if (!aligned16(a->Q) || !aligned16(a->O) || !aligned16(a->workspace) ||

@@ -101,16 +101,18 @@ struct AttendParams {
     long long dbg_o_bytes, dbg_scores;    // debug builds: O's bytes, the workspace's scores
 };
 
-// Shapes.  What limits a step is the latency of its chain (copy, product,
-// softmax, product), so many warps with short steps do better than few with
-// long ones, down to a step's fixed cost: steps of 16 positions, 32 for 64-byte
-// rows, and as many warps as registers allow beside about 96 KiB of ring per
-// CTA.
+// Shapes.  A step is a chain (copy, product, softmax, product) with a fixed cost
+// of some hundred instructions, and a warp has no more than one on the way, so
+// the SM wants many warps, each with as much in a step as the ring allows: 96
+// KiB per CTA, steps of 16 positions, 32 where a row has 128 bytes or less (e4m3
+// 128 wide, 8 warps with steps of 16: 2.8 TB/s, 6 with 32: 6.3).  Six warps of two
+// stages beat four of three where 168 registers do (16-bit, 256 wide: 6.5
+// against 6.1 TB/s); two or three eights of heads need 255.
 template <bool kE4m3, int DP, int NT>
 struct AttendShape {
     static constexpr int kRow = DP * (kE4m3 ? 1 : 2);                     // bytes of a row in shared memory
     static constexpr int kKeys = kRow >= 256 ? 16 : 32;                   // positions of a warp's step
-    static constexpr int kWarps = DP * NT >= 256 && kRow < 512 ? 4 : 6;        // 255 registers a thread, or 168
+    static constexpr int kWarps = DP * NT >= 256 && kRow < 512 ? 4 : 6;   // 255 registers a thread, or 168
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kStages = kWarps == 4 && NT < 3 ? 3 : kKeys * kRow >= 4096 ? 2 : 4;
     static constexpr int kTile = kWarps * kKeys;
@@ -268,20 +270,33 @@ __device__ __forceinline__ void cursor_load(AttendCursor &u, const AttendParams 
     u.tiles = attend_tiles(u.n, p.window, tile, pad, &u.lo);
 }
 
-__device__ __forceinline__ void cursor_next(AttendCursor &u, const AttendParams &p, int tile, int pad) {
-    if (++u.tile < u.tiles) return;
+// To the next item; true when that is another sequence's (whose n, lo and tiles
+// are still to be set).
+__device__ __forceinline__ bool cursor_item(AttendCursor &u, const AttendParams &p) {
     u.tile = 0;
     if (p.lanes == 1) {
-        if (++u.block < p.blocks) return;
+        if (++u.block < p.blocks) return false;
         u.block = 0;
-        if (++u.head < p.cache.heads) return;
+        if (++u.head < p.cache.heads) return false;
         u.head = 0;
     }
-    if (u.b + 1 < p.table.batch) {
-        ++u.b;
-        cursor_load(u, p, tile, pad);
-    }
+    if (u.b + 1 >= p.table.batch) return false;
+    ++u.b;
+    return true;
 }
+
+__device__ __forceinline__ void cursor_next(AttendCursor &u, const AttendParams &p, int tile, int pad) {
+    if (++u.tile < u.tiles) return;
+    if (cursor_item(u, p)) cursor_load(u, p, tile, pad);
+}
+
+// A block's run, found by its first warp or by all: every warp goes by the same
+// numbers, also by the same lengths, so that all meet at the same barriers
+// whatever another stream does to the lengths meanwhile.
+struct AttendRun {
+    long long all, first, last;
+    int ctas, pad, b, h, tile, n;
+};
 
 template <bool kBf16, bool kE4m3, int DP, int NT>
 __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendShape<kE4m3, DP, NT>::kCtas)
@@ -293,7 +308,8 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
     constexpr int kBlocks = S::kKeys / 16;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long s_sum[S::kWarps];
-    __shared__ int s_start[3];
+    __shared__ AttendRun s_run;
+    __shared__ int s_next;                          // length of the sequence after the one at hand
     __shared__ float s_m[S::kWarps][S::kHeads], s_l[S::kWarps][S::kHeads];
     __shared__ float s_w[kAttendFanIn][S::kHeads];
     __shared__ float s_inv[S::kHeads], s_ref[S::kHeads];
@@ -311,56 +327,52 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
     const int heads_all = p.lanes > 1 ? 1 : p.cache.heads * p.blocks;    // that a run goes through
     const int runs = static_cast<int>(gridDim.x) / p.lanes, lane_cta = static_cast<int>(blockIdx.x) % p.lanes;
     const int cta = static_cast<int>(blockIdx.x) / p.lanes;
-    int pad = 1, start_b = 0, start_h = 0, start_tile = 0, ctas;
-    long long all, first, last;
     if (p.table.batch <= 32) {
-        // One sequence a lane, in every warp for itself.
-        bool bad = false;
-        int lo, tiles = 0;
-        if (lane < p.table.batch) {
-            const int n = kv_length(p.table.lengths[lane], p.table.width, p.cache.page_size, &bad);
-            if (bad && threadIdx.x < 32 && blockIdx.x == 0) record_status(p.status, kStatusCache);
-            tiles = attend_tiles(n, p.window, S::kTile, 1, &lo);
-        }
-        int length = 0;
-        if (static_cast<long long>(p.table.batch) * heads_all <= runs) {
-            long long units[kAttendLengths];
+        // One sequence a lane of the first warp.
+        if (warp == 0) {
+            bool bad = false;
+            int lo, n = 0, tiles = 0;
+            if (lane < p.table.batch) {
+                n = kv_length(p.table.lengths[lane], p.table.width, p.cache.page_size, &bad);
+                if (bad && blockIdx.x == 0) record_status(p.status, kStatusCache);
+                tiles = attend_tiles(n, p.window, S::kTile, 1, &lo);
+            }
+            AttendRun r;
+            int length = 0;
+            if (static_cast<long long>(p.table.batch) * heads_all <= runs) {
+                long long units[kAttendLengths];
 #pragma unroll
-            for (int k = 0; k < kAttendLengths; ++k)
-                units[k] = static_cast<long long>(__reduce_add_sync(0xffffffffu, (tiles + attend_length(k) - 1) / attend_length(k))) * heads_all;
-            length = attend_pad(units, static_cast<long long>(__reduce_add_sync(0xffffffffu, tiles)) * heads_all, runs);
-            pad = max(length, 1);
-            tiles = (tiles + pad - 1) / pad * pad;
+                for (int k = 0; k < kAttendLengths; ++k)
+                    units[k] = static_cast<long long>(__reduce_add_sync(0xffffffffu, (tiles + attend_length(k) - 1) / attend_length(k))) * heads_all;
+                length = attend_pad(units, static_cast<long long>(__reduce_add_sync(0xffffffffu, tiles)) * heads_all, runs);
+            }
+            r.pad = max(length, 1);
+            tiles = (tiles + r.pad - 1) / r.pad * r.pad;
+            const int upto = warp_scan(tiles);
+            r.all = static_cast<long long>(__shfl_sync(0xffffffffu, upto, 31)) * heads_all;
+            r.ctas = static_cast<int>(length > 0 ? attend_div(r.all, length) : min(static_cast<long long>(runs), r.all));
+            const int c = min(cta, r.ctas - 1);
+            r.first = attend_first(c, r.ctas, r.all);
+            r.last = attend_first(c + 1, r.ctas, r.all);
+            const long long at = static_cast<long long>(upto - tiles) * heads_all;
+            const unsigned found = __ballot_sync(0xffffffffu, r.first >= at && r.first < at + static_cast<long long>(tiles) * heads_all);
+            r.b = max(__ffs(found) - 1, 0);
+            const int its = __shfl_sync(0xffffffffu, tiles, r.b);
+            const long long in = r.first - static_cast<long long>(__shfl_sync(0xffffffffu, upto, r.b) - its) * heads_all;
+            r.h = static_cast<int>(attend_div(in, its));
+            r.tile = static_cast<int>(in - static_cast<long long>(r.h) * its);
+            r.n = __shfl_sync(0xffffffffu, n, r.b);
+            if (lane == 0) s_run = r;
         }
-        int upto = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += u;
-        }
-        all = static_cast<long long>(__shfl_sync(0xffffffffu, upto, 31)) * heads_all;
-        ctas = static_cast<int>(length > 0 ? attend_div(all, length) : min(static_cast<long long>(runs), all));
-        if (cta >= ctas) return;
-        first = attend_first(cta, ctas, all);
-        last = attend_first(cta + 1, ctas, all);
-        const long long at = static_cast<long long>(upto - tiles) * heads_all;
-        const unsigned found = __ballot_sync(0xffffffffu, first >= at && first < at + static_cast<long long>(tiles) * heads_all);
-        start_b = max(__ffs(found) - 1, 0);
-        const int its = max(__shfl_sync(0xffffffffu, tiles, start_b), 1);
-        const long long in = first - static_cast<long long>(__shfl_sync(0xffffffffu, upto, start_b) - its) * heads_all;
-        start_h = static_cast<int>(attend_div(in, its));
-        start_tile = static_cast<int>(in - static_cast<long long>(start_h) * its);
     } else {
         const int each = (p.table.batch + S::kThreads - 1) / S::kThreads;
         const int b_lo = min(p.table.batch, static_cast<int>(threadIdx.x) * each), b_hi = min(p.table.batch, b_lo + each);
+        bool bad = false;
+        int lo;
         long long mine = 0;
-        for (int b = b_lo; b < b_hi; ++b) {
-            bool bad = false;
-            int lo;
-            const int n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
-            if (bad && blockIdx.x == 0) record_status(p.status, kStatusCache);
-            mine += attend_tiles(n, p.window, S::kTile, 1, &lo);
-        }
+        for (int b = b_lo; b < b_hi; ++b)
+            mine += attend_tiles(kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad), p.window, S::kTile, 1, &lo);
+        if (bad && blockIdx.x == 0) record_status(p.status, kStatusCache);
         long long upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -368,50 +380,54 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
             if (lane >= o) upto += u;
         }
         if (lane == 31) s_sum[warp] = upto;
-        if (threadIdx.x < 3) s_start[threadIdx.x] = 0;
         __syncthreads();
-        all = 0;
+        AttendRun r;
+        r.all = 0;
 #pragma unroll
         for (int w = 0; w < S::kWarps; ++w) {
             if (w < warp) upto += s_sum[w];
-            all += s_sum[w];
+            r.all += s_sum[w];
         }
-        all *= heads_all;
-        ctas = static_cast<int>(min(static_cast<long long>(runs), all));
-        if (cta >= ctas) return;
-        first = attend_first(cta, ctas, all);
-        last = attend_first(cta + 1, ctas, all);
+        r.all *= heads_all;
+        r.pad = 1;
+        r.ctas = static_cast<int>(min(static_cast<long long>(runs), r.all));
+        const int c = min(cta, r.ctas - 1);
+        r.first = attend_first(c, r.ctas, r.all);
+        r.last = attend_first(c + 1, r.ctas, r.all);
+        r.b = r.h = r.tile = r.n = 0;
+        if (threadIdx.x == 0) s_run = r;
+        __syncthreads();
         long long at = (upto - mine) * heads_all;
-        if (first >= at && first < upto * heads_all)
+        if (r.first >= at && r.first < upto * heads_all)
             for (int b = b_lo; b < b_hi; ++b) {
-                bool bad = false;
-                int lo;
                 const int n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
                 const int tiles = attend_tiles(n, p.window, S::kTile, 1, &lo);
-                if (first < at + static_cast<long long>(tiles) * heads_all) {
-                    const long long in = first - at;
-                    s_start[0] = b;
-                    s_start[1] = static_cast<int>(attend_div(in, tiles));
-                    s_start[2] = static_cast<int>(in - static_cast<long long>(s_start[1]) * tiles);
+                if (r.first < at + static_cast<long long>(tiles) * heads_all) {
+                    const long long in = r.first - at;
+                    s_run.b = b;
+                    s_run.h = static_cast<int>(attend_div(in, tiles));
+                    s_run.tile = static_cast<int>(in - static_cast<long long>(s_run.h) * tiles);
+                    s_run.n = n;
                     break;
                 }
                 at += static_cast<long long>(tiles) * heads_all;
             }
-        __syncthreads();
-        start_b = s_start[0];
-        start_h = s_start[1];
-        start_tile = s_start[2];
     }
-    const int steps = static_cast<int>(last - first);
+    __syncthreads();
+    const int ctas = s_run.ctas, pad = s_run.pad;
+    if (cta >= ctas) return;
+    const long long all = s_run.all, first = s_run.first;
+    const int steps = static_cast<int>(s_run.last - first);
 
     // ---- loading: the places of the next step's rows are looked up, then copied
     AttendCursor load;
-    load.b = start_b;
-    const int h_first = p.lanes > 1 ? lane_cta : start_h;
+    load.b = s_run.b;
+    const int h_first = min(p.lanes > 1 ? lane_cta : s_run.h, p.cache.heads * p.blocks - 1);
     load.head = h_first / p.blocks;
     load.block = h_first - load.head * p.blocks;
-    load.tile = start_tile;
-    cursor_load(load, p, S::kTile, pad);
+    load.tile = s_run.tile;
+    load.n = s_run.n;
+    load.tiles = attend_tiles(load.n, p.window, S::kTile, pad, &load.lo);
     AttendCursor use = load;
     int page = -1, slot = 0, load_head = 0;    // lane i: of the step's position i
     unsigned want = 0;                         // positions that there are
@@ -550,6 +566,12 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
     };
     request_q(use);
     begin();
+    // The first thread has the next sequence's length for all warps.
+    auto next_length = [&]() {
+        bool bad = false;
+        return kv_length(p.table.lengths[min(use.b + 1, p.table.batch - 1)], p.table.width, p.cache.page_size, &bad);
+    };
+    int next = threadIdx.x == 0 ? next_length() : 0;
     int stage = 0;
     for (int step = 0; step < steps; ++step) {
         const int head = use.head, h0 = use.block * S::kHeads, hn = min(S::kHeads, p.group - h0);    // the block's heads
@@ -758,11 +780,13 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
             const long long item = first + step - use.tile;      // the item's first tile among all
             const long long item_end = item + use.tiles;
             const bool whole = begun == 0 && ends;
+            bool other = false;                                  // the next item is another sequence's
             if (more) {
-                cursor_next(use, p, S::kTile, pad);
+                other = cursor_item(use, p);
                 request_q(use);
-                begun = use.tile;
+                begun = 0;
             }
+            if (threadIdx.x == 0) s_next = next;
             // ---- join the warps: one reference, then the outputs one warp after the other
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -776,6 +800,11 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                     }
                 }
             __syncthreads();
+            if (other) {
+                use.n = s_next;
+                use.tiles = attend_tiles(use.n, p.window, S::kTile, pad, &use.lo);
+                if (threadIdx.x == 0) next = next_length();
+            }
             float a[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)

@@ -84,4 +84,15 @@ __host__ __device__ inline long long kv_scale_offset(const KvView &c, int page, 
     return page * c.scale_page_stride + slot * c.scale_slot_stride + head * c.scale_head_stride;
 }
 
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ int warp_scan(int v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
 }  // namespace tgemm

@@ -50,17 +50,6 @@ __host__ __device__ inline uint32_t kv_weight_key(uint32_t bits) {
     return (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;
 }
 
-// Inclusive sum over the warp's lanes.
-__device__ __forceinline__ int warp_scan(int v) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
-    return v;
-}
-
 // Grid: (cluster size, heads, batch), a cluster along x.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParams p) {
@@ -70,7 +59,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
     __shared__ int groups[3][kSelectGroups];     // sums of 32 bins
     __shared__ int warp_sums[2][kWarps];
     __shared__ int s_counts[2], s_before[2];     // larger and equal keys: this block's, those of the blocks before
-    __shared__ int s_digit, s_need;
+    __shared__ int s_digit, s_need, s_n;
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
     const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -79,24 +68,29 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
     for (int i = threadIdx.x; i < 3 * kSelectBins; i += kThreads) (&hist[0][0])[i] = 0;
     griddep_wait();
     griddep_launch_dependents();
-    bool bad = false;
-    int n = kv_length(p.table.lengths[b], p.table.width, p.from.page_size, &bad);
-    if (n > p.weights.width) {
-        n = p.weights.width;
-        bad = true;
+    if (threadIdx.x == 0) {
+        bool bad = false;
+        int length = kv_length(p.table.lengths[b], p.table.width, p.from.page_size, &bad);
+        if (length > p.weights.width) {
+            length = p.weights.width;
+            bad = true;
+        }
+        if (bad && rank == 0) record_status(p.status, kStatusCache);
+        s_n = length;
     }
-    if (bad && rank == 0 && threadIdx.x == 0) record_status(p.status, kStatusCache);
-    const int k = min(n, p.keep), r = min(p.recent, k);
+    __syncthreads();                             // the histograms are zero
+    const int n = s_n, k = min(n, p.keep), r = min(p.recent, k);
     const float *w = p.weights.base + b * p.weights.batch_stride + head * p.weights.head_stride;
     float *to_w = p.to_weights.base + b * p.to_weights.batch_stride + head * p.to_weights.head_stride;
     int *kept = p.kept + (static_cast<long long>(b) * p.from.heads + head) * p.keep;
     if (head == 0 && rank == 0 && threadIdx.x == 0) p.to_lengths[b] = k;
     const int first = n - r, best = k - r;       // of the first `first` positions, `best` stay
-    const int slice = (first + blocks - 1) / blocks, lo = min(first, rank * slice), size = min(first, lo + slice) - lo;
+    const int slice = (first + blocks - 1) / blocks, lo = min(first, rank * slice);
     const float *const mine = w + lo;
+    const bool some = best > 0 && best < first;
+    const int size = some ? min(first, lo + slice) - lo : 0;
     const bool cached = size <= p.cached;
     auto key_at = [&](int i) { return cached ? keys[i] : kv_weight_key(__float_as_uint(mine[i])); };
-    const bool some = best > 0 && best < first;  // the same for every block of the cluster
     if (some && cached) {
 #pragma unroll 8
         for (int i = threadIdx.x; i < size; i += kThreads) keys[i] = kv_weight_key(__float_as_uint(mine[i]));
@@ -113,9 +107,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
                 kept[j] = j;
                 to_w[j] = w[j];
             }
-        return;
+        if (blocks == 1) return;
+        // The blocks of a cluster go on together to every barrier, whatever length each of them has read.
     }
-    __syncthreads();                             // the histograms are zero, the keys there
+    __syncthreads();                             // the keys are there
 
     uint32_t prefix = 0;
     int need = best;                             // rank of the limit among the keys with this prefix
@@ -250,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
         const int ties = at_equal + __popc(me & below);
         if (is_larger || (is_equal && ties < need)) {
             const int at = at_larger + __popc(ml & below) + min(ties, need);
-            if (TGEMM_CHECK(at >= 0 && at < p.keep, kChkKvOutput, p.status)) {
+            if (at < p.keep && TGEMM_CHECK(at >= 0 && at < best, kChkKvOutput, p.status)) {
                 kept[at] = lo + i;
                 to_w[at] = mine[i];
             }
@@ -273,7 +268,10 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(const EvictPa
     griddep_launch_dependents();
     const int head = blockIdx.y, b = blockIdx.z;
     const int *kept = p.kept + (static_cast<long long>(b) * p.from.heads + head) * p.keep;
-    const int k = p.to_lengths[b];
+    __shared__ int s_k;
+    if (threadIdx.x == 0) s_k = min(p.to_lengths[b], p.keep);
+    __syncthreads();
+    const int k = s_k;
     const int piece = threadIdx.x % kLanes, in_pass = threadIdx.x / kLanes;
     const bool inside = piece * 16 < p.from.row_bytes;
     for (int i0 = blockIdx.x * kRows; i0 < k; i0 += gridDim.x * kRows) {

@@ -386,7 +386,8 @@ tgemm_status tgemm_kv_append(const tgemm_kv_append_args *args, tgemm_stream_t st
  *   O[b, h] = sum_j p_j V[b, j],  p = softmax of s_j over max(0, n - window) <= j < n,  n = lengths[b],
  *   s_j = scale * Q[b, h] . K[b, j], passed through cap * tanh(s / cap) when cap > 0;
  *
- * window = 0: all positions.  A sequence of length 0 gets zeros.  Rows past n,
+ * window = 0: all positions.  batch * q_heads * (what the page lists can hold)
+ * is at most 2^42.  A sequence of length 0 gets zeros.  Rows past n,
  * NaN and infinity among them, have no influence.  With weights,
  * weights[b, g, j] grows by the sum of p_j over the query heads of group g.
  *

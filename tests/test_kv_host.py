@@ -114,6 +114,7 @@ def test_append_refusals(kw, code):
     (dict(window=-1), INVALID), (dict(ws=0), INVALID), (dict(wsb=16), INVALID), (dict(ws=AT["workspace"] + 8), ALIGN),
     (dict(Q=AT["Q"] + 2), ALIGN), (dict(qb=1028), ALIGN), (dict(oh=68), ALIGN), (dict(oh=56), INVALID), (dict(O=AT["Q"] + 1024), ALIAS),
     (dict(O=AT["k"]), ALIAS), (dict(ws=AT["v"]), ALIAS), (dict(lengths=0), INVALID), (dict(stride=4), INVALID),
+    (dict(batch=65535, width=1 << 20, stride=1 << 20), INVALID), (dict(width=(1 << 26) + 1, stride=1 << 27), INVALID),
 ])
 def test_attention_decode_refusals(kw, code):
     assert attend(**kw) == code
