@@ -237,7 +237,7 @@ int padded_dim(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 // Eights of query heads that a block takes.  Every block copies the rows for
 // itself, so the fewest blocks read fastest (24 heads over 1.2 GB of 16-bit
-// rows: three eights at once 231 us, 16 + 8 302 us), but a block's parts take
+// rows: three eights at once 224 us, 16 + 8 302 us), but a block's parts take
 // longer to join the more heads it has (24 heads, 7 windows of 8192: 34 us
 // against 26): three only where a run has 16 tiles of 64 or more.  256-wide rows leave
 // registers for one eight, and widening e4m3 rows leaves no gain for three.

@@ -112,12 +112,12 @@ template <bool kE4m3, int DP, int NT>
 struct AttendShape {
     static constexpr int kRow = DP * (kE4m3 ? 1 : 2);                     // bytes of a row in shared memory
     static constexpr int kKeys = kRow >= 256 ? 16 : 32;                   // positions of a warp's step
-    static constexpr int kWarps = DP * NT >= 256 && kRow < 512 ? 4 : 6;   // 255 registers a thread, or 168
+    static constexpr int kWarps = (DP * NT >= 192 && kRow < 512) || (kE4m3 && NT == 2) ? 4 : 6;   // 255 registers a thread, or 168
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kStages = kWarps == 4 && NT < 3 ? 3 : kKeys * kRow >= 4096 ? 2 : 4;
     static constexpr int kTile = kWarps * kKeys;
     static constexpr int kHeads = 8 * NT;
     static constexpr int kStage = 2 * kKeys * kRow;                       // keys, values
+    static constexpr int kStages = kRow >= 512 || DP * NT > 256 ? 2 : 98304 / (kWarps * kStage);
     static constexpr int kSide = kE4m3 ? 2 * kKeys * 4 + 16 : 16;         // a stage's scales and mask
     static constexpr int kSides = kWarps * kStages * kStage;              // where the sides begin
     static constexpr int kOffsets = kSides + kWarps * kStages * kSide;    // a step's rows in the pools
@@ -133,6 +133,9 @@ struct AttendShape {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
     const int bytes = ok ? 16 : 0;          // 0: the destination is filled with zeros, nothing is read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool ok) {
     const int bytes = ok ? 4 : 0;
@@ -178,11 +181,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 values (the low 16 bits) as two fp16 ones.
-__device__ __forceinline__ uint32_t widen2(uint32_t x) {
-    uint32_t y;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<unsigned short>(x)));
-    return y;
+// Four e4m3 values as fp16: the lower two and the upper two.
+__device__ __forceinline__ void widen4(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
 }
 
 // Counts up to `last` and from there back to 0; returns the count before.  The
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
     // A lane copies piece `piece` of rows in_copy, in_copy + kRowsPerCopy, ...; the pieces of a row are
     // exchanged by its low bits (xor), so that ldmatrix finds eight rows in different banks.
     const int piece = lane % kChunks, in_copy = lane / kChunks;
-    const bool inside = piece * 16 < p.cache.row_bytes;         // past dim: zeros
+    const bool inside = piece * 16 < p.cache.row_bytes, whole_row = p.cache.row_bytes == S::kRow;     // past dim: zeros
     const unsigned char *const kpool = p.cache.k + (inside ? piece * 16 : 0);
     const unsigned char *const vpool = p.cache.v + (inside ? piece * 16 : 0);
     auto swizzle = [](int row) { return kChunks >= 8 ? (row & 7) : ((row >> 1) & (kChunks - 1)); };
@@ -472,15 +475,24 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
         if (lane == 0) *reinterpret_cast<unsigned *>(side) = ok;
         __syncwarp();
         if (want) {
-            const bool full = inside && ok == kAll;
+            // swizzle(row) of row i * kRowsPerCopy + in_copy is swizzle(in_copy) ^ swizzle(i * kRowsPerCopy)
+            if (ok == kAll && whole_row) {
 #pragma unroll
-            for (int i = 0; i < S::kKeys / kRowsPerCopy; ++i) {
-                const long long o = offsets[i * kRowsPerCopy + in_copy];
-                // swizzle(row) of row i * kRowsPerCopy + in_copy is swizzle(in_copy) ^ swizzle(i * kRowsPerCopy)
-                const uint32_t to = dst + i * kRowsPerCopy * S::kRow + (copy_to ^ (swizzle(i * kRowsPerCopy) << 4));
-                const bool good = full || (inside && o >= 0);
-                cp_async16(to, kpool + (good ? o : 0), good);
-                cp_async16(to + S::kKeys * S::kRow, vpool + (good ? o : 0), good);
+                for (int i = 0; i < S::kKeys / kRowsPerCopy; ++i) {
+                    const long long o = offsets[i * kRowsPerCopy + in_copy];
+                    const uint32_t to = dst + i * kRowsPerCopy * S::kRow + (copy_to ^ (swizzle(i * kRowsPerCopy) << 4));
+                    cp_async16(to, kpool + o);
+                    cp_async16(to + S::kKeys * S::kRow, vpool + o);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < S::kKeys / kRowsPerCopy; ++i) {
+                    const long long o = offsets[i * kRowsPerCopy + in_copy];
+                    const uint32_t to = dst + i * kRowsPerCopy * S::kRow + (copy_to ^ (swizzle(i * kRowsPerCopy) << 4));
+                    const bool good = inside && o >= 0;
+                    cp_async16(to, kpool + (good ? o : 0), good);
+                    cp_async16(to + S::kKeys * S::kRow, vpool + (good ? o : 0), good);
+                }
             }
         }
         cp_async_commit();
@@ -605,8 +617,9 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                         // a[0] / a[1]: rows g / g + 8 of dims 32 c + 4 t4 .. + 3; a[2] / a[3]: of the next 16 dims
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const uint32_t w[4] = {widen2(a[2 * i]), widen2(a[2 * i + 1]), widen2(a[2 * i] >> 16),
-                                                   widen2(a[2 * i + 1] >> 16)};
+                            uint32_t w[4];
+                            widen4(a[2 * i], w[0], w[2]);
+                            widen4(a[2 * i + 1], w[1], w[3]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
                                 mma16816<false>(acc[i % kChains][nt], w, qf[nt][2 * c + i][0], qf[nt][2 * c + i][1]);
@@ -759,8 +772,9 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                         ldmatrix4_trans(a, va + (vx ^ (c << 5)));
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const uint32_t x = __byte_perm(a[2 * i], 0, 0x3120), y = __byte_perm(a[2 * i + 1], 0, 0x3120);
-                            const uint32_t w[4] = {widen2(x), widen2(x >> 16), widen2(y), widen2(y >> 16)};
+                            uint32_t w[4];
+                            widen4(__byte_perm(a[2 * i], 0, 0x3120), w[0], w[1]);
+                            widen4(__byte_perm(a[2 * i + 1], 0, 0x3120), w[2], w[3]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * c + i], w, pf[nt][0], pf[nt][1]);
                         }
