@@ -228,7 +228,9 @@ cudaError_t launch_gather(const EvictParams &p, int64_t most, int heads, int bat
     switch (row_lanes(p.from.row_bytes)) {
         case 8: return launch_gather_lanes<kE4m3, 8>(p, most, heads, batch, s);
         case 16: return launch_gather_lanes<kE4m3, 16>(p, most, heads, batch, s);
-        default: return launch_gather_lanes<kE4m3, 32>(p, most, heads, batch, s);
+        default:                                   // e4m3 rows have 256 bytes at most
+            if constexpr (kE4m3) return cudaErrorInvalidValue;
+            else return launch_gather_lanes<kE4m3, 32>(p, most, heads, batch, s);
     }
 }
 

@@ -245,6 +245,22 @@ def test_attend_one_sequence_split_over_the_gpu(cuda_lib):
     run_attend(cuda_lib, f, 3, with_weights=True)
 
 
+@pytest.mark.parametrize("lengths", [[700, 0, 33], [3000], [50] * 40 + [900]])
+@pytest.mark.parametrize("cache,dtype,group", [("16", "fp16", 1), ("e4m3", "bf16", 3), ("16", "bf16", 12)])
+def test_attend_more_heads_than_share_a_run(cuda_lib, lengths, cache, dtype, group):
+    """So many key heads that every block goes through several of them."""
+    f = Filled(cuda_lib, lengths, 72, 32, 16, dtype, cache, seed=len(lengths))
+    run_attend(cuda_lib, f, 72 * group, with_weights=group == 3)
+    assert cuda_lib.tgemm_last_device_status() == 0
+
+
+def test_attend_many_heads_on_one(cuda_lib):
+    """Blocks of heads beyond three eights, and three eights at once where the work is long."""
+    for group, n in ((33, 300), (48, 5000), (24, 40000), (71, 90)):
+        f = Filled(cuda_lib, [n, 7], 1, 64, 16, "bf16", seed=group)
+        run_attend(cuda_lib, f, group, with_weights=True)
+
+
 def test_attend_large_batch(cuda_lib):
     lengths = [(37 * b) % 150 for b in range(700)]
     f = Filled(cuda_lib, lengths, 2, 64, 16, "bf16", seed=8)
@@ -437,6 +453,29 @@ def test_evict_within_one_pool(cuda_lib):
 @pytest.mark.parametrize("n,keep", [(5000, 1024), (3001, 3000), (9001, 1), (40000, 2048), (70001, 7)])
 def test_evict_long(cuda_lib, n, keep):
     run_evict(cuda_lib, [n], 1, 64, 16, "fp16", "16", keep, min(keep // 2, 100), seed=n)
+
+
+def test_evict_with_room_for_very_long_sequences(cuda_lib):
+    """A page list and weights that could hold more keys than the selection keeps in shared memory: they are read
+    again in each pass."""
+    tg = cuda_lib
+    n, keep, room = 9000, 700, 400016
+    f = Filled(tg, [n, 650], 2, 64, 16, "fp16", seed=22, width=room // 16)
+    w = torch.rand(2, 2, room, generator=torch.Generator().manual_seed(23)).mul(64).floor()
+    to_table, pages = make_table([keep, 650], 16, 0, 3)
+    tk, tv = make_pool(pages, 16, 2, 64, torch.float16, "pshd", "cuda")
+    kept = torch.empty(2, 2, keep, dtype=torch.int32, device="cuda")
+    tl, tw = torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty(2, 2, keep, device="cuda")
+    tg.kv_evict(f.cache, f.table, f.lengths, w.cuda(), tg.PagedCache(tk, tv), to_table.cuda(), kept, tl, tw, recent=50)
+    torch.cuda.synchronize()
+    assert tl.tolist() == [keep, 650] and tg.tgemm_last_device_status() == 0
+    for b, length in enumerate((n, 650)):
+        k = min(length, keep)
+        dst = torch.arange(k)
+        for h in range(2):
+            ref = evict_reference(w[b, h].numpy(), length, keep, 50)
+            assert kept[b, h, :k].tolist() == ref and (kept[b, h, k:] == -1).all()
+            assert torch.equal(tk[to_table[b].long()[dst // 16], dst % 16, h].double().cpu(), f.k64[b][ref, h])
 
 
 @pytest.mark.parametrize("kind", ["equal", "special", "negative", "rising"])
