@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
     __shared__ int groups[3][kSelectGroups];     // sums of 32 bins
     __shared__ int warp_sums[2][kWarps];
     __shared__ int s_counts[2], s_before[2];     // larger and equal keys: this block's, those of the blocks before
-    __shared__ int s_digit, s_need, s_n;
+    __shared__ int s_digit, s_need, s_count, s_n;
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
     const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
     }
     __syncthreads();                             // the keys are there
 
-    uint32_t prefix = 0;
+    uint32_t prefix = 0, counted = ~0u;          // the limit, and its bits that count
     int need = best;                             // rank of the limit among the keys with this prefix
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
                     if (above < need && above + c[i] >= need) {
                         s_digit = low + i;
                         s_need = need - above;
+                        s_count = c[i];
                     }
                     above += c[i];
                 }
@@ -190,6 +191,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
         __syncthreads();
         prefix |= static_cast<uint32_t>(s_digit) << shift;
         need = s_need;
+        // All keys that share these bits stay: the others do not matter.  (Only where no other block waits.)
+        if (blocks == 1 && need == s_count) {
+            counted = ~0u << shift;
+            break;
+        }
     }
 
     // Each warp has a contiguous part of the slice: its larger and equal keys are counted, then written after
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
     int larger = 0, equal = 0;
 #pragma unroll 4
     for (int i = from + lane; i < to; i += 32) {
-        const uint32_t key = key_at(i);
+        const uint32_t key = key_at(i) & counted;
         larger += key > prefix;
         equal += key == prefix;
     }
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
 #pragma unroll 4
     for (int i0 = from; i0 < to; i0 += 32) {
         const int i = i0 + lane;
-        const uint32_t key = i < to ? key_at(i) : 0u;
+        const uint32_t key = i < to ? key_at(i) & counted : 0u;
         const bool is_larger = i < to && key > prefix, is_equal = i < to && key == prefix;
         const unsigned ml = __ballot_sync(0xffffffffu, is_larger), me = __ballot_sync(0xffffffffu, is_equal);
         const int ties = at_equal + __popc(me & below);
