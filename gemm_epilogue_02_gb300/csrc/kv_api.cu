@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -447,9 +448,12 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args
     p.o_head_stride = a->o_head_stride * 2;
     p.window = static_cast<int>(std::min<int64_t>(a->window, INT32_MAX));
     constexpr double kLog2e = 1.4426950408889634;
-    p.capped = a->cap > 0.0;
-    p.first = static_cast<float>(p.capped ? a->scale * 2.0 * kLog2e / a->cap : a->scale * kLog2e);
-    p.last = static_cast<float>(a->cap * kLog2e);
+    // A cap above 2^64 changes no score below 2^52 by fp32's half step; what passes fp32's range is cut to it, so
+    // that a product of 0 keeps a score of 0.
+    p.capped = a->cap > 0.0 && a->cap <= 0x1p64;
+    const double first = p.capped ? a->scale * 2.0 * kLog2e / a->cap : a->scale * kLog2e;
+    p.first = static_cast<float>(std::clamp<double>(first, -FLT_MAX, FLT_MAX));
+    p.last = p.capped ? static_cast<float>(a->cap * kLog2e) : 0.0f;
     p.page_shift = -1;
     for (int i = 0; i <= 20; ++i)
         if (cache->page_size == 1 << i) p.page_shift = i;

@@ -231,6 +231,39 @@ def test_attend_capped(cuda_lib, cap, cache, dtype):
 
 
 @pytest.mark.parametrize("cache,dtype", KINDS)
+@pytest.mark.parametrize("cap", [200.0, 1e4, 1e6, 1e12, 1e19, 1e30, 1e300])
+def test_attend_large_caps(cuda_lib, cap, cache, dtype):
+    """A cap far above the scores leaves them as they are: the error of a capped
+    score goes by the score, not by the cap.  tanh's relative error, in units of
+    2^-24: the series 5 roundings; 1 - 2 / (1 + 2^x) from x = -1/2 or 1/2 on
+    (tanh >= 0.17) 2 for 2^x, 5 q + 1 for the rest with q <= 1.17: at most 48 of tanh."""
+    dim, n = 128, 700
+    f = Filled(cuda_lib, [n], 2, dim, 16, dtype, cache, seed=5, k_gain=3.0)
+    q = (torch.randn(1, 8, dim, generator=torch.Generator().manual_seed(2)) * 3.0).to(TDT[dtype])
+    out, w = torch.empty_like(q, device="cuda"), torch.zeros(1, 2, n, device="cuda")
+    cuda_lib.attention_decode(q.cuda(), f.cache, f.table, f.lengths, out, cap=cap, weights=w)
+    o, p, mag, reach, top = attend64(q[0], f.k64[0], f.v64[0], dim ** -0.5, cap)
+    like = 3 * reach.clamp(max=cap)          # 48 units of the score as 16 of a cap
+    bound = attend_bound(o, mag, reach, top, n, dim, dtype, "fp16" if cache == "e4m3" else dtype, like)
+    assert ((out[0].double().cpu() - o).abs() <= bound).all()
+    add = p.view(2, 4, n).sum(1)
+    e = (2 * score_error(reach, dim, like) + 2 * (n + 64) * 2.0 ** -24).view(2, 4).amax(-1, keepdim=True)
+    assert ((w[0].double().cpu() - add).abs() <= (2.0 ** -22 + 2 * e) * add).all()
+
+
+@pytest.mark.parametrize("cap", [1e-30, 1e-45, 1e-300])
+def test_attend_caps_near_zero(cuda_lib, cap):
+    """Scores that all become 0: the average of the values, with keys that give a score of 0 among them."""
+    f = Filled(cuda_lib, [100], 1, 64, 16, "bf16", seed=8)
+    q = torch.randn(1, 2, 64, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    q[0, 1] = 0
+    out = torch.empty_like(q, device="cuda")
+    cuda_lib.attention_decode(q.cuda(), f.cache, f.table, f.lengths, out, cap=cap)
+    o, p, mag, reach, top = attend64(q[0], f.k64[0], f.v64[0], 0.0)
+    assert ((out[0].double().cpu() - o).abs() <= attend_bound(o, mag, reach, top, 100, 64, "bf16", "bf16", 0.0)).all()
+
+
+@pytest.mark.parametrize("cache,dtype", KINDS)
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 1.0])
 def test_attend_peaked_and_other_scales(cuda_lib, scale, cache, dtype):
     """scale 1 makes scores of a few tens: the softmax is close to one-hot and
