@@ -40,15 +40,18 @@
 // rows of one operand: with 8 heads at most 1/8 of it would be used, and P would
 // have to go through shared or tensor memory, to speed up what is not the bound.)
 // The softmax keeps a running reference m (at first the maximum; moved when
-// exceeded by a factor 2^8, so that the output is rarely rescaled) and the sum
+// that grows by a factor 2^8, so that the output is rarely rescaled) and the sum
 // of the unrounded weights in fp32; P is rounded to the 16-bit type of the
 // product (half a step of 2^-8 or 2^-11, averaged over the positions), as the
-// tensor core takes no wider operand at this rate.
+// tensor core takes no wider operand at this rate.  fp16 rounds what is below
+// 2^-25 to zero: there the reference stays 2^7 below the maximum, so that P
+// uses the range up to 2^15 and only weights below 2^-32 of the largest that the
+// warp has met are lost (the same times for every case measured).
 //
 // e4m3 rows are widened to fp16 exactly.  The row's key scale multiplies its
 // score; its value scale joins the exponent, w_j = 2^(t_j + log2 vs_j - m), and
-// comes off the sum again (w_j / vs_j), so P stays near 1 and in fp16's range
-// whatever the scales are.  bf16 queries enter that product as fp16 after a
+// comes off the sum again (w_j / vs_j), so P stays in fp16's range whatever the
+// scales are.  bf16 queries enter that product as fp16 after a
 // power of two per head has been taken out.
 //
 // Weights.  p_j is known only when the item is joined, so the scores (fp32) go
@@ -67,6 +70,8 @@ constexpr int kAttendFanIn = 32;          // parts joined at once (more: in two 
 static_assert(kAttendMaxCtas <= kAttendFanIn * kAttendFanIn, "two levels join every CTA's part");
 constexpr int kAttendDirect = 8;          // parts that threads join on their own
 constexpr float kAttendGrow = 8.0f;       // log2 of the factor that moves the reference
+constexpr float kAttendBelow = 7.0f;      // log2 of the maximum over the reference that it sets, where P is fp16
+static_assert(kAttendGrow + kAttendBelow <= 15.0f, "P in fp16's range");
 
 // The workspace: arrival counters (zero between calls), the parts' outputs
 // and their (m, l), then, with weights, each head's (m, l) and scores.
@@ -321,6 +326,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
     kv_attend_kernel(const AttendParams p) {
     using S = AttendShape<kE4m3, DP, NT>;
     constexpr bool kMmaBf16 = kBf16 && !kE4m3;      // e4m3 is widened to fp16
+    constexpr float kBelow = kMmaBf16 ? 0.0f : kAttendBelow;
     constexpr int kChunks = S::kRow / 16;           // 16-byte pieces of a row
     constexpr int kRowsPerCopy = 32 / kChunks;      // rows that a warp's copy instruction covers
     constexpr int kBlocks = S::kKeys / 16;
@@ -707,7 +713,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                             for (int nt = 0; nt < NT; ++nt) s[nt][kb][2 * r] = s[nt][kb][2 * r + 1] = -INFINITY;
                         }
             }
-            // the reference moves when some score exceeds it by more than 2^kAttendGrow
+            // the reference moves when some score exceeds the maximum that set it by more than 2^kAttendGrow
             bool grow = false;
             float top[NT][2];
 #pragma unroll
@@ -718,7 +724,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
 #pragma unroll
                     for (int kb = 0; kb < kBlocks; ++kb) x = fmaxf(x, fmaxf(s[nt][kb][i], s[nt][kb][2 + i]));
                     top[nt][i] = x;
-                    grow |= x > m[nt][i] + kAttendGrow;
+                    grow |= x > m[nt][i] + (kAttendGrow + kBelow);
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -729,7 +735,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                         float x = top[nt][i];
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        const float next = fmaxf(m[nt][i], x);
+                        const float next = fmaxf(m[nt][i], x - kBelow);
                         a[i] = next == -INFINITY ? 1.0f : exp2_fast(m[nt][i] - next);
                         m[nt][i] = next;
                         l[nt][i] *= a[i];

@@ -272,6 +272,34 @@ def test_attend_peaked_and_other_scales(cuda_lib, scale, cache, dtype):
     run_attend(cuda_lib, f, 4, scale=scale, q_gain=2.0)
 
 
+@pytest.mark.parametrize("cache,dtype", KINDS)
+def test_attend_long_tail(cuda_lib, cache, dtype):
+    """One position outweighs each other one by about 2^26, and the answer is theirs alone: rounded to fp16 a weight
+    may be off by 2^-25 of what is 1, and the largest weight is at least 2^7.  Rows that one block each takes."""
+    n, dim, batch, heads = 600, 64, 8, 38
+    f = Filled(cuda_lib, [n] * batch, heads, dim, 16, dtype, cache, seed=9)
+    pages = f.table_host[:, 0].long().cuda()
+    if cache == "e4m3":
+        f.k.view(torch.uint8)[pages, 0] = 0x7E     # 448
+        f.ks[pages, 0] = 8.0 / 448.0
+        f.v.view(torch.uint8).fill_(0x38)          # 1
+        f.v.view(torch.uint8)[pages, 0] = 0
+        f.vs.fill_(1.0)
+    else:
+        f.k[pages, 0] = 8.0
+        f.v.fill_(1.0)
+        f.v[pages, 0] = 0.0
+    q, scale = torch.ones(batch, heads, dim, dtype=TDT[dtype]), 26 * 0.6931 / 512
+    out = torch.empty_like(q, device="cuda")
+    cuda_lib.attention_decode(q.cuda(), f.cache, f.table, f.lengths, out, scale=scale)
+    for b in range(batch):
+        f.k64[b][0], f.v64[b][:] = 8.0, 1.0
+        f.v64[b][0] = 0.0
+        o, p, mag, reach, top = attend64(q[b], f.k64[b], f.v64[b], scale)
+        bound = attend_bound(o, mag, reach, top * 2.0 ** -7, n, dim, dtype, "fp16" if cache == "e4m3" else dtype, 0.0)
+        assert ((out[b].double().cpu() - o).abs() <= bound).all()
+
+
 def test_attend_one_sequence_split_over_the_gpu(cuda_lib):
     """One key head: the whole GPU works on one row, joined in two levels."""
     f = Filled(cuda_lib, [50000], 1, 64, 16, "bf16", seed=7)
