@@ -219,8 +219,8 @@ cudaError_t launch_select(const RuntimeInfo &rt, EvictParams &p, int64_t positio
 template <bool kE4m3, int kLanes>
 cudaError_t launch_gather_lanes(const EvictParams &p, int64_t most, int heads, int batch, cudaStream_t s) {
     constexpr int kUnroll = 4, kRows = kGatherThreads / kLanes * kUnroll;
-    const int64_t chunks = std::max<int64_t>(1, (most + kRows - 1) / kRows);
-    const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(heads), static_cast<unsigned>(batch));
+    const int64_t chunks = std::min<int64_t>(65535, std::max<int64_t>(1, (most + kRows - 1) / kRows));
+    const dim3 grid(static_cast<unsigned>(heads * batch), static_cast<unsigned>(chunks));
     return launch(kv_gather_kernel<kE4m3, kLanes, kUnroll>, grid, kGatherThreads, 0, s, p);
 }
 
