@@ -66,7 +66,8 @@
 namespace tgemm {
 
 constexpr int kAttendMaxCtas = 320;       // CTAs at most (workspace slots)
-constexpr int kAttendFanIn = 32;          // parts joined at once (more: in two levels)
+constexpr int kAttendFanIn = 18;          // parts joined at once, at most
+constexpr int kAttendOneLevel = 16;       // parts of an item joined at once (more: in two levels)
 static_assert(kAttendMaxCtas <= kAttendFanIn * kAttendFanIn, "two levels join every CTA's part");
 constexpr int kAttendDirect = 8;          // parts that threads join on their own
 constexpr float kAttendGrow = 8.0f;       // log2 of the factor that moves the reference
@@ -278,6 +279,18 @@ __host__ __device__ inline int attend_owner(long long t, long long ctas, long lo
     // The bounds hold by themselves; lengths that another stream changes meanwhile must not lead out of the slots.
     const long long c = t < 0 ? 0 : attend_div((t + 1) * ctas - 1, total);
     return static_cast<int>(c < ctas ? c : ctas - 1);
+}
+
+// Of more than kAttendOneLevel parts, about as many are joined at once as there
+// are groups of them.  262143 positions, 8 key heads of 8: 159.4 us, 160.8 with 32
+// at once; 7 windows of 8192, 8 heads on one: 15.75, 17.26; 200000 e4m3 positions,
+// 2 key heads: 30.2, 31.7; 2 contexts of 32768: 50.1, 50.9; 4096 positions alone:
+// 13.35, 13.06.  (With this from 8 parts on, 1000 positions alone took 11.6
+// instead of 10.5.)
+__host__ __device__ inline int attend_fan(int parts) {
+    int fan = 1;
+    while (fan * fan < parts) ++fan;
+    return fan;
 }
 
 // The slot of run c's part of an item whose first part is run `first`'s, for the
@@ -884,7 +897,12 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
             if (!whole) {
                 const int c0 = attend_owner(item, ctas, all), c1 = attend_owner(item_end - 1, ctas, all);
                 const int parts = max(c1 - c0 + 1, 1), mine_at = min(max(cta - c0, 0), parts - 1);
-                const int group = mine_at / kAttendFanIn, groups = (parts + kAttendFanIn - 1) / kAttendFanIn;
+                int fan = kAttendFanIn, group = 0, groups = 1;
+                if (parts > kAttendOneLevel) {
+                    fan = attend_fan(parts);
+                    group = mine_at / fan;
+                    groups = (parts + fan - 1) / fan;
+                }
                 auto slot_of = [&](int part) { return attend_slot(c0 + part, c0, lane_cta, p.lanes); };
                 auto put = [&](int to) {
                     if (!TGEMM_CHECK(to >= 0 && to < 2 * kAttendMaxCtas, kChkKvSpace, p.status)) return;
@@ -1012,14 +1030,14 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                     __syncthreads();
                 };
                 put(slot_of(mine_at));
-                const int part0 = group * kAttendFanIn, count = min(kAttendFanIn, parts - part0);
+                const int part0 = group * fan, count = min(fan, parts - part0);
                 bool here = arrive(p.space.parts + slot_of(part0), count);
                 if (here) {
                     join(part0, 1, count);
                     if (groups > 1) {
                         put(slot_of(part0));
                         here = arrive(p.space.groups + slot_of(0), groups);
-                        if (here) join(0, kAttendFanIn, groups);
+                        if (here) join(0, fan, groups);
                     }
                 }
                 answer = here;
