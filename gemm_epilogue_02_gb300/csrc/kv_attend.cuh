@@ -970,8 +970,11 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                         return;
                     }
                     // Each warp sums every kWarps-th part, two parts' loads in flight, then the warps' sums are
-                    // added in a fixed order as above; up to eight float4s of a lane at a time.
-                    constexpr int kAllOfLane = S::kHeads * DP / 4 / 32, kEach = kAllOfLane < 8 ? kAllOfLane : 8;
+                    // added in a fixed order as above; up to eight float4s of a lane at a time (a divisor of all:
+                    // merge ends with the last).
+                    constexpr int kAllOfLane = S::kHeads * DP / 4 / 32;
+                    constexpr int kEach = kAllOfLane < 8 ? kAllOfLane : kAllOfLane % 8 == 0 ? 8 : 6;
+                    static_assert(kAllOfLane * 128 == S::kHeads * DP && kAllOfLane % kEach == 0, "whole turns");
 #pragma unroll 1
                     for (int c0 = 0; c0 < kAllOfLane && c0 * 128 < hn * DP; c0 += kEach) {
                         float4 sum[kEach] = {};

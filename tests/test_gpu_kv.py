@@ -322,6 +322,16 @@ def test_attend_many_heads_on_one(cuda_lib):
         run_attend(cuda_lib, f, group, with_weights=True)
 
 
+@pytest.mark.parametrize("cache,dtype", KINDS)
+@pytest.mark.parametrize("dim", [64, 80, 96, 128])
+@pytest.mark.parametrize("group,width", [(9, 2000), (12, 4000), (16, 2000), (17, 2000), (24, 2000), (24, 4000), (33, 4000), (39, 4000)])
+def test_attend_several_eights_of_heads(cuda_lib, group, width, dim, cache, dtype):
+    """Page lists that could hold long contexts: a block takes two or three eights of heads."""
+    f = Filled(cuda_lib, [1, 77, 1500], 2, dim, 16, dtype, cache, seed=dim + group, width=width)
+    run_attend(cuda_lib, f, 2 * group, with_weights=group in (9, 24), cap=30.0 if group == 16 else 0.0)
+    assert cuda_lib.tgemm_last_device_status() == 0
+
+
 def test_attend_large_batch(cuda_lib):
     lengths = [(37 * b) % 150 for b in range(700)]
     f = Filled(cuda_lib, lengths, 2, 64, 16, "bf16", seed=8)
