@@ -238,15 +238,21 @@ cudaError_t launch_gather(const EvictParams &p, int64_t most, int heads, int bat
 // ---------------------------------------------------------------- attention
 int padded_dim(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-// Eights of query heads that a block takes.  Every block copies the rows for
-// itself, so the fewest blocks read fastest (24 heads over 1.2 GB of 16-bit
-// rows: three eights at once 224 us, 16 + 8 302 us), but a block's parts take
-// longer to join the more heads it has (24 heads, 7 windows of 8192: 34 us
-// against 26): three only where a run has 16 tiles of 64 or more.  256-wide rows leave
-// registers for one eight, and widening e4m3 rows leaves no gain for three.
+// Eights of query heads that a block takes, by the tiles of 64 positions that
+// there can be for each of two blocks an SM.  Every block copies the rows for
+// itself, so where the copies bound it the fewest blocks are best: three eights
+// at once from 16 tiles on (24 heads over 1.2 GB of 16-bit rows: 224 us, 16 + 8
+// 302 us).  But a block of one eight has more warps, shorter steps and less to
+// join, and below 6 tiles that counts more (24 heads, 7 windows of 8192: one 19.3
+// us, two 23.1, three 34; 16 heads, 16 contexts of 300 with 4 key heads: one 11.6,
+// two 13.6; with 2 tiles, 16000 e4m3 positions alone, 15.7 and 19.6; with 7, 16
+// contexts of 2000: 12 heads 23.0 and 19.9, 24 heads 29.9 and 28.8).  256-wide
+// rows leave registers for one eight, and widening e4m3 rows leaves no gain for
+// three.
 int head_tiles(int64_t group, int64_t dim, bool e4m3, int64_t batch, int64_t heads, int64_t positions, int num_sms) {
-    if (group <= 8 || dim > 128) return 1;
-    if (e4m3 || group <= 16 || batch * heads * (positions / 64) < int64_t(16) * 2 * num_sms) return 2;
+    const int64_t tiles = batch * heads * (positions / 64), places = 2 * num_sms;
+    if (group <= 8 || dim > 128 || tiles < 6 * places) return 1;
+    if (e4m3 || group <= 16 || tiles < 16 * places) return 2;
     const int64_t eights = (group + 7) / 8;
     return (eights + 2) / 3 < (eights + 1) / 2 ? 3 : 2;
 }
