@@ -138,8 +138,9 @@ bool all_device(int device, std::initializer_list<const void *> ps) {
 }
 
 // A programmatic dependent of the stream's previous kernel: every kernel here
-// waits for it (griddepcontrol.wait) before it touches global memory.
-// cluster: blocks along x that form a cluster (1: none).
+// waits for it (griddepcontrol.wait) before it touches global memory, also what
+// an earlier kernel than the previous has written: only this wait makes earlier
+// writes visible.  cluster: blocks along x that form a cluster (1: none).
 template <typename P>
 cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P &p, int cluster = 1) {
     cudaLaunchConfig_t lc;

@@ -1075,16 +1075,12 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
 // weights[b, head, j] += sum over the group of 2^(t_j - m) / l.  A position's
 // scores lie together; a thread adds for kSpreadEach positions, kSpreadThreads
 // apart, whose first eight heads it requests together.
-//
-// Lengths, page lists and the weights so far are read before the wait for
-// kv_attend_kernel: its blocks have waited for what came before them by the time
-// this kernel can begin, and it writes none of them (16 contexts up to 16384, 8
-// key heads, 64 query heads: both kernels 66.0 us, 67.6 with the wait first).
 constexpr int kSpreadThreads = 128, kSpreadEach = 4;
 
 __global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendParams p) {
     constexpr int kPairs = 4;             // of heads, per request
     const int head = blockIdx.y, b = blockIdx.z;
+    griddep_wait();
     bool bad = false;
     int n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
     int lo;
@@ -1113,7 +1109,6 @@ __global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendP
             int page, slot;
             is[e] = kv_row(list, at[e], p.cache.page_size, p.cache.pages, &page, &slot) && is[e];   // else it has no score
         }
-        griddep_wait();
         for (int h0 = 0; h0 < p.group; h0 += 2 * kPairs) {
             float2 t[kSpreadEach][kPairs], ml[2 * kPairs];
 #pragma unroll
@@ -1148,7 +1143,6 @@ __global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendP
         for (int e = 0; e < kSpreadEach; ++e)
             if (is[e]) w[at[e]] = old[e] + sum[e];
     }
-    griddep_wait();                       // also where there was nothing to add: this kernel ends after the other
 }
 
 }  // namespace tgemm

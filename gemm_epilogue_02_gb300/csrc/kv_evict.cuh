@@ -263,13 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
 
 // Copying the kept rows: as in kv_append_kernel a block first finds the places
 // of a chunk of rows and then streams them, keys and values, all requested
-// before the first is stored.  The rows that stay whatever the weights are (the
-// recent ones, and all of a sequence that loses none) come first and do not wait
-// for the selection: its blocks have waited for what came before them by the
-// time this kernel can begin, and it writes neither lengths nor page lists nor
-// rows (16 sequences up to 8192 to 2048: 54 us, 60 when all wait and a sequence's
-// chunks follow one another).  Grid: (heads * batch, chunks at most), the last
-// chunk first.
+// before the first is stored.  Grid: (heads * batch, chunks at most).
 constexpr int kGatherThreads = 256;
 
 template <bool kE4m3, int kLanes, int kUnroll>
@@ -279,6 +273,7 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(const EvictPa
     __shared__ int s_n;
     const int b = static_cast<int>(blockIdx.x) / p.from.heads, head = static_cast<int>(blockIdx.x) - b * p.from.heads;
     const int *kept = p.kept + (static_cast<long long>(b) * p.from.heads + head) * p.keep;
+    griddep_wait();
     if (threadIdx.x == 0) {
         bool bad = false;
         s_n = min(kv_length(p.table.lengths[b], p.table.width, p.from.page_size, &bad), p.weights.width);
@@ -287,9 +282,8 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(const EvictPa
     const int n = s_n, k = min(n, p.keep), best = k - min(p.recent, k), shift = n - k;
     const int piece = threadIdx.x % kLanes, in_pass = threadIdx.x / kLanes;
     const bool inside = piece * 16 < p.from.row_bytes;
-    for (int chunk = (k + kRows - 1) / kRows - 1 - static_cast<int>(blockIdx.y); chunk >= 0; chunk -= static_cast<int>(gridDim.y)) {
-        const int i0 = chunk * kRows, row = i0 + static_cast<int>(threadIdx.x);
-        if (shift > 0 && i0 < best) griddep_wait();
+    for (int i0 = static_cast<int>(blockIdx.y) * kRows; i0 < k; i0 += static_cast<int>(gridDim.y) * kRows) {
+        const int row = i0 + static_cast<int>(threadIdx.x);
         if (threadIdx.x < kRows) {
             long long src = 0, dst = -1;
             if (row < k) {
@@ -337,7 +331,6 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(const EvictPa
         }
         __syncthreads();
     }
-    griddep_wait();                              // also where nothing waited: this kernel ends after the selection
 }
 
 }  // namespace tgemm
