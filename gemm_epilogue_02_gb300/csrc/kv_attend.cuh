@@ -49,10 +49,12 @@
 // warp has met are lost (the same times for every case measured).
 //
 // e4m3 rows are widened to fp16 exactly.  The row's key scale multiplies its
-// score; its value scale joins the exponent, w_j = 2^(t_j + log2 vs_j - m), and
-// comes off the sum again (w_j / vs_j), so P stays in fp16's range whatever the
-// scales are.  bf16 queries enter that product as fp16 after a
-// power of two per head has been taken out.
+// score.  Its value scale vs_j = f 2^e, 1 <= f < 2, joins the weight that
+// multiplies the row, f 2^(t_j + e - mu), with a reference mu of its own that
+// follows the largest t_j + e: P stays in fp16's range whatever the scales are
+// (any that fp32 holds), and the sum, 2^(t_j - m), does not know of them.  The
+// outputs change to the reference m when the warps are joined.  bf16 queries
+// enter the first product as fp16 after a power of two per head has been taken out.
 //
 // Weights.  p_j is known only when the item is joined, so the scores (fp32) go
 // to the workspace and a second kernel adds 2^(t_j - m) / sum over the group.
@@ -72,6 +74,7 @@ static_assert(kAttendMaxCtas <= kAttendFanIn * kAttendFanIn, "two levels join ev
 constexpr int kAttendDirect = 8;          // parts that threads join on their own
 constexpr float kAttendGrow = 8.0f;       // log2 of the factor that moves the reference
 constexpr float kAttendBelow = 7.0f;      // log2 of the maximum over the reference that it sets, where P is fp16
+constexpr float kAttendScaledBelow = kAttendBelow - 1.0f;     // where a factor f < 2 multiplies P
 static_assert(kAttendGrow + kAttendBelow <= 15.0f, "P in fp16's range");
 
 // The workspace: arrival counters (zero between calls), the parts' outputs
@@ -225,6 +228,16 @@ __device__ __forceinline__ float tanh2(float x) {
     return x2 < 0.25f ? series : far;
 }
 
+// x = f * 2^e, 1 <= |f| < 2; e = -infinity for 0; an infinity or NaN is its own f.
+__device__ __forceinline__ void split_scale(float x, float &e, float &f) {
+    const bool small = fabsf(x) < 0x1p-126f;
+    const float y = small ? x * 0x1p32f : x;
+    const uint32_t bits = __float_as_uint(y);
+    const int field = static_cast<int>((bits >> 23) & 255u);
+    e = field == 0 ? -INFINITY : static_cast<float>(field - (small ? 159 : 127));
+    f = field == 255 ? x : __uint_as_float((bits & 0x807FFFFFu) | 0x3F800000u);
+}
+
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pair16(float lo, float hi) {
     if (kBf16) {
@@ -339,7 +352,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
     kv_attend_kernel(const AttendParams p) {
     using S = AttendShape<kE4m3, DP, NT>;
     constexpr bool kMmaBf16 = kBf16 && !kE4m3;      // e4m3 is widened to fp16
-    constexpr float kBelow = kMmaBf16 ? 0.0f : kAttendBelow;
+    constexpr float kBelow = kBf16 || kE4m3 ? 0.0f : kAttendBelow;
     constexpr int kChunks = S::kRow / 16;           // 16-byte pieces of a row
     constexpr int kRowsPerCopy = 32 / kChunks;      // rows that a warp's copy instruction covers
     constexpr int kBlocks = S::kKeys / 16;
@@ -551,6 +564,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
     uint32_t qf[NT][DP / 16][2];
     float qscale[NT][2];                   // to log2 units, for heads 2 t4 and 2 t4 + 1
     float o[NT][DP / 16][4], m[NT][2], l[NT][2];
+    float mu[NT][2];                       // e4m3: the outputs' own reference
     int begun = use.tile;                  // first tile of this CTA's part
     // The item's queries are requested (request_q) as soon as the previous item's last product is done,
     // and made ready (begin) after it is joined.
@@ -601,7 +615,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 qscale[nt][i] = p.first * __shfl_sync(0xffffffffu, unit, (2 * t4 + i) * 4);
-                m[nt][i] = -INFINITY;
+                m[nt][i] = mu[nt][i] = -INFINITY;
                 l[nt][i] = 0.0f;
             }
 #pragma unroll
@@ -666,21 +680,17 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                     for (int i = 0; i < 4; ++i)
                         s[nt][kb][i] = kChains == 2 ? acc[0][nt][i] + acc[kChains - 1][nt][i] : acc[0][nt][i];
             }
-            // scores in log2 units; the value scales join the exponent
-            float lv[kBlocks][2], inv[kBlocks][2];
+            // scores in log2 units; the value scales
+            float ve[kBlocks][2], vf[kBlocks][2];
             const float *scales = reinterpret_cast<const float *>(side + 16);
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     float ks = 1.0f;
-                    if (kE4m3) {
-                        // (a scale of 0 stands for values of 0, whatever their weight; rows left out have it too)
+                    if (kE4m3) {                 // (rows left out have scales of 0)
                         ks = scales[16 * kb + g + 8 * r];
-                        float vs = scales[S::kKeys + 16 * kb + g + 8 * r];
-                        vs = vs < 0x1p-100f ? 0x1p-100f : vs;
-                        lv[kb][r] = __log2f(vs);
-                        inv[kb][r] = __fdividef(1.0f, vs);
+                        split_scale(scales[S::kKeys + 16 * kb + g + 8 * r], ve[kb][r], vf[kb][r]);
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -708,14 +718,6 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                                     make_float2(s[nt][kb][2 * r], s[nt][kb][2 * r + 1]);
                         }
             }
-            if (kE4m3) {
-#pragma unroll
-                for (int kb = 0; kb < kBlocks; ++kb)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s[nt][kb][i] += lv[kb][i >> 1];
-            }
             if (mask != kAll) {
 #pragma unroll
                 for (int kb = 0; kb < kBlocks; ++kb)
@@ -726,18 +728,23 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                             for (int nt = 0; nt < NT; ++nt) s[nt][kb][2 * r] = s[nt][kb][2 * r + 1] = -INFINITY;
                         }
             }
-            // the reference moves when some score exceeds the maximum that set it by more than 2^kAttendGrow
+            // a reference moves when some score exceeds the maximum that set it by more than 2^kAttendGrow
             bool grow = false;
-            float top[NT][2];
+            float top[NT][2], top_u[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float x = -INFINITY;
+                    float x = -INFINITY, u = -INFINITY;
 #pragma unroll
-                    for (int kb = 0; kb < kBlocks; ++kb) x = fmaxf(x, fmaxf(s[nt][kb][i], s[nt][kb][2 + i]));
+                    for (int kb = 0; kb < kBlocks; ++kb) {
+                        x = fmaxf(x, fmaxf(s[nt][kb][i], s[nt][kb][2 + i]));
+                        if (kE4m3) u = fmaxf(u, fmaxf(s[nt][kb][i] + ve[kb][0], s[nt][kb][2 + i] + ve[kb][1]));
+                    }
                     top[nt][i] = x;
+                    top_u[nt][i] = u;
                     grow |= x > m[nt][i] + (kAttendGrow + kBelow);
+                    if (kE4m3) grow |= u > mu[nt][i] + (kAttendGrow + kAttendScaledBelow);
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -745,13 +752,21 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                     float a[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float x = top[nt][i];
+                        float x = top[nt][i], u = top_u[nt][i];
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        for (int d = 4; d < 32; d <<= 1) {
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                            if (kE4m3) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
+                        }
                         const float next = fmaxf(m[nt][i], x - kBelow);
                         a[i] = next == -INFINITY ? 1.0f : exp2_fast(m[nt][i] - next);
                         m[nt][i] = next;
                         l[nt][i] *= a[i];
+                        if (kE4m3) {
+                            const float next_u = fmaxf(mu[nt][i], u - kAttendScaledBelow);
+                            a[i] = next_u == -INFINITY ? 1.0f : exp2_fast(mu[nt][i] - next_u);
+                            mu[nt][i] = next_u;
+                        }
                     }
 #pragma unroll
                     for (int mt = 0; mt < DP / 16; ++mt) {
@@ -763,11 +778,14 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                 }
             }
             // weights, their sum, and O^T += V^T P^T
-            float ref[NT][2];
+            float ref[NT][2], ref_u[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) ref[nt][i] = m[nt][i] == -INFINITY ? 0.0f : m[nt][i];
+                for (int i = 0; i < 2; ++i) {
+                    ref[nt][i] = m[nt][i] == -INFINITY ? 0.0f : m[nt][i];
+                    ref_u[nt][i] = mu[nt][i] == -INFINITY ? 0.0f : mu[nt][i];
+                }
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb) {
                 uint32_t pf[NT][2];
@@ -778,8 +796,10 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                         float w[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            w[i] = exp2_fast(s[nt][kb][2 * r + i] - ref[nt][i]);
-                            l[nt][i] += kE4m3 ? w[i] * inv[kb][r] : w[i];
+                            const float t = s[nt][kb][2 * r + i];
+                            w[i] = exp2_fast(t - ref[nt][i]);
+                            l[nt][i] += w[i];
+                            if (kE4m3) w[i] = exp2_fast((t + ve[kb][r]) - ref_u[nt][i]) * vf[kb][r];
                         }
                         pf[nt][r] = movmatrix_trans(pair16<kMmaBf16>(w[0], w[1]));
                     }
@@ -865,7 +885,8 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                     const float base = ref == -INFINITY ? 0.0f : ref;
 #pragma unroll
                     for (int w = 0; w < S::kWarps; ++w) sum += s_l[w][h] * exp2_fast(s_m[w][h] - base);
-                    a[nt][i] = exp2_fast(m[nt][i] - base);
+                    // (e4m3: the root of the factor, which fp32 holds whatever the scales are)
+                    a[nt][i] = kE4m3 ? exp2_fast(0.5f * (mu[nt][i] - base)) : exp2_fast(m[nt][i] - base);
                     if (warp == 0 && g == 0) {
                         s_ref[h] = ref;
                         s_inv[h] = sum;
@@ -885,7 +906,8 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                             for (int i = 0; i < 4; ++i) {
                                 const int d = 16 * mt + (kE4m3 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
                                 float *at = merge + (8 * nt + 2 * t4 + (i & 1)) * S::kPitch + d;
-                                const float x = o[nt][mt][i] * a[nt][i & 1];
+                                float x = o[nt][mt][i] * a[nt][i & 1];
+                                if (kE4m3) x *= a[nt][i & 1];
                                 *at = round == 0 ? x : *at + x;
                             }
                     }
