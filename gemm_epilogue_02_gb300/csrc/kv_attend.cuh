@@ -51,9 +51,10 @@
 // e4m3 rows are widened to fp16 exactly.  The row's key scale multiplies its
 // score.  Its value scale vs_j = f 2^e, 1 <= f < 2, joins the weight that
 // multiplies the row, f 2^(t_j + e - mu), with a reference mu of its own that
-// follows the largest t_j + e: P stays in fp16's range whatever the scales are
-// (any that fp32 holds), and the sum, 2^(t_j - m), does not know of them.  The
-// outputs change to the reference m when the warps are joined.  bf16 queries
+// follows the largest t_j + e of the rows that are not all zeros: P stays in
+// fp16's range whatever the scales are (any that fp32 holds), what is lost is
+// below 2^-31 of the largest weight times scale of these rows that the warp has
+// met, and the sum, 2^(t_j - m), does not know of the scales.  The outputs change to the reference m when the warps are joined.  bf16 queries
 // enter the first product as fp16 after a power of two per head has been taken out.
 //
 // Weights.  p_j is known only when the item is joined, so the scores (fp32) go
@@ -166,6 +167,12 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
+}
+// The bits that any of four words in shared memory has.
+__device__ __forceinline__ uint32_t lds_or(uint32_t addr) {
+    uint32_t a, b, c, d;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+    return a | b | c | d;
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t y;
@@ -747,6 +754,32 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                     if (kE4m3) grow |= u > mu[nt][i] + (kAttendGrow + kAttendScaledBelow);
                 }
             if (__any_sync(0xffffffffu, grow)) {
+                if constexpr (kE4m3) {
+                    // A row of zeros (kv_append gives it a scale of 1) adds nothing whatever its weight, so it sets no
+                    // reference: it counts as one with a scale of 0.  Its four lanes look at a quarter each.
+#pragma unroll
+                    for (int kb = 0; kb < kBlocks; ++kb)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const uint32_t at = src + (S::kKeys + 16 * kb + g + 8 * r) * S::kRow + t4 * (S::kRow / 4);
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int c = 0; c < S::kRow / 64; ++c) any |= lds_or(at + 16 * c);
+                            any |= __shfl_xor_sync(0xffffffffu, any, 1);
+                            any |= __shfl_xor_sync(0xffffffffu, any, 2);
+                            if ((any & 0x7F7F7F7Fu) == 0u) ve[kb][r] = -INFINITY;
+                        }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float u = -INFINITY;
+#pragma unroll
+                            for (int kb = 0; kb < kBlocks; ++kb)
+                                u = fmaxf(u, fmaxf(s[nt][kb][i] + ve[kb][0], s[nt][kb][2 + i] + ve[kb][1]));
+                            top_u[nt][i] = u;
+                        }
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float a[2];

@@ -120,3 +120,36 @@ def test_scales_that_are_nothing_or_nearly(cuda_lib, value):
         c["v64"].append(elements * value)
         c["vs"].append(torch.full((n, 2), value, dtype=torch.float64))
     check(tg, c, rows(2, 4, 64, "bf16", 4), "bf16", 0.125)
+
+
+@pytest.mark.parametrize("dtype,value", [("bf16", 1.0), ("bf16", 1e-3), ("bf16", 1e-6), ("bf16", 1e-7), ("bf16", 1e-30), ("fp16", 1.0),
+                                         ("fp16", 2e-4)])
+@pytest.mark.parametrize("ahead", [0.0, 14.4, 26.0, 60.0])
+@pytest.mark.parametrize("zero", [0.0, -0.0])
+def test_one_row_of_zeros_beside_small_values(cuda_lib, zero, ahead, dtype, value):
+    """A row of zeros, 2^ahead times as heavy as each other row, adds nothing and costs the others no precision: one
+    key head that the whole GPU shares, and many that one block each takes."""
+    dim = 64
+    for batch, n, heads in ((1, 600, 1), (1, 9000, 1), (8, 300, 38), (2, 2, 1)):
+        K, V = [], []
+        for b in range(batch):
+            k, v = torch.zeros(n, heads, dim), rows(n, heads, dim, dtype, b + n, 1.0).float().abs().clamp(0.25, 2.0) * value
+            at = (n // 3) * (b % 3)
+            k[at] = 1.0
+            v[at] = zero
+            K.append(k.to(TDT[dtype]))
+            V.append(v.to(TDT[dtype]))
+        c = appended(cuda_lib, K, V)
+        assert (torch.cat(c["vs"]) == 1).any()
+        check(cuda_lib, c, torch.ones(batch, heads * 2, dim, dtype=TDT[dtype]), dtype, ahead * 0.6931471805599453 / dim)
+
+
+@pytest.mark.parametrize("dim,group", [(64, 3), (80, 16), (128, 8), (256, 4)])
+def test_rows_of_zeros_everywhere(cuda_lib, dim, group):
+    """Every third row zero, and a sequence of nothing else."""
+    n = [900, 50, 1]
+    K, V = [rows(i, 2, dim, "bf16", i, 3.0) for i in n], [rows(i, 2, dim, "bf16", i + 1, 1e-4) for i in n]
+    V[0][::3] = 0
+    V[1][:] = 0
+    c = appended(cuda_lib, K, V)
+    check(cuda_lib, c, rows(3, 2 * group, dim, "bf16", 5, 3.0), "bf16", dim ** -0.5)
