@@ -41,9 +41,8 @@
 // have to go through shared or tensor memory, to speed up what is not the bound.)
 // The softmax keeps a running reference m (at first the maximum; moved when
 // that grows by a factor 2^8, so that the output is rarely rescaled) and the sum
-// of the unrounded weights in fp32; P is rounded to the 16-bit type of the
-// product (half a step of 2^-8 or 2^-11, averaged over the positions), as the
-// tensor core takes no wider operand at this rate.  fp16 rounds what is below
+// of the weights in fp32.  The tensor core takes no wider operand than 16 bits at
+// this rate, so P goes in as two of them (split16).  fp16 rounds what is below
 // 2^-25 to zero: there the reference stays 2^7 below the maximum, so that P
 // uses the range up to 2^15 and only weights below 2^-32 of the largest that the
 // warp has met are lost (the same times for every case measured).
@@ -54,8 +53,9 @@
 // follows the largest t_j + e of the rows that are not all zeros: P stays in
 // fp16's range whatever the scales are (any that fp32 holds), what is lost is
 // below 2^-31 of the largest weight times scale of these rows that the warp has
-// met, and the sum, 2^(t_j - m), does not know of the scales.  The outputs change to the reference m when the warps are joined.  bf16 queries
-// enter the first product as fp16 after a power of two per head has been taken out.
+// met, and the sum, 2^(t_j - m), does not know of the scales.  The outputs change
+// to the reference m when the warps are joined.  bf16 queries enter the first
+// product as fp16 after a power of two per head has been taken out.
 //
 // Weights.  p_j is known only when the item is joined, so the scores (fp32) go
 // to the workspace and a second kernel adds 2^(t_j - m) / sum over the group.
@@ -253,6 +253,26 @@ __device__ __forceinline__ uint32_t pair16(float lo, float hi) {
     }
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Two weights w >= 0 as sums of 16-bit values: `high` towards zero, and what that
+// leaves, rounded: off by at most 2^-16 of w (bf16), 2^-21 or 2^-25 absolutely
+// (fp16).  Neither is 0 where w is not tiny, nor negative, so that an infinity
+// among the values stays one: for bf16 w's last bit is set before (2^-23 of it),
+// for fp16 `high` is taken of a little less.
+template <bool kBf16>
+__device__ __forceinline__ void split16(float w0, float w1, uint32_t &high, uint32_t &rest) {
+    if (kBf16) {
+        const uint32_t a = __float_as_uint(w0) | 1u, b = __float_as_uint(w1) | 1u;
+        high = __byte_perm(a, b, 0x7632);
+        rest = pair16<true>(__uint_as_float(a) - __uint_as_float(a & 0xFFFF0000u),
+                            __uint_as_float(b) - __uint_as_float(b & 0xFFFF0000u));
+    } else {
+        constexpr float kLess = 1.0f - 0x1p-12f, kStep = 0x1.fffffep-25f;      // just below fp16's smallest step
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(high) : "f"(fmaf(w1, kLess, -kStep)), "f"(fmaf(w0, kLess, -kStep)));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&high));
+        rest = pair16<false>(w0 - f.x, w1 - f.y);
+    }
 }
 
 // ---------------------------------------------------------------- the runs
@@ -821,7 +841,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                 }
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb) {
-                uint32_t pf[NT][2];
+                uint32_t pf[NT][2], pr[NT][2];           // high parts, and the rest
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -834,7 +854,10 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                             l[nt][i] += w[i];
                             if (kE4m3) w[i] = exp2_fast((t + ve[kb][r]) - ref_u[nt][i]) * vf[kb][r];
                         }
-                        pf[nt][r] = movmatrix_trans(pair16<kMmaBf16>(w[0], w[1]));
+                        uint32_t high, rest;
+                        split16<kMmaBf16>(w[0], w[1], high, rest);
+                        pf[nt][r] = movmatrix_trans(high);
+                        pr[nt][r] = movmatrix_trans(rest);
                     }
                 }
                 if (!kE4m3) {
@@ -842,11 +865,17 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                     const int row = (lane & 7) + (lane >> 4) * 8;
                     const uint32_t va = src + (S::kKeys + 16 * kb + row) * S::kRow, vx = (((lane >> 3) & 1) ^ swizzle(row)) << 4;
 #pragma unroll
-                    for (int mt = 0; mt < DP / 16; ++mt) {
-                        uint32_t a[4];
+                    for (int mt = 0; mt < DP / 16; mt += 2) {
+                        uint32_t a[4], b[4];
                         ldmatrix4_trans(a, va + (vx ^ (mt << 5)));
+                        ldmatrix4_trans(b, va + (vx ^ ((mt + 1) << 5)));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816<kMmaBf16>(o[nt][mt], a, pf[nt][0], pf[nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816<kMmaBf16>(o[nt][mt], a, pf[nt][0], pf[nt][1]);
+                            mma16816<kMmaBf16>(o[nt][mt + 1], b, pf[nt][0], pf[nt][1]);
+                            mma16816<kMmaBf16>(o[nt][mt], a, pr[nt][0], pr[nt][1]);
+                            mma16816<kMmaBf16>(o[nt][mt + 1], b, pr[nt][0], pr[nt][1]);
+                        }
                     }
                 } else {
                     // matrices of byte pairs: (positions 0-7 | 8-15: bit 3) x (dims 0-15 | 16-31: bit 4); a
@@ -857,14 +886,18 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                     for (int c = 0; c < DP / 32; ++c) {
                         uint32_t a[4];
                         ldmatrix4_trans(a, va + (vx ^ (c << 5)));
+                        uint32_t w[2][4];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            uint32_t w[4];
-                            widen4(__byte_perm(a[2 * i], 0, 0x3120), w[0], w[1]);
-                            widen4(__byte_perm(a[2 * i + 1], 0, 0x3120), w[2], w[3]);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * c + i], w, pf[nt][0], pf[nt][1]);
+                            widen4(__byte_perm(a[2 * i], 0, 0x3120), w[i][0], w[i][1]);
+                            widen4(__byte_perm(a[2 * i + 1], 0, 0x3120), w[i][2], w[i][3]);
                         }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma16816<false>(o[nt][2 * c + (i & 1)], w[i & 1], i < 2 ? pf[nt][0] : pr[nt][0],
+                                                i < 2 ? pf[nt][1] : pr[nt][1]);
                     }
                 }
             }

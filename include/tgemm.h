@@ -392,9 +392,12 @@ tgemm_status tgemm_kv_append(const tgemm_kv_append_args *args, tgemm_stream_t st
  * weights[b, g, j] grows by the sum of p_j over the query heads of group g.
  *
  * Arithmetic: products of 16-bit values (e4m3 elements are widened exactly)
- * accumulated in fp32; softmax in fp32 with a running maximum, its weights
- * rounded to the 16-bit type (fp16 for an e4m3 cache) before they multiply V;
- * each output rounded once to dtype.
+ * accumulated in fp32; softmax in fp32 with a running maximum, each weight
+ * multiplying V as the sum of two 16-bit values (off by at most 2^-16 of itself
+ * with bf16 keys and values, 2^-21 with fp16 and e4m3); each output rounded once
+ * to dtype.  With fp16 keys and values weights below 2^-32 of the largest are
+ * lost; with e4m3, where weight times value scale is below 2^-31 of the largest
+ * such product of a row that is not all zeros.
  *
  * workspace: device memory of tgemm_attention_decode_workspace() bytes,
  * 16-byte aligned, that held zeros before its first use; the call leaves it fit

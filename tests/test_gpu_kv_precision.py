@@ -1,0 +1,73 @@
+"""How exactly attention over the paged cache keeps its softmax weights: as
+fp32 values split into two of 16 bits, so that an output that comes of large
+values of both signs is as good as its weights.
+
+The bound.  Besides its exponent (kv_helpers.score_error) and the fp32 sums, a
+weight is off by 2^-16 of itself (bf16 products) or 2^-21 (fp16; e4m3 rows are
+widened to it), or by 2^-25 of what is 2^6 or more."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from kv_helpers import HALF_STEP, TDT, Filled, attend64, score_error
+
+pytestmark = pytest.mark.gpu
+
+SPLIT = {"fp16": 2.0 ** -21, "bf16": 2.0 ** -16}
+KINDS = [("16", "fp16"), ("16", "bf16"), ("e4m3", "fp16"), ("e4m3", "bf16")]
+
+
+@pytest.mark.parametrize("cache,dtype", KINDS)
+@pytest.mark.parametrize("dim,group,width", [(64, 1, None), (64, 12, None), (64, 16, 4000), (64, 24, 4000), (80, 3, None), (128, 8, None),
+                                             (128, 16, 4000), (128, 24, 4000), (256, 5, None)])
+def test_outputs_that_cancel(cuda_lib, dim, group, width, cache, dtype):
+    """Values of the same size and either sign: the weights' own errors are what is left.  Few positions, so that
+    these do not average out."""
+    lengths = [2, 3, 5, 17, 40]
+    f = Filled(cuda_lib, lengths, 4, dim, 16, dtype, cache, seed=dim + group, width=width)
+    if cache == "e4m3":
+        f.vs.nan_to_num_(1.0)
+        f.vs.fill_(1.0)
+    for b, n in enumerate(lengths):
+        for j in range(n):
+            page, sign = int(f.table_host[b, j // 16]), 1.0 - 2.0 * (j % 2)
+            if cache == "e4m3":
+                f.v.view(torch.uint8)[page, j % 16] = 0x38 if sign > 0 else 0xB8
+            else:
+                f.v[page, j % 16] = sign
+            f.v64[b][j] = sign
+    q = (torch.randn(len(lengths), 4 * group, dim, generator=torch.Generator().manual_seed(1)) * 0.1).to(TDT[dtype])
+    out = torch.empty_like(q, device="cuda")
+    cuda_lib.attention_decode(q.cuda(), f.cache, f.table, f.lengths, out, scale=dim ** -0.5)
+    for b, n in enumerate(lengths):
+        o, p, mag, reach, top = attend64(q[b], f.k64[b], f.v64[b], dim ** -0.5)
+        e = 2 * score_error(reach, dim, 0.0).unsqueeze(-1) + 2 * (n + 64) * 2.0 ** -24
+        u = SPLIT["fp16" if cache == "e4m3" else dtype]
+        low = 2.0 ** -25 if dtype == "fp16" else 2.0 ** -134
+        bound = HALF_STEP[dtype] * o.abs() + (1 + HALF_STEP[dtype]) * ((u + 2 * e) * mag + n * 2.0 ** -31 * top.unsqueeze(-1)) + low
+        worst = ((out[b].double().cpu() - o).abs() - bound).max()
+        assert worst <= 0, (b, float(worst))
+    assert cuda_lib.tgemm_last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim,group,width", [(64, 1, None), (64, 16, 4000), (128, 8, None), (128, 24, 4000), (256, 3, None)])
+def test_an_infinite_value_stays_infinite(cuda_lib, dim, group, width, dtype):
+    """An infinity in a row that counts makes its head's outputs in that dim infinite, with its sign, and no other:
+    on the heaviest row (whose weight is a power of two) as on others."""
+    f = Filled(cuda_lib, [1, 60, 300], 2, dim, 16, dtype, seed=dim, width=width)
+    where = [(0, 0, 0, 3, 1.0), (1, 17, 1, 5, -1.0), (2, 0, 0, 8, 1.0), (2, 299, 1, 0, -1.0), (2, 100, 0, 9, -1.0)]
+    for b, j, h, d, sign in where:
+        f.v[int(f.table_host[b, j // 16]), j % 16, h, d] = sign * float("inf")
+    q = (torch.randn(3, 2 * group, dim, generator=torch.Generator().manual_seed(2)) * 0.5).to(TDT[dtype]).cuda()
+    for weigh in (q, torch.zeros_like(q)):          # scores as they come, and all equal: every weight a power of two
+        out = torch.empty_like(q)
+        cuda_lib.attention_decode(weigh, f.cache, f.table, f.lengths, out)
+        want = torch.zeros(3, 2 * group, dim)
+        for b, j, h, d, sign in where:
+            want[b, h * group:(h + 1) * group, d] = sign
+        got = out.float().cpu()
+        assert not torch.isnan(got).any()
+        assert torch.equal(torch.isinf(got), want != 0)
+        assert (torch.sign(got)[want != 0] == want[want != 0]).all()
