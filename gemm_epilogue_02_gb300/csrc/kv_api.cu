@@ -458,7 +458,7 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args
     // A cap above 2^64 changes no score below 2^52 by fp32's half step; what passes fp32's range is cut to it, so
     // that a product of 0 keeps a score of 0.
     p.capped = a->cap > 0.0 && a->cap <= 0x1p64;
-    const double first = p.capped ? a->scale * 2.0 * kLog2e / a->cap : a->scale * kLog2e;
+    const double first = p.capped ? a->scale / a->cap : a->scale * kLog2e;
     p.first = static_cast<float>(std::clamp<double>(first, -FLT_MAX, FLT_MAX));
     p.last = p.capped ? static_cast<float>(a->cap * kLog2e) : 0.0f;
     p.page_shift = -1;

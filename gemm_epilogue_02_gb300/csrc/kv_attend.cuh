@@ -103,7 +103,7 @@ struct AttendParams {
     int lanes;                            // CTAs that share a run: heads * blocks, or 1
     int window;
     int page_shift;                       // log2 of the page size, -1: not a power of two
-    // A score in log2 units is first * (q . k); capped, last * tanh2(first * (q . k)).
+    // A score in log2 units is first * (q . k); capped, last * tanh(first * (q . k)).
     float first, last;
     bool capped;
     unsigned int *status;
@@ -217,22 +217,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// tanh(x ln 2 / 2) = 1 - 2 / (1 + 2^x).  Near zero that would leave the fp32
-// step of 1, which a large cap multiplies into the score (cap 1e4: 1e-3; 1e6:
-// 0.1), so there it is the series up to the seventh power: relative error below
-// 2^-18 everywhere.  (7 windows of 8192, 24 heads: 23.15 us, 22.93
-// without the series.)
-__device__ __forceinline__ float tanh2(float x) {
-    constexpr double h = 0.34657359027997265;      // ln 2 / 2
-    const float x2 = x * x;
-    const float series = x * fmaf(x2, fmaf(x2, fmaf(x2, static_cast<float>(-17 * h * h * h * h * h * h * h / 315),
-                                                    static_cast<float>(2 * h * h * h * h * h / 15)),
-                                           static_cast<float>(-h * h * h / 3)),
-                                  static_cast<float>(h));
-    const float far = 1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x));
-    return x2 < 0.25f ? series : far;
 }
 
 // x = f * 2^e, 1 <= |f| < 2; e = -infinity for 0; an infinity or NaN is its own f.
@@ -725,7 +709,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                         for (int i = 0; i < 2; ++i) {
                             float &x = s[nt][kb][2 * r + i];
                             x *= kE4m3 ? qscale[nt][i] * ks : qscale[nt][i];
-                            if (p.capped) x = p.last * tanh2(x);
+                            if (p.capped) x = p.last * tanhf(x);
                         }
                 }
             if (p.space.scores) {

@@ -71,3 +71,39 @@ def test_an_infinite_value_stays_infinite(cuda_lib, dim, group, width, dtype):
         assert not torch.isnan(got).any()
         assert torch.equal(torch.isinf(got), want != 0)
         assert (torch.sign(got)[want != 0] == want[want != 0]).all()
+
+
+@pytest.mark.parametrize("cache,dtype", KINDS)
+@pytest.mark.parametrize("low,high", [(0.150, 0.176), (0.30, 0.33), (0.01, 0.04), (0.80, 0.84)])
+def test_capped_scores_are_as_good_as_others(cuda_lib, low, high, cache, dtype):
+    """Two positions whose q k is exact: the added weight of the lighter one shows the error of their scores'
+    difference.  Of each score, in units of 2^-24 of it: the quotient's product with q k 1, tanh 2, the product with
+    the cap 1 (the quotient scale / cap and the cap are the same for both: 3 of the difference, with the subtraction
+    of the reference); then 2^-22 for each of two exponentials and the join's factor, and a few roundings of the sum
+    and the quotient."""
+    dim, heads, cap = 64, 8, 1000.0
+    f = Filled(cuda_lib, [2], heads, dim, 16, dtype, cache, seed=1)
+    page = int(f.table_host[0, 0])
+    k = torch.tensor([[round(low * 256) / 256 * 512 + h, round(high * 256) / 256 * 512 + 2 * h] for h in range(heads)],
+                     dtype=torch.float64)                                   # [heads, 2], whole numbers below 512
+    for pool in (f.k, f.v):
+        pool.view(torch.uint8)[page, :2] = 0
+    if cache == "e4m3":         # an element of 1, the rest in the row's scale
+        f.vs[page, :2] = 1.0
+        f.ks[page, :2] = k.T.float().cuda()
+        f.k.view(torch.uint8)[page, :2, :, 0] = 0x38
+    else:
+        f.k[page, :2, :, 0] = (k.T / 2).to(TDT[dtype]).cuda() * 2
+        k = f.k[page, :2, :, 0].double().cpu().T
+    q = torch.zeros(1, heads, dim, dtype=TDT[dtype])
+    q[0, :, 0] = 1.0
+    out, w = torch.empty_like(q, device="cuda"), torch.zeros(1, heads, 2, device="cuda")
+    for i in range(64):
+        scale = 2.0 * (1 - i / 5000)
+        w.zero_()
+        cuda_lib.attention_decode(q.cuda(), f.cache, f.table, f.lengths, out, scale=scale, cap=cap, weights=w)
+        s = cap * torch.tanh(k * scale / cap)
+        p = torch.softmax(s, 1)
+        e = 2.0 ** -24 * (4 * s.abs().sum(1) + 3 * (s[:, 1] - s[:, 0]).abs() + 16) + 3 * 2.0 ** -22
+        assert ((w[0, :, 0].double().cpu() - p[:, 0]).abs() <= e * p[:, 0]).all(), i
+    assert cuda_lib.tgemm_last_device_status() == 0
