@@ -50,6 +50,15 @@ __host__ __device__ inline uint32_t kv_weight_key(uint32_t bits) {
     return (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;
 }
 
+// Where a kept position goes among the `best`: after the larger keys before it and as many of the equal ones as are
+// wanted; false where that is none of them (weights that another stream changes between the selection's passes leave
+// it without a sound count).
+__host__ __device__ inline bool kv_kept_place(int larger, int ties, int need, int best, int *at) {
+    const long long place = static_cast<long long>(larger) + (ties < need ? ties : need);
+    *at = static_cast<int>(place);
+    return place >= 0 && place < best;
+}
+
 // Grid: (cluster size, heads, batch), a cluster along x.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParams p) {
@@ -250,8 +259,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
         const unsigned ml = __ballot_sync(0xffffffffu, is_larger), me = __ballot_sync(0xffffffffu, is_equal);
         const int ties = at_equal + __popc(me & below);
         if (is_larger || (is_equal && ties < need)) {
-            const int at = at_larger + __popc(ml & below) + min(ties, need);
-            if (at < p.keep && TGEMM_CHECK(at >= 0 && at < best, kChkKvOutput, p.status)) {
+            int at;
+            const bool inside = kv_kept_place(at_larger + __popc(ml & below), ties, need, best, &at);
+            if (TGEMM_CHECK(inside, kChkKvOutput, p.status) && inside) {
                 kept[at] = lo + i;
                 to_w[at] = mine[i];
             }

@@ -1,0 +1,37 @@
+"""Where the paged cache's outputs go when the data of a call changes while it
+runs, which no call may turn into an access outside its arrays: the functions
+that decide it, as compiled for the host."""
+from __future__ import annotations
+
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+from gemm_epilogue_02_gb300.build import ARCH, nvcc
+
+
+@pytest.fixture(scope="module")
+def places(tmp_path_factory):
+    lib = str(tmp_path_factory.mktemp("kv") / "libkvplaces.so")
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "kv_host_places.cu")
+    subprocess.run([nvcc(), *ARCH, "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", "-o", lib, src], check=True,
+                   capture_output=True)
+    return ctypes.CDLL(lib)
+
+
+def test_kept_positions_stay_among_the_best(places):
+    """Counts that do not belong together (a limit found in other weights than those that are placed by it) give no
+    place outside 0 .. best - 1."""
+    at = ctypes.c_int()
+    odd = (-2 ** 31, -7, -1, 0, 1, 5, 63, 64, 100, 2 ** 31 - 1)
+    for larger in (0, 1, 5, 63, 64, 1000, 2 ** 31 - 1):
+        for ties in (0, 1, 64, 2 ** 31 - 1):
+            for need in odd:
+                for best in (0, 1, 6, 64, 2 ** 30):
+                    ok = places.check_kept_place(larger, ties, need, best, ctypes.byref(at))
+                    want = larger + min(ties, need)
+                    assert ok == (0 <= want < best)
+                    if ok:
+                        assert at.value == want
