@@ -274,6 +274,13 @@ __host__ __device__ inline int attend_tiles(int n, int window, int tile, int pad
     return (t + pad - 1) / pad * pad;
 }
 
+// How many of the positions of a warp's step, which begin `in_tile` into tile `tile`, the workspace has scores for: all
+// of those that the step has rows of, unless the lengths change while the kernel runs.
+__host__ __device__ inline long long attend_scored(int lo, int tile, int tile_size, int in_tile, long long positions) {
+    const long long at = lo + static_cast<long long>(tile) * tile_size + in_tile;
+    return at < positions ? positions - at : 0;
+}
+
 // With up to 32 sequences and few tiles, runs of one length that end with their item (its
 // tiles padded to a multiple) join faster than equal ones that begin and end
 // anywhere.  The shortest of these lengths is taken that makes at most `runs`
@@ -716,6 +723,8 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
                 float *const scores = p.space.scores +
                                       ((static_cast<long long>(use.b) * p.cache.heads + head) * p.positions + use.lo +
                                        use.tile * S::kTile + warp * S::kKeys) * p.scored + h0 + 2 * t4;
+                const int room = static_cast<int>(min(attend_scored(use.lo, use.tile, S::kTile, warp * S::kKeys, p.positions),
+                                                      static_cast<long long>(S::kKeys)));
 #pragma unroll
                 for (int kb = 0; kb < kBlocks; ++kb)
 #pragma unroll
@@ -723,7 +732,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             const int row = 16 * kb + g + 8 * r;
-                            if (((mask >> row) & 1u) && 8 * nt + 2 * t4 < hn &&
+                            if (((mask >> row) & 1u) && row < room && 8 * nt + 2 * t4 < hn &&
                                 TGEMM_CHECK(scores - p.space.scores + row * p.scored + 8 * nt + 2 <= p.dbg_scores, kChkKvSpace, p.status))
                                 *reinterpret_cast<float2 *>(scores + row * p.scored + 8 * nt) =
                                     make_float2(s[nt][kb][2 * r], s[nt][kb][2 * r + 1]);

@@ -6,3 +6,7 @@
 extern "C" int check_kept_place(int larger, int ties, int need, int best, int *at) {
     return tgemm::kv_kept_place(larger, ties, need, best, at) ? 1 : 0;
 }
+
+extern "C" long long check_scored(int lo, int tile, int tile_size, int in_tile, long long positions) {
+    return tgemm::attend_scored(lo, tile, tile_size, in_tile, positions);
+}

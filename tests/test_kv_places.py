@@ -18,7 +18,9 @@ def places(tmp_path_factory):
     src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "kv_host_places.cu")
     subprocess.run([nvcc(), *ARCH, "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", "-o", lib, src], check=True,
                    capture_output=True)
-    return ctypes.CDLL(lib)
+    p = ctypes.CDLL(lib)
+    p.check_scored.argtypes, p.check_scored.restype = [ctypes.c_int] * 4 + [ctypes.c_longlong], ctypes.c_longlong
+    return p
 
 
 def test_kept_positions_stay_among_the_best(places):
@@ -35,3 +37,13 @@ def test_kept_positions_stay_among_the_best(places):
                     assert ok == (0 <= want < best)
                     if ok:
                         assert at.value == want
+
+
+def test_scores_stay_inside_what_the_page_lists_hold(places):
+    """A step's positions past what the workspace has room for have no score, whatever tile they are said to be in."""
+    for positions in (0, 1, 95, 96, 1000, 2 ** 30):
+        for lo in (0, 1, positions // 2, max(0, positions - 1)):
+            for tile in (0, 1, 10, 11184810, 11184826):
+                for in_tile in (0, 16, 80):
+                    first = lo + tile * 96 + in_tile
+                    assert places.check_scored(lo, tile, 96, in_tile, positions) == max(0, positions - first)
