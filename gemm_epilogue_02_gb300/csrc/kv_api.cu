@@ -373,7 +373,8 @@ extern "C" tgemm_status tgemm_kv_append(const tgemm_kv_append_args *a, tgemm_str
         (cache->heads > 1 && a->head_stride % 8 != 0))
         return TGEMM_ERR_ALIGNMENT;
     const Extent nk = {a->K, bytes}, nv = {a->V, bytes};
-    if (overlaps(nk, ck) || overlaps(nk, cv) || overlaps(nv, ck) || overlaps(nv, cv) || cache->k == cache->v)
+    if (overlaps(nk, ck) || overlaps(nk, cv) || overlaps(nv, ck) || overlaps(nv, cv) ||
+        (cache->pages > 0 && cache->k == cache->v))
         return TGEMM_ERR_ALIAS;
     RuntimeInfo rt;
     st = runtime_current(&rt);
@@ -447,6 +448,10 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args
     if (!all_device(rt.device, {a->Q, a->O, a->seq.pages, a->seq.lengths, a->weights.data, a->workspace, cache->k, cache->v,
                                 cache->e4m3 ? cache->k_scale : nullptr, cache->e4m3 ? cache->v_scale : nullptr}))
         return TGEMM_ERR_INVALID_ARG;
+    if (cache->pages == 0) {      // the copies of nothing (rows left out) still name an address
+        p.cache.k = p.cache.v = static_cast<unsigned char *>(a->workspace);
+        p.cache.k_scale = p.cache.v_scale = static_cast<float *>(a->workspace);
+    }
     p.q = static_cast<const unsigned char *>(a->Q);
     p.o = static_cast<unsigned char *>(a->O);
     p.q_batch_stride = a->q_batch_stride * 2;
