@@ -200,6 +200,7 @@ cudaError_t launch_select_threads(const RuntimeInfo &rt, EvictParams &p, int64_t
     static std::atomic<uint64_t> ready{0};      // bit per device
     const uint64_t bit = uint64_t(1) << rt.device;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
+        const RelaxedCapture relaxed;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectMaxCached * 4);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
@@ -297,6 +298,7 @@ cudaError_t launch_attend(const RuntimeInfo &rt, const AttendParams &p, cudaStre
     static std::atomic<uint64_t> ready{0};      // bit per device
     const uint64_t bit = uint64_t(1) << rt.device;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
+        const RelaxedCapture relaxed;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);

@@ -39,8 +39,8 @@ struct CounterBuf {
 };
 
 struct DeviceInfo {
-    std::once_flag once;
-    bool ok = false;        // CC 10.3
+    std::mutex set_up;      // the first call's
+    std::atomic<int> state{0};   // 0: not set up yet, 1: ready, 2: not of compute capability 10.3
     int num_sms = 0;
     unsigned int *status = nullptr;
     cudaMemPool_t pool = nullptr;
@@ -60,42 +60,52 @@ DeviceInfo g_dev[kMaxDevices];
 unsigned long long *g_trace_buffer = nullptr;
 #endif
 
+// The device's properties, looked up by the first call on it.  That call may be
+// made during a stream capture, in which looking up a symbol is not allowed
+// unless the thread says that it does not mind; a call that fails is tried again
+// by the next.
 bool device_info(int dev, DeviceInfo **out) {
     if (dev < 0 || dev >= kMaxDevices) return false;
     DeviceInfo &d = g_dev[dev];
-    std::call_once(d.once, [&]() {
-        int major = 0, minor = 0, sms = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-            cudaGetLastError();
-            return;
-        }
-        if (major != 10 || minor != 3) return;
-        void *sym = nullptr;
-        if (cudaGetSymbolAddress(&sym, g_device_status) != cudaSuccess) {
-            cudaGetLastError();
-            return;
-        }
-        cudaMemPoolProps props;
-        std::memset(&props, 0, sizeof(props));
-        props.allocType = cudaMemAllocationTypePinned;
-        props.location.type = cudaMemLocationTypeDevice;
-        props.location.id = dev;
-        cudaMemPool_t pool = nullptr;
-        if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) {
-            cudaGetLastError();
-            return;
-        }
-        uint64_t keep = UINT64_MAX;   // keep freed scratch in the pool for the next call
-        cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
-        d.num_sms = sms;
-        d.status = static_cast<unsigned int *>(sym);
-        d.pool = pool;
-        d.ok = true;
-    });
     *out = &d;
-    return d.ok;
+    int state = d.state.load(std::memory_order_acquire);
+    if (state != 0) return state == 1;
+    std::lock_guard<std::mutex> g(d.set_up);
+    if ((state = d.state.load(std::memory_order_relaxed)) != 0) return state == 1;
+    const RelaxedCapture relaxed;
+    int major = 0, minor = 0, sms = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    if (major != 10 || minor != 3) {
+        d.state.store(2, std::memory_order_release);
+        return false;
+    }
+    void *sym = nullptr;
+    if (cudaGetSymbolAddress(&sym, g_device_status) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    cudaMemPoolProps props;
+    std::memset(&props, 0, sizeof(props));
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = dev;
+    cudaMemPool_t pool = nullptr;
+    if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    uint64_t keep = UINT64_MAX;   // keep freed scratch in the pool for the next call
+    cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    d.num_sms = sms;
+    d.status = static_cast<unsigned int *>(sym);
+    d.pool = pool;
+    d.state.store(1, std::memory_order_release);
+    return true;
 }
 
 tgemm_status current_device(DeviceInfo **d) {
@@ -799,7 +809,7 @@ bool noalloc_setup(int dev, NoAllocDevice **out) {
         }
         d.info.num_sms = sms;
         d.info.status = static_cast<unsigned int *>(status);
-        d.info.ok = true;
+        d.info.state.store(1);
         d.scratch = scratch;
         d.ok = true;
     });
