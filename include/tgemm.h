@@ -364,8 +364,9 @@ typedef struct {
  * lengths[b] counts them already: the last of them goes to position
  * lengths[b] - 1.  Tokens outside starts[0] .. starts[batch] - 1 are left out.
  * An e4m3 row's scale is max |x| / 448 (1 for a row of zeros) and its elements
- * x / scale, rounded to nearest even.  With weights, those of the new positions
- * are set to 0.
+ * x / scale, rounded to nearest even.  A NaN stays one and does not count in its
+ * row's maximum; an infinity makes the scale infinite, so that its row reads as
+ * NaN.  With weights, those of the new positions are set to 0.
  */
 typedef struct {
     const tgemm_kv_cache *cache;

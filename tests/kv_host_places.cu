@@ -10,3 +10,13 @@ extern "C" int check_kept_place(int larger, int ties, int need, int best, int *a
 extern "C" long long check_scored(int lo, int tile, int tile_size, int in_tile, long long positions) {
     return tgemm::attend_scored(lo, tile, tile_size, in_tile, positions);
 }
+
+extern "C" int check_fan(int parts) { return tgemm::attend_fan(parts); }
+
+extern "C" int check_slot(int c, int first, int lane, int lanes) { return tgemm::attend_slot(c, first, lane, lanes); }
+
+extern "C" void check_join_limits(int *out) {
+    out[0] = tgemm::kAttendMaxCtas;
+    out[1] = tgemm::kAttendFanIn;
+    out[2] = tgemm::kAttendOneLevel;
+}

@@ -47,3 +47,31 @@ def test_scores_stay_inside_what_the_page_lists_hold(places):
                 for in_tile in (0, 16, 80):
                     first = lo + tile * 96 + in_tile
                     assert places.check_scored(lo, tile, 96, in_tile, positions) == max(0, positions - first)
+
+
+def test_parts_are_joined_in_groups_that_fit(places):
+    """The groups that attention's parts are joined in, for every number of parts that there can be: each part in one
+    group, no more parts or groups than a block has room for, a counter and a slot of its own for every group."""
+    limits = (ctypes.c_int * 3)()
+    places.check_join_limits(limits)
+    ctas, most, one_level = limits
+    assert one_level <= most
+    for parts in range(1, ctas + 1):
+        fan, groups = most, 1
+        if parts > one_level:
+            fan = places.check_fan(parts)
+            groups = -(-parts // fan)
+        assert 1 <= fan <= most and 1 <= groups <= most and (groups - 1) * fan < parts <= groups * fan
+        if groups == 1:
+            assert parts <= most
+            continue
+        seen = []
+        for group in range(groups):
+            first = group * fan
+            members = list(range(first, first + min(fan, parts - first)))
+            assert members and all(m // fan == group for m in members)
+            seen += members
+        assert seen == list(range(parts))
+        for first_run in (0, ctas - parts):
+            heads = [places.check_slot(first_run + g * fan, first_run, 0, 1) for g in range(groups)]
+            assert len(set(heads)) == groups and min(heads) >= 0 and max(heads) < 2 * ctas
