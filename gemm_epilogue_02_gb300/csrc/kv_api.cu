@@ -241,16 +241,19 @@ cudaError_t launch_gather(const EvictParams &p, int64_t most, int heads, int bat
 int padded_dim(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 // Eights of query heads that a block takes, by the tiles of 64 positions that
-// there can be for each of two blocks an SM.  Every block copies the rows for
-// itself, so where the copies bound it the fewest blocks are best: three eights
-// at once from 16 tiles on (24 heads over 1.2 GB of 16-bit rows: 224 us, 16 + 8
-// 302 us).  But a block of one eight has more warps, shorter steps and less to
-// join, and below 6 tiles that counts more (24 heads, 7 windows of 8192: one 19.3
-// us, two 23.1, three 34; 16 heads, 16 contexts of 300 with 4 key heads: one 11.6,
-// two 13.6; with 2 tiles, 16000 e4m3 positions alone, 15.7 and 19.6; with 7, 16
-// contexts of 2000: 12 heads 23.0 and 19.9, 24 heads 29.9 and 28.8).  256-wide
-// rows leave registers for one eight, and widening e4m3 rows leaves no gain for
-// three.
+// there can be for each of two blocks an SM (the host knows what the page lists
+// can hold, not the lengths: lists with much room to spare are taken for long
+// contexts).  Every block copies the rows for itself, so where the copies bound
+// it the fewest blocks are best: three eights at once from 16 tiles on (24 heads,
+// 32 contexts of 9000, 8 key heads, 16 bits: 232 us, two and one 309, one at a
+// time 339; 16 heads: two 182, one at a time 229; e4m3 16 heads: two 139, one
+// 176).  But a block of one eight has more warps, shorter steps and less to join,
+// and below 6 tiles that counts more (24 heads, 7 contexts of 8192, 96 wide: one
+// 21.2 us, two 23.3, three 27.2; 16 heads, 16 contexts of 300 with 4 key heads:
+// one 11.8, two 13.6; with 2 tiles, 16000 e4m3 positions alone, 17.1 and 21.9;
+// with 7, 16 contexts of 2000, 8 key heads: 12 heads 38.3 and 32.8, 24 heads 50.2
+// and 49.3, three 44.7).  256-wide rows leave registers for one eight, and
+// widening e4m3 rows leaves no gain for three.
 int head_tiles(int64_t group, int64_t dim, bool e4m3, int64_t batch, int64_t heads, int64_t positions, int num_sms) {
     const int64_t tiles = batch * heads * (positions / 64), places = 2 * num_sms;
     if (group <= 8 || dim > 128 || tiles < 6 * places) return 1;
@@ -462,11 +465,13 @@ extern "C" tgemm_status tgemm_attention_decode(const tgemm_attention_decode_args
     p.o_head_stride = a->o_head_stride * 2;
     p.window = static_cast<int>(std::min<int64_t>(a->window, INT32_MAX));
     constexpr double kLog2e = 1.4426950408889634;
-    // A cap above 2^64 changes no score below 2^52 by fp32's half step; what passes fp32's range is cut to it, so
-    // that a product of 0 keeps a score of 0.
+    // A cap above 2^64 changes no score below 2^52 by fp32's half step.  A product of 0 has to keep a score of 0, so
+    // the factor is cut to fp32's range, and before a tanh to 2^60, which leaves e4m3's scales room: what that changes
+    // is a score below a cap that is no more than 2^-60 of the scale.
     p.capped = a->cap > 0.0 && a->cap <= 0x1p64;
     const double first = p.capped ? a->scale / a->cap : a->scale * kLog2e;
-    p.first = static_cast<float>(std::clamp<double>(first, -FLT_MAX, FLT_MAX));
+    const double most_first = p.capped ? 0x1p60 : FLT_MAX;
+    p.first = static_cast<float>(std::clamp<double>(first, -most_first, most_first));
     p.last = p.capped ? static_cast<float>(a->cap * kLog2e) : 0.0f;
     p.page_shift = -1;
     for (int i = 0; i <= 20; ++i)

@@ -107,3 +107,23 @@ def test_capped_scores_are_as_good_as_others(cuda_lib, low, high, cache, dtype):
         e = 2.0 ** -24 * (4 * s.abs().sum(1) + 3 * (s[:, 1] - s[:, 0]).abs() + 16) + 3 * 2.0 ** -22
         assert ((w[0, :, 0].double().cpu() - p[:, 0]).abs() <= e * p[:, 0]).all(), i
     assert cuda_lib.tgemm_last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("cap", [1e-10, 1e-30, 1e-45, 1e-300])
+def test_caps_near_zero_over_keys_of_zero(cuda_lib, cap, dtype):
+    """e4m3: scores that all become 0, of keys with scales above 1, some with elements of 0: the average of the
+    values."""
+    f = Filled(cuda_lib, [100], 2, 64, 16, dtype, "e4m3", seed=8)
+    f.ks.nan_to_num_(1.0)
+    f.ks.fill_(37.0)
+    f.k.view(torch.uint8)[f.table_host[0, 2].item()] = 0
+    q = (torch.randn(1, 4, 64, generator=torch.Generator().manual_seed(3)) * 5000).to(TDT[dtype])
+    q[0, 3] = 0
+    out = torch.full_like(q, float("nan"), device="cuda")
+    cuda_lib.attention_decode(q.cuda(), f.cache, f.table, f.lengths, out, cap=cap)
+    o, p, mag, reach, top = attend64(q[0], torch.zeros_like(f.k64[0]), f.v64[0], 0.0)
+    e = 2 * 2.0 ** -22 + 2 * (100 + 64) * 2.0 ** -24 + 4 * cap
+    bound = (HALF_STEP[dtype] * o.abs() + (1 + HALF_STEP[dtype]) * ((SPLIT["fp16"] + 2 * e) * mag + 100 * 2.0 ** -31 * top.unsqueeze(-1))
+             + (2.0 ** -25 if dtype == "fp16" else 2.0 ** -134))
+    assert ((out[0].double().cpu() - o).abs() <= bound).all()
