@@ -54,9 +54,9 @@ __host__ __device__ inline uint32_t kv_weight_key(uint32_t bits) {
 // wanted; false where that is none of them (weights that another stream changes between the selection's passes leave
 // it without a sound count).
 __host__ __device__ inline bool kv_kept_place(int larger, int ties, int need, int best, int *at) {
-    const long long place = static_cast<long long>(larger) + (ties < need ? ties : need);
+    const unsigned place = static_cast<unsigned>(larger) + static_cast<unsigned>(ties < need ? ties : need);
     *at = static_cast<int>(place);
-    return place >= 0 && place < best;
+    return place < static_cast<unsigned>(best);              // a sum below 0 wraps to 2^31 or more
 }
 
 // Grid: (cluster size, heads, batch), a cluster along x.
