@@ -18,8 +18,8 @@
 // per (key head, block), as many as fit the GPU at once: a ragged batch, or a
 // single long sequence, loads every SM alike, and the heads of a position are
 // read at about the same time, which is what DRAM wants where they lie side by
-// side (with every CTA on its own, 64-byte rows of 8 heads came at 2.8 TB/s
-// instead of 5.7, and blocks of one head read its rows twice).  Each CTA finds
+// side (with every CTA on its own, 64-byte rows of 8 heads come at 2.7 TB/s
+// instead of 5.2, and blocks of one head read its rows twice).  Each CTA finds
 // its run from the lengths, which only the device knows.  With so many heads
 // that a run each would leave places empty, runs go through the heads instead.
 // A run that ends inside an item leaves (maximum, sum, output) of its part in
@@ -114,9 +114,11 @@ struct AttendParams {
 // of some hundred instructions, and a warp has no more than one on the way, so
 // the SM wants many warps, each with as much in a step as the ring allows: 96
 // KiB per CTA, steps of 16 positions, 32 where a row has 128 bytes or less (e4m3
-// 128 wide, 8 warps with steps of 16: 2.8 TB/s, 6 with 32: 6.3).  Six warps of two
-// stages beat four of three where 168 registers do (16-bit, 256 wide: 6.5
-// against 6.1 TB/s); two or three eights of heads need 255.
+// 128 wide, 8 warps with steps of 16: 2.1 TB/s, 6 with 32: 6.2).  Six warps of two
+// stages beat four of three for 16-bit rows of 256 dims, whose CTA is alone on its
+// SM (6.5 against 6.3 TB/s); two or three eights of heads need 255 registers, and
+// spill even so where they are three of 128 dims (428 bytes stored; two of 64,
+// with 168 registers: 84).
 template <bool kE4m3, int DP, int NT>
 struct AttendShape {
     static constexpr int kRow = DP * (kE4m3 ? 1 : 2);                     // bytes of a row in shared memory
@@ -243,7 +245,9 @@ __device__ __forceinline__ uint32_t pair16(float lo, float hi) {
 // leaves, rounded: off by at most 2^-16 of w (bf16), 2^-21 or 2^-25 absolutely
 // (fp16).  Neither is 0 where w is not tiny, nor negative, so that an infinity
 // among the values stays one: for bf16 w's last bit is set before (2^-23 of it),
-// for fp16 `high` is taken of a little less.
+// for fp16 `high` is taken of a little less.  (32 contexts of 9000, 128 wide, 8
+// heads on each of 8: 178.6 us, with w rounded once 178.8; 24 heads 228.9 and
+// 215.5; e4m3, 8 heads 107.0 and 105.6, 16 heads 138.7 and 123.6.)
 template <bool kBf16>
 __device__ __forceinline__ void split16(float w0, float w1, uint32_t &high, uint32_t &rest) {
     if (kBf16) {
@@ -313,10 +317,10 @@ __host__ __device__ inline int attend_owner(long long t, long long ctas, long lo
 }
 
 // Of more than kAttendOneLevel parts, about as many are joined at once as there
-// are groups of them.  262143 positions, 8 key heads of 8: 159.4 us, 160.8 with 32
-// at once; 7 windows of 8192, 8 heads on one: 15.75, 17.26; 200000 e4m3 positions,
-// 2 key heads: 30.2, 31.7; 2 contexts of 32768: 50.1, 50.9; 4096 positions alone:
-// 13.35, 13.06.  (With this from 8 parts on, 1000 positions alone took 11.6
+// are groups of them.  262143 positions, 8 key heads of 8: 161.8 us, 163.0 with 32
+// at once; 7 contexts of 8192, 8 heads on one: 15.6, 17.1; 200000 e4m3 positions,
+// 2 key heads: 32.1, 32.3; 2 contexts of 32768: 51.1, 51.8; 4096 positions alone:
+// 13.5, 13.1.  (With this from 8 parts on, 1000 positions alone took 11.6
 // instead of 10.5.)
 __host__ __device__ inline int attend_fan(int parts) {
     int fan = 1;

@@ -398,7 +398,8 @@ tgemm_status tgemm_kv_append(const tgemm_kv_append_args *args, tgemm_stream_t st
  * with bf16 keys and values, 2^-21 with fp16 and e4m3); each output rounded once
  * to dtype.  With fp16 keys and values weights below 2^-32 of the largest are
  * lost; with e4m3, where weight times value scale is below 2^-31 of the largest
- * such product of a row that is not all zeros.
+ * such product of a row that is not all zeros.  Values near 2^119 and above may
+ * overflow fp32 before the sum of the weights is divided out.
  *
  * workspace: device memory of tgemm_attention_decode_workspace() bytes,
  * 16-byte aligned, that held zeros before its first use; the call leaves it fit
