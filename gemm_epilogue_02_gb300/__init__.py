@@ -16,10 +16,20 @@ from ._binding import (  # noqa: F401
     tgemm_debug_last_check, tgemm_kv_append, tgemm_kv_evict, tgemm_last_device_status, tgemm_plan, tgemm_run,
     tgemm_run_ex, tgemm_run_host, tgemm_run_noalloc,
     tgemm_status_string, tgemm_version,
+    KV_BOUNDS_ARGS, KV_COMPACT_ARGS, KV_FORK_ARGS, KV_FREE_ARGS, KV_GROW_ARGS, KV_SELECT_ARGS, KvPageBounds,
+    QK_NORM_ROPE_ARGS, QK_NORM_ROPE_BACKWARD_ARGS, RotaryStruct, tgemm_attention_decode_lists, tgemm_kv_bounds,
+    tgemm_kv_compact, tgemm_kv_compact_workspace, tgemm_kv_fork, tgemm_kv_free, tgemm_kv_grow, tgemm_kv_select,
+    tgemm_qk_norm_rope, tgemm_qk_norm_rope_backward, tgemm_qk_norm_rope_backward_workspace,
 )
 from .build import build  # noqa: F401
 from .kv import (  # noqa: F401
     PagedCache, attention_decode, attention_decode_workspace, kv_append, kv_evict,
+)
+from .pages import (  # noqa: F401
+    PageBounds, kv_bounds, kv_compact, kv_compact_workspace, kv_fork, kv_free, kv_grow, kv_select,
+)
+from .rope import (  # noqa: F401
+    Rotary, qk_norm_rope, qk_norm_rope_backward, qk_norm_rope_backward_workspace,
 )
 
 EPILOGUES = {"none": TGEMM_EPI_NONE, "relu": TGEMM_EPI_RELU, "bias": TGEMM_EPI_BIAS,

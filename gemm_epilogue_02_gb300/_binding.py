@@ -23,7 +23,10 @@ STATUS = {0: "TGEMM_OK", 1: "TGEMM_ERR_INVALID_ARG", 2: "TGEMM_ERR_ALIGNMENT",
 EXPORTED = ("tgemm_run", "tgemm_run_ex", "tgemm_run_host", "tgemm_status_string",
             "tgemm_last_device_status", "tgemm_version", "tgemm_run_noalloc", "tgemm_plan",
             "tgemm_attention_fwd", "tgemm_debug_last_check", "tgemm_kv_append", "tgemm_attention_decode",
-            "tgemm_attention_decode_workspace", "tgemm_kv_evict")
+            "tgemm_attention_decode_workspace", "tgemm_kv_evict", "tgemm_attention_decode_lists", "tgemm_kv_bounds",
+            "tgemm_kv_select", "tgemm_kv_grow", "tgemm_kv_fork", "tgemm_kv_free", "tgemm_kv_compact",
+            "tgemm_kv_compact_workspace", "tgemm_qk_norm_rope", "tgemm_qk_norm_rope_backward",
+            "tgemm_qk_norm_rope_backward_workspace")
 PLAN_FIELDS = ("bn", "cg", "stages", "tiles", "groups", "split_k", "split_first", "narrow_first",
                "narrow_parts", "units")
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -41,13 +44,34 @@ class KvCache(ctypes.Structure):
                 + [(n, ctypes.c_int32) for n in ("page_size", "heads", "dim", "e4m3")])
 
 
-# The argument structures of the paged-cache calls, as struct.pack formats (every
+class KvPageBounds(ctypes.Structure):
+    """tgemm_kv_page_bounds."""
+    _fields_ = [("bounds", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class RotaryStruct(ctypes.Structure):
+    """tgemm_rotary."""
+    _fields_ = [("turns", ctypes.c_void_p), ("axes", ctypes.c_void_p), ("pairs", ctypes.c_int64), ("interleaved", ctypes.c_int64)]
+
+
+# The argument structures of the calls below, as struct.pack formats (every
 # field takes 8 bytes): pointers and sizes Q / q, real numbers d.
 _SEQUENCES = "QQqqq"          # pages, lengths, pages_width, pages_stride, batch
 _WEIGHTS = "Qqqq"             # data, width, batch_stride, head_stride
 KV_APPEND_ARGS = struct.Struct("=Q" + _SEQUENCES + _WEIGHTS + "QQQqqqq")
 ATTENTION_DECODE_ARGS = struct.Struct("=Q" + _SEQUENCES + _WEIGHTS + "QQqqqqqqddQqq")
 KV_EVICT_ARGS = struct.Struct("=Q" + _SEQUENCES + _WEIGHTS + "Q" + _SEQUENCES + _WEIGHTS + "QQqq")
+_LISTS = "QQqqq"              # pages, lengths, width, stride, batch
+KV_BOUNDS_ARGS = struct.Struct("=QQ" + _SEQUENCES + "Qq")
+KV_SELECT_ARGS = struct.Struct("=QQ" + _SEQUENCES + "QqqqQQqqqqqq")
+KV_GROW_ARGS = struct.Struct("=QQ" + _LISTS + "Q")
+KV_FORK_ARGS = struct.Struct("=QQ" + _SEQUENCES + "Q" + _LISTS)
+KV_FREE_ARGS = struct.Struct("=QQ" + _LISTS)
+KV_COMPACT_ARGS = struct.Struct("=QQQ" + _SEQUENCES + "QqqQQQq")
+_ROWS = "Qqq"                 # data, token_stride, head_stride
+_NORM_ROPE = 4 * _ROWS + "QQQqqqqqqqQqqdq"
+QK_NORM_ROPE_ARGS = struct.Struct("=" + _NORM_ROPE)
+QK_NORM_ROPE_BACKWARD_ARGS = struct.Struct("=" + _NORM_ROPE + 2 * _ROWS + "QQQq")
 
 
 class TgemmError(RuntimeError):
@@ -81,12 +105,20 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.tgemm_plan.restype = i32
     lib.tgemm_attention_fwd.argtypes = [p, p, p, p, i64, i64, i64, i64, i32, i32, p]
     lib.tgemm_attention_fwd.restype = i32
-    for name in ("tgemm_kv_append", "tgemm_attention_decode", "tgemm_kv_evict"):
+    for name in ("tgemm_kv_append", "tgemm_attention_decode", "tgemm_kv_evict", "tgemm_kv_bounds", "tgemm_kv_select",
+                 "tgemm_kv_grow", "tgemm_kv_fork", "tgemm_kv_free", "tgemm_kv_compact", "tgemm_qk_norm_rope",
+                 "tgemm_qk_norm_rope_backward"):
         f = getattr(lib, name)
         f.argtypes = [p, p]
         f.restype = i32
     lib.tgemm_attention_decode_workspace.argtypes = [i64, i64, i64, i64, i64, i32, p]
     lib.tgemm_attention_decode_workspace.restype = i32
+    lib.tgemm_attention_decode_lists.argtypes = [p, i64, p]
+    lib.tgemm_attention_decode_lists.restype = i32
+    for name in ("tgemm_kv_compact_workspace", "tgemm_qk_norm_rope_backward_workspace"):
+        f = getattr(lib, name)
+        f.argtypes = [i64, p]
+        f.restype = i32
     return lib
 
 
@@ -211,3 +243,58 @@ def tgemm_attention_decode_workspace(batch: int, q_heads: int, kv_heads: int, di
     if st != 0:
         raise TgemmError(st, "tgemm_attention_decode_workspace")
     return int(out.value)
+
+
+def tgemm_attention_decode_lists(args: bytes, pages_head_stride: int, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_attention_decode_lists(args, pages_head_stride, stream)
+
+
+def tgemm_kv_bounds(args: bytes, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_kv_bounds(args, stream)
+
+
+def tgemm_kv_select(args: bytes, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_kv_select(args, stream)
+
+
+def tgemm_kv_grow(args: bytes, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_kv_grow(args, stream)
+
+
+def tgemm_kv_fork(args: bytes, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_kv_fork(args, stream)
+
+
+def tgemm_kv_free(args: bytes, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_kv_free(args, stream)
+
+
+def tgemm_kv_compact(args: bytes, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_kv_compact(args, stream)
+
+
+def _workspace_bytes(name: str, n: int) -> int:
+    out = ctypes.c_int64()
+    st = getattr(load(), name)(n, ctypes.byref(out))
+    if st != 0:
+        raise TgemmError(st, name)
+    return int(out.value)
+
+
+def tgemm_kv_compact_workspace(pages: int) -> int:
+    """Bytes of workspace of tgemm_kv_compact (host logic, no GPU)."""
+    return _workspace_bytes("tgemm_kv_compact_workspace", pages)
+
+
+# Head norms with the position rotation: `args` as above.
+def tgemm_qk_norm_rope(args: bytes, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_qk_norm_rope(args, stream)
+
+
+def tgemm_qk_norm_rope_backward(args: bytes, stream: int = 0) -> int:
+    return (_lib if _lib is not None else load()).tgemm_qk_norm_rope_backward(args, stream)
+
+
+def tgemm_qk_norm_rope_backward_workspace(dim: int) -> int:
+    """Bytes of workspace of tgemm_qk_norm_rope_backward (host logic, no GPU)."""
+    return _workspace_bytes("tgemm_qk_norm_rope_backward_workspace", dim)

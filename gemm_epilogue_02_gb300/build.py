@@ -1,8 +1,10 @@
 """Build step for the CUDA library: nvcc, sm_103a only, in-tree.
 
-Produces gemm_epilogue_02_gb300/libtgemm.so (git-ignored) from the two
-translation units csrc/tgemm_api.cu (GEMM, attention) and csrc/kv_api.cu (the
-paged key-value cache), and its debug build libtgemm_debug.so (-DTGEMM_DEBUG:
+Produces gemm_epilogue_02_gb300/libtgemm.so (git-ignored) from the translation
+units csrc/tgemm_api.cu (GEMM, attention), csrc/kv_api.cu (the paged key-value
+cache), csrc/page_api.cu (bounds and choice of its pages, and the pages as a
+resource) and csrc/rope_api.cu (head norms with the position rotation), and its
+debug build libtgemm_debug.so (-DTGEMM_DEBUG:
 the device-side bounds and alignment checks of csrc/debug_checks.cuh), all
 compiled in parallel.  The CUDA runtime is linked statically and the
 driver's tensor-map encoder is looked up at run time, so the libraries load
@@ -17,7 +19,7 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", f) for f in ("tgemm_api.cu", "kv_api.cu")]
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("tgemm_api.cu", "kv_api.cu", "page_api.cu", "rope_api.cu")]
 # Every header the translation units include: those of csrc and the C ABI.
 DEPS = sorted(glob.glob(os.path.join(HERE, "csrc", "*.cuh")) + glob.glob(os.path.join(HERE, "csrc", "*.h"))) + [
     os.path.join(ROOT, "include", "tgemm.h")]

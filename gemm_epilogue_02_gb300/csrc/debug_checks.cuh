@@ -32,6 +32,7 @@ enum DebugCheck : uint32_t {
     kChkKvRow = 9,          // paged cache: a row written outside its pool
     kChkKvOutput = 10,      // paged cache: an output of attention or eviction outside its array
     kChkKvSpace = 11,       // paged cache: a part or score outside the workspace
+    kChkRope = 12,          // rotated rows or their gradients outside their array
 };
 
 // First check that failed since the host last read it (0: none); one word per

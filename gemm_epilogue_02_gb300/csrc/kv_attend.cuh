@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(AttendShape<kE4m3, DP, NT>::kThreads, AttendSh
             i = p.page_shift >= 0 ? pos >> p.page_shift
                                   : static_cast<int>(static_cast<unsigned>(pos) / static_cast<unsigned>(p.cache.page_size));
         slot = pos - i * p.cache.page_size;
-        page = in ? p.table.pages[load.b * p.table.stride + i] : -1;
+        page = in ? p.table.pages[load.b * p.table.stride + load.head * p.table.head_stride + i] : -1;
         want = __ballot_sync(0xffffffffu, in);
         if (++looked < steps) cursor_next(load, p, S::kTile, pad);
     };

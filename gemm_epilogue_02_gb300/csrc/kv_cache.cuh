@@ -40,6 +40,7 @@ struct KvTable {
     const int *pages;          // [batch, stride], `width` columns used
     const int *lengths;        // [batch]
     long long stride;
+    long long head_stride;     // between the lists of a sequence's heads (attention; 0: the heads share one)
     int width;
     int batch;
 };

@@ -37,8 +37,10 @@ private:
 bool runtime_is_device_memory(const void *p, int device);
 
 #ifdef TGEMM_DEBUG
-// Debug build: reads and clears the first failed check of kv_api.cu's kernels.
+// Debug build: reads and clears the first failed check of a translation unit's kernels.
 int kv_debug_last_check();
+int page_debug_last_check();
+int rope_debug_last_check();
 #endif
 
 }  // namespace tgemm

@@ -81,6 +81,16 @@ def _table(page_table, index):
     return page_table.data_ptr(), shape[1], stride[0], shape[0]
 
 
+def _head_table(page_table, cache):
+    """(pages, width, batch stride, batch, head stride) of a page table with a list for each key head."""
+    shape, stride = page_table.shape, page_table.stride()
+    if page_table.dtype is not torch.int32 or shape[1] != cache.heads or (stride[2] != 1 and shape[2] > 1):
+        raise ValueError("page lists of each head must be int32 [batch, heads, pages] with unit stride of pages")
+    if page_table.get_device() != cache._index:
+        raise ValueError("the page table must be on the cache's device")
+    return page_table.data_ptr(), shape[2], stride[0], shape[0], stride[1]
+
+
 def _vector(name, t, n, index):
     """The address of a contiguous int32 [n] tensor."""
     if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
@@ -97,16 +107,16 @@ def _weights(name, w, batch, heads, index):
     return w.data_ptr(), shape[2], stride[0], stride[1]
 
 
-def _launch(index, stream, fn, args):
-    """fn(args, stream) with the cache's device current; raises on a status."""
+def _launch(index, stream, fn, *args):
+    """fn(*args, stream) with the cache's device current; raises on a status."""
     if index < 0:
         raise ValueError("the cache must be on a CUDA device")
     s = _raw_stream(index) if stream is None else stream.cuda_stream
     if index == _current_device():
-        st = fn(args, s)
+        st = fn(*args, s)
     else:
         with torch.cuda.device(index):
-            st = fn(args, s)
+            st = fn(*args, s)
     if st != 0:
         raise _b.TgemmError(st, fn.__name__)
 
@@ -148,7 +158,7 @@ def attention_decode_workspace(Q: torch.Tensor, cache: PagedCache, page_table: t
     smaller ones): zeroed device memory, to be kept between calls.  Calls that
     may overlap on the GPU need one each."""
     n = _b.tgemm_attention_decode_workspace(Q.shape[0], Q.shape[1], cache.heads, cache.dim,
-                                            page_table.shape[1] * cache.page_size, bool(weights))
+                                            page_table.shape[-1] * cache.page_size, bool(weights))
     return torch.zeros(n, dtype=torch.uint8, device=cache.device)
 
 
@@ -161,9 +171,12 @@ def attention_decode(Q: torch.Tensor, cache: PagedCache, page_table: torch.Tenso
     cache's heads.  scale defaults to 1 / sqrt(dim); cap > 0 passes the scaled
     scores through cap * tanh(s / cap).  weights (float32 [batch, heads,
     positions]) grow by each group's summed attention.  Without a workspace one
-    is allocated and zeroed for the call."""
+    is allocated and zeroed for the call.  A page table of three dimensions,
+    [batch, heads, pages] as kv_select() writes it, has a list for each key head;
+    positions are then those of the lists."""
     index = cache._index
-    pages, width, stride, batch = _table(page_table, index)
+    lists = page_table.dim() == 3
+    pages, width, stride, batch, head_stride = (_head_table(page_table, cache) if lists else (*_table(page_table, index), 0))
     length = _vector("lengths", lengths, batch, index)
     shape, sq, so, dtype = Q.shape, Q.stride(), O.stride(), Q.dtype
     if len(shape) != 3 or O.shape != shape or shape[0] != batch or shape[2] != cache.dim or shape[1] % cache.heads:
@@ -182,10 +195,13 @@ def attention_decode(Q: torch.Tensor, cache: PagedCache, page_table: torch.Tenso
             workspace = attention_decode_workspace(Q, cache, page_table, weights is not None)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the cache's device")
-    _launch(index, stream, _b.tgemm_attention_decode,
-            _decode(cache._address, pages, length, width, stride, batch, *w, Q.data_ptr(), O.data_ptr(), shape[1],
-                    sq[0], sq[1], so[0], so[1], window, cache.dim ** -0.5 if scale is None else scale, cap,
-                    workspace.data_ptr(), workspace.nbytes, _DT[dtype]))
+    args = _decode(cache._address, pages, length, width, stride, batch, *w, Q.data_ptr(), O.data_ptr(), shape[1],
+                   sq[0], sq[1], so[0], so[1], window, cache.dim ** -0.5 if scale is None else scale, cap,
+                   workspace.data_ptr(), workspace.nbytes, _DT[dtype])
+    if lists:
+        _launch(index, stream, _b.tgemm_attention_decode_lists, args, head_stride)
+    else:
+        _launch(index, stream, _b.tgemm_attention_decode, args)
     return O
 
 

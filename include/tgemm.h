@@ -245,8 +245,9 @@ tgemm_status tgemm_last_device_status(void);
  * outside its scratch, 6 an arrival counter outside its buffer, 7 an
  * attention output store outside O, 8 a repack store outside its
  * destination, 9 a row of the paged cache written outside its pool, 10 an
- * output of tgemm_attention_decode or tgemm_kv_evict outside its array, 11 a
- * part or score outside the workspace.  The failing access is skipped (nothing traps); a skipped
+ * output of tgemm_attention_decode, tgemm_kv_evict, tgemm_kv_bounds or
+ * tgemm_kv_select outside its array, 11 a part or score outside the workspace,
+ * 12 a rotated row or its gradient outside its array.  The failing access is skipped (nothing traps); a skipped
  * copy leaves its pipeline slot incomplete, which the bounded waits end.
  * Synchronises the device.  Returns -1 in the release build, which compiles
  * no checks.  Testing only: TGEMM_DEBUG_PLANT=c_store makes the debug build's
@@ -339,7 +340,7 @@ typedef struct {
 } tgemm_kv_weights;
 
 /*
- * Common to the three calls below.
+ * Common to the calls on the cache below.
  *
  * Page numbers, lengths and starts are on the device, so the kernels check
  * them: one that lies outside the pool or the table (a negative length too) is
@@ -454,6 +455,236 @@ typedef struct {
     int64_t keep, recent;
 } tgemm_kv_evict_args;
 tgemm_status tgemm_kv_evict(const tgemm_kv_evict_args *args, tgemm_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Sparse attention: pages that a cheap score selects.
+ *
+ * For each page and key head, each channel's least and largest key in 8 bits:
+ *   bounds  int8 [pages, heads, 2, dim], contiguous, 16-byte aligned: lo, then hi
+ *   scale   fp32 [pages, heads]: s, the least power of two (2^-100 at least)
+ *           such that no key of the page exceeds 127 s in magnitude
+ *   lo = floor(min k / s), hi = ceil(max k / s), so that s lo <= k <= s hi.
+ * The keys of an e4m3 cache are the fp32 products scale * element.  A NaN counts
+ * as not there, an infinity as the largest finite number.  dim is a multiple of 16.
+ */
+typedef struct {
+    int8_t *bounds;
+    float *scale;
+} tgemm_kv_page_bounds;
+
+/*
+ * tgemm_kv_bounds — the bounds of the pages that the newest tokens complete.
+ * Sequence b has brought starts[b + 1] - starts[b] tokens (starts: int32 [batch
+ * + 1], device; NULL: one each), which lengths[b] counts already: the pages
+ * whose last position is among them are read whole and their bounds written.
+ * Call it after tgemm_kv_append.  A page that is not full has no bounds.
+ */
+typedef struct {
+    const tgemm_kv_cache *cache;
+    const tgemm_kv_page_bounds *bounds;
+    tgemm_kv_sequences seq;
+    const int32_t *starts;
+    int64_t dtype;                                  /* of the keys of a 16-bit cache */
+} tgemm_kv_bounds_args;
+tgemm_status tgemm_kv_bounds(const tgemm_kv_bounds_args *args, tgemm_stream_t stream);
+
+/*
+ * tgemm_kv_select — of each sequence's pages, each key head keeps at most `keep`:
+ * the first `first`, the last `recent` (1 at least: the last page may not be
+ * full), and of those between them the ones of largest score (ties to the lowest
+ * position).  With z the query of a head (Q [batch, q_heads, dim], as in
+ * tgemm_attention_decode) in whole numbers of a power of two t, found as s is
+ * above (rounded to nearest even), a page's score is the largest over the head's
+ * group of
+ *     t s sum_d max(z_d lo_d, z_d hi_d)
+ * in fp32, which is exact while it stays in fp32's range.  Written, for
+ * tgemm_attention_decode_lists:
+ *   to_pages    int32 [batch, heads, keep]: page numbers in order of position, -1 past them
+ *   to_lengths  int32 [batch]: positions on them
+ * first + recent <= keep; at most 2^17 pages in a list and 128 query heads on a
+ * key head.  A page number outside the cache is recorded and scores lowest.
+ */
+typedef struct {
+    const tgemm_kv_cache *cache;
+    const tgemm_kv_page_bounds *bounds;
+    tgemm_kv_sequences seq;
+    const void *Q;
+    int64_t q_heads, q_batch_stride, q_head_stride;
+    int32_t *to_pages;
+    int32_t *to_lengths;
+    int64_t to_batch_stride, to_head_stride;
+    int64_t keep, first, recent;
+    int64_t dtype;                                  /* tgemm_dtype of Q */
+} tgemm_kv_select_args;
+tgemm_status tgemm_kv_select(const tgemm_kv_select_args *args, tgemm_stream_t stream);
+
+/*
+ * tgemm_attention_decode_lists — tgemm_attention_decode with a page list for each
+ * key head: seq.pages is [batch, heads, pages_width] with strides seq.pages_stride
+ * and pages_head_stride (at least pages_width; 0: the heads share a list).
+ * Positions, the window's and the weights' too, are those of the lists.
+ */
+tgemm_status tgemm_attention_decode_lists(const tgemm_attention_decode_args *args, int64_t pages_head_stride,
+                                          tgemm_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The pages as a resource.  uses, int32 [pages] on the device, counts the
+ * sequences that hold each page; 0: free.  A list that a call below writes is not
+ * one that the same call reads, except where it says so.  New pages are the
+ * lowest free ones, in the order of the sequences.  What cannot be done (no page
+ * left, a list without room, a bad length, parent or page number) is recorded as
+ * TGEMM_ERR_CACHE and left out.  The sums of 1024 sequences' list widths stay
+ * below 2^31.
+ */
+
+/*
+ * tgemm_kv_grow — room for new tokens: lengths[b] grows by tokens[b] (int32
+ * [batch], device; NULL: one each), and the list by the pages that this takes.
+ * From the first sequence on whose pages are not there, those that need any stay
+ * as they are.
+ */
+typedef struct {
+    const tgemm_kv_cache *cache;
+    int32_t *uses;
+    int32_t *pages;                                 /* [batch, pages_stride] */
+    int32_t *lengths;
+    int64_t pages_width, pages_stride, batch;
+    const int32_t *tokens;
+} tgemm_kv_grow_args;
+tgemm_status tgemm_kv_grow(const tgemm_kv_grow_args *args, tgemm_stream_t stream);
+
+/*
+ * tgemm_kv_fork — child c takes over the positions of sequence parents[c] of
+ * `seq` (int32 [children], device; -1: none, the child is empty): full pages are
+ * shared, the rows of a last, partly filled page are copied to a page of the
+ * child's own.  Where no page is left a child has the full pages alone.  The
+ * children's lists and lengths (whose old contents are lost, not freed) may be
+ * other rows of the parents' arrays, as long as no child is a parent.
+ */
+typedef struct {
+    const tgemm_kv_cache *cache;
+    int32_t *uses;
+    tgemm_kv_sequences seq;
+    const int32_t *parents;
+    int32_t *to_pages;                              /* [children, to_stride] */
+    int32_t *to_lengths;
+    int64_t to_width, to_stride, children;
+} tgemm_kv_fork_args;
+tgemm_status tgemm_kv_fork(const tgemm_kv_fork_args *args, tgemm_stream_t stream);
+
+/* tgemm_kv_free — the sequences give their pages back: each is held once less, and lengths become 0. */
+typedef struct {
+    const tgemm_kv_cache *cache;
+    int32_t *uses;
+    const int32_t *pages;                           /* [batch, pages_stride] */
+    int32_t *lengths;
+    int64_t pages_width, pages_stride, batch;
+} tgemm_kv_free_args;
+tgemm_status tgemm_kv_free(const tgemm_kv_free_args *args, tgemm_stream_t stream);
+
+/*
+ * tgemm_kv_compact — of the pages in use, those numbered n = (their number) and
+ * above move, in order, to the free ones below n, in order, with scales and, if
+ * given, bounds.  `seq` has all sequences that hold pages.  Written:
+ *   to_pages  int32 [batch, to_stride]: the lists with the new numbers (entries past a length are left)
+ *   to_uses   int32 [pages]: the counts
+ *   in_use    int32 [1]: n; from page n on the pool is free
+ * to_pages may be seq.pages (with its stride), to_uses may be uses.  workspace:
+ * device memory of tgemm_kv_compact_workspace() bytes, 16-byte aligned; calls
+ * that may overlap on the GPU need one each.
+ */
+typedef struct {
+    const tgemm_kv_cache *cache;
+    const tgemm_kv_page_bounds *bounds;             /* NULL: none */
+    const int32_t *uses;
+    tgemm_kv_sequences seq;
+    int32_t *to_pages;
+    int64_t to_width, to_stride;
+    int32_t *to_uses;
+    int32_t *in_use;
+    void *workspace;
+    int64_t workspace_bytes;
+} tgemm_kv_compact_args;
+tgemm_status tgemm_kv_compact(const tgemm_kv_compact_args *args, tgemm_stream_t stream);
+
+/* Bytes of workspace that tgemm_kv_compact needs for a cache of `pages` pages.  Host logic only. */
+tgemm_status tgemm_kv_compact_workspace(int64_t pages, int64_t *bytes);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Norms of queries and keys for each head, with the position rotation in the
+ * same pass.
+ */
+
+/* Rows of heads, [tokens, heads, dim]: base and strides (elements, multiples of 8; bases 16-byte aligned). */
+typedef struct {
+    void *data;
+    int64_t token_stride, head_stride;
+} tgemm_rows;
+
+/*
+ * A rotation of the first 2 * pairs elements of a row, host memory:
+ *   turns        uint64 [pairs]: how far a pair turns per position, as a fraction
+ *                of 2^64 of a whole turn (frequency / (2 pi) * 2^64)
+ *   axes         int32 [pairs]: whose positions count (NULL: all 0)
+ *   interleaved  0: pair i is elements i and i + pairs (pairs a multiple of 4);
+ *                1: elements 2 i and 2 i + 1
+ */
+typedef struct {
+    const uint64_t *turns;
+    const int32_t *axes;
+    int64_t pairs, interleaved;
+} tgemm_rotary;
+
+/*
+ * tgemm_qk_norm_rope — for each row x of the queries and keys of a token
+ *
+ *   y = R(x * r * weight),   r = 1 / sqrt(mean x^2 + eps)
+ *
+ * (norm = 0: y = R(x), no weights), R turning pair i by the angle
+ * (positions[axes[i], token] + shift) * frequency_i; rotary NULL: no rotation.
+ * Weights have dim contiguous elements of `dtype`, or fp32 with weight_f32 = 1;
+ * NULL: ones.  positions is int32 [axes, tokens], device, any values; angles are
+ * right to 2^-31 of a turn wherever they are.  All in fp32, rounded once.  dim is a
+ * multiple of 8, at most 256.  q_heads or k_heads may be 0.  q_out and k_out may
+ * be q and k themselves (the same strides), and may lie side by side with others
+ * in one array; they overlap nothing else.
+ */
+typedef struct {
+    tgemm_rows q, k, q_out, k_out;
+    const void *q_weight, *k_weight;
+    const int32_t *positions;
+    int64_t axis_stride, axes, tokens, q_heads, k_heads, dim, shift;
+    const tgemm_rotary *rotary;
+    int64_t weight_f32, norm;
+    double eps;
+    int64_t dtype;
+} tgemm_qk_norm_rope_args;
+tgemm_status tgemm_qk_norm_rope(const tgemm_qk_norm_rope_args *args, tgemm_stream_t stream);
+
+/*
+ * tgemm_qk_norm_rope_backward — the gradients of tgemm_qk_norm_rope: of q and k,
+ * written to forward.q_out and forward.k_out (which may be q and k, or q_grad and
+ * k_grad, themselves), from those of what it wrote, q_grad and k_grad; and of the
+ * weights, fp32 [dim], written, not added (NULL: not wanted; they need norm = 1
+ * and the workspace, device memory of tgemm_qk_norm_rope_backward_workspace()
+ * bytes, 16-byte aligned, with any contents; calls that may overlap on the GPU
+ * need one each).  Sums are fp32 in a fixed order: results are deterministic.
+ * With norm = 0 q and k are not read.
+ */
+typedef struct {
+    tgemm_qk_norm_rope_args forward;
+    tgemm_rows q_grad, k_grad;
+    float *q_weight_grad, *k_weight_grad;
+    void *workspace;
+    int64_t workspace_bytes;
+} tgemm_qk_norm_rope_backward_args;
+tgemm_status tgemm_qk_norm_rope_backward(const tgemm_qk_norm_rope_backward_args *args, tgemm_stream_t stream);
+
+/* Bytes of workspace that tgemm_qk_norm_rope_backward needs.  Host logic only. */
+tgemm_status tgemm_qk_norm_rope_backward_workspace(int64_t dim, int64_t *bytes);
 
 /*
  * tgemm_plan — the work plan tgemm_run (and tgemm_run_ex / tgemm_run_host per
