@@ -42,8 +42,7 @@ struct RopeParams {
     long long axis_stride, tokens;
     float *partials;                        // [blocks][2][dim]
     float eps;
-    int norm, weight_f32, shift, dim, pairs;
-    int chunks;                             // parts that a token's rows are cut into
+    int norm, weight_f32, shift, dim, pairs, axes;
     int blocks;                             // of the pass that left the partial sums
     unsigned int *status;
     long long dbg_y[2];                     // debug builds: bytes of what is written
@@ -134,23 +133,6 @@ __device__ __forceinline__ int rope_element(int i, int j, const int (&unit)[2]) 
     return unit[j] * V + i;
 }
 
-template <bool kBf16, int V, bool kInterleaved>
-__device__ __forceinline__ void rope_weights(const void *w, bool f32, int dim, const int (&unit)[2], float (&a)[V], float (&b)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int e = rope_element<V, kInterleaved>(i, j, unit);
-            float x = 1.0f;
-            if (w && e < dim) {
-                if (f32) x = static_cast<const float *>(w)[e];
-                else if (kBf16) x = __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[e]);
-                else x = __half2float(static_cast<const __half *>(w)[e]);
-            }
-            (j ? b : a)[i] = x;
-        }
-}
-
 // Where lane `l` of a row's kLanes has its two units.
 template <int V, bool kInterleaved>
 __device__ __forceinline__ void rope_units(int l, int dim, int pairs, int (&unit)[2], bool (&is)[2]) {
@@ -167,6 +149,42 @@ __device__ __forceinline__ void rope_units(int l, int dim, int pairs, int (&unit
     is[1] = unit[1] < units;
 }
 
+// The weights in shared memory, as each lane of a row takes them: 16 bytes of lane l at [chunk][l].
+template <int V, int kLanes>
+struct RopeWeights {
+    float4 part[2 * V / 4][kLanes];
+};
+
+template <bool kBf16, int V, int kLanes, bool kInterleaved>
+__device__ __forceinline__ void rope_stage_weights(RopeWeights<V, kLanes> &to, const void *w, bool f32, int dim, int pairs) {
+    for (int i = threadIdx.x; i < 2 * V * kLanes; i += kRopeThreads) {
+        const int l = i / (2 * V), k = i - l * (2 * V);              // lane l's a[0 .. V - 1], then b
+        int unit[2];
+        bool is[2];
+        rope_units<V, kInterleaved>(l, dim, pairs, unit, is);
+        const int j = k / V, at = k - j * V;
+        const int e = kInterleaved ? (at / (V / 2) ? unit[1] : unit[0]) * V + 2 * (at % (V / 2)) + j : (j ? unit[1] : unit[0]) * V + at;
+        float x = 1.0f;
+        if (w && e < dim) {
+            if (f32) x = static_cast<const float *>(w)[e];
+            else if (kBf16) x = __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[e]);
+            else x = __half2float(static_cast<const __half *>(w)[e]);
+        }
+        reinterpret_cast<float *>(&to.part[k / 4][l])[k % 4] = x;
+    }
+}
+
+// chunk k of lane l: weights 4 k .. 4 k + 3 of its a and b in a row
+template <int V, int kLanes>
+__device__ __forceinline__ void rope_weights(const RopeWeights<V, kLanes> &from, int l, float (&a)[V], float (&b)[V]) {
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) {
+        const float4 x = from.part[k][l], y = from.part[V / 4 + k][l];
+        a[4 * k] = x.x, a[4 * k + 1] = x.y, a[4 * k + 2] = x.z, a[4 * k + 3] = x.w;
+        b[4 * k] = y.x, b[4 * k + 1] = y.y, b[4 * k + 2] = y.z, b[4 * k + 3] = y.w;
+    }
+}
+
 template <int N>
 __device__ __forceinline__ float rope_sum(float x) {
 #pragma unroll
@@ -174,190 +192,246 @@ __device__ __forceinline__ float rope_sum(float x) {
     return x;
 }
 
-// The angles of one token's pairs.
-template <int V>
-__device__ __forceinline__ void rope_angles(const RopeParams &p, long long token, const unsigned long long (&turns)[V],
-                                            const unsigned (&axis)[V], int first, float (&c)[V], float (&s)[V]) {
-    long long pos = 0;
-    unsigned last = ~0u;
+// The angles of a token's pairs.  The rows of a warp belong to one token, so each
+// of their lanes works out kOwn of the row's pairs and takes the others from the
+// lanes of the other rows.
+template <int V, int kLanes>
+struct RopeAngles {
+    static constexpr int kRows = 32 / kLanes, kOwn = V / kRows;
+    static_assert(kOwn >= 1 && kOwn * kRows == V, "a lane's pairs");
+    unsigned long long turns[kOwn];
+    int axis[kOwn];
+    int first;                              // of the lane's own pairs
+
+    __device__ __forceinline__ void init(const RopeParams &p, int l, int row) {
+        first = l * V + row * kOwn;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        c[i] = 1.0f;
-        s[i] = 0.0f;
-        if (first + i < p.pairs) {
-            if (axis[i] != last) {
-                last = axis[i];
-                pos = static_cast<long long>(p.positions[last * p.axis_stride + token]) + p.shift;
-            }
-            const unsigned long long t = static_cast<unsigned long long>(pos) * turns[i];
-            sincospif(static_cast<float>(static_cast<int>(t >> 32)) * 0x1p-31f, &s[i], &c[i]);
+        for (int j = 0; j < kOwn; ++j) {
+            const int at = min(first + j, kRopePairs - 1);
+            turns[j] = p.turns[at];         // 0 past the last pair: turned by nothing
+            axis[j] = p.axis[at];
         }
     }
-}
+    // places: lane a's position on axis a
+    __device__ __forceinline__ void turn(int places, int shift, int l, float (&c)[V], float (&s)[V]) const {
+        float oc[kOwn], os[kOwn];
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+            const long long pos = static_cast<long long>(__shfl_sync(0xffffffffu, places, axis[j])) + shift;
+            const unsigned long long t = static_cast<unsigned long long>(pos) * turns[j];
+            sincospif(static_cast<float>(static_cast<int>(t >> 32)) * 0x1p-31f, &os[j], &oc[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            c[i] = __shfl_sync(0xffffffffu, oc[i % kOwn], i / kOwn * kLanes + l);
+            s[i] = __shfl_sync(0xffffffffu, os[i % kOwn], i / kOwn * kLanes + l);
+        }
+    }
+};
 
-// kLanes lanes have a row, a warp 32 / kLanes rows of one token's queries or
-// keys at a time; its sines and cosines stay in registers for all of them.
+// Work.  A pass is 32 / kLanes rows, of one token's queries or of its keys, for a
+// warp; the passes of all tokens in a row are cut into equal runs, one a warp.
+struct RopeCursor {
+    long long token;
+    int pass;
+};
+
+// Passes ahead of the one at hand whose rows are on their way.
 template <bool kBf16, int V, int kLanes, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kRows = 32 / kLanes, kUnroll = 2;
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int kRows = 32 / kLanes, kWarps = kRopeThreads / 32, kAhead = 2;
+    __shared__ RopeWeights<V, kLanes> s_w[2];
     const int lane = threadIdx.x & 31, l = lane % kLanes, row = lane / kLanes;
     int unit[2];
     bool is[2];
     rope_units<V, kInterleaved>(l, p.dim, p.pairs, unit, is);
-    unsigned long long turns[V];
-    unsigned axis[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int at = min(l * V + i, kRopePairs - 1);
-        turns[i] = p.turns[at];
-        axis[i] = p.axis[at];
-    }
+    RopeAngles<V, kLanes> angles;
+    angles.init(p, l, row);
+    const float inv_dim = 1.0f / static_cast<float>(p.dim);
+    const int passes_q = (p.side[0].heads + kRows - 1) / kRows, passes = passes_q + (p.side[1].heads + kRows - 1) / kRows;
+    const long long warps = static_cast<long long>(gridDim.x) * kWarps, warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const long long all = p.tokens * passes, begin = warp * all / warps;
+    int left = static_cast<int>((warp + 1) * all / warps - begin);
+    RopeCursor use, load;
+    use.token = begin / passes;
+    use.pass = static_cast<int>(begin - use.token * passes);
+    load = use;
     griddep_wait();
     griddep_launch_dependents();
-    float wa[2][V], wb[2][V];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) rope_weights<kBf16, V, kInterleaved>(p.side[q].w, p.weight_f32, p.dim, unit, wa[q], wb[q]);
-    const float inv_dim = 1.0f / static_cast<float>(p.dim);
-    const long long items = p.tokens * p.chunks;
-    const long long warps = static_cast<long long>(gridDim.x) * (kRopeThreads / 32);
-    const int passes_q = (p.side[0].heads + kRows - 1) / kRows, passes = passes_q + (p.side[1].heads + kRows - 1) / kRows;
-    for (long long item = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5); item < items; item += warps) {
-        const long long token = p.chunks == 1 ? item : item / p.chunks;
-        const int chunk = static_cast<int>(item - token * p.chunks);
-        const int from = static_cast<int>(static_cast<long long>(chunk) * passes / p.chunks);
-        const int to = static_cast<int>(static_cast<long long>(chunk + 1) * passes / p.chunks);
-        float c[V], s[V];
-        rope_angles<V>(p, token, turns, axis, l * V, c, s);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const RopeSide &side = p.side[q];
-            const int lo = q ? max(from - passes_q, 0) : min(from, passes_q), hi = q ? max(to - passes_q, 0) : min(to, passes_q);
-            const unsigned char *const x = side.x + token * side.x_token;
-            unsigned char *const y = side.y + token * side.y_token;
-            for (int pass = lo; pass < hi; pass += kUnroll) {
-                RopeRaw<V> raw[kUnroll];
-                bool in[kUnroll][2];
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int head = (pass + u) * kRows + row;
-                    const bool there = pass + u < hi && head < side.heads;
-                    in[u][0] = there && is[0];
-                    in[u][1] = there && is[1];
-                    rope_read<V>(raw[u], x + (there ? head : 0) * side.x_head, unit, in[u]);
-                }
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    float a[V], b[V], r = 1.0f;
-                    rope_split<kBf16, V, kInterleaved>(raw[u], a, b);
-                    if (p.norm) {
-                        float sum = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < V; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
-                        r = rsqrtf(fmaf(rope_sum<kLanes>(sum), inv_dim, p.eps));
-                    }
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float f = a[i] * r * wa[q][i], g = b[i] * r * wb[q][i];
-                        a[i] = f * c[i] - g * s[i];
-                        b[i] = g * c[i] + f * s[i];
-                    }
-                    const long long at = ((pass + u) * kRows + row) * side.y_head;
-                    if ((in[u][0] || in[u][1]) &&
-                        TGEMM_CHECK(token * side.y_token + at + 2 * p.dim <= p.dbg_y[q], kChkRope, p.status))
-                        rope_write<kBf16, V, kInterleaved>(y + at, a, b, unit, in[u]);
-                }
-            }
+    auto next = [&](RopeCursor &u) {
+        if (++u.pass == passes) {
+            u.pass = 0;
+            ++u.token;
         }
+    };
+    int loads = left;
+    RopeRaw<V> ring[kAhead];
+    auto request = [&](RopeRaw<V> &raw) {
+        const bool q = load.pass >= passes_q;
+        const RopeSide &side = p.side[q ? 1 : 0];
+        const int head = (load.pass - (q ? passes_q : 0)) * kRows + row;
+        const bool there = loads > 0 && head < side.heads;
+        const bool in[2] = {there && is[0], there && is[1]};
+        rope_read<V>(raw, side.x + load.token * side.x_token + (there ? head : 0) * side.x_head, unit, in);
+        if (--loads > 0) next(load);
+    };
+    auto places_of = [&](long long token) {
+        return lane < p.axes && token < p.tokens ? p.positions[lane * p.axis_stride + token] : 0;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) request(ring[i]);
+    int places = places_of(use.token);
+    rope_stage_weights<kBf16, V, kLanes, kInterleaved>(s_w[0], p.side[0].w, p.weight_f32, p.dim, p.pairs);
+    rope_stage_weights<kBf16, V, kLanes, kInterleaved>(s_w[1], p.side[1].w, p.weight_f32, p.dim, p.pairs);
+    __syncthreads();
+    float c[V], s[V];
+    bool fresh = true;                      // the token's angles are to be worked out
+    for (; left > 0; --left) {
+        if (fresh) {
+            angles.turn(places, p.shift, l, c, s);
+            places = places_of(use.token + 1);
+        }
+        float a[V], b[V], wa[V], wb[V];
+        rope_split<kBf16, V, kInterleaved>(ring[0], a, b);
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) ring[i] = ring[i + 1];
+        request(ring[kAhead - 1]);
+        const bool q = use.pass >= passes_q;
+        const RopeSide &side = p.side[q ? 1 : 0];
+        const int head = (use.pass - (q ? passes_q : 0)) * kRows + row;
+        rope_weights(s_w[q ? 1 : 0], l, wa, wb);
+        float r = 1.0f;
+        if (p.norm) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
+            r = rsqrtf(fmaf(rope_sum<kLanes>(sum), inv_dim, p.eps));
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float f = a[i] * r * wa[i], g = b[i] * r * wb[i];
+            a[i] = f * c[i] - g * s[i];
+            b[i] = g * c[i] + f * s[i];
+        }
+        const bool there = head < side.heads;
+        const bool in[2] = {there && is[0], there && is[1]};
+        const long long at = use.token * side.y_token + (there ? head : 0) * side.y_head;
+        if (there && TGEMM_CHECK(at + 2 * p.dim <= p.dbg_y[q ? 1 : 0], kChkRope, p.status))
+            rope_write<kBf16, V, kInterleaved>(side.y + at, a, b, unit, in);
+        const long long token = use.token;
+        next(use);
+        fresh = use.token != token;
     }
 }
 
 template <bool kBf16, int V, int kLanes, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_backward_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kRows = 32 / kLanes, kWarps = kRopeThreads / 32;
+    __shared__ RopeWeights<V, kLanes> s_w[2];
     __shared__ float s_dw[kWarps][2][2 * kRopePairs];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % kLanes, row = lane / kLanes;
+    const int lane = threadIdx.x & 31, l = lane % kLanes, row = lane / kLanes;
     int unit[2];
     bool is[2];
     rope_units<V, kInterleaved>(l, p.dim, p.pairs, unit, is);
-    unsigned long long turns[V];
-    unsigned axis[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int at = min(l * V + i, kRopePairs - 1);
-        turns[i] = p.turns[at];
-        axis[i] = p.axis[at];
-    }
+    RopeAngles<V, kLanes> angles;
+    angles.init(p, l, row);
+    const float inv_dim = 1.0f / static_cast<float>(p.dim);
+    const int passes_q = (p.side[0].heads + kRows - 1) / kRows, passes = passes_q + (p.side[1].heads + kRows - 1) / kRows;
+    const long long warps = static_cast<long long>(gridDim.x) * kWarps, warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const long long all = p.tokens * passes, begin = warp * all / warps;
+    int left = static_cast<int>((warp + 1) * all / warps - begin);
+    RopeCursor use, load;
+    use.token = passes > 0 ? begin / passes : 0;
+    use.pass = passes > 0 ? static_cast<int>(begin - use.token * passes) : 0;
+    load = use;
     griddep_wait();
     griddep_launch_dependents();
-    const float inv_dim = 1.0f / static_cast<float>(p.dim);
-    const long long items = p.tokens * p.chunks;
-    const long long warps = static_cast<long long>(gridDim.x) * kWarps;
-    const int passes_q = (p.side[0].heads + kRows - 1) / kRows, passes = passes_q + (p.side[1].heads + kRows - 1) / kRows;
+    auto next = [&](RopeCursor &u) {
+        if (++u.pass == passes) {
+            u.pass = 0;
+            ++u.token;
+        }
+    };
+    int loads = left;
+    RopeRaw<V> next_x, next_g;
+    auto request = [&]() {
+        const bool q = load.pass >= passes_q;
+        const RopeSide &side = p.side[q ? 1 : 0];
+        const int head = (load.pass - (q ? passes_q : 0)) * kRows + row;
+        const bool there = loads > 0 && head < side.heads;
+        const bool in[2] = {there && is[0], there && is[1]};
+        const bool x_in[2] = {in[0] && p.norm, in[1] && p.norm};
+        rope_read<V>(next_g, side.g + load.token * side.g_token + (there ? head : 0) * side.g_head, unit, in);
+        rope_read<V>(next_x, side.x + load.token * side.x_token + (there ? head : 0) * side.x_head, unit, x_in);
+        if (--loads > 0) next(load);
+    };
+    auto places_of = [&](long long token) {
+        return lane < p.axes && token < p.tokens ? p.positions[lane * p.axis_stride + token] : 0;
+    };
+    request();
+    int places = places_of(use.token);
+    rope_stage_weights<kBf16, V, kLanes, kInterleaved>(s_w[0], p.side[0].w, p.weight_f32, p.dim, p.pairs);
+    rope_stage_weights<kBf16, V, kLanes, kInterleaved>(s_w[1], p.side[1].w, p.weight_f32, p.dim, p.pairs);
+    __syncthreads();
     float da[2][V], db[2][V];
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < V; ++i) da[q][i] = db[q][i] = 0.0f;
-    for (long long item = static_cast<long long>(blockIdx.x) * kWarps + warp; item < items; item += warps) {
-        const long long token = p.chunks == 1 ? item : item / p.chunks;
-        const int chunk = static_cast<int>(item - token * p.chunks);
-        const int from = static_cast<int>(static_cast<long long>(chunk) * passes / p.chunks);
-        const int to = static_cast<int>(static_cast<long long>(chunk + 1) * passes / p.chunks);
-        float c[V], s[V];
-        rope_angles<V>(p, token, turns, axis, l * V, c, s);
+    float c[V], s[V];
+    bool fresh = true;                      // the token's angles are to be worked out
+    auto step = [&](float (&da)[V], float (&db)[V], const RopeWeights<V, kLanes> &weights, const RopeSide &side, int pass, long long dbg) {
+        float a[V], b[V], x[V], y[V];
+        rope_split<kBf16, V, kInterleaved>(next_g, a, b);
+        rope_split<kBf16, V, kInterleaved>(next_x, x, y);
+        request();
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const RopeSide &side = p.side[q];
-            const int lo = q ? max(from - passes_q, 0) : min(from, passes_q), hi = q ? max(to - passes_q, 0) : min(to, passes_q);
-            if (lo >= hi) continue;
-            float wa[V], wb[V];
-            rope_weights<kBf16, V, kInterleaved>(side.w, p.weight_f32, p.dim, unit, wa, wb);
-            for (int pass = lo; pass < hi; ++pass) {
-                const int head = pass * kRows + row;
-                const bool there = head < side.heads;
-                const bool in[2] = {there && is[0], there && is[1]};
-                const long long h = there ? head : 0;
-                RopeRaw<V> rx, rg;
-                rope_read<V>(rg, side.g + token * side.g_token + h * side.g_head, unit, in);
-                if (p.norm) rope_read<V>(rx, side.x + token * side.x_token + h * side.x_head, unit, in);
-                float a[V], b[V], x[V], y[V];
-                rope_split<kBf16, V, kInterleaved>(rg, a, b);
+        for (int i = 0; i < V; ++i) {
+            const float f = a[i] * c[i] + b[i] * s[i];
+            b[i] = b[i] * c[i] - a[i] * s[i];
+            a[i] = f;
+        }
+        if (p.norm) {
+            float sum = 0.0f, dot = 0.0f;
+            {
+                float wa[V], wb[V];
+                rope_weights(weights, l, wa, wb);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float f = a[i] * c[i] + b[i] * s[i];
-                    b[i] = b[i] * c[i] - a[i] * s[i];
-                    a[i] = f;
+                    sum = fmaf(x[i], x[i], fmaf(y[i], y[i], sum));
+                    dot = fmaf(a[i] * wa[i], x[i], fmaf(b[i] * wb[i], y[i], dot));
                 }
-                if (p.norm) {
-                    rope_split<kBf16, V, kInterleaved>(rx, x, y);
-                    float sum = 0.0f, dot = 0.0f;
+            }
+            sum = rope_sum<kLanes>(sum);
+            dot = rope_sum<kLanes>(dot);
+            const float r = rsqrtf(fmaf(sum, inv_dim, p.eps)), back = r * r * dot * inv_dim;
+            float wa[V], wb[V];
+            rope_weights(weights, l, wa, wb);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        sum = fmaf(x[i], x[i], fmaf(y[i], y[i], sum));
-                        dot = fmaf(a[i] * wa[i], x[i], fmaf(b[i] * wb[i], y[i], dot));
-                    }
-                    sum = rope_sum<kLanes>(sum);
-                    dot = rope_sum<kLanes>(dot);
-                    const float r = rsqrtf(fmaf(sum, inv_dim, p.eps)), back = r * r * dot * inv_dim;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        da[q][i] = fmaf(a[i], x[i] * r, da[q][i]);
-                        db[q][i] = fmaf(b[i], y[i] * r, db[q][i]);
-                        a[i] = r * fmaf(-x[i], back, a[i] * wa[i]);
-                        b[i] = r * fmaf(-y[i], back, b[i] * wb[i]);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        a[i] *= wa[i];
-                        b[i] *= wb[i];
-                    }
-                }
-                const long long at = token * side.y_token + h * side.y_head;
-                if (there && TGEMM_CHECK(at + 2 * p.dim <= p.dbg_y[q], kChkRope, p.status))
-                    rope_write<kBf16, V, kInterleaved>(side.y + at, a, b, unit, in);
+            for (int i = 0; i < V; ++i) {
+                da[i] = fmaf(a[i], x[i] * r, da[i]);
+                db[i] = fmaf(b[i], y[i] * r, db[i]);
+                a[i] = r * fmaf(-x[i], back, a[i] * wa[i]);
+                b[i] = r * fmaf(-y[i], back, b[i] * wb[i]);
             }
         }
+        const int head = pass * kRows + row;
+        const bool there = head < side.heads;
+        const bool in[2] = {there && is[0], there && is[1]};
+        const long long at = use.token * side.y_token + (there ? head : 0) * side.y_head;
+        if (there && TGEMM_CHECK(at + 2 * p.dim <= dbg, kChkRope, p.status))
+            rope_write<kBf16, V, kInterleaved>(side.y + at, a, b, unit, in);
+    };
+    for (; left > 0; --left) {
+        if (fresh) {
+            angles.turn(places, p.shift, l, c, s);
+            places = places_of(use.token + 1);
+        }
+        if (use.pass < passes_q) step(da[0], db[0], s_w[0], p.side[0], use.pass, p.dbg_y[0]);
+        else step(da[1], db[1], s_w[1], p.side[1], use.pass - passes_q, p.dbg_y[1]);
+        const long long token = use.token;
+        next(use);
+        fresh = use.token != token;
     }
     if (!p.partials) return;
     // The block's sums of the weight gradients: rows of a warp, then the warps.
@@ -371,7 +445,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_backward_kernel(const __gri
 #pragma unroll
                 for (int o = kLanes; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
                 const int e = rope_element<V, kInterleaved>(i, j, unit);
-                if (row == 0 && e < p.dim) s_dw[warp][q][e] = x;
+                if (row == 0 && e < p.dim) s_dw[threadIdx.x >> 5][q][e] = x;
             }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * p.dim; i += kRopeThreads) {

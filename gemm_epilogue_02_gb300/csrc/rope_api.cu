@@ -61,7 +61,7 @@ tgemm_status check_common(const tgemm_qk_norm_rope_args *a, RopeParams *p, int *
     const tgemm_rotary *r = a->rotary;
     if (a->tokens < 0 || a->tokens > INT32_MAX || a->q_heads < 0 || a->k_heads < 0 || a->q_heads > 65535 || a->k_heads > 65535 ||
         a->dim < 8 || a->dim > 2 * kRopePairs || a->dim % 8 != 0 || !valid_dtype(a->dtype) || (a->norm != 0 && a->norm != 1) ||
-        (a->weight_f32 != 0 && a->weight_f32 != 1) || a->shift < INT32_MIN || a->shift > INT32_MAX || a->axes < 0 || a->axes > 255)
+        (a->weight_f32 != 0 && a->weight_f32 != 1) || a->shift < INT32_MIN || a->shift > INT32_MAX || a->axes < 0 || a->axes > 32)
         return TGEMM_ERR_INVALID_ARG;
     if (a->norm ? !(a->eps >= 0.0) || !std::isfinite(a->eps) : (a->q_weight || a->k_weight)) return TGEMM_ERR_INVALID_ARG;
     if (!a->norm && !r) return TGEMM_ERR_INVALID_ARG;
@@ -88,6 +88,7 @@ tgemm_status check_common(const tgemm_qk_norm_rope_args *a, RopeParams *p, int *
     if (!aligned4(a->positions) || reinterpret_cast<uintptr_t>(a->q_weight) % weight || reinterpret_cast<uintptr_t>(a->k_weight) % weight)
         return TGEMM_ERR_ALIGNMENT;
     p->positions = a->positions;
+    p->axes = r && r->pairs > 0 ? static_cast<int>(a->axes) : 0;
     p->axis_stride = a->axis_stride;
     p->tokens = a->tokens;
     p->dim = static_cast<int>(a->dim);
@@ -122,29 +123,20 @@ void set_side(RopeSide &s, const Rows &x, const Rows &y, const Rows *g, const vo
     s.heads = static_cast<int>(x.heads);
 }
 
-// Parts of a token's rows: one where there are tokens for all warps, else as many as that takes.
-void set_chunks(RopeParams &p, int lanes, int unroll, int64_t warps) {
+// A warp a pass, or as many blocks as fit the GPU at once.
+unsigned rope_blocks(const RopeParams &p, int lanes, int64_t most) {
     const int rows = 32 / lanes;
     const int64_t passes = (p.side[0].heads + rows - 1) / rows + (p.side[1].heads + rows - 1) / rows;
-    const int64_t most = std::max<int64_t>(1, (passes + unroll - 1) / unroll);
-    p.chunks = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (warps + p.tokens - 1) / std::max<int64_t>(1, p.tokens))));
-}
-
-unsigned rope_blocks(const RopeParams &p, int64_t most) {
-    const int64_t blocks = (p.tokens * p.chunks + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    const int64_t blocks = (p.tokens * passes + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
     return static_cast<unsigned>(std::max<int64_t>(1, std::min(blocks, most)));
 }
 
 template <bool kBf16, int V, int kLanes, bool kInterleaved>
 cudaError_t launch_rope(const RuntimeInfo &rt, RopeParams &p, bool backward, cudaStream_t s) {
-    constexpr int kWarps = kRopeThreads / 32;
-    if (!backward) {
-        set_chunks(p, kLanes, 2, static_cast<int64_t>(rt.num_sms) * 2 * kWarps);
-        return launch(rope_kernel<kBf16, V, kLanes, kInterleaved>, dim3(rope_blocks(p, static_cast<int64_t>(rt.num_sms) * 8)), kRopeThreads,
-                      0, s, p);
-    }
-    set_chunks(p, kLanes, 1, static_cast<int64_t>(rt.num_sms) * 2 * kWarps);
-    const unsigned blocks = rope_blocks(p, std::min<int64_t>(kRopeMaxBlocks, static_cast<int64_t>(rt.num_sms) * 2));
+    if (!backward)
+        return launch(rope_kernel<kBf16, V, kLanes, kInterleaved>, dim3(rope_blocks(p, kLanes, static_cast<int64_t>(rt.num_sms) * 2)),
+                      kRopeThreads, 0, s, p);
+    const unsigned blocks = rope_blocks(p, kLanes, std::min<int64_t>(kRopeMaxBlocks, static_cast<int64_t>(rt.num_sms) * 2));
     p.blocks = static_cast<int>(blocks);
     const cudaError_t e = launch(rope_backward_kernel<kBf16, V, kLanes, kInterleaved>, dim3(blocks), kRopeThreads, 0, s, p);
     if (e != cudaSuccess || !p.partials) return e;

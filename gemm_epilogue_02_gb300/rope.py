@@ -31,8 +31,8 @@ class Rotary:
     def __init__(self, frequencies, axes=None, interleaved: bool = False):
         rates = [float(f) for f in frequencies]
         axes = [0] * len(rates) if axes is None else [int(a) for a in axes]
-        if len(axes) != len(rates) or any(a < 0 or a > 254 for a in axes):
-            raise ValueError("axes must name an axis, 0 to 254, for each frequency")
+        if len(axes) != len(rates) or any(a < 0 or a > 31 for a in axes):
+            raise ValueError("axes must name an axis, 0 to 31, for each frequency")
         if not interleaved and len(rates) % 4:
             raise ValueError("pairs that are not interleaved must be a multiple of 4")
         try:
