@@ -17,6 +17,7 @@ namespace tgemm {
 namespace {
 
 constexpr int kChooseMaxPages = 1 << 17;      // of a page list: eight blocks' keys then fit their shared memory
+constexpr int kChooseMaxBytes = 224 * 1024;   // of a block's dynamic shared memory
 
 tgemm_status check_bounds(const tgemm_kv_page_bounds *b, const tgemm_kv_cache *c, KvBounds *view, Extent *e, Extent *es) {
     if (!b || c->dim % 16 != 0) return TGEMM_ERR_INVALID_ARG;
@@ -67,46 +68,68 @@ bool cache_overlaps(const tgemm_kv_cache *c, const Extent &k, const Extent &v, c
 int row_lanes(int bytes) { return bytes <= 128 ? 8 : bytes <= 256 ? 16 : 32; }
 
 // ---------------------------------------------------------------- bounds and choice
+template <bool kBf16, bool kE4m3, int kLanes>
+cudaError_t launch_bounds_lanes(const RuntimeInfo &rt, const BoundsParams &p, cudaStream_t s) {
+    // Pages that there can be, a warp each.
+    constexpr int kRows = 32 / kLanes;
+    const int64_t most = p.starts ? static_cast<int64_t>(p.table.batch) * p.table.width : p.table.batch;
+    const int64_t blocks = std::max<int64_t>(1, (most * p.cache.heads + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32));
+    auto grid = [&](int ctas) { return dim3(static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(rt.num_sms) * ctas))); };
+    // Pages that four requests of a lane cover need no more.
+    if (p.cache.page_size <= 4 * kRows)
+        return launch(page_bounds_kernel<kBf16, kE4m3, kLanes, 4>, grid(kE4m3 ? 3 : 4), kBoundsThreads, 0, s, p);
+    return launch(page_bounds_kernel<kBf16, kE4m3, kLanes, 8>, grid(kE4m3 ? 2 : 4), kBoundsThreads, 0, s, p);
+}
+
 template <bool kBf16, bool kE4m3>
 cudaError_t launch_bounds(const RuntimeInfo &rt, const BoundsParams &p, cudaStream_t s) {
-    // Pages that there can be, a warp each.
-    const int64_t most = p.starts ? static_cast<int64_t>(p.table.batch) * p.table.width : p.table.batch;
-    const int64_t blocks = (most * p.cache.heads + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32);
-    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(blocks, static_cast<int64_t>(rt.num_sms) * kBoundsCtas))));
     switch (row_lanes(p.cache.row_bytes)) {
-        case 8: return launch(page_bounds_kernel<kBf16, kE4m3, 8>, grid, kBoundsThreads, 0, s, p);
-        case 16: return launch(page_bounds_kernel<kBf16, kE4m3, 16>, grid, kBoundsThreads, 0, s, p);
+        case 8: return launch_bounds_lanes<kBf16, kE4m3, 8>(rt, p, s);
+        case 16: return launch_bounds_lanes<kBf16, kE4m3, 16>(rt, p, s);
         default:                                   // e4m3 rows have 256 bytes at most
             if constexpr (kE4m3) return cudaErrorInvalidValue;
-            else return launch(page_bounds_kernel<kBf16, kE4m3, 32>, grid, kBoundsThreads, 0, s, p);
+            else return launch_bounds_lanes<kBf16, kE4m3, 32>(rt, p, s);
     }
 }
 
-template <int kThreads, bool kBf16, int kChunks>
-cudaError_t launch_choose_shape(const RuntimeInfo &rt, ChooseParams &p, int cluster, cudaStream_t s) {
-    auto kernel = page_choose_kernel<kThreads, kBf16, kChunks>;
+template <int kThreads, bool kBf16, int kChunks, int kStages>
+cudaError_t launch_choose_stages(const RuntimeInfo &rt, ChooseParams &p, int cluster, cudaStream_t s) {
+    using Shape = ChooseShape<kThreads, kChunks, kStages>;
+    auto kernel = page_choose_kernel<kThreads, kBf16, kChunks, kStages>;
     static std::atomic<uint64_t> ready{0};      // bit per device
     const uint64_t bit = uint64_t(1) << rt.device;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
         const RelaxedCapture relaxed;
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   choose_bytes(kChooseMaxPages / 8, kChooseGroup, kChunks * 64));
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kChooseMaxBytes);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    p.cached = (p.table.width + cluster - 1) / cluster;
     const dim3 grid(static_cast<unsigned>(cluster), static_cast<unsigned>(p.cache.heads), static_cast<unsigned>(p.table.batch));
-    return launch(kernel, grid, kThreads, static_cast<size_t>(choose_bytes(p.cached, p.group, p.cache.dim)), s, p, cluster);
+    return launch(kernel, grid, kThreads, static_cast<size_t>(Shape::bytes(p.cached, p.group, p.cache.dim)), s, p, cluster);
+}
+
+template <int kThreads, bool kBf16, int kChunks>
+cudaError_t launch_choose_shape(const RuntimeInfo &rt, ChooseParams &p, cudaStream_t s) {
+    // A block does 128 pages a microsecond, and a cluster's barriers cost it three: with lists of up to 512 pages a block
+    // alone is best, beyond them as many of a cluster as leave each an SM (1251 pages, 8 heads: one 16.1 us, two 14.1, four
+    // 11.6, eight 10.8; 251 pages: one 6.0, two 9.2; 128 lists of 2048: one 24, two 37).
+    int cluster = 1;
+    const int64_t lists = static_cast<int64_t>(p.table.batch) * p.cache.heads;
+    if (p.table.width > 512)
+        while (cluster < 8 && 2 * cluster * lists <= rt.num_sms) cluster *= 2;
+    while (cluster < 8 && cluster * (kChooseMaxPages / 8) < p.table.width) cluster *= 2;
+    p.cached = (p.table.width + cluster - 1) / cluster;
+    // Three stages let an SM have two blocks; queries of large groups over long lists leave room for two.
+    if (ChooseShape<kThreads, kChunks, 3>::bytes(p.cached, p.group, p.cache.dim) <= kChooseMaxBytes)
+        return launch_choose_stages<kThreads, kBf16, kChunks, 3>(rt, p, cluster, s);
+    return launch_choose_stages<kThreads, kBf16, kChunks, 2>(rt, p, cluster, s);
 }
 
 template <bool kBf16>
 cudaError_t launch_choose(const RuntimeInfo &rt, ChooseParams &p, cudaStream_t s) {
-    constexpr int kThreads = 256;
-    int cluster = 1;
-    while (cluster < 8 && cluster * 1024 < p.table.width) cluster *= 2;
-    if (p.cache.dim <= 64) return launch_choose_shape<kThreads, kBf16, 1>(rt, p, cluster, s);
-    if (p.cache.dim <= 128) return launch_choose_shape<kThreads, kBf16, 2>(rt, p, cluster, s);
-    return launch_choose_shape<kThreads, kBf16, 4>(rt, p, cluster, s);
+    if (p.cache.dim <= 64) return launch_choose_shape<256, kBf16, 1>(rt, p, s);
+    if (p.cache.dim <= 128) return launch_choose_shape<256, kBf16, 2>(rt, p, s);
+    return launch_choose_shape<128, kBf16, 4>(rt, p, s);
 }
 
 }  // namespace

@@ -10,14 +10,17 @@
 // whole numbers of a power of two found in the same way, sum_d max(q_d lo_d, q_d
 // hi_d), times both powers; a page's score is the largest over the group's
 // heads.  The sum is that of q+ hi + q- lo (q+ = max(q, 0), q- = min(q, 0)), two
-// products of 8-bit whole numbers with pages as rows and heads as columns.  A
-// sum is below 2^23, so the score is exact in fp32, and the same pages are
-// chosen however the work is split.
+// products with pages as rows and heads as columns.  The whole numbers are widened
+// to fp16 for them (m16n8k16 takes 2.1 cycles of an SM, m16n8k32 of 8-bit whole
+// numbers 16.3) with 1152 added, which the accumulators of 64 dims each begin
+// without: what they hold stays below 2^24, so every sum is exact in fp32 in any
+// order, and the same pages are chosen however the work is split.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "copy_async.cuh"
 #include "kv_cache.cuh"
 #include "kv_rank.cuh"
 
@@ -71,7 +74,7 @@ struct BoundsParams {
     unsigned int *status;
 };
 
-constexpr int kBoundsThreads = 256, kBoundsCtas = 4;     // per SM
+constexpr int kBoundsThreads = 256;
 
 // Pages of sequence b that its newest tokens complete: [*from, return).
 __host__ __device__ inline int kv_completed(int n, long long fresh, int page_size, int *from) {
@@ -83,7 +86,7 @@ __host__ __device__ inline int kv_completed(int n, long long fresh, int page_siz
 }
 
 template <bool kBf16>
-__device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b) {       // a NaN gives way to a number
     if (kBf16) {
         const __nv_bfloat162 m = __hmin2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&m);
@@ -105,13 +108,40 @@ __device__ __forceinline__ float2 bounds_widen(uint32_t w) {
     if (kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
+__device__ __forceinline__ float min3(float a, float b, float c) {           // NaN gives way to numbers
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// A warp's minima of its rows' groups of kLanes lanes, `values` of each lane:
+// group 2^k's lanes hand half of what they have to the other's, down to each group
+// having its share (group r: share r of the kRows shares, in order).  The least
+// is taken of all, so bounds from above go in with their signs changed.
+template <int kLanes, int N, typename T, typename Min>
+__device__ __forceinline__ void bounds_scatter(T (&x)[N], int row, Min least) {
+    int n = N;
+#pragma unroll
+    for (int o = 16; o >= kLanes; o >>= 1) {
+        n /= 2;
+        const bool upper = (row * kLanes) & o;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            if (i < n) {
+                const T give = upper ? x[i] : x[i + n], keep = upper ? x[i + n] : x[i];
+                x[i] = least(keep, __shfl_xor_sync(0xffffffffu, give, o));
+            }
+    }
+}
 
 // A warp has one page and head at a time; kLanes lanes hold a row in 16-byte
-// pieces, 32 / kLanes rows at once.  Neighbouring warps have neighbouring heads
-// of a page.
-template <bool kBf16, bool kE4m3, int kLanes>
-__global__ void __launch_bounds__(kBoundsThreads, kBoundsCtas) page_bounds_kernel(const BoundsParams p) {
-    constexpr int kWarps = kBoundsThreads / 32, kRows = 32 / kLanes, kPer = kE4m3 ? 16 : 8, kUnroll = 8;
+// pieces, 32 / kLanes rows at once, kUnroll of them requested together.
+// Neighbouring warps have neighbouring heads of a page.  Reading the keys bounds it
+// with 16 bits and pages of 64 (200000 positions of 8 heads, 128 wide: 66.5 us, 1.00
+// of the copy rate); small pages and e4m3 cost instructions.
+template <bool kBf16, bool kE4m3, int kLanes, int kUnroll>
+__global__ void __launch_bounds__(kBoundsThreads, kE4m3 ? (kUnroll > 4 ? 2 : 3) : 4) page_bounds_kernel(const BoundsParams p) {
+    constexpr int kWarps = kBoundsThreads / 32, kRows = 32 / kLanes, kPer = kE4m3 ? 16 : 8;
     __shared__ int s_end[kBoundsThreads + 1];      // pages of the sequences of this round, summed up
     __shared__ int s_from[kBoundsThreads];
     __shared__ int s_sum[kWarps];
@@ -143,26 +173,39 @@ __global__ void __launch_bounds__(kBoundsThreads, kBoundsCtas) page_bounds_kerne
         s_from[threadIdx.x] = from;
         __syncthreads();
         const long long items = static_cast<long long>(s_end[kBoundsThreads]) * p.cache.heads;
-        // Warp `me` has the items i with (base + i) % warps == me.
-        for (long long i = (me + warps - base % warps) % warps; i < items; i += warps) {
-            const int at = static_cast<int>(i / p.cache.heads), head = static_cast<int>(i - static_cast<long long>(at) * p.cache.heads);
+        // The page of item i, and its head.
+        auto find = [&](long long i, int *head) {
+            const int at = static_cast<int>(i / p.cache.heads);
+            *head = static_cast<int>(i - static_cast<long long>(at) * p.cache.heads);
             int lo = 0, hi = kBoundsThreads;       // s_end[lo] <= at < s_end[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 if (s_end[mid] <= at) lo = mid;
                 else hi = mid;
             }
-            const int page = p.table.pages[(b0 + lo) * p.table.stride + s_from[lo] + at - s_end[lo]];
+            return p.table.pages[(b0 + lo) * p.table.stride + s_from[lo] + at - s_end[lo]];
+        };
+        // Warp `me` has the items i with (base + i) % warps == me; the next one's page is looked up a step ahead.
+        long long i = (me + warps - base % warps) % warps;
+        int next_head = 0, next_page = i < items ? find(i, &next_head) : 0;
+        for (; i < items; i += warps) {
+            const int page = next_page, head = next_head;
+            if (i + warps < items) next_page = find(i + warps, &next_head);
             if (page < 0 || page >= p.cache.pages) {
                 if (lane == 0) record_status(p.status, kStatusCache);
                 continue;
             }
             const unsigned char *const keys = p.cache.k + kv_offset(p.cache, page, 0, head) + (inside ? piece * 16 : 0);
             const float *const scales = kE4m3 ? p.cache.k_scale + kv_scale_offset(p.cache, page, 0, head) : nullptr;
-            float least[kPer], most[kPer];
+            // Each channel's least key, and its largest with the sign changed: after the exchange a lane has kOwn of
+            // these 2 * kPer, those of `share`.
+            constexpr int kOwn = 2 * kPer / kRows;
+            float least[kOwn];
             if constexpr (!kE4m3) {
                 constexpr uint32_t kNan = 0x7FFF7FFFu;      // gives way to any number
-                uint32_t a[4] = {kNan, kNan, kNan, kNan}, z[4] = {kNan, kNan, kNan, kNan};
+                uint32_t m[8], z[4];                        // least; largest
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m[j] = z[j] = kNan;
                 for (int s0 = row; s0 < p.cache.page_size; s0 += kRows * kUnroll) {
                     uint4 x[kUnroll];
 #pragma unroll
@@ -177,33 +220,28 @@ __global__ void __launch_bounds__(kBoundsThreads, kBoundsCtas) page_bounds_kerne
                         const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            a[j] = min_pair<kBf16>(a[j], w[j]);
+                            m[j] = min_pair<kBf16>(m[j], w[j]);
                             z[j] = most_pair<kBf16>(z[j], w[j]);
                         }
                     }
                 }
 #pragma unroll
-                for (int o = kLanes; o < 32; o <<= 1)
+                for (int j = 0; j < 4; ++j) m[4 + j] = z[j] ^ 0x80008000u;
+                bounds_scatter<kLanes>(m, row, [](uint32_t a, uint32_t b) { return min_pair<kBf16>(a, b); });
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        a[j] = min_pair<kBf16>(a[j], __shfl_xor_sync(0xffffffffu, a[j], o));
-                        z[j] = most_pair<kBf16>(z[j], __shfl_xor_sync(0xffffffffu, z[j], o));
-                    }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = bounds_widen<kBf16>(a[j]), g = bounds_widen<kBf16>(z[j]);
+                for (int j = 0; j < kOwn / 2; ++j) {
+                    const float2 f = bounds_widen<kBf16>(m[j]);
                     least[2 * j] = f.x, least[2 * j + 1] = f.y;
-                    most[2 * j] = g.x, most[2 * j + 1] = g.y;
                 }
             } else {
+                float m[2 * kPer];
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) least[j] = most[j] = __uint_as_float(0x7FFFFFFFu);
-                constexpr int kSome = 4;
-                for (int s0 = row; s0 < p.cache.page_size; s0 += kRows * kSome) {
-                    uint4 x[kSome];
-                    float scale[kSome];
+                for (int j = 0; j < 2 * kPer; ++j) m[j] = __uint_as_float(0x7FFFFFFFu);
+                for (int s0 = row; s0 < p.cache.page_size; s0 += kRows * kUnroll) {
+                    uint4 x[kUnroll];
+                    float scale[kUnroll];
 #pragma unroll
-                    for (int u = 0; u < kSome; ++u) {
+                    for (int u = 0; u < kUnroll; ++u) {
                         const int slot = s0 + u * kRows;
                         x[u] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
                         scale[u] = 1.0f;
@@ -212,66 +250,72 @@ __global__ void __launch_bounds__(kBoundsThreads, kBoundsCtas) page_bounds_kerne
                             scale[u] = scales[slot * p.cache.scale_slot_stride];
                         }
                     }
+                    // Two rows at a time.
 #pragma unroll
-                    for (int u = 0; u < kSome; ++u) {
-                        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                    for (int u = 0; u < kUnroll; u += 2) {
+                        if (s0 - row + u * kRows >= p.cache.page_size) break;      // all rows of the warp
+                        const uint32_t w[2][4] = {{x[u].x, x[u].y, x[u].z, x[u].w}, {x[u + 1].x, x[u + 1].y, x[u + 1].z, x[u + 1].w}};
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(
-                                    static_cast<__nv_fp8x2_storage_t>((w[j] >> (16 * h)) & 0xFFFFu), __NV_E4M3);
-                                const float2 f = __half22float2(__half2(r));
-                                const float v0 = f.x * scale[u], v1 = f.y * scale[u];
+                                float2 v[2];
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(
+                                        static_cast<__nv_fp8x2_storage_t>((w[k][j] >> (16 * h)) & 0xFFFFu), __NV_E4M3);
+                                    v[k] = __half22float2(__half2(r));
+                                    v[k] = make_float2(v[k].x * scale[u + k], v[k].y * scale[u + k]);
+                                }
                                 const int e = 4 * j + 2 * h;
-                                least[e] = fminf(least[e], v0), most[e] = fmaxf(most[e], v0);
-                                least[e + 1] = fminf(least[e + 1], v1), most[e + 1] = fmaxf(most[e + 1], v1);
+                                m[e] = min3(m[e], v[0].x, v[1].x);
+                                m[e + 1] = min3(m[e + 1], v[0].y, v[1].y);
+                                m[kPer + e] = min3(m[kPer + e], -v[0].x, -v[1].x);
+                                m[kPer + e + 1] = min3(m[kPer + e + 1], -v[0].y, -v[1].y);
                             }
                     }
                 }
+                bounds_scatter<kLanes>(m, row, [](float a, float b) { return fminf(a, b); });
 #pragma unroll
-                for (int o = kLanes; o < 32; o <<= 1)
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j) {
-                        least[j] = fminf(least[j], __shfl_xor_sync(0xffffffffu, least[j], o));
-                        most[j] = fmaxf(most[j], __shfl_xor_sync(0xffffffffu, most[j], o));
-                    }
+                for (int j = 0; j < kOwn; ++j) least[j] = m[j];
             }
             float top = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
+            for (int j = 0; j < kOwn; ++j) {
                 least[j] = kv_finite(least[j]);
-                most[j] = kv_finite(most[j]);
-                top = fmaxf(top, fmaxf(-least[j], most[j]));
+                top = fmaxf(top, -least[j]);
             }
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float s = kv_bounds_scale(top), up = kv_bounds_inverse(s);
+            // (numbers >= 0 have the order of their bits)
+            const float s = kv_bounds_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)))), up = kv_bounds_inverse(s);
             const long long to = static_cast<long long>(page) * p.cache.heads + head;
-            uint32_t out[2][kPer / 4];
+            // Shares 0 .. kRows / 2 - 1 are the lower bounds' channels in order, the others the upper ones'.  With one row
+            // at a time a lane has both.
+            uint32_t out[kOwn / 4];
 #pragma unroll
-            for (int j = 0; j < kPer / 4; ++j) {
-                out[0][j] = out[1][j] = 0;
+            for (int j = 0; j < kOwn / 4; ++j) {
+                out[j] = 0;
+                const bool upper = kRows == 1 ? j >= kOwn / 8 : row >= kRows / 2;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float x = least[4 * j + i], y = most[4 * j + i];
-                    // (a product that fp32 rounds to zero still is a number below or above it)
+                    const float x = least[4 * j + i];
+                    // (a product that fp32 rounds to zero still stands for a number below it)
                     const int f = min(static_cast<int>(floorf(x * up)), x < 0.0f ? -1 : 127);
-                    const int c = max(static_cast<int>(ceilf(y * up)), y > 0.0f ? 1 : -127);
-                    out[0][j] |= (static_cast<uint32_t>(f) & 255u) << (8 * i);
-                    out[1][j] |= (static_cast<uint32_t>(c) & 255u) << (8 * i);
+                    out[j] |= (static_cast<uint32_t>(upper ? -f : f) & 255u) << (8 * i);
                 }
             }
-            if (row == 0 && inside && TGEMM_CHECK(to < p.bounds.dbg_rows, kChkKvOutput, p.status)) {
+            if (inside && TGEMM_CHECK(to < p.bounds.dbg_rows, kChkKvOutput, p.status)) {
                 signed char *const dst = p.bounds.base + to * 2 * p.cache.dim + piece * kPer;
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if constexpr (kE4m3)
-                        *reinterpret_cast<uint4 *>(dst + w * p.cache.dim) = make_uint4(out[w][0], out[w][1], out[w][kPer / 8], out[w][kPer / 4 - 1]);
-                    else
-                        *reinterpret_cast<uint2 *>(dst + w * p.cache.dim) = make_uint2(out[w][0], out[w][1]);
+                if constexpr (kRows == 1) {
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0], out[1]);
+                    *reinterpret_cast<uint2 *>(dst + p.cache.dim) = make_uint2(out[kOwn / 4 - 2], out[kOwn / 4 - 1]);
+                } else {
+                    constexpr int kShares = kRows / 2;       // of kPer channels
+                    signed char *const at = dst + (row / kShares) * p.cache.dim + (row % kShares) * kOwn;
+                    if constexpr (kOwn == 4) *reinterpret_cast<uint32_t *>(at) = out[0];
+                    else if constexpr (kOwn == 8) *reinterpret_cast<uint2 *>(at) = make_uint2(out[0], out[1]);
+                    else *reinterpret_cast<uint4 *>(at) = make_uint4(out[0], out[1], out[kOwn / 4 - 2], out[kOwn / 4 - 1]);
                 }
-                if (piece == 0) p.bounds.scale[to] = s;
+                if (lane == 0) p.bounds.scale[to] = s;
             }
         }
         base += items;
@@ -296,21 +340,40 @@ struct ChooseParams {
 };
 
 constexpr int kChooseMaxCached = 32 * 1024;        // keys of a block's slice (128 KiB)
-constexpr int kChooseGroup = 128;                  // query heads of a key head, at most
+constexpr int kChooseGroup = 64;                  // query heads of a key head, at most
 
-// Bytes of shared memory: keys, then the queries' two halves with their scales.
-// Rows lie an odd multiple of 64 bytes apart: the 16-byte reads of two of them fall into different banks.
-__host__ __device__ inline int choose_pitch(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 192 : 320; }
-__host__ __device__ inline int choose_bytes(int cached, int group, int dim) {
-    const int heads = (group + 7) / 8 * 8;
-    return (cached + 3) / 4 * 16 + heads * (2 * choose_pitch(dim) + 4);
+// Bytes of shared memory: keys, then the queries' two halves (fp16) with their scales.  Rows lie 16 bytes more than a
+// multiple of 128 apart: the 16-byte reads of two of them fall into different banks.
+__host__ __device__ constexpr int choose_pitch(int dim) { return (dim <= 64 ? 128 : dim <= 128 ? 256 : 512) + 16; }
+// A page's bounds in a warp's ring: the 16-byte pieces of row r are exchanged by choose_swizzle(r) (xor), for the same
+// reason.
+constexpr int choose_row(int chunks) { return chunks * 128; }
+__device__ __forceinline__ int choose_swizzle(int row) { return ((row & 1) << 2) | ((row >> 1) & 3); }
+// The ring, or, after it, what the ranking takes; keys; queries with their scales and the accumulators' beginnings.
+template <int kThreads, int kChunks, int kStages>
+struct ChooseShape {
+    static constexpr int kStage = 16 * choose_row(kChunks) + 128;         // a step's rows, their scales and which there are
+    static constexpr int kRing = kThreads / 32 * kStages * kStage;
+    static constexpr int kRank = (static_cast<int>(sizeof(RankShared<kThreads>)) + 15) / 16 * 16;
+    static constexpr int kFront = kRing > kRank ? kRing : kRank;
+    __host__ __device__ static constexpr int bytes(int cached, int group, int dim) {
+        return kFront + (cached + 3) / 4 * 16 + (group + 7) / 8 * 8 * (2 * choose_pitch(dim) + 4 + 8 * kChunks);
+    }
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Four 8-bit whole numbers as fp16, 1152 more than they are: x + 128 put below 1024's bits.
+constexpr float kChooseBias = 1152.0f;
+__device__ __forceinline__ void widen_s8(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = x ^ 0x80808080u, base = 0x64646464u;
+    lo = __byte_perm(u, base, 0x4140);
+    hi = __byte_perm(u, base, 0x4342);
 }
 
 // What there is to choose from: of `count` pages the first `first` and the last `recent` stay, and `best` of those between.
@@ -330,24 +393,26 @@ __host__ __device__ inline ChooseSpan choose_span(int n, int page_size, int keep
 
 // Grid: (cluster size, heads, batch), a cluster along x that shares a sequence
 // and key head.  kChunks: 64-byte pieces of a row of bounds.
-template <int kThreads, bool kBf16, int kChunks>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) page_choose_kernel(const ChooseParams p) {
-    constexpr int kWarps = kThreads / 32;
-    extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ RankShared<kThreads> sh;
+template <int kThreads, bool kBf16, int kChunks, int kStages>
+__global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChooseParams p) {
+    using Shape = ChooseShape<kThreads, kChunks, kStages>;
+    constexpr int kWarps = kThreads / 32, kRow = choose_row(kChunks), kPitch = kChunks * 128 + 16;     // choose_pitch()
+    extern __shared__ __align__(128) unsigned char choose_smem[];
+    RankShared<kThreads> &sh = *reinterpret_cast<RankShared<kThreads> *>(choose_smem);
     __shared__ int s_n;
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
     const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int head = blockIdx.y, b = blockIdx.z;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int heads8 = (p.group + 7) / 8 * 8, pitch = choose_pitch(p.cache.dim);
+    const int heads8 = (p.group + 7) / 8 * 8, pitch = kPitch;
+    unsigned char *const ring = choose_smem + warp * kStages * Shape::kStage;
+    uint32_t *const keys = reinterpret_cast<uint32_t *>(choose_smem + Shape::kFront);
     unsigned char *const positive = reinterpret_cast<unsigned char *>(keys) + (p.cached + 3) / 4 * 16;
     unsigned char *const negative = positive + heads8 * pitch;
     float *const s_scale = reinterpret_cast<float *>(negative + heads8 * pitch);
-    kv_rank_clear(sh);
+    float *const s_bias = s_scale + heads8;                      // [2 * kChunks][heads8]: of lo's and hi's sums over 64 dims
     griddep_wait();
-    griddep_launch_dependents();
     if (threadIdx.x == 0) {
         bool bad = false;
         s_n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
@@ -373,11 +438,27 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) page_choose_kernel(
         const float s = kv_bounds_scale(top), up = kv_bounds_inverse(s);
 #pragma unroll
         for (int i = 0; i < kPer; i += 2) {
-            const int y0 = static_cast<int>(rintf(x[i] * up)), y1 = static_cast<int>(rintf(x[i + 1] * up));
-            const int at = h * pitch + lane * kPer + i;
-            *reinterpret_cast<unsigned short *>(positive + at) = static_cast<unsigned short>(max(y0, 0) | (max(y1, 0) << 8));
-            *reinterpret_cast<unsigned short *>(negative + at) =
-                static_cast<unsigned short>((min(y0, 0) & 255) | ((min(y1, 0) & 255) << 8));
+            const float y0 = rintf(x[i] * up), y1 = rintf(x[i + 1] * up);
+            const int at = h * pitch + 2 * (lane * kPer + i);
+            *reinterpret_cast<__half2 *>(positive + at) = __floats2half2_rn(fmaxf(y0, 0.0f), fmaxf(y1, 0.0f));
+            *reinterpret_cast<__half2 *>(negative + at) = __floats2half2_rn(fminf(y0, 0.0f), fminf(y1, 0.0f));
+        }
+        // Lanes of the same 64 dims: 32 / kChunks of them.
+        float below = 0.0f, above = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            below += fminf(rintf(x[i] * up), 0.0f);
+            above += fmaxf(rintf(x[i] * up), 0.0f);
+        }
+#pragma unroll
+        for (int o = 16 / kChunks; o > 0; o >>= 1) {
+            below += __shfl_xor_sync(0xffffffffu, below, o);
+            above += __shfl_xor_sync(0xffffffffu, above, o);
+        }
+        if (lane % (32 / kChunks) == 0) {
+            const int c = lane / (32 / kChunks);
+            s_bias[2 * c * heads8 + h] = -kChooseBias * below;
+            s_bias[(2 * c + 1) * heads8 + h] = -kChooseBias * above;
         }
         if (lane == 0) s_scale[h] = s;
     }
@@ -388,65 +469,108 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) page_choose_kernel(
     int *const to = p.to_pages + b * p.to_batch_stride + head * p.to_head_stride;
     if (head == 0 && rank == 0 && threadIdx.x == 0)
         p.to_lengths[b] = n - (span.count - span.keep) * p.cache.page_size;
+    const bool some = span.best > 0;
+    // The blocks of a cluster go on together to every barrier, whatever length each of them has read.
+    const int slice = min((span.middle + blocks - 1) / blocks, p.cached);
+    const int lo = span.first + min(span.middle, rank * slice), size = some ? min(span.middle, (rank + 1) * slice) - (lo - span.first) : 0;
+    // Lane i < 16 has page i of the warp's next 16; the ones after them are looked up a step ahead.
+    auto lookup = [&](int i0) { return lane < 16 && i0 + lane < size ? list[lo + i0 + lane] : -1; };
+    int next = lookup(warp * 16);
     // What stays whatever its score, and -1 past the pages kept.
     for (int i = rank * kThreads + threadIdx.x; i < p.keep; i += blocks * kThreads) {
         if (i >= span.keep) to[i] = -1;
         else if (i < span.first) to[i] = list[i];
         else if (i >= span.first + span.best) to[i] = list[span.count - span.keep + i];
     }
-    const bool some = span.best > 0;
-    if (!some && blocks == 1) return;
-    // The blocks of a cluster go on together to every barrier, whatever length each of them has read.
-    const int slice = min((span.middle + blocks - 1) / blocks, p.cached);
-    const int lo = span.first + min(span.middle, rank * slice), size = some ? min(span.middle, (rank + 1) * slice) - (lo - span.first) : 0;
+    if (!some && blocks == 1) {
+        griddep_launch_dependents();
+        return;
+    }
 
-    // Scores: a warp has 16 pages at a time, lane (g, t4) 16 bytes of each 64 of pages g and g + 8.
-    const int g = lane >> 2, t4 = lane & 3;
-    const long long row_bytes = 2 * static_cast<long long>(p.cache.dim);
-    for (int i0 = warp * 16; i0 < size; i0 += kWarps * 16) {
-        int page = -1;
-        if (lane < 16 && i0 + lane < size) page = list[lo + i0 + lane];
-        const bool valid = page >= 0 && page < p.cache.pages;
-        const unsigned ok = __ballot_sync(0xffffffffu, valid), want = __ballot_sync(0xffffffffu, lane < 16 && i0 + lane < size);
-        if (ok != want && lane == 0) record_status(p.status, kStatusCache);
-        uint4 a[2][2][kChunks];                                  // [lo, hi][page g, g + 8]
-        float scale[2];
+    // Scores: a warp has 16 pages at a time, whose bounds are copied to its ring kStages - 1 steps ahead.  A row is
+    // both bounds of a page and head, 2 * dim bytes in one piece.
+    const int g = lane >> 2, t4 = lane & 3, pieces = p.cache.dim / 8;
+    const bool mine = lane % (8 * kChunks) < pieces;
+    const int page_bytes = p.cache.heads * 2 * p.cache.dim;
+    const signed char *const from = p.bounds.base + static_cast<long long>(head) * 2 * p.cache.dim + (mine ? lane % (8 * kChunks) * 16 : 0);
+    const uint32_t to_ring = smem_u32(ring);
+    int at_piece[kChunks][2];                                    // where the lane's piece of 64 dims is in row g (and g + 8)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int pg = __shfl_sync(0xffffffffu, page, g + 8 * r);
-            const bool is = (ok >> (g + 8 * r)) & 1u;
-            const long long at = is ? static_cast<long long>(pg) * p.cache.heads + head : 0;
-            scale[r] = is ? p.bounds.scale[at] : 0.0f;
+    for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                const int d = c * 64 + t4 * 16;
+        for (int w = 0; w < 2; ++w)
+            at_piece[c][w] = g * kRow + ((min(w * pieces / 2 + c * 4 + t4, 8 * kChunks - 1) ^ choose_swizzle(g)) << 4);
+    int ahead = warp * 16;
+    auto request = [&](int stage) {
+        const int page = next, i0 = ahead;
+        ahead += kWarps * 16;
+        next = lookup(ahead);
+        const bool there = lane < 16 && i0 + lane < size, valid = there && page >= 0 && page < p.cache.pages;
+        const unsigned ok = __ballot_sync(0xffffffffu, valid);
+        if (ok != __ballot_sync(0xffffffffu, there) && lane == 0) record_status(p.status, kStatusCache);
+        const uint32_t to = to_ring + stage * Shape::kStage;
+        if (lane < 16) cp_async4(to + 16 * kRow + 4 * lane, p.bounds.scale + (valid ? static_cast<long long>(page) * p.cache.heads + head : 0), valid);
+        if (lane == 0) *reinterpret_cast<unsigned *>(ring + stage * Shape::kStage + 16 * kRow + 64) = ok;
+        // A lane copies one 16-byte piece of every 32 / kPieces rows.
+        constexpr int kPieces = 8 * kChunks, kEach = 32 / kPieces;
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    a[w][r][c] = make_uint4(0, 0, 0, 0);
-                    if (is && d < p.cache.dim)
-                        a[w][r][c] = *reinterpret_cast<const uint4 *>(p.bounds.base + at * row_bytes + w * p.cache.dim + d);
-                }
-            }
+        for (int u = 0; u < 16 / kEach; ++u) {
+            const int r = u * kEach + lane / kPieces, pg = __shfl_sync(0xffffffffu, page, r);
+            if (((ok >> r) & 1u) && mine)
+                cp_async16(to + r * kRow + ((lane % kPieces ^ choose_swizzle(r)) << 4), from + static_cast<long long>(pg) * page_bytes);
         }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) request(k);
+    int stage = 0;
+    for (int i0 = warp * 16; i0 < size; i0 += kWarps * 16) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        // the stage that the step before has read takes the one kStages - 1 steps on
+        request(stage == 0 ? kStages - 1 : stage - 1);
+        const unsigned char *const at_hand = ring + stage * Shape::kStage;
+        const unsigned ok = *reinterpret_cast<const unsigned *>(at_hand + 16 * kRow + 64);
+        const float *const stage_scale = reinterpret_cast<const float *>(at_hand + 16 * kRow);
+        const float scale[2] = {stage_scale[g], stage_scale[g + 8]};
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         float best[2] = {-INFINITY, -INFINITY};
         for (int h0 = 0; h0 < heads8; h0 += 8) {
-            int acc[4] = {0, 0, 0, 0};
+            float acc[2 * kChunks][4];
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                const int at = (h0 + g) * pitch + c * 64 + t4 * 16;
-                const uint4 qn = *reinterpret_cast<const uint4 *>(negative + at), qp = *reinterpret_cast<const uint4 *>(positive + at);
-                mma_s8(acc, a[0][0][c].x, a[0][1][c].x, a[0][0][c].y, a[0][1][c].y, qn.x, qn.y);
-                mma_s8(acc, a[0][0][c].z, a[0][1][c].z, a[0][0][c].w, a[0][1][c].w, qn.z, qn.w);
-                mma_s8(acc, a[1][0][c].x, a[1][1][c].x, a[1][0][c].y, a[1][1][c].y, qp.x, qp.y);
-                mma_s8(acc, a[1][0][c].z, a[1][1][c].z, a[1][0][c].w, a[1][1][c].w, qp.z, qp.w);
-            }
+            for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const float2 bias = *reinterpret_cast<const float2 *>(s_bias + (2 * c + w) * heads8 + h0 + 2 * t4);
+                    float (&sum)[4] = acc[2 * c + w];
+                    sum[0] = sum[2] = bias.x;
+                    sum[1] = sum[3] = bias.y;
+                    const unsigned char *const queries = (w ? positive : negative) + (h0 + g) * pitch + c * 128 + t4 * 32;
+                    const uint4 q0 = *reinterpret_cast<const uint4 *>(queries), q1 = *reinterpret_cast<const uint4 *>(queries + 16);
+                    const uint32_t q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+                    // Past dim the queries are 0 and the bounds whatever the ring holds, as whole numbers.
+                    const unsigned char *const at = at_hand + at_piece[c][w];
+                    const uint4 xa = *reinterpret_cast<const uint4 *>(at), ya = *reinterpret_cast<const uint4 *>(at + 8 * kRow);
+                    const uint32_t x[4] = {xa.x, xa.y, xa.z, xa.w}, y[4] = {ya.x, ya.y, ya.z, ya.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t x0, x1, y0, y1;
+                        widen_s8(x[j], x0, x1);
+                        widen_s8(y[j], y0, y1);
+                        mma_f16(sum, x0, y0, x1, y1, q[2 * j], q[2 * j + 1]);
+                    }
+                }
+#pragma unroll
+            for (int c = 1; c < 2 * kChunks; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[0][i] += acc[c][i];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int h = h0 + 2 * t4 + i;
                 const float s = s_scale[h];
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    if (h < p.group) best[r] = fmaxf(best[r], static_cast<float>(acc[2 * r + i]) * scale[r] * s);
+                    if (h < p.group) best[r] = fmaxf(best[r], acc[0][2 * r + i] * scale[r] * s);
             }
         }
 #pragma unroll
@@ -454,9 +578,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) page_choose_kernel(
             best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
             best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
             const int i = i0 + g + 8 * r;
-            if (t4 == 0 && i < size) keys[i] = (ok >> (g + 8 * r)) & 1u ? kv_weight_key(__float_as_uint(best[r])) : 0u;
+            if (t4 == 0 && i < size)
+                keys[i] = (ok >> (g + 8 * r)) & 1u ? kv_weight_key(__float_as_uint(best[r])) : 0u;
         }
     }
+    griddep_launch_dependents();                 // what follows would take the places of blocks that have not begun
+    cp_async_wait<0>();
+    __syncthreads();
+    kv_rank_clear(sh);                           // in the ring's place
     __syncthreads();
     kv_rank(
         sh, size, span.best, p.status, [&](int i) { return keys[i]; },

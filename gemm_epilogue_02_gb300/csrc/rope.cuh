@@ -25,6 +25,7 @@ namespace tgemm {
 
 constexpr int kRopePairs = 128;             // at most (dim 256)
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBackThreads = 128, kRopeBackCtas = 3;     // per SM
 constexpr int kRopeMaxBlocks = 1024;        // whose partial sums of weight gradients the workspace holds
 
 struct RopeSide {
@@ -155,9 +156,9 @@ struct RopeWeights {
     float4 part[2 * V / 4][kLanes];
 };
 
-template <bool kBf16, int V, int kLanes, bool kInterleaved>
+template <bool kBf16, int V, int kLanes, bool kInterleaved, int kThreads = kRopeThreads>
 __device__ __forceinline__ void rope_stage_weights(RopeWeights<V, kLanes> &to, const void *w, bool f32, int dim, int pairs) {
-    for (int i = threadIdx.x; i < 2 * V * kLanes; i += kRopeThreads) {
+    for (int i = threadIdx.x; i < 2 * V * kLanes; i += kThreads) {
         const int l = i / (2 * V), k = i - l * (2 * V);              // lane l's a[0 .. V - 1], then b
         int unit[2];
         bool is[2];
@@ -239,7 +240,7 @@ struct RopeCursor {
 // Passes ahead of the one at hand whose rows are on their way.
 template <bool kBf16, int V, int kLanes, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kRows = 32 / kLanes, kWarps = kRopeThreads / 32, kAhead = 2;
+    constexpr int kRows = 32 / kLanes, kWarps = kRopeThreads / 32, kAhead = 3;
     __shared__ RopeWeights<V, kLanes> s_w[2];
     const int lane = threadIdx.x & 31, l = lane % kLanes, row = lane / kLanes;
     int unit[2];
@@ -286,16 +287,15 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
     __syncthreads();
     float c[V], s[V];
     bool fresh = true;                      // the token's angles are to be worked out
-    for (; left > 0; --left) {
+    // A slot of the ring is refilled as soon as it is unpacked: moving rows that are on their way would wait for them.
+    auto step = [&](RopeRaw<V> &raw) {
         if (fresh) {
             angles.turn(places, p.shift, l, c, s);
             places = places_of(use.token + 1);
         }
         float a[V], b[V], wa[V], wb[V];
-        rope_split<kBf16, V, kInterleaved>(ring[0], a, b);
-#pragma unroll
-        for (int i = 0; i + 1 < kAhead; ++i) ring[i] = ring[i + 1];
-        request(ring[kAhead - 1]);
+        rope_split<kBf16, V, kInterleaved>(raw, a, b);
+        request(raw);
         const bool q = use.pass >= passes_q;
         const RopeSide &side = p.side[q ? 1 : 0];
         const int head = (use.pass - (q ? passes_q : 0)) * kRows + row;
@@ -321,12 +321,17 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
         const long long token = use.token;
         next(use);
         fresh = use.token != token;
+    };
+    while (left > 0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (left-- > 0) step(ring[i]);
     }
 }
 
 template <bool kBf16, int V, int kLanes, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kRows = 32 / kLanes, kWarps = kRopeThreads / 32;
+__global__ void __launch_bounds__(kRopeBackThreads, kRopeBackCtas) rope_backward_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int kRows = 32 / kLanes, kWarps = kRopeBackThreads / 32, kAhead = 2;
     __shared__ RopeWeights<V, kLanes> s_w[2];
     __shared__ float s_dw[kWarps][2][2 * kRopePairs];
     const int lane = threadIdx.x & 31, l = lane % kLanes, row = lane / kLanes;
@@ -353,8 +358,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_kernel(const __
         }
     };
     int loads = left;
-    RopeRaw<V> next_x, next_g;
-    auto request = [&]() {
+    RopeRaw<V> ring_x[kAhead], ring_g[kAhead];
+    auto request = [&](RopeRaw<V> &next_x, RopeRaw<V> &next_g) {
         const bool q = load.pass >= passes_q;
         const RopeSide &side = p.side[q ? 1 : 0];
         const int head = (load.pass - (q ? passes_q : 0)) * kRows + row;
@@ -368,10 +373,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_kernel(const __
     auto places_of = [&](long long token) {
         return lane < p.axes && token < p.tokens ? p.positions[lane * p.axis_stride + token] : 0;
     };
-    request();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) request(ring_x[i], ring_g[i]);
     int places = places_of(use.token);
-    rope_stage_weights<kBf16, V, kLanes, kInterleaved>(s_w[0], p.side[0].w, p.weight_f32, p.dim, p.pairs);
-    rope_stage_weights<kBf16, V, kLanes, kInterleaved>(s_w[1], p.side[1].w, p.weight_f32, p.dim, p.pairs);
+    rope_stage_weights<kBf16, V, kLanes, kInterleaved, kRopeBackThreads>(s_w[0], p.side[0].w, p.weight_f32, p.dim, p.pairs);
+    rope_stage_weights<kBf16, V, kLanes, kInterleaved, kRopeBackThreads>(s_w[1], p.side[1].w, p.weight_f32, p.dim, p.pairs);
     __syncthreads();
     float da[2][V], db[2][V];
 #pragma unroll
@@ -380,11 +386,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_kernel(const __
         for (int i = 0; i < V; ++i) da[q][i] = db[q][i] = 0.0f;
     float c[V], s[V];
     bool fresh = true;                      // the token's angles are to be worked out
-    auto step = [&](float (&da)[V], float (&db)[V], const RopeWeights<V, kLanes> &weights, const RopeSide &side, int pass, long long dbg) {
+    auto step = [&](RopeRaw<V> &raw_x, RopeRaw<V> &raw_g, float (&da)[V], float (&db)[V], const RopeWeights<V, kLanes> &weights,
+                    const RopeSide &side, int pass, long long dbg) {
         float a[V], b[V], x[V], y[V];
-        rope_split<kBf16, V, kInterleaved>(next_g, a, b);
-        rope_split<kBf16, V, kInterleaved>(next_x, x, y);
-        request();
+        rope_split<kBf16, V, kInterleaved>(raw_g, a, b);
+        rope_split<kBf16, V, kInterleaved>(raw_x, x, y);
+        request(raw_x, raw_g);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float f = a[i] * c[i] + b[i] * s[i];
@@ -422,16 +429,20 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_kernel(const __
         if (there && TGEMM_CHECK(at + 2 * p.dim <= dbg, kChkRope, p.status))
             rope_write<kBf16, V, kInterleaved>(side.y + at, a, b, unit, in);
     };
-    for (; left > 0; --left) {
-        if (fresh) {
-            angles.turn(places, p.shift, l, c, s);
-            places = places_of(use.token + 1);
+    while (left > 0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (left-- <= 0) break;
+            if (fresh) {
+                angles.turn(places, p.shift, l, c, s);
+                places = places_of(use.token + 1);
+            }
+            if (use.pass < passes_q) step(ring_x[i], ring_g[i], da[0], db[0], s_w[0], p.side[0], use.pass, p.dbg_y[0]);
+            else step(ring_x[i], ring_g[i], da[1], db[1], s_w[1], p.side[1], use.pass - passes_q, p.dbg_y[1]);
+            const long long token = use.token;
+            next(use);
+            fresh = use.token != token;
         }
-        if (use.pass < passes_q) step(da[0], db[0], s_w[0], p.side[0], use.pass, p.dbg_y[0]);
-        else step(da[1], db[1], s_w[1], p.side[1], use.pass - passes_q, p.dbg_y[1]);
-        const long long token = use.token;
-        next(use);
-        fresh = use.token != token;
     }
     if (!p.partials) return;
     // The block's sums of the weight gradients: rows of a warp, then the warps.
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_backward_kernel(const __
                 if (row == 0 && e < p.dim) s_dw[threadIdx.x >> 5][q][e] = x;
             }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.dim; i += kRopeThreads) {
+    for (int i = threadIdx.x; i < 2 * p.dim; i += kRopeBackThreads) {
         const int q = i >= p.dim, e = i - q * p.dim;
         float x = 0.0f;
 #pragma unroll

@@ -124,21 +124,22 @@ void set_side(RopeSide &s, const Rows &x, const Rows &y, const Rows *g, const vo
 }
 
 // A warp a pass, or as many blocks as fit the GPU at once.
-unsigned rope_blocks(const RopeParams &p, int lanes, int64_t most) {
+unsigned rope_blocks(const RopeParams &p, int lanes, int threads, int64_t most) {
     const int rows = 32 / lanes;
     const int64_t passes = (p.side[0].heads + rows - 1) / rows + (p.side[1].heads + rows - 1) / rows;
-    const int64_t blocks = (p.tokens * passes + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    const int64_t blocks = (p.tokens * passes + threads / 32 - 1) / (threads / 32);
     return static_cast<unsigned>(std::max<int64_t>(1, std::min(blocks, most)));
 }
 
 template <bool kBf16, int V, int kLanes, bool kInterleaved>
 cudaError_t launch_rope(const RuntimeInfo &rt, RopeParams &p, bool backward, cudaStream_t s) {
     if (!backward)
-        return launch(rope_kernel<kBf16, V, kLanes, kInterleaved>, dim3(rope_blocks(p, kLanes, static_cast<int64_t>(rt.num_sms) * 2)),
+        return launch(rope_kernel<kBf16, V, kLanes, kInterleaved>, dim3(rope_blocks(p, kLanes, kRopeThreads, static_cast<int64_t>(rt.num_sms) * 2)),
                       kRopeThreads, 0, s, p);
-    const unsigned blocks = rope_blocks(p, kLanes, std::min<int64_t>(kRopeMaxBlocks, static_cast<int64_t>(rt.num_sms) * 2));
+    const unsigned blocks =
+        rope_blocks(p, kLanes, kRopeBackThreads, std::min<int64_t>(kRopeMaxBlocks, static_cast<int64_t>(rt.num_sms) * kRopeBackCtas));
     p.blocks = static_cast<int>(blocks);
-    const cudaError_t e = launch(rope_backward_kernel<kBf16, V, kLanes, kInterleaved>, dim3(blocks), kRopeThreads, 0, s, p);
+    const cudaError_t e = launch(rope_backward_kernel<kBf16, V, kLanes, kInterleaved>, dim3(blocks), kRopeBackThreads, 0, s, p);
     if (e != cudaSuccess || !p.partials) return e;
     return launch(rope_weight_kernel, dim3(static_cast<unsigned>((2 * p.dim + 31) / 32)), kRopeThreads, 0, s, p);
 }

@@ -502,7 +502,7 @@ tgemm_status tgemm_kv_bounds(const tgemm_kv_bounds_args *args, tgemm_stream_t st
  * tgemm_attention_decode_lists:
  *   to_pages    int32 [batch, heads, keep]: page numbers in order of position, -1 past them
  *   to_lengths  int32 [batch]: positions on them
- * first + recent <= keep; at most 2^17 pages in a list and 128 query heads on a
+ * first + recent <= keep; at most 2^17 pages in a list and 64 query heads on a
  * key head.  A page number outside the cache is recorded and scores lowest.
  */
 typedef struct {
