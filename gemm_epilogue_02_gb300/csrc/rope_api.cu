@@ -23,6 +23,10 @@ struct Rows {
 };
 
 tgemm_status check_rows(const tgemm_rows &r, int64_t tokens, int64_t heads, int64_t dim, bool written, Rows *out) {
+    if (tokens == 0 || heads == 0) {             // whatever the strides are
+        out->heads = heads;
+        return TGEMM_OK;
+    }
     const int64_t size[2] = {tokens, heads}, stride[2] = {r.token_stride, r.head_stride};
     const int64_t inner_size[1] = {heads}, inner_stride[1] = {r.head_stride};
     if (!extent(size, stride, 2, dim, 2, written, &out->bytes) || !extent(inner_size, inner_stride, 1, dim, 2, written, &out->inner))

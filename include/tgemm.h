@@ -497,7 +497,7 @@ tgemm_status tgemm_kv_bounds(const tgemm_kv_bounds_args *args, tgemm_stream_t st
  * tgemm_attention_decode) in whole numbers of a power of two t, found as s is
  * above (rounded to nearest even), a page's score is the largest over the head's
  * group of
- *     t s sum_d max(z_d lo_d, z_d hi_d)
+ *     t s sum_d max(z_d lo_d, z_d hi_d)   (z_d lo_d for z_d < 0, z_d hi_d for z_d > 0)
  * in fp32, which is exact while it stays in fp32's range.  Written, for
  * tgemm_attention_decode_lists:
  *   to_pages    int32 [batch, heads, keep]: page numbers in order of position, -1 past them
