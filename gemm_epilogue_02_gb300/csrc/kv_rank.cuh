@@ -55,12 +55,13 @@ __device__ __forceinline__ void kv_rank_clear(RankShared<kThreads> &sh) {
 // This block has `size` keys, key_at(0) .. key_at(size - 1); put(at, i) is called for each of its keys i that is among the
 // `best`, at = 0 .. best - 1 its place among them.  Called by all threads of all blocks of a cluster (whatever their sizes),
 // after a barrier that follows kv_rank_clear().
-template <int kThreads, typename KeyAt, typename Put>
+// kAlone: by one block, whether it has a cluster or not.
+template <bool kAlone = false, int kThreads, typename KeyAt, typename Put>
 __device__ __forceinline__ void kv_rank(RankShared<kThreads> &sh, int size, int best, unsigned int *status, KeyAt key_at, Put put) {
     constexpr int kWarps = kThreads / 32;
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
-    const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int blocks = kAlone ? 1 : static_cast<int>(cluster.num_blocks()), rank = kAlone ? 0 : static_cast<int>(cluster.block_rank());
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t prefix = 0, counted = ~0u;          // the limit, and its bits that count
     int need = best;                             // rank of the limit among the keys with this prefix

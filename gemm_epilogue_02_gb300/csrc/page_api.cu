@@ -17,6 +17,7 @@ namespace tgemm {
 namespace {
 
 constexpr int kChooseMaxPages = 1 << 17;      // of a page list: eight blocks' keys then fit their shared memory
+constexpr int kChooseGather = 1 << 12;        // pages of a list whose keys a cluster's first block ranks alone
 constexpr int kChooseMaxBytes = 224 * 1024;   // of a block's dynamic shared memory
 
 tgemm_status check_bounds(const tgemm_kv_page_bounds *b, const tgemm_kv_cache *c, KvBounds *view, Extent *e, Extent *es) {
@@ -70,15 +71,15 @@ int row_lanes(int bytes) { return bytes <= 128 ? 8 : bytes <= 256 ? 16 : 32; }
 // ---------------------------------------------------------------- bounds and choice
 template <bool kBf16, bool kE4m3, int kLanes>
 cudaError_t launch_bounds_lanes(const RuntimeInfo &rt, const BoundsParams &p, cudaStream_t s) {
-    // Pages that there can be, a warp each.
-    constexpr int kRows = 32 / kLanes;
-    const int64_t most = p.starts ? static_cast<int64_t>(p.table.batch) * p.table.width : p.table.batch;
-    const int64_t blocks = std::max<int64_t>(1, (most * p.cache.heads + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32));
-    auto grid = [&](int ctas) { return dim3(static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(rt.num_sms) * ctas))); };
-    // Pages that four requests of a lane cover need no more.
-    if (p.cache.page_size <= 4 * kRows)
-        return launch(page_bounds_kernel<kBf16, kE4m3, kLanes, 4>, grid(kE4m3 ? 3 : 4), kBoundsThreads, 0, s, p);
-    return launch(page_bounds_kernel<kBf16, kE4m3, kLanes, 8>, grid(kE4m3 ? 2 : 4), kBoundsThreads, 0, s, p);
+    constexpr int kGroups = 32 / kLanes;
+    const int64_t most = (p.starts ? static_cast<int64_t>(p.table.batch) * p.table.width : p.table.batch) * p.cache.heads;
+    auto grid = [&](int items, int ctas) {       // for as many pages as there can be
+        const int64_t units = (most + items - 1) / items, blocks = (units + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32);
+        return dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(blocks, static_cast<int64_t>(rt.num_sms) * ctas))));
+    };
+    if (p.cache.page_size <= kBoundsAlone && kGroups > 1)
+        return launch(page_bounds_kernel<kBf16, kE4m3, kLanes, 8, kGroups != 1>, grid(kGroups, kE4m3 ? 2 : 4), kBoundsThreads, 0, s, p);
+    return launch(page_bounds_kernel<kBf16, kE4m3, kLanes, 8, false>, grid(1, kE4m3 ? 2 : 4), kBoundsThreads, 0, s, p);
 }
 
 template <bool kBf16, bool kE4m3>
@@ -119,6 +120,8 @@ cudaError_t launch_choose_shape(const RuntimeInfo &rt, ChooseParams &p, cudaStre
         while (cluster < 8 && 2 * cluster * lists <= rt.num_sms) cluster *= 2;
     while (cluster < 8 && cluster * (kChooseMaxPages / 8) < p.table.width) cluster *= 2;
     p.cached = (p.table.width + cluster - 1) / cluster;
+    p.gather = cluster > 1 && p.table.width <= kChooseGather;
+    if (p.gather) p.cached = p.table.width;
     // Three stages let an SM have two blocks; queries of large groups over long lists leave room for two.
     if (ChooseShape<kThreads, kChunks, 3>::bytes(p.cached, p.group, p.cache.dim) <= kChooseMaxBytes)
         return launch_choose_stages<kThreads, kBf16, kChunks, 3>(rt, p, cluster, s);
@@ -256,8 +259,15 @@ tgemm_status check_pages(const tgemm_kv_cache *cache, int32_t *uses, int32_t *pa
     return TGEMM_OK;
 }
 
+// Bytes of the children's last pages up to which a cluster does all: beyond, two launches fill the GPU.
+constexpr int64_t kForkFew = 1 << 20;
+
 template <int kLanes>
 cudaError_t launch_fork_lanes(const RuntimeInfo &rt, const PagesParams &p, cudaStream_t s) {
+    const int64_t page_bytes = static_cast<int64_t>(p.cache.page_size) * p.cache.heads * p.cache.row_bytes * 2;
+    if (p.to.batch * page_bytes <= kForkFew) return launch(page_fork_few_kernel<kLanes>, dim3(kForkBlocks), kTakeThreads, 0, s, p, kForkBlocks);
+    const cudaError_t e = launch(page_take_kernel<true>, dim3(1), kTakeThreads, 0, s, p);
+    if (e != cudaSuccess) return e;
     constexpr int kRows = kPageThreads / kLanes * 4;
     const int64_t rows = static_cast<int64_t>(p.cache.page_size) * p.cache.heads;
     const int64_t want = std::max<int64_t>((rows + kRows - 1) / kRows, (p.table.width + kPageThreads - 1) / kPageThreads);
@@ -321,8 +331,6 @@ extern "C" tgemm_status tgemm_kv_fork(const tgemm_kv_fork_args *a, tgemm_stream_
     p.parents = a->parents;
     p.status = rt.status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch(page_take_kernel<true>, dim3(1), kTakeThreads, 0, s, p);
-    if (e != cudaSuccess) return done(e);
     switch (row_lanes(p.cache.row_bytes)) {
         case 8: return done(launch_fork_lanes<8>(rt, p, s));
         case 16: return done(launch_fork_lanes<16>(rt, p, s));

@@ -75,6 +75,10 @@ struct BoundsParams {
 };
 
 constexpr int kBoundsThreads = 256;
+// Positions of a page, at most, whose rows one group of lanes goes through alone.  200000 positions of 8 heads, 128 wide, in
+// pages of 16: 16 bits 69 us (groups together: 72), e4m3 63 (112); pages of 32: 69 (68), 57 (71).  Pages of 64: 68 (67), 54
+// (61), but one page that comes alone 10 us (6.4).
+constexpr int kBoundsAlone = 32;
 
 // Pages of sequence b that its newest tokens complete: [*from, return).
 __host__ __device__ inline int kv_completed(int n, long long fresh, int page_size, int *from) {
@@ -113,13 +117,27 @@ __device__ __forceinline__ float min3(float a, float b, float c) {           // 
     asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Both of a times s.
+__device__ __forceinline__ float2 scale2(float2 a, float s) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, s, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmul.rn.f32x2 d, a, s;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(s));
+    return d;
+}
 
 // A warp's minima of its rows' groups of kLanes lanes, `values` of each lane:
 // group 2^k's lanes hand half of what they have to the other's, down to each group
 // having its share (group r: share r of the kRows shares, in order).  The least
 // is taken of all, so bounds from above go in with their signs changed.
-template <int kLanes, int N, typename T, typename Min>
+template <int kLanes, bool kAlone, int N, typename T, typename Min>
 __device__ __forceinline__ void bounds_scatter(T (&x)[N], int row, Min least) {
+    if (kAlone) return;
     int n = N;
 #pragma unroll
     for (int o = 16; o >= kLanes; o >>= 1) {
@@ -134,24 +152,27 @@ __device__ __forceinline__ void bounds_scatter(T (&x)[N], int row, Min least) {
     }
 }
 
-// A warp has one page and head at a time; kLanes lanes hold a row in 16-byte
-// pieces, 32 / kLanes rows at once, kUnroll of them requested together.
-// Neighbouring warps have neighbouring heads of a page.  Reading the keys bounds it
-// with 16 bits and pages of 64 (200000 positions of 8 heads, 128 wide: 66.5 us, 1.00
-// of the copy rate); small pages and e4m3 cost instructions.
-template <bool kBf16, bool kE4m3, int kLanes, int kUnroll>
+// kLanes lanes hold a row in 16-byte pieces; kUnroll rows of a lane are requested
+// together.  An item is a page and head.  kAlone: each group of kLanes lanes has an
+// item of its own and goes through its rows one by one, so that what an item costs
+// besides its rows is shared by the groups; otherwise the groups share an item's
+// rows, which a long page wants that comes alone.  Neighbouring groups and warps
+// have neighbouring heads of a page.  With 16 bits the reading bounds it; widening
+// and scaling e4m3 costs more than that.
+template <bool kBf16, bool kE4m3, int kLanes, int kUnroll, bool kAlone>
 __global__ void __launch_bounds__(kBoundsThreads, kE4m3 ? (kUnroll > 4 ? 2 : 3) : 4) page_bounds_kernel(const BoundsParams p) {
-    constexpr int kWarps = kBoundsThreads / 32, kRows = 32 / kLanes, kPer = kE4m3 ? 16 : 8;
+    constexpr int kWarps = kBoundsThreads / 32, kGroups = 32 / kLanes, kPer = kE4m3 ? 16 : 8;
+    constexpr int kRows = kAlone ? 1 : kGroups, kItems = kAlone ? kGroups : 1;       // rows at once; items of a warp
     __shared__ int s_end[kBoundsThreads + 1];      // pages of the sequences of this round, summed up
     __shared__ int s_from[kBoundsThreads];
     __shared__ int s_sum[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int piece = lane % kLanes, row = lane / kLanes;
-    const bool inside = piece * 16 < p.cache.row_bytes;
+    const int piece = lane % kLanes, row = kAlone ? 0 : lane / kLanes, group = kAlone ? lane / kLanes : 0;
     griddep_wait();
     griddep_launch_dependents();
     const long long warps = static_cast<long long>(gridDim.x) * kWarps, me = static_cast<long long>(blockIdx.x) * kWarps + warp;
-    long long base = 0;                            // items of the rounds before
+    const int skip_pages = static_cast<int>(warps * kItems / p.cache.heads), skip_heads = static_cast<int>(warps * kItems % p.cache.heads);
+    long long base = 0;                            // units of kItems items in the rounds before
     for (int b0 = 0; b0 < p.table.batch; b0 += kBoundsThreads) {
         const int b = b0 + static_cast<int>(threadIdx.x);
         int mine = 0, from = 0;
@@ -172,33 +193,46 @@ __global__ void __launch_bounds__(kBoundsThreads, kE4m3 ? (kUnroll > 4 ? 2 : 3) 
         if (threadIdx.x == 0) s_end[0] = 0;
         s_from[threadIdx.x] = from;
         __syncthreads();
-        const long long items = static_cast<long long>(s_end[kBoundsThreads]) * p.cache.heads;
-        // The page of item i, and its head.
-        auto find = [&](long long i, int *head) {
-            const int at = static_cast<int>(i / p.cache.heads);
-            *head = static_cast<int>(i - static_cast<long long>(at) * p.cache.heads);
-            int lo = 0, hi = kBoundsThreads;       // s_end[lo] <= at < s_end[hi]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (s_end[mid] <= at) lo = mid;
-                else hi = mid;
-            }
-            return p.table.pages[(b0 + lo) * p.table.stride + s_from[lo] + at - s_end[lo]];
-        };
-        // Warp `me` has the items i with (base + i) % warps == me; the next one's page is looked up a step ahead.
+        const long long items = static_cast<long long>(s_end[kBoundsThreads]) * p.cache.heads, units = (items + kItems - 1) / kItems;
+        // Warp `me` has the units i with (base + i) % warps == me; the next one's pages are looked up a step ahead.  Item j is
+        // head j % heads of page j / heads, counted over the round's sequences.
         long long i = (me + warps - base % warps) % warps;
-        int next_head = 0, next_page = i < items ? find(i, &next_head) : 0;
-        for (; i < items; i += warps) {
-            const int page = next_page, head = next_head;
-            if (i + warps < items) next_page = find(i + warps, &next_head);
-            if (page < 0 || page >= p.cache.pages) {
-                if (lane == 0) record_status(p.status, kStatusCache);
-                continue;
+        long long item = i * kItems + group;
+        int at = static_cast<int>(item / p.cache.heads), at_head = static_cast<int>(item - static_cast<long long>(at) * p.cache.heads), of = 0;
+        if (item < items)                                      // the first one's sequence
+            for (int step = kBoundsThreads / 2; step > 0; step /= 2)
+                if (s_end[of + step] <= at) of += step;
+        // The page of the lane's item, -1 past the last, and its head; then on to the next.
+        auto find = [&](int *head) {
+            *head = at_head;
+            int page = -1;
+            if (item < items) {
+                while (s_end[of + 1] <= at) ++of;              // (an item that there is lies below the last sum)
+                page = p.table.pages[(b0 + of) * p.table.stride + s_from[of] + at - s_end[of]];
+                if (page < 0 || page >= p.cache.pages) {
+                    record_status(p.status, kStatusCache);
+                    page = -1;
+                }
             }
+            item += warps * kItems;
+            at += skip_pages;
+            at_head += skip_heads;
+            if (at_head >= p.cache.heads) {
+                at_head -= p.cache.heads;
+                ++at;
+            }
+            return page;
+        };
+        int next_head, next_page = find(&next_head);
+        for (; i < units; i += warps) {
+            const bool there = next_page >= 0;
+            const int page = there ? next_page : 0, head = next_head;
+            next_page = find(&next_head);
+            const bool inside = there && piece * 16 < p.cache.row_bytes;
             const unsigned char *const keys = p.cache.k + kv_offset(p.cache, page, 0, head) + (inside ? piece * 16 : 0);
             const float *const scales = kE4m3 ? p.cache.k_scale + kv_scale_offset(p.cache, page, 0, head) : nullptr;
             // Each channel's least key, and its largest with the sign changed: after the exchange a lane has kOwn of
-            // these 2 * kPer, those of `share`.
+            // these 2 * kPer.
             constexpr int kOwn = 2 * kPer / kRows;
             float least[kOwn];
             if constexpr (!kE4m3) {
@@ -227,7 +261,7 @@ __global__ void __launch_bounds__(kBoundsThreads, kE4m3 ? (kUnroll > 4 ? 2 : 3) 
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) m[4 + j] = z[j] ^ 0x80008000u;
-                bounds_scatter<kLanes>(m, row, [](uint32_t a, uint32_t b) { return min_pair<kBf16>(a, b); });
+                bounds_scatter<kLanes, kAlone>(m, row, [](uint32_t a, uint32_t b) { return min_pair<kBf16>(a, b); });
 #pragma unroll
                 for (int j = 0; j < kOwn / 2; ++j) {
                     const float2 f = bounds_widen<kBf16>(m[j]);
@@ -264,18 +298,19 @@ __global__ void __launch_bounds__(kBoundsThreads, kE4m3 ? (kUnroll > 4 ? 2 : 3) 
                                 for (int k = 0; k < 2; ++k) {
                                     const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(
                                         static_cast<__nv_fp8x2_storage_t>((w[k][j] >> (16 * h)) & 0xFFFFu), __NV_E4M3);
-                                    v[k] = __half22float2(__half2(r));
-                                    v[k] = make_float2(v[k].x * scale[u + k], v[k].y * scale[u + k]);
+                                    v[k] = scale2(__half22float2(__half2(r)), scale[u + k]);
                                 }
                                 const int e = 4 * j + 2 * h;
                                 m[e] = min3(m[e], v[0].x, v[1].x);
                                 m[e + 1] = min3(m[e + 1], v[0].y, v[1].y);
-                                m[kPer + e] = min3(m[kPer + e], -v[0].x, -v[1].x);
-                                m[kPer + e + 1] = min3(m[kPer + e + 1], -v[0].y, -v[1].y);
+                                m[kPer + e] = max3(m[kPer + e], v[0].x, v[1].x);
+                                m[kPer + e + 1] = max3(m[kPer + e + 1], v[0].y, v[1].y);
                             }
                     }
                 }
-                bounds_scatter<kLanes>(m, row, [](float a, float b) { return fminf(a, b); });
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) m[kPer + j] = -m[kPer + j];
+                bounds_scatter<kLanes, kAlone>(m, row, [](float a, float b) { return fminf(a, b); });
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j) least[j] = m[j];
             }
@@ -285,8 +320,14 @@ __global__ void __launch_bounds__(kBoundsThreads, kE4m3 ? (kUnroll > 4 ? 2 : 3) 
                 least[j] = kv_finite(least[j]);
                 top = fmaxf(top, -least[j]);
             }
-            // (numbers >= 0 have the order of their bits)
-            const float s = kv_bounds_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)))), up = kv_bounds_inverse(s);
+            if constexpr (kAlone) {
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            } else {
+                // (numbers >= 0 have the order of their bits)
+                top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+            }
+            const float s = kv_bounds_scale(top), up = kv_bounds_inverse(s);
             const long long to = static_cast<long long>(page) * p.cache.heads + head;
             // Shares 0 .. kRows / 2 - 1 are the lower bounds' channels in order, the others the upper ones'.  With one row
             // at a time a lane has both.
@@ -305,7 +346,10 @@ __global__ void __launch_bounds__(kBoundsThreads, kE4m3 ? (kUnroll > 4 ? 2 : 3) 
             }
             if (inside && TGEMM_CHECK(to < p.bounds.dbg_rows, kChkKvOutput, p.status)) {
                 signed char *const dst = p.bounds.base + to * 2 * p.cache.dim + piece * kPer;
-                if constexpr (kRows == 1) {
+                if constexpr (kRows == 1 && kE4m3) {
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+                    *reinterpret_cast<uint4 *>(dst + p.cache.dim) = make_uint4(out[kOwn / 4 - 4], out[kOwn / 4 - 3], out[kOwn / 4 - 2], out[kOwn / 4 - 1]);
+                } else if constexpr (kRows == 1) {
                     *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0], out[1]);
                     *reinterpret_cast<uint2 *>(dst + p.cache.dim) = make_uint2(out[kOwn / 4 - 2], out[kOwn / 4 - 1]);
                 } else {
@@ -315,10 +359,10 @@ __global__ void __launch_bounds__(kBoundsThreads, kE4m3 ? (kUnroll > 4 ? 2 : 3) 
                     else if constexpr (kOwn == 8) *reinterpret_cast<uint2 *>(at) = make_uint2(out[0], out[1]);
                     else *reinterpret_cast<uint4 *>(at) = make_uint4(out[0], out[1], out[kOwn / 4 - 2], out[kOwn / 4 - 1]);
                 }
-                if (lane == 0) p.bounds.scale[to] = s;
+                if (piece == 0 && row == 0) p.bounds.scale[to] = s;
             }
         }
-        base += items;
+        base += units;
         __syncthreads();                           // the sums have been read
     }
 }
@@ -336,6 +380,7 @@ struct ChooseParams {
     int *to_lengths;
     int keep, first, recent;
     int cached;                                    // keys that a block has room for
+    bool gather;                                   // a cluster's first block has room for the keys of all
     unsigned int *status;
 };
 
@@ -413,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChoosePa
     float *const s_scale = reinterpret_cast<float *>(negative + heads8 * pitch);
     float *const s_bias = s_scale + heads8;                      // [2 * kChunks][heads8]: of lo's and hi's sums over 64 dims
     griddep_wait();
+    if (p.gather) cluster.barrier_arrive();      // this block has begun: the others may write to its shared memory
     if (threadIdx.x == 0) {
         bool bad = false;
         s_n = kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad);
@@ -471,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChoosePa
         p.to_lengths[b] = n - (span.count - span.keep) * p.cache.page_size;
     const bool some = span.best > 0;
     // The blocks of a cluster go on together to every barrier, whatever length each of them has read.
-    const int slice = min((span.middle + blocks - 1) / blocks, p.cached);
+    const int slice = min((span.middle + blocks - 1) / blocks, p.cached);      // (of a gathered list: p.cached for all)
     const int lo = span.first + min(span.middle, rank * slice), size = some ? min(span.middle, (rank + 1) * slice) - (lo - span.first) : 0;
     // Lane i < 16 has page i of the warp's next 16; the ones after them are looked up a step ahead.
     auto lookup = [&](int i0) { return lane < 16 && i0 + lane < size ? list[lo + i0 + lane] : -1; };
@@ -584,6 +630,23 @@ __global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChoosePa
     }
     griddep_launch_dependents();                 // what follows would take the places of blocks that have not begun
     cp_async_wait<0>();
+    if (p.gather) {
+        // The first block ranks the keys of all: two barriers of the cluster instead of five.
+        uint32_t *const all_keys = cluster.map_shared_rank(keys, 0);
+        cluster.barrier_wait();
+        __syncthreads();
+        if (rank > 0)
+            for (int i = threadIdx.x; i < size; i += kThreads)
+                if (lo - span.first + i < p.cached) all_keys[lo - span.first + i] = keys[i];
+        cluster.sync();
+        if (rank > 0) return;
+        kv_rank_clear(sh);                       // in the ring's place
+        __syncthreads();
+        kv_rank<true>(
+            sh, some ? min(span.middle, p.cached) : 0, span.best, p.status, [&](int i) { return keys[i]; },
+            [&](int at, int i) { to[span.first + at] = list[span.first + i]; });
+        return;
+    }
     __syncthreads();
     kv_rank_clear(sh);                           // in the ring's place
     __syncthreads();

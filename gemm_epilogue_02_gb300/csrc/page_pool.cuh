@@ -5,7 +5,8 @@
 //                      pages that new tokens need (grow), or the page for the rows
 //                      of a child's last, partly filled page (fork)
 //   page_fork_kernel     the children's lists (their parents' full pages, counted
-//                      once more) and the rows of those last pages
+//                      once more) and the rows of those last pages;
+//                      page_fork_few_kernel does both
 //   page_free_kernel     counts a sequence's pages once less
 //   page_plan_kernel     compaction: which pages move where, and the new counts
 //   page_move_kernel     moves them, and translates the lists
@@ -79,8 +80,9 @@ __host__ __device__ inline int fork_length(const int *lengths, int batch, int pa
     return n;
 }
 
+// By one block of kTakeThreads.
 template <bool kFork>
-__global__ void __launch_bounds__(kTakeThreads, 1) page_take_kernel(const PagesParams p) {
+__device__ __forceinline__ void take_pages(const PagesParams &p) {
     constexpr int kWarps = kTakeThreads / 32;
     __shared__ int s_free[kTakeRound];                     // free pages found, in order
     __shared__ int s_end[kTakeThreads + 1];                // pages wanted by the sequences of this round, summed up
@@ -88,8 +90,6 @@ __global__ void __launch_bounds__(kTakeThreads, 1) page_take_kernel(const PagesP
     __shared__ int s_sums[33];
     __shared__ int s_found;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, size = p.cache.page_size;
-    griddep_wait();
-    griddep_launch_dependents();
     long long pos = 0;                                     // pages looked at
     int at = 0, have = 0;                                  // of s_free
     for (int b0 = 0; b0 < p.to.batch; b0 += kTakeThreads) {
@@ -206,6 +206,13 @@ __global__ void __launch_bounds__(kTakeThreads, 1) page_take_kernel(const PagesP
     }
 }
 
+template <bool kFork>
+__global__ void __launch_bounds__(kTakeThreads, 1) page_take_kernel(const PagesParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    take_pages<kFork>(p);
+}
+
 // ---------------------------------------------------------------- copies of rows
 constexpr int kPageThreads = 256;
 
@@ -216,20 +223,18 @@ __device__ __forceinline__ void page_row(const KvView &c, int r, bool slots_firs
     *head = slots_first ? q : rest;
 }
 
-// Grid: (chunks, children).
-template <int kLanes>
-__global__ void __launch_bounds__(kPageThreads) page_fork_kernel(const PagesParams p) {
-    constexpr int kPass = kPageThreads / kLanes, kUnroll = 4;
-    griddep_wait();
-    griddep_launch_dependents();
-    const int c = blockIdx.y, size = p.cache.page_size, parent = p.parents[c];
+// The list of child c and the rows of its last page, by block `chunk` of `chunks`.
+template <int kThreads, int kLanes>
+__device__ __forceinline__ void fork_child(const PagesParams &p, int c, int chunk, int chunks) {
+    constexpr int kPass = kThreads / kLanes, kUnroll = 4;
+    const int size = p.cache.page_size, parent = p.parents[c];
     bool bad = false;
     const int n = fork_length(p.table.lengths, p.table.batch, parent, p.table.width, size, p.to.width, &bad);
     const int full = n / size, rest = p.to.lengths[c] > full * size ? n - full * size : 0;
     if (n == 0) return;
     const int *const list = p.table.pages + parent * p.table.stride;
     int *const to = p.to.pages + c * p.to.stride;
-    for (int i = blockIdx.x * kPageThreads + threadIdx.x; i < full; i += gridDim.x * kPageThreads) {
+    for (int i = chunk * kThreads + threadIdx.x; i < full; i += chunks * kThreads) {
         const int page = list[i];
         to[i] = page;
         if (page >= 0 && page < p.cache.pages) atomicAdd(p.uses + page, 1);
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(kPageThreads) page_fork_kernel(const PagesPara
     const int rows = rest * p.cache.heads, piece = threadIdx.x % kLanes, in_pass = threadIdx.x / kLanes;
     const bool inside = piece * 16 < p.cache.row_bytes;
     const long long from_page = src * p.cache.page_stride, to_page = dst * p.cache.page_stride;
-    for (int r0 = blockIdx.x * kPass * kUnroll; r0 < rows; r0 += gridDim.x * kPass * kUnroll) {
+    for (int r0 = chunk * kPass * kUnroll; r0 < rows; r0 += chunks * kPass * kUnroll) {
         uint4 x[kUnroll][2];
         long long o[kUnroll];
 #pragma unroll
@@ -266,12 +271,33 @@ __global__ void __launch_bounds__(kPageThreads) page_fork_kernel(const PagesPara
             }
     }
     if (p.cache.k_scale)
-        for (int r = blockIdx.x * kPageThreads + threadIdx.x; r < rows; r += gridDim.x * kPageThreads) {
+        for (int r = chunk * kThreads + threadIdx.x; r < rows; r += chunks * kThreads) {
             const int slot = r / p.cache.heads, head = r - slot * p.cache.heads;
             const long long a = kv_scale_offset(p.cache, src, slot, head), z = kv_scale_offset(p.cache, dst, slot, head);
             p.cache.k_scale[z] = p.cache.k_scale[a];
             p.cache.v_scale[z] = p.cache.v_scale[a];
         }
+}
+
+// Grid: (chunks, children).
+template <int kLanes>
+__global__ void __launch_bounds__(kPageThreads) page_fork_kernel(const PagesParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    fork_child<kPageThreads, kLanes>(p, blockIdx.y, blockIdx.x, gridDim.x);
+}
+
+// Both in one launch, for little to copy: the first block of a cluster finds the pages, then all copy.
+constexpr int kForkBlocks = 8;
+
+template <int kLanes>
+__global__ void __launch_bounds__(kTakeThreads, 1) page_fork_few_kernel(const PagesParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int rank = static_cast<int>(cluster_ctarank());
+    if (rank == 0) take_pages<true>(p);
+    cluster_sync();                                        // releases what the first block has written, and acquires it
+    for (int c = rank; c < p.to.batch; c += kForkBlocks) fork_child<kTakeThreads, kLanes>(p, c, 0, 1);
 }
 
 // One block a sequence: its pages' counts go down, its length to 0.
@@ -313,34 +339,57 @@ struct CompactParams {
     unsigned int *status;
 };
 
+// Pages in rounds of kTakeRound: thread t has pages 8 t .. 8 t + 7 of a round, which
+// are read once (again where there are several rounds).
 __global__ void __launch_bounds__(kTakeThreads, 1) page_plan_kernel(const CompactParams p) {
     __shared__ int s_sums[33];
     griddep_wait();
     griddep_launch_dependents();
-    const int pages = static_cast<int>(p.cache.pages);
+    const int pages = static_cast<int>(p.cache.pages), rounds = (pages + kTakeRound - 1) / kTakeRound;
+    int u[kTakeDeep];
+    auto read = [&](int round) {
+        const int first = round * kTakeRound + static_cast<int>(threadIdx.x) * kTakeDeep;
+#pragma unroll
+        for (int i = 0; i < kTakeDeep; ++i) u[i] = first + i < pages ? p.uses[first + i] : 0;
+        return first;
+    };
     int mine = 0, total;
-    for (int i = threadIdx.x; i < pages; i += kTakeThreads) mine += p.uses[i] > 0;
+    for (int r = 0; r < rounds; ++r) {
+        read(r);
+#pragma unroll
+        for (int i = 0; i < kTakeDeep; ++i) mine += u[i] > 0;
+    }
     block_scan(mine, s_sums, &total);
     int holes = 0, moved = 0;
-    for (int i0 = 0; i0 < pages; i0 += kTakeThreads) {
-        const int i = i0 + static_cast<int>(threadIdx.x);
-        const bool in = i < pages, used = in && p.uses[i] > 0;
-        const bool hole = in && i < total && !used, moves = used && i >= total;
-        int n;
-        // Both at once: a block has 1024 of either at most.
-        const int upto = block_scan((hole ? 1 : 0) | (moves ? 1 << 16 : 0), s_sums, &n);
-        if (hole) p.below[holes + (upto & 0xFFFF) - 1] = i;
-        if (moves) p.above[moved + (upto >> 16) - 1] = i;
-        if (in && i >= total) p.map[i] = moves ? moved + (upto >> 16) - 1 : -1;
+    for (int r = 0; r < rounds; ++r) {
+        const int first = rounds == 1 ? static_cast<int>(threadIdx.x) * kTakeDeep : read(r);
+        // Both at once: a round has 8192 of either at most.
+        int both = 0, n;
+#pragma unroll
+        for (int i = 0; i < kTakeDeep; ++i) {
+            const bool used = u[i] > 0, in = first + i < pages;
+            both += (in && first + i < total && !used ? 1 : 0) | (first + i >= total && used ? 1 << 16 : 0);
+        }
+        const int before = block_scan(both, s_sums, &n) - both;
+        int hole = holes + (before & 0xFFFF), move = moved + (before >> 16);
+#pragma unroll
+        for (int i = 0; i < kTakeDeep; ++i) {
+            const int page = first + i;
+            if (page < total) {
+                if (page < pages) {
+                    if (u[i] > 0) p.to_uses[page] = u[i];
+                    else p.below[hole++] = page;
+                }
+            } else if (page < pages) {
+                p.map[page] = u[i] > 0 ? move : -1;
+                if (u[i] > 0) p.above[move++] = page;
+            }
+        }
         holes += n & 0xFFFF;
         moved += n >> 16;
     }
     moved = min(moved, holes);                             // the same, unless another stream changes a count meanwhile
     __syncthreads();
-    for (int i = threadIdx.x; i < total; i += kTakeThreads) {
-        const int u = p.uses[i];
-        if (u > 0) p.to_uses[i] = u;
-    }
     for (int i = threadIdx.x; i < moved; i += kTakeThreads) p.to_uses[p.below[i]] = p.uses[p.above[i]];
     __syncthreads();                                       // to_uses may be uses
     for (int i = total + threadIdx.x; i < pages; i += kTakeThreads) p.to_uses[i] = 0;

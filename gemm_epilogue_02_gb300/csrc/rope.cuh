@@ -25,8 +25,10 @@ namespace tgemm {
 
 constexpr int kRopePairs = 128;             // at most (dim 256)
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBackThreads = 128, kRopeBackCtas = 3;     // per SM
-constexpr int kRopeMaxBlocks = 1024;        // whose partial sums of weight gradients the workspace holds
+constexpr int kRopeBackThreads = 384, kRopeBackCtas = 1;     // per SM
+constexpr int kRopeMaxBlocks = 1024;        // whose sums of weight gradients the workspace holds
+constexpr int kRopeFan = 32;                // blocks' sums that are added up at once, at most
+static_assert(kRopeMaxBlocks <= kRopeFan * kRopeFan, "two levels add up every block's sums");
 
 struct RopeSide {
     const unsigned char *x, *g;             // rows, and (backward) gradients of what the forward pass wrote
@@ -37,14 +39,22 @@ struct RopeSide {
     int heads;
 };
 
+struct RopeArray {
+    unsigned char *base;
+    long long token, head;
+};
+
 struct RopeParams {
     RopeSide side[2];                       // queries, keys
     const int *positions;                   // [axes, tokens]
     long long axis_stride, tokens;
-    float *partials;                        // [blocks][2][dim]
+    // The workspace (null: no weight gradients are wanted): arrivals, zero between calls; sums of the blocks and of groups
+    // of them, [kRopeMaxBlocks + kRopeFan][2][dim].
+    unsigned *arrivals;                     // [kRopeFan + 1]
+    float *partials;
     float eps;
     int norm, weight_f32, shift, dim, pairs, axes;
-    int blocks;                             // of the pass that left the partial sums
+    int fan;                                // blocks of a group
     unsigned int *status;
     long long dbg_y[2];                     // debug builds: bytes of what is written
     unsigned long long turns[kRopePairs];
@@ -175,15 +185,33 @@ __device__ __forceinline__ void rope_stage_weights(RopeWeights<V, kLanes> &to, c
     }
 }
 
-// chunk k of lane l: weights 4 k .. 4 k + 3 of its a and b in a row
+// Chunk k of lane l: weights 4 k .. 4 k + 3 of its a, then of its b.
 template <int V, int kLanes>
-__device__ __forceinline__ void rope_weights(const RopeWeights<V, kLanes> &from, int l, float (&a)[V], float (&b)[V]) {
+__device__ __forceinline__ void rope_weights(const RopeWeights<V, kLanes> &from, int l, float2 (&a)[V / 2], float2 (&b)[V / 2]) {
 #pragma unroll
     for (int k = 0; k < V / 4; ++k) {
         const float4 x = from.part[k][l], y = from.part[V / 4 + k][l];
-        a[4 * k] = x.x, a[4 * k + 1] = x.y, a[4 * k + 2] = x.z, a[4 * k + 3] = x.w;
-        b[4 * k] = y.x, b[4 * k + 1] = y.y, b[4 * k + 2] = y.z, b[4 * k + 3] = y.w;
+        a[2 * k] = make_float2(x.x, x.y), a[2 * k + 1] = make_float2(x.z, x.w);
+        b[2 * k] = make_float2(y.x, y.y), b[2 * k + 1] = make_float2(y.z, y.w);
     }
+}
+
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
 
 template <int N>
@@ -214,7 +242,7 @@ struct RopeAngles {
         }
     }
     // places: lane a's position on axis a
-    __device__ __forceinline__ void turn(int places, int shift, int l, float (&c)[V], float (&s)[V]) const {
+    __device__ __forceinline__ void turn(int places, int shift, int l, float2 (&c)[V / 2], float2 (&s)[V / 2]) const {
         float oc[kOwn], os[kOwn];
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) {
@@ -224,23 +252,84 @@ struct RopeAngles {
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            c[i] = __shfl_sync(0xffffffffu, oc[i % kOwn], i / kOwn * kLanes + l);
-            s[i] = __shfl_sync(0xffffffffu, os[i % kOwn], i / kOwn * kLanes + l);
+            const float x = __shfl_sync(0xffffffffu, oc[i % kOwn], i / kOwn * kLanes + l);
+            const float y = __shfl_sync(0xffffffffu, os[i % kOwn], i / kOwn * kLanes + l);
+            (i % 2 ? c[i / 2].y : c[i / 2].x) = x;
+            (i % 2 ? s[i / 2].y : s[i / 2].x) = y;
         }
     }
 };
 
 // Work.  A pass is 32 / kLanes rows, of one token's queries or of its keys, for a
 // warp; the passes of all tokens in a row are cut into equal runs, one a warp.
+// N arrays of rows are followed together (addresses of the lane's row).
+template <int kRows, int N>
 struct RopeCursor {
     long long token;
-    int pass;
+    int side, left, head;                   // passes of the side that are left, this one among them; the lane's row
+    unsigned char *at[N];
+
+    // array(side, i): base and strides of array i
+    template <typename Array>
+    __device__ __forceinline__ void enter(const RopeParams &p, int row, int pass, Array array) {
+        left = (p.side[side].heads + kRows - 1) / kRows - pass;
+        head = pass * kRows + row;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const RopeArray a = array(p.side[side], i);
+            at[i] = a.base + token * a.token + static_cast<long long>(head) * a.head;
+        }
+    }
+    template <typename Array>
+    __device__ __forceinline__ void begin(const RopeParams &p, long long pass, int passes_q, int passes, int row, Array array) {
+        token = passes > 0 ? pass / passes : 0;
+        int in = passes > 0 ? static_cast<int>(pass - token * passes) : 0;
+        side = in >= passes_q ? 1 : 0;
+        enter(p, row, in - (side ? passes_q : 0), array);
+    }
+    // The next pass there is; true when it is another token's.
+    template <typename Array>
+    __device__ __forceinline__ bool next(const RopeParams &p, int row, Array array) {
+        if (--left > 0) {
+            head += kRows;
+#pragma unroll
+            for (int i = 0; i < N; ++i) at[i] += kRows * array(p.side[side], i).head;
+            return false;
+        }
+        const int heads = p.side[1 - side].heads;
+        const bool other = side == 1 || heads == 0;
+        if (other) ++token;
+        if (heads > 0) side = 1 - side;
+        enter(p, row, 0, array);
+        return other;
+    }
 };
 
-// Passes ahead of the one at hand whose rows are on their way.
+template <bool kBf16, int V, bool kInterleaved>
+__device__ __forceinline__ void rope_split2(const RopeRaw<V> &raw, float2 (&a)[V / 2], float2 (&b)[V / 2]) {
+    float x[V], y[V];
+    rope_split<kBf16, V, kInterleaved>(raw, x, y);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        a[i] = make_float2(x[2 * i], x[2 * i + 1]);
+        b[i] = make_float2(y[2 * i], y[2 * i + 1]);
+    }
+}
+template <bool kBf16, int V, bool kInterleaved>
+__device__ __forceinline__ void rope_write2(unsigned char *row, const float2 (&a)[V / 2], const float2 (&b)[V / 2], const int (&unit)[2],
+                                            const bool (&is)[2]) {
+    float x[V], y[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        x[2 * i] = a[i].x, x[2 * i + 1] = a[i].y;
+        y[2 * i] = b[i].x, y[2 * i + 1] = b[i].y;
+    }
+    rope_write<kBf16, V, kInterleaved>(row, x, y, unit, is);
+}
+
 template <bool kBf16, int V, int kLanes, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kRows = 32 / kLanes, kWarps = kRopeThreads / 32, kAhead = 3;
+    constexpr int kRows = 32 / kLanes, kWarps = kRopeThreads / 32, kAhead = 3;     // passes whose rows are on their way
     __shared__ RopeWeights<V, kLanes> s_w[2];
     const int lane = threadIdx.x & 31, l = lane % kLanes, row = lane / kLanes;
     int unit[2];
@@ -252,29 +341,20 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
     const int passes_q = (p.side[0].heads + kRows - 1) / kRows, passes = passes_q + (p.side[1].heads + kRows - 1) / kRows;
     const long long warps = static_cast<long long>(gridDim.x) * kWarps, warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const long long all = p.tokens * passes, begin = warp * all / warps;
-    int left = static_cast<int>((warp + 1) * all / warps - begin);
-    RopeCursor use, load;
-    use.token = begin / passes;
-    use.pass = static_cast<int>(begin - use.token * passes);
-    load = use;
+    int left = static_cast<int>((warp + 1) * all / warps - begin), loads = left;
+    auto inputs = [](const RopeSide &s, int) { return RopeArray{const_cast<unsigned char *>(s.x), s.x_token, s.x_head}; };
+    auto outputs = [](const RopeSide &s, int) { return RopeArray{s.y, s.y_token, s.y_head}; };
+    RopeCursor<kRows, 1> load, use;
+    load.begin(p, begin, passes_q, passes, row, inputs);
+    use.begin(p, begin, passes_q, passes, row, outputs);
     griddep_wait();
     griddep_launch_dependents();
-    auto next = [&](RopeCursor &u) {
-        if (++u.pass == passes) {
-            u.pass = 0;
-            ++u.token;
-        }
-    };
-    int loads = left;
     RopeRaw<V> ring[kAhead];
     auto request = [&](RopeRaw<V> &raw) {
-        const bool q = load.pass >= passes_q;
-        const RopeSide &side = p.side[q ? 1 : 0];
-        const int head = (load.pass - (q ? passes_q : 0)) * kRows + row;
-        const bool there = loads > 0 && head < side.heads;
+        const bool there = loads > 0 && load.head < p.side[load.side].heads;
         const bool in[2] = {there && is[0], there && is[1]};
-        rope_read<V>(raw, side.x + load.token * side.x_token + (there ? head : 0) * side.x_head, unit, in);
-        if (--loads > 0) next(load);
+        rope_read<V>(raw, load.at[0], unit, in);
+        if (--loads > 0) load.next(p, row, inputs);
     };
     auto places_of = [&](long long token) {
         return lane < p.axes && token < p.tokens ? p.positions[lane * p.axis_stride + token] : 0;
@@ -285,7 +365,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
     rope_stage_weights<kBf16, V, kLanes, kInterleaved>(s_w[0], p.side[0].w, p.weight_f32, p.dim, p.pairs);
     rope_stage_weights<kBf16, V, kLanes, kInterleaved>(s_w[1], p.side[1].w, p.weight_f32, p.dim, p.pairs);
     __syncthreads();
-    float c[V], s[V];
+    float2 c[V / 2], s[V / 2];
     bool fresh = true;                      // the token's angles are to be worked out
     // A slot of the ring is refilled as soon as it is unpacked: moving rows that are on their way would wait for them.
     auto step = [&](RopeRaw<V> &raw) {
@@ -293,34 +373,29 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
             angles.turn(places, p.shift, l, c, s);
             places = places_of(use.token + 1);
         }
-        float a[V], b[V], wa[V], wb[V];
-        rope_split<kBf16, V, kInterleaved>(raw, a, b);
+        float2 a[V / 2], b[V / 2], wa[V / 2], wb[V / 2];
+        rope_split2<kBf16, V, kInterleaved>(raw, a, b);
         request(raw);
-        const bool q = use.pass >= passes_q;
-        const RopeSide &side = p.side[q ? 1 : 0];
-        const int head = (use.pass - (q ? passes_q : 0)) * kRows + row;
-        rope_weights(s_w[q ? 1 : 0], l, wa, wb);
+        rope_weights(s_w[use.side], l, wa, wb);
         float r = 1.0f;
         if (p.norm) {
-            float sum = 0.0f;
+            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
-            r = rsqrtf(fmaf(rope_sum<kLanes>(sum), inv_dim, p.eps));
+            for (int i = 0; i < V / 2; ++i) sum = fma2(a[i], a[i], fma2(b[i], b[i], sum));
+            r = rsqrtf(fmaf(rope_sum<kLanes>(sum.x + sum.y), inv_dim, p.eps));
         }
+        const float2 rr = make_float2(r, r);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float f = a[i] * r * wa[i], g = b[i] * r * wb[i];
-            a[i] = f * c[i] - g * s[i];
-            b[i] = g * c[i] + f * s[i];
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 f = mul2(mul2(a[i], rr), wa[i]), g = mul2(mul2(b[i], rr), wb[i]);
+            a[i] = fma2(f, c[i], mul2(g, make_float2(-s[i].x, -s[i].y)));
+            b[i] = fma2(g, c[i], mul2(f, s[i]));
         }
-        const bool there = head < side.heads;
+        const bool there = use.head < p.side[use.side].heads;
         const bool in[2] = {there && is[0], there && is[1]};
-        const long long at = use.token * side.y_token + (there ? head : 0) * side.y_head;
-        if (there && TGEMM_CHECK(at + 2 * p.dim <= p.dbg_y[q ? 1 : 0], kChkRope, p.status))
-            rope_write<kBf16, V, kInterleaved>(side.y + at, a, b, unit, in);
-        const long long token = use.token;
-        next(use);
-        fresh = use.token != token;
+        if (there && TGEMM_CHECK(use.at[0] - p.side[use.side].y + 2 * p.dim <= p.dbg_y[use.side], kChkRope, p.status))
+            rope_write2<kBf16, V, kInterleaved>(use.at[0], a, b, unit, in);
+        fresh = left > 0 && use.next(p, row, outputs);
     };
     while (left > 0) {
 #pragma unroll
@@ -329,11 +404,21 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
     }
 }
 
+// Counts up to `last` and from there back to 0; returns the count before.  The
+// block's writes before it (through a barrier) are visible to the blocks that
+// count after it, and theirs before to this one.
+__device__ __forceinline__ unsigned rope_count(unsigned *counter, unsigned last) {
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(last) : "memory");
+    return old;
+}
+
 template <bool kBf16, int V, int kLanes, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeBackThreads, kRopeBackCtas) rope_backward_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kRows = 32 / kLanes, kWarps = kRopeBackThreads / 32, kAhead = 2;
     __shared__ RopeWeights<V, kLanes> s_w[2];
-    __shared__ float s_dw[kWarps][2][2 * kRopePairs];
+    __shared__ float4 s_sum[2][kWarps][2 * (V / 4)][32];
+    __shared__ bool s_last;
     const int lane = threadIdx.x & 31, l = lane % kLanes, row = lane / kLanes;
     int unit[2];
     bool is[2];
@@ -344,31 +429,25 @@ __global__ void __launch_bounds__(kRopeBackThreads, kRopeBackCtas) rope_backward
     const int passes_q = (p.side[0].heads + kRows - 1) / kRows, passes = passes_q + (p.side[1].heads + kRows - 1) / kRows;
     const long long warps = static_cast<long long>(gridDim.x) * kWarps, warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const long long all = p.tokens * passes, begin = warp * all / warps;
-    int left = static_cast<int>((warp + 1) * all / warps - begin);
-    RopeCursor use, load;
-    use.token = passes > 0 ? begin / passes : 0;
-    use.pass = passes > 0 ? static_cast<int>(begin - use.token * passes) : 0;
-    load = use;
+    int left = static_cast<int>((warp + 1) * all / warps - begin), loads = left;
+    auto inputs = [](const RopeSide &s, int i) {
+        return i ? RopeArray{const_cast<unsigned char *>(s.x), s.x_token, s.x_head}
+                 : RopeArray{const_cast<unsigned char *>(s.g), s.g_token, s.g_head};
+    };
+    auto outputs = [](const RopeSide &s, int) { return RopeArray{s.y, s.y_token, s.y_head}; };
+    RopeCursor<kRows, 2> load;
+    RopeCursor<kRows, 1> use;
+    load.begin(p, begin, passes_q, passes, row, inputs);
+    use.begin(p, begin, passes_q, passes, row, outputs);
     griddep_wait();
     griddep_launch_dependents();
-    auto next = [&](RopeCursor &u) {
-        if (++u.pass == passes) {
-            u.pass = 0;
-            ++u.token;
-        }
-    };
-    int loads = left;
     RopeRaw<V> ring_x[kAhead], ring_g[kAhead];
     auto request = [&](RopeRaw<V> &next_x, RopeRaw<V> &next_g) {
-        const bool q = load.pass >= passes_q;
-        const RopeSide &side = p.side[q ? 1 : 0];
-        const int head = (load.pass - (q ? passes_q : 0)) * kRows + row;
-        const bool there = loads > 0 && head < side.heads;
-        const bool in[2] = {there && is[0], there && is[1]};
-        const bool x_in[2] = {in[0] && p.norm, in[1] && p.norm};
-        rope_read<V>(next_g, side.g + load.token * side.g_token + (there ? head : 0) * side.g_head, unit, in);
-        rope_read<V>(next_x, side.x + load.token * side.x_token + (there ? head : 0) * side.x_head, unit, x_in);
-        if (--loads > 0) next(load);
+        const bool there = loads > 0 && load.head < p.side[load.side].heads;
+        const bool in[2] = {there && is[0], there && is[1]}, x_in[2] = {in[0] && p.norm, in[1] && p.norm};
+        rope_read<V>(next_g, load.at[0], unit, in);
+        rope_read<V>(next_x, load.at[1], unit, x_in);
+        if (--loads > 0) load.next(p, row, inputs);
     };
     auto places_of = [&](long long token) {
         return lane < p.axes && token < p.tokens ? p.positions[lane * p.axis_stride + token] : 0;
@@ -379,55 +458,72 @@ __global__ void __launch_bounds__(kRopeBackThreads, kRopeBackCtas) rope_backward
     rope_stage_weights<kBf16, V, kLanes, kInterleaved, kRopeBackThreads>(s_w[0], p.side[0].w, p.weight_f32, p.dim, p.pairs);
     rope_stage_weights<kBf16, V, kLanes, kInterleaved, kRopeBackThreads>(s_w[1], p.side[1].w, p.weight_f32, p.dim, p.pairs);
     __syncthreads();
-    float da[2][V], db[2][V];
+    // The weight gradients' sums of the side at hand; those of the other are in shared memory.
+    float2 da[V / 2], db[V / 2];
+    float4 *const mine = &s_sum[0][threadIdx.x >> 5][0][lane];
+    auto fetch = [&](int side) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+        for (int k = 0; k < V / 4; ++k) {
+            const float4 x = mine[(side * kWarps * 2 * (V / 4) + k) * 32], y = mine[(side * kWarps * 2 * (V / 4) + V / 4 + k) * 32];
+            da[2 * k] = make_float2(x.x, x.y), da[2 * k + 1] = make_float2(x.z, x.w);
+            db[2 * k] = make_float2(y.x, y.y), db[2 * k + 1] = make_float2(y.z, y.w);
+        }
+    };
+    auto store = [&](int side) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) da[q][i] = db[q][i] = 0.0f;
-    float c[V], s[V];
+        for (int k = 0; k < V / 4; ++k) {
+            mine[(side * kWarps * 2 * (V / 4) + k) * 32] = make_float4(da[2 * k].x, da[2 * k].y, da[2 * k + 1].x, da[2 * k + 1].y);
+            mine[(side * kWarps * 2 * (V / 4) + V / 4 + k) * 32] = make_float4(db[2 * k].x, db[2 * k].y, db[2 * k + 1].x, db[2 * k + 1].y);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) da[i] = db[i] = make_float2(0.0f, 0.0f);
+    store(0);
+    store(1);
+    int side_at_hand = 0;
+    float2 c[V / 2], s[V / 2];
     bool fresh = true;                      // the token's angles are to be worked out
-    auto step = [&](RopeRaw<V> &raw_x, RopeRaw<V> &raw_g, float (&da)[V], float (&db)[V], const RopeWeights<V, kLanes> &weights,
-                    const RopeSide &side, int pass, long long dbg) {
-        float a[V], b[V], x[V], y[V];
-        rope_split<kBf16, V, kInterleaved>(raw_g, a, b);
-        rope_split<kBf16, V, kInterleaved>(raw_x, x, y);
+    auto step = [&](RopeRaw<V> &raw_x, RopeRaw<V> &raw_g) {
+        const RopeSide &side = p.side[use.side];
+        const RopeWeights<V, kLanes> &weights = s_w[use.side];
+        float2 a[V / 2], b[V / 2], x[V / 2], y[V / 2];
+        rope_split2<kBf16, V, kInterleaved>(raw_g, a, b);
+        rope_split2<kBf16, V, kInterleaved>(raw_x, x, y);
         request(raw_x, raw_g);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float f = a[i] * c[i] + b[i] * s[i];
-            b[i] = b[i] * c[i] - a[i] * s[i];
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 f = fma2(a[i], c[i], mul2(b[i], s[i]));
+            b[i] = fma2(b[i], c[i], mul2(a[i], make_float2(-s[i].x, -s[i].y)));
             a[i] = f;
         }
         if (p.norm) {
-            float sum = 0.0f, dot = 0.0f;
+            float2 sums = make_float2(0.0f, 0.0f), dots = make_float2(0.0f, 0.0f);
             {
-                float wa[V], wb[V];
+                float2 wa[V / 2], wb[V / 2];
                 rope_weights(weights, l, wa, wb);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    sum = fmaf(x[i], x[i], fmaf(y[i], y[i], sum));
-                    dot = fmaf(a[i] * wa[i], x[i], fmaf(b[i] * wb[i], y[i], dot));
+                for (int i = 0; i < V / 2; ++i) {
+                    sums = fma2(x[i], x[i], fma2(y[i], y[i], sums));
+                    dots = fma2(mul2(a[i], wa[i]), x[i], fma2(mul2(b[i], wb[i]), y[i], dots));
                 }
             }
-            sum = rope_sum<kLanes>(sum);
-            dot = rope_sum<kLanes>(dot);
-            const float r = rsqrtf(fmaf(sum, inv_dim, p.eps)), back = r * r * dot * inv_dim;
-            float wa[V], wb[V];
+            const float sum = rope_sum<kLanes>(sums.x + sums.y), dot = rope_sum<kLanes>(dots.x + dots.y);
+            const float r = rsqrtf(fmaf(sum, inv_dim, p.eps)), back = -r * r * dot * inv_dim;
+            const float2 rr = make_float2(r, r), bb = make_float2(back, back);
+            float2 wa[V / 2], wb[V / 2];
             rope_weights(weights, l, wa, wb);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                da[i] = fmaf(a[i], x[i] * r, da[i]);
-                db[i] = fmaf(b[i], y[i] * r, db[i]);
-                a[i] = r * fmaf(-x[i], back, a[i] * wa[i]);
-                b[i] = r * fmaf(-y[i], back, b[i] * wb[i]);
+            for (int i = 0; i < V / 2; ++i) {
+                da[i] = fma2(a[i], mul2(x[i], rr), da[i]);
+                db[i] = fma2(b[i], mul2(y[i], rr), db[i]);
+                a[i] = mul2(rr, fma2(x[i], bb, mul2(a[i], wa[i])));
+                b[i] = mul2(rr, fma2(y[i], bb, mul2(b[i], wb[i])));
             }
         }
-        const int head = pass * kRows + row;
-        const bool there = head < side.heads;
+        const bool there = use.head < side.heads;
         const bool in[2] = {there && is[0], there && is[1]};
-        const long long at = use.token * side.y_token + (there ? head : 0) * side.y_head;
-        if (there && TGEMM_CHECK(at + 2 * p.dim <= dbg, kChkRope, p.status))
-            rope_write<kBf16, V, kInterleaved>(side.y + at, a, b, unit, in);
+        if (there && TGEMM_CHECK(use.at[0] - side.y + 2 * p.dim <= p.dbg_y[use.side], kChkRope, p.status))
+            rope_write2<kBf16, V, kInterleaved>(use.at[0], a, b, unit, in);
     };
     while (left > 0) {
 #pragma unroll
@@ -437,58 +533,62 @@ __global__ void __launch_bounds__(kRopeBackThreads, kRopeBackCtas) rope_backward
                 angles.turn(places, p.shift, l, c, s);
                 places = places_of(use.token + 1);
             }
-            if (use.pass < passes_q) step(ring_x[i], ring_g[i], da[0], db[0], s_w[0], p.side[0], use.pass, p.dbg_y[0]);
-            else step(ring_x[i], ring_g[i], da[1], db[1], s_w[1], p.side[1], use.pass - passes_q, p.dbg_y[1]);
-            const long long token = use.token;
-            next(use);
-            fresh = use.token != token;
+            if (use.side != side_at_hand) {
+                store(side_at_hand);
+                side_at_hand = use.side;
+                fetch(side_at_hand);
+            }
+            step(ring_x[i], ring_g[i]);
+            fresh = left > 0 && use.next(p, row, outputs);
         }
     }
     if (!p.partials) return;
-    // The block's sums of the weight gradients: rows of a warp, then the warps.
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float x = j ? db[q][i] : da[q][i];
-#pragma unroll
-                for (int o = kLanes; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                const int e = rope_element<V, kInterleaved>(i, j, unit);
-                if (row == 0 && e < p.dim) s_dw[threadIdx.x >> 5][q][e] = x;
-            }
+    // The block's sums of the weight gradients, over the warps and the rows of each.
+    store(side_at_hand);
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.dim; i += kRopeBackThreads) {
-        const int q = i >= p.dim, e = i - q * p.dim;
+    const int width = 2 * p.dim;
+    float *const own = p.partials + static_cast<long long>(blockIdx.x) * width;
+    for (int i = threadIdx.x; i < 2 * kLanes * 2 * V; i += kRopeBackThreads) {
+        const int q = i / (kLanes * 2 * V), at = i - q * (kLanes * 2 * V), lane_of = at / (2 * V), k = at - lane_of * (2 * V);
+        int u[2];
+        bool in[2];
+        rope_units<V, kInterleaved>(lane_of, p.dim, p.pairs, u, in);
+        const int e = rope_element<V, kInterleaved>(k % V, k / V, u);
+        if (e >= p.dim) continue;
         float x = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) x += s_dw[w][q][e];
-        p.partials[static_cast<long long>(blockIdx.x) * 2 * p.dim + i] = x;
-    }
-}
-
-// Adds the blocks' sums up in a fixed order, 32 columns a block.
-__global__ void __launch_bounds__(kRopeThreads) rope_weight_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kWarps = kRopeThreads / 32;
-    __shared__ float s_sum[kWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = static_cast<int>(blockIdx.x) * 32 + lane;
-    griddep_wait();
-    griddep_launch_dependents();
-    float x = 0.0f;
-    if (col < 2 * p.dim) {
-#pragma unroll 8
-        for (int b = warp; b < p.blocks; b += kWarps) x += p.partials[static_cast<long long>(b) * 2 * p.dim + col];
-    }
-    s_sum[warp][lane] = x;
-    __syncthreads();
-    if (warp == 0 && col < 2 * p.dim) {
-        float sum = 0.0f;
+        for (int w = 0; w < kWarps; ++w)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += s_sum[w][lane];
-        const int q = col >= p.dim;
-        float *const dw = p.side[q].dw;
-        if (dw) dw[col - q * p.dim] = sum;
+            for (int r = 0; r < kRows; ++r) x += reinterpret_cast<const float *>(&s_sum[q][w][k / 4][r * kLanes + lane_of])[k % 4];
+        own[q * p.dim + e] = x;
+    }
+    // The last block of a group to arrive adds the group's sums up, the last group those of all: in a fixed order, whoever
+    // is last.
+    const int blocks = static_cast<int>(gridDim.x), group = static_cast<int>(blockIdx.x) / p.fan, first = group * p.fan;
+    const int members = min(p.fan, blocks - first), groups = (blocks + p.fan - 1) / p.fan;
+    auto arrive = [&](unsigned *counter, int count) {
+        __syncthreads();
+        if (threadIdx.x == 0) s_last = rope_count(counter, static_cast<unsigned>(count - 1)) == static_cast<unsigned>(count - 1);
+        __syncthreads();
+        return s_last;
+    };
+    auto total = [&](const float *rows, int count, int column) {
+        float x = 0.0f;
+#pragma unroll 8
+        for (int r = 0; r < count; ++r) x += __ldcg(rows + static_cast<long long>(r) * width + column);
+        return x;
+    };
+    if (!arrive(p.arrivals + group, members)) return;
+    const float *rows = p.partials + static_cast<long long>(first) * width;
+    float *const all_groups = p.partials + static_cast<long long>(kRopeMaxBlocks) * width;
+    if (groups > 1) {
+        for (int i = threadIdx.x; i < width; i += kRopeBackThreads) all_groups[static_cast<long long>(group) * width + i] = total(rows, members, i);
+        if (!arrive(p.arrivals + kRopeFan, groups)) return;
+        rows = all_groups;
+    }
+    for (int i = threadIdx.x; i < width; i += kRopeBackThreads) {
+        const int q = i >= p.dim, e = i - q * p.dim;
+        if (p.side[q].dw) p.side[q].dw[e] = total(rows, groups > 1 ? groups : members, i);
     }
 }
 

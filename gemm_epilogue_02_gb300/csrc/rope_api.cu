@@ -142,10 +142,9 @@ cudaError_t launch_rope(const RuntimeInfo &rt, RopeParams &p, bool backward, cud
                       kRopeThreads, 0, s, p);
     const unsigned blocks =
         rope_blocks(p, kLanes, kRopeBackThreads, std::min<int64_t>(kRopeMaxBlocks, static_cast<int64_t>(rt.num_sms) * kRopeBackCtas));
-    p.blocks = static_cast<int>(blocks);
-    const cudaError_t e = launch(rope_backward_kernel<kBf16, V, kLanes, kInterleaved>, dim3(blocks), kRopeBackThreads, 0, s, p);
-    if (e != cudaSuccess || !p.partials) return e;
-    return launch(rope_weight_kernel, dim3(static_cast<unsigned>((2 * p.dim + 31) / 32)), kRopeThreads, 0, s, p);
+    p.fan = 1;
+    while (p.fan * p.fan < static_cast<int>(blocks)) ++p.fan;
+    return launch(rope_backward_kernel<kBf16, V, kLanes, kInterleaved>, dim3(blocks), kRopeBackThreads, 0, s, p);
 }
 
 template <bool kBf16>
@@ -169,7 +168,9 @@ cudaError_t launch_rope_dtype(const RuntimeInfo &rt, RopeParams &p, int64_t dtyp
                                : launch_rope_shape<false>(rt, p, v, interleaved, backward, s);
 }
 
-int64_t workspace_bytes(int64_t dim) { return static_cast<int64_t>(kRopeMaxBlocks) * 2 * dim * 4; }
+constexpr int64_t kArrivals = 256;               // bytes
+static_assert((kRopeFan + 1) * 4 <= kArrivals, "a counter for each group and one for all");
+int64_t workspace_bytes(int64_t dim) { return kArrivals + static_cast<int64_t>(kRopeMaxBlocks + kRopeFan) * 2 * dim * 4; }
 
 }  // namespace
 
@@ -291,7 +292,10 @@ extern "C" tgemm_status tgemm_qk_norm_rope_backward(const tgemm_qk_norm_rope_bac
     }
     p.side[0].dw = b->q_weight_grad;
     p.side[1].dw = b->k_weight_grad;
-    p.partials = weights ? static_cast<float *>(b->workspace) : nullptr;
+    if (weights) {
+        p.arrivals = static_cast<unsigned *>(b->workspace);
+        p.partials = reinterpret_cast<float *>(static_cast<unsigned char *>(b->workspace) + kArrivals);
+    }
     p.status = rt.status;
     return done(launch_rope_dtype(rt, p, a->dtype, v, interleaved, true, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -15,7 +15,7 @@ import torch
 
 from . import _binding as _b
 
-_F16, _BF16, _E4M3 = torch.float16, torch.bfloat16, torch.float8_e4m3fn
+_F16, _BF16, _E4M3, _I32 = torch.float16, torch.bfloat16, torch.float8_e4m3fn, torch.int32
 _DT = {_F16: _b.TGEMM_F16, _BF16: _b.TGEMM_BF16}
 _NO_WEIGHTS = (0, 0, 0, 0)
 # The current stream's handle and the current device, without building the
@@ -74,26 +74,31 @@ class PagedCache:
 def _table(page_table, index):
     """(pages, width, stride, batch) of a page table."""
     shape, stride = page_table.shape, page_table.stride()
-    if len(shape) != 2 or page_table.dtype is not torch.int32 or (stride[1] != 1 and shape[1] > 1):
+    if len(shape) != 2 or page_table.dtype is not _I32 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError("the page table must be int32 [batch, pages] with unit stride of pages")
     if page_table.get_device() != index:
         raise ValueError("the page table must be on the cache's device")
-    return page_table.data_ptr(), shape[1], stride[0], shape[0]
+    batch, width = shape
+    return page_table.data_ptr(), width, stride[0], batch
 
 
-def _head_table(page_table, cache):
-    """(pages, width, batch stride, batch, head stride) of a page table with a list for each key head."""
+def _lists(page_table, index, heads):
+    """(pages, width, stride, batch, head stride) of a page table that has a list for each key head or (head stride 0) one
+    that they share."""
     shape, stride = page_table.shape, page_table.stride()
-    if page_table.dtype is not torch.int32 or shape[1] != cache.heads or (stride[2] != 1 and shape[2] > 1):
-        raise ValueError("page lists of each head must be int32 [batch, heads, pages] with unit stride of pages")
-    if page_table.get_device() != cache._index:
+    if (len(shape) != 2 and (len(shape) != 3 or shape[1] != heads)) or page_table.dtype is not _I32 or (
+            stride[-1] != 1 and shape[-1] > 1):
+        raise ValueError("the page table must be int32 [batch, pages] or [batch, heads, pages] with unit stride of pages")
+    if page_table.get_device() != index:
         raise ValueError("the page table must be on the cache's device")
-    return page_table.data_ptr(), shape[2], stride[0], shape[0], stride[1]
+    if len(shape) == 2:
+        return page_table.data_ptr(), shape[1], stride[0], shape[0], 0
+    return page_table.data_ptr(), shape[2], stride[0], shape[0], stride[1] if heads > 1 else 0
 
 
 def _vector(name, t, n, index):
     """The address of a contiguous int32 [n] tensor."""
-    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
+    if t.dtype is not _I32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
         raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on the cache's device")
     return t.data_ptr()
 
@@ -107,16 +112,16 @@ def _weights(name, w, batch, heads, index):
     return w.data_ptr(), shape[2], stride[0], stride[1]
 
 
-def _launch(index, stream, fn, *args):
-    """fn(*args, stream) with the cache's device current; raises on a status."""
+def _launch(index, stream, fn, args):
+    """fn(args, stream) with the cache's device current; raises on a status."""
     if index < 0:
         raise ValueError("the cache must be on a CUDA device")
     s = _raw_stream(index) if stream is None else stream.cuda_stream
     if index == _current_device():
-        st = fn(*args, s)
+        st = fn(args, s)
     else:
         with torch.cuda.device(index):
-            st = fn(*args, s)
+            st = fn(args, s)
     if st != 0:
         raise _b.TgemmError(st, fn.__name__)
 
@@ -175,8 +180,7 @@ def attention_decode(Q: torch.Tensor, cache: PagedCache, page_table: torch.Tenso
     [batch, heads, pages] as kv_select() writes it, has a list for each key head;
     positions are then those of the lists."""
     index = cache._index
-    lists = page_table.dim() == 3
-    pages, width, stride, batch, head_stride = (_head_table(page_table, cache) if lists else (*_table(page_table, index), 0))
+    pages, width, stride, batch, head_stride = _lists(page_table, index, cache.heads)
     length = _vector("lengths", lengths, batch, index)
     shape, sq, so, dtype = Q.shape, Q.stride(), O.stride(), Q.dtype
     if len(shape) != 3 or O.shape != shape or shape[0] != batch or shape[2] != cache.dim or shape[1] % cache.heads:
@@ -195,13 +199,15 @@ def attention_decode(Q: torch.Tensor, cache: PagedCache, page_table: torch.Tenso
             workspace = attention_decode_workspace(Q, cache, page_table, weights is not None)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the cache's device")
-    args = _decode(cache._address, pages, length, width, stride, batch, *w, Q.data_ptr(), O.data_ptr(), shape[1],
-                   sq[0], sq[1], so[0], so[1], window, cache.dim ** -0.5 if scale is None else scale, cap,
-                   workspace.data_ptr(), workspace.nbytes, _DT[dtype])
-    if lists:
-        _launch(index, stream, _b.tgemm_attention_decode_lists, args, head_stride)
-    else:
-        _launch(index, stream, _b.tgemm_attention_decode, args)
+    call = _b.tgemm_attention_decode
+    if head_stride:
+        def tgemm_attention_decode_lists(args, stream):
+            return _b.tgemm_attention_decode_lists(args, head_stride, stream)
+        call = tgemm_attention_decode_lists
+    _launch(index, stream, call,
+            _decode(cache._address, pages, length, width, stride, batch, *w, Q.data_ptr(), O.data_ptr(), shape[1],
+                    sq[0], sq[1], so[0], so[1], window, cache.dim ** -0.5 if scale is None else scale, cap,
+                    workspace.data_ptr(), workspace.nbytes, _DT[dtype]))
     return O
 
 

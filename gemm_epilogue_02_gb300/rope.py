@@ -51,57 +51,83 @@ class Rotary:
         self._address = ctypes.addressof(c)
 
 
-def _rows(name, t, like, index):
-    """(address, token stride, head stride) of rows of heads with the shape and dtype of `like`."""
-    stride = t.stride()
-    if t.shape != like.shape or t.dtype is not like.dtype or stride[2] != 1 or t.get_device() != index:
-        raise ValueError(f"{name} must be [tokens, heads, dim] of its input's shape, dtype and device with unit stride of dim")
-    return t.data_ptr(), stride[0], stride[1]
+_BAD_ROWS = "{} must be [tokens, heads, dim] of its input's shape and dtype with unit stride of dim"
+
+
+def _refuse(Q, K, positions, rotary, eps, weights):
+    """Says what is wrong with arguments that _common() does not take."""
+    if Q.dim() != 3 or Q.dtype not in _DT or Q.stride(2) != 1:
+        raise ValueError("Q must be float16 or bfloat16 [tokens, q_heads, dim] with unit stride of dim")
+    if K is not None and (K.dim() != 3 or K.shape[0] != Q.shape[0] or K.shape[2] != Q.shape[2] or K.dtype is not Q.dtype
+                          or K.stride(2) != 1):
+        raise ValueError("K must be [tokens, k_heads, dim] of Q's tokens, dim and dtype with unit stride of dim")
+    for w in weights:
+        if w is not None and (w.shape != Q.shape[2:] or w.stride(0) != 1 or w.dtype not in (Q.dtype, torch.float32)):
+            raise ValueError("weights must be contiguous [dim] tensors, float32 or of Q's dtype")
+    if eps is None and any(w is not None for w in weights):
+        raise ValueError("weights go with the norm: eps must be a number")
+    if rotary is None:
+        raise ValueError("neither a norm nor a rotation")
+    if 2 * rotary.pairs > Q.shape[2]:
+        raise ValueError("the rotation has more pairs than a head")
+    if positions is None:
+        raise ValueError("a rotation needs positions")
+    raise ValueError("q_weight and k_weight must share dtype, and positions be int32 [axes, tokens] (or [tokens]) with unit stride "
+                     "of tokens")
 
 
 def _common(Q, K, positions, rotary, q_weight, k_weight, eps, shift):
-    """(device index, heads of K, the arguments after the rows)."""
-    index, shape, dtype = Q.get_device(), Q.shape, Q.dtype
-    if len(shape) != 3 or dtype not in _DT or Q.stride(2) != 1:
-        raise ValueError("Q must be float16 or bfloat16 [tokens, q_heads, dim] with unit stride of dim")
-    k_heads = 0
+    """(Q's shape, dtype and row arguments, K's shape and row arguments, the arguments after the rows).  Every attribute of
+    a tensor is read once; the library itself finds tensors that are not on its device."""
+    shape, dtype, (t, h, d) = Q.shape, Q.dtype, Q.stride() if Q.dim() == 3 else (0, 0, 0)
+    code = _DT.get(dtype)
+    good = d == 1 and code is not None
+    tokens, q_heads, dim = shape if good else (0, 0, 0)
+    q, k, k_shape, k_heads = (Q.data_ptr(), t, h), _NO_ROWS, None, 0
     if K is not None:
-        if K.dim() != 3 or K.shape[0] != shape[0] or K.shape[2] != shape[2] or K.dtype is not dtype or K.stride(2) != 1 or (
-                K.get_device() != index):
-            raise ValueError("K must be [tokens, k_heads, dim] of Q's tokens, dim, dtype and device with unit stride of dim")
-        k_heads = K.shape[1]
-    wide = None
-    weights = []
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            weights.append(0)
-            continue
-        if w.dtype is not dtype and w.dtype is not torch.float32:
-            raise ValueError(f"{name} must be float32 or of Q's dtype")
-        if w.dim() != 1 or w.numel() != shape[2] or not w.is_contiguous() or w.get_device() != index:
-            raise ValueError(f"{name} must be a contiguous [dim] tensor on Q's device")
-        if wide is not None and wide != (w.dtype is torch.float32):
-            raise ValueError("q_weight and k_weight must share dtype")
-        wide = w.dtype is torch.float32
-        weights.append(w.data_ptr())
-    if eps is None and (q_weight is not None or k_weight is not None):
-        raise ValueError("weights go with the norm: eps must be a number")
-    where, axis_stride, axes, plan = 0, 0, 0, 0
+        k_shape = K.shape
+        good = good and len(k_shape) == 3 and k_shape[0] == tokens and k_shape[2] == dim and K.dtype is dtype
+        if good:
+            k_heads = k_shape[1]
+            t, h, d = K.stride()
+            k = (K.data_ptr(), t, h)
+            good = d == 1
+    wide, w = None, [0, 0]
+    for i, x in enumerate((q_weight, k_weight)):
+        if x is not None and good:
+            kind = x.dtype
+            good = x.shape == shape[2:] and x.stride() == (1,) and (kind is dtype or kind is torch.float32) and wide in (None, kind) and (
+                eps is not None)
+            wide = kind
+            w[i] = x.data_ptr()
+    where = axis_stride = axes = plan = 0
     if rotary is not None:
         plan, axes = rotary._address, rotary.axes
-        if 2 * rotary.pairs > shape[2]:
-            raise ValueError("the rotation has more pairs than a head")
-        if positions is None:
-            raise ValueError("a rotation needs positions")
-        p = positions.unsqueeze(0) if positions.dim() == 1 else positions
-        if p.dtype is not torch.int32 or p.dim() != 2 or p.shape[1] != shape[0] or p.shape[0] < axes or (
-                p.stride(1) != 1 and shape[0] > 1) or p.get_device() != index:
-            raise ValueError("positions must be int32 [axes, tokens] (or [tokens]) on Q's device with unit stride of tokens")
-        where, axis_stride = p.data_ptr(), p.stride(0)
+        good = good and 2 * rotary.pairs <= dim and positions is not None and positions.dtype is torch.int32
+        if good:
+            p = positions.shape
+            if len(p) == 1:
+                good = p[0] == tokens and axes <= 1 and positions.stride() == (1,)
+            else:
+                axis_stride, s = positions.stride() if len(p) == 2 else (0, 0)
+                good = s == 1 and p[1] == tokens and p[0] >= axes
+            where = positions.data_ptr()
     elif eps is None:
-        raise ValueError("neither a norm nor a rotation")
-    return index, k_heads, (weights[0], weights[1], where, axis_stride, axes, shape[0], shape[1], k_heads, shape[2], shift, plan,
-                            int(bool(wide)), int(eps is not None), 0.0 if eps is None else eps, _DT[dtype])
+        good = False
+    if not good:
+        _refuse(Q, K, positions, rotary, eps, (q_weight, k_weight))
+    return shape, dtype, q, k_shape, k, (w[0], w[1], where, axis_stride, axes, tokens, q_heads, k_heads, dim, shift, plan,
+                                         wide is torch.float32, eps is not None, eps or 0.0, code)
+
+
+def _rows(name, t, shape, dtype):
+    """The row arguments of a tensor of that shape and dtype."""
+    if t is None or t.shape != shape or t.dtype is not dtype:
+        raise ValueError(_BAD_ROWS.format(name))
+    token, head, d = t.stride()
+    if d != 1:
+        raise ValueError(_BAD_ROWS.format(name))
+    return t.data_ptr(), token, head
 
 
 def qk_norm_rope(Q: torch.Tensor, K: torch.Tensor, positions: torch.Tensor, rotary: Rotary, Q_out: torch.Tensor,
@@ -113,18 +139,18 @@ def qk_norm_rope(Q: torch.Tensor, K: torch.Tensor, positions: torch.Tensor, rota
     None: ones), and turned by `rotary` (None: not turned) at the token's positions
     (int32 [axes, tokens] or [tokens], plus `shift`: with the lengths that kv_append()
     takes, shift=-1).  Q_out may be Q and K_out K."""
-    index, k_heads, rest = _common(Q, K, positions, rotary, q_weight, k_weight, eps, shift)
+    shape, dtype, q, k_shape, k, rest = _common(Q, K, positions, rotary, q_weight, k_weight, eps, shift)
     if (K is None) != (K_out is None):
         raise ValueError("K and K_out go together")
-    q, q_out = _rows("Q", Q, Q, index), _rows("Q_out", Q_out, Q, index)
-    k, k_out = (_NO_ROWS, _NO_ROWS) if K is None else (_rows("K", K, K, index), _rows("K_out", K_out, K, index))
-    _launch(index, stream, _b.tgemm_qk_norm_rope, _forward(*q, *k, *q_out, *k_out, *rest))
+    k_out = _NO_ROWS if K is None else _rows("K_out", K_out, k_shape, dtype)
+    _launch(Q.get_device(), stream, _b.tgemm_qk_norm_rope, _forward(*q, *k, *_rows("Q_out", Q_out, shape, dtype), *k_out, *rest))
 
 
 def qk_norm_rope_backward_workspace(Q: torch.Tensor, K: torch.Tensor = None) -> torch.Tensor:
-    """A workspace for qk_norm_rope_backward() with weights' gradients, with any
-    contents.  Calls that may overlap on the GPU need one each."""
-    return torch.empty(_b.tgemm_qk_norm_rope_backward_workspace(Q.shape[2]), dtype=torch.uint8, device=Q.device)
+    """A workspace for qk_norm_rope_backward() with weights' gradients: zeroed device
+    memory, to be kept between calls, of any number of tokens and heads.  Calls that
+    may overlap on the GPU need one each."""
+    return torch.zeros(_b.tgemm_qk_norm_rope_backward_workspace(Q.shape[2]), dtype=torch.uint8, device=Q.device)
 
 
 def qk_norm_rope_backward(Q_out_grad: torch.Tensor, K_out_grad: torch.Tensor, Q: torch.Tensor, K: torch.Tensor,
@@ -135,30 +161,32 @@ def qk_norm_rope_backward(Q_out_grad: torch.Tensor, K_out_grad: torch.Tensor, Q:
     """The gradients of qk_norm_rope(): Q_grad and K_grad (which may be Q_out_grad
     and K_out_grad, or Q and K) from those of its outputs, and the weights'
     (float32 [dim], written; None: not wanted).  Sums are in a fixed order.  Without
-    a workspace one is allocated for the call if weights' gradients are wanted."""
-    index, k_heads, rest = _common(Q, K, positions, rotary, q_weight, k_weight, eps, shift)
-    if any((t is None) != (K is None) for t in (K_out_grad, K_grad)):
-        raise ValueError("K, K_out_grad and K_grad go together")
-    grads = []
-    for name, t in (("q_weight_grad", q_weight_grad), ("k_weight_grad", k_weight_grad)):
-        if t is not None and (t.dtype is not torch.float32 or t.dim() != 1 or t.numel() != Q.shape[2] or not t.is_contiguous()
-                              or t.get_device() != index):
-            raise ValueError(f"{name} must be a contiguous float32 [dim] tensor on Q's device")
-        grads.append(0 if t is None else t.data_ptr())
-    if eps is None and any(grads):
-        raise ValueError("weights go with the norm: eps must be a number")
-    rows = [_rows(n, t, Q, index) for n, t in (("Q", Q), ("Q_grad", Q_grad), ("Q_out_grad", Q_out_grad))]
-    rows += [_NO_ROWS] * 3 if K is None else [_rows(n, t, K, index)
-                                              for n, t in (("K", K), ("K_grad", K_grad), ("K_out_grad", K_out_grad))]
-    if index < 0:
-        raise ValueError("Q must be on a CUDA device")
-    if not any(grads):
-        workspace = None
-    elif workspace is None:
-        with torch.cuda.stream(stream):   # the memory belongs to the stream that uses it
-            workspace = qk_norm_rope_backward_workspace(Q)
-    elif workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError("the workspace must be contiguous and on Q's device")
+    a workspace one is allocated and zeroed for the call if weights' gradients are
+    wanted."""
+    shape, dtype, q, k_shape, k, rest = _common(Q, K, positions, rotary, q_weight, k_weight, eps, shift)
+    index = Q.get_device()
+    if K is None:
+        if K_out_grad is not None or K_grad is not None:
+            raise ValueError("K, K_out_grad and K_grad go together")
+        k_grad = k_out_grad = _NO_ROWS
+    else:
+        k_grad, k_out_grad = _rows("K_grad", K_grad, k_shape, dtype), _rows("K_out_grad", K_out_grad, k_shape, dtype)
+    dw = [0, 0]
+    for i, t in enumerate((q_weight_grad, k_weight_grad)):
+        if t is not None:
+            if eps is None or t.dtype is not torch.float32 or t.shape != shape[2:] or t.stride() != (1,):
+                raise ValueError("weights' gradients go with the norm and must be contiguous float32 [dim] tensors")
+            dw[i] = t.data_ptr()
+    space = room = 0
+    if q_weight_grad is not None or k_weight_grad is not None:
+        if index < 0:
+            raise ValueError("Q must be on a CUDA device")
+        if workspace is None:
+            with torch.cuda.stream(stream):   # the zeros belong to the stream that uses them
+                workspace = qk_norm_rope_backward_workspace(Q)
+        elif not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
+        space, room = workspace.data_ptr(), workspace.nbytes
     _launch(index, stream, _b.tgemm_qk_norm_rope_backward,
-            _backward(*rows[0], *rows[3], *rows[1], *rows[4], *rest, *rows[2], *rows[5], *grads,
-                      0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes))
+            _backward(*q, *k, *_rows("Q_grad", Q_grad, shape, dtype), *k_grad, *rest,
+                      *_rows("Q_out_grad", Q_out_grad, shape, dtype), *k_out_grad, dw[0], dw[1], space, room))

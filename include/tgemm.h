@@ -669,10 +669,11 @@ tgemm_status tgemm_qk_norm_rope(const tgemm_qk_norm_rope_args *args, tgemm_strea
  * written to forward.q_out and forward.k_out (which may be q and k, or q_grad and
  * k_grad, themselves), from those of what it wrote, q_grad and k_grad; and of the
  * weights, fp32 [dim], written, not added (NULL: not wanted; they need norm = 1
- * and the workspace, device memory of tgemm_qk_norm_rope_backward_workspace()
- * bytes, 16-byte aligned, with any contents; calls that may overlap on the GPU
- * need one each).  Sums are fp32 in a fixed order: results are deterministic.
- * With norm = 0 q and k are not read.
+ * and the workspace).  Sums are fp32 in a fixed order: results are deterministic.
+ * With norm = 0 q and k are not read.  workspace: device memory of
+ * tgemm_qk_norm_rope_backward_workspace() bytes, 16-byte aligned, that held zeros
+ * before its first use; the call leaves it fit for the next.  Calls that may
+ * overlap on the GPU need one each.
  */
 typedef struct {
     tgemm_qk_norm_rope_args forward;

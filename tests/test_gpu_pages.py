@@ -203,6 +203,17 @@ def test_lists_that_the_heads_share_are_as_before(cuda_lib):
     assert torch.equal(a, b)
 
 
+def test_one_head_with_any_stride(cuda_lib):
+    """A size of 1 may have any stride."""
+    f = Filled(tg, [100, 3], 1, 64, 16, "fp16", seed=12)
+    q = torch.randn(2, 4, 64, device="cuda").half()
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    tg.attention_decode(q, f.cache, f.table, f.lengths, a)
+    tg.attention_decode(q, f.cache, f.table.as_strided((2, 1, f.table.shape[1]), (f.table.stride(0), 1, 1)), f.lengths, b)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
 def test_ties_go_to_the_lowest_position(cuda_lib):
     """Pages of equal keys, queries of zeros: equal scores everywhere."""
     f = Filled(tg, [400], 2, 64, 8, "fp16", seed=13)
