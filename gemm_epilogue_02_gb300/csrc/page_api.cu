@@ -261,6 +261,8 @@ tgemm_status check_pages(const tgemm_kv_cache *cache, int32_t *uses, int32_t *pa
 
 // Bytes of the children's last pages up to which a cluster does all: beyond, two launches fill the GPU.
 constexpr int64_t kForkFew = 1 << 20;
+// The same for compaction: bytes of a pool (half of them move at most), and sequences.
+constexpr int64_t kCompactFew = 4 << 20, kCompactLists = 64;
 
 template <int kLanes>
 cudaError_t launch_fork_lanes(const RuntimeInfo &rt, const PagesParams &p, cudaStream_t s) {
@@ -278,6 +280,12 @@ cudaError_t launch_fork_lanes(const RuntimeInfo &rt, const PagesParams &p, cudaS
 
 template <int kLanes>
 cudaError_t launch_move_lanes(const RuntimeInfo &rt, const CompactParams &p, cudaStream_t s) {
+    const int64_t page_bytes = static_cast<int64_t>(p.cache.page_size) * p.cache.heads * p.cache.row_bytes * 2;
+    if (p.cache.pages * page_bytes <= kCompactFew && p.table.batch <= kCompactLists)
+        return launch(page_compact_few_kernel<kLanes>, dim3(kForkBlocks), kTakeThreads, 0, s, p, kForkBlocks);
+    const cudaError_t e = p.cache.pages <= kTakeThreads ? launch(page_plan_kernel<1>, dim3(1), kTakeThreads, 0, s, p)
+                                                        : launch(page_plan_kernel<kTakeDeep>, dim3(1), kTakeThreads, 0, s, p);
+    if (e != cudaSuccess) return e;
     constexpr int kRows = kPageThreads / kLanes * 4;
     const int64_t rows = static_cast<int64_t>(p.cache.page_size) * p.cache.heads;
     const int64_t want = std::max<int64_t>((rows + kRows - 1) / kRows * ((p.cache.pages + 1) / 2), p.table.batch);
@@ -424,8 +432,6 @@ extern "C" tgemm_status tgemm_kv_compact(const tgemm_kv_compact_args *a, tgemm_s
     p.slots_first = cache->slot_stride < cache->head_stride;
     p.status = rt.status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch(page_plan_kernel, dim3(1), kTakeThreads, 0, s, p);
-    if (e != cudaSuccess) return done(e);
     switch (row_lanes(p.cache.row_bytes)) {
         case 8: return done(launch_move_lanes<8>(rt, p, s));
         case 16: return done(launch_move_lanes<16>(rt, p, s));

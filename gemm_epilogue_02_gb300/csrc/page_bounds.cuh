@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChoosePa
         const unsigned ok = __ballot_sync(0xffffffffu, valid);
         if (ok != __ballot_sync(0xffffffffu, there) && lane == 0) record_status(p.status, kStatusCache);
         const uint32_t to = to_ring + stage * Shape::kStage;
-        if (lane < 16) cp_async4(to + 16 * kRow + 4 * lane, p.bounds.scale + (valid ? static_cast<long long>(page) * p.cache.heads + head : 0), valid);
+        if (valid) cp_async4(to + 16 * kRow + 4 * lane, p.bounds.scale + static_cast<long long>(page) * p.cache.heads + head, true);
         if (lane == 0) *reinterpret_cast<unsigned *>(ring + stage * Shape::kStage + 16 * kRow + 64) = ok;
         // A lane copies one 16-byte piece of every 32 / kPieces rows.
         constexpr int kPieces = 8 * kChunks, kEach = 32 / kPieces;

@@ -9,7 +9,8 @@
 //                      page_fork_few_kernel does both
 //   page_free_kernel     counts a sequence's pages once less
 //   page_plan_kernel     compaction: which pages move where, and the new counts
-//   page_move_kernel     moves them, and translates the lists
+//   page_move_kernel     moves them, and translates the lists;
+//                      page_compact_few_kernel does both
 //
 // The counts are whole numbers, and which page goes where follows from order
 // alone, so nothing depends on how the work is split.  The planning kernels read
@@ -339,41 +340,41 @@ struct CompactParams {
     unsigned int *status;
 };
 
-// Pages in rounds of kTakeRound: thread t has pages 8 t .. 8 t + 7 of a round, which
-// are read once (again where there are several rounds).
-__global__ void __launch_bounds__(kTakeThreads, 1) page_plan_kernel(const CompactParams p) {
+// By one block of kTakeThreads.  Pages come in rounds: thread t has pages kDeep t ..
+// of a round, which are read once (again where there are several rounds).
+template <int kDeep>
+__device__ __forceinline__ void plan_moves(const CompactParams &p) {
+    constexpr int kRound = kTakeThreads * kDeep;
     __shared__ int s_sums[33];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int pages = static_cast<int>(p.cache.pages), rounds = (pages + kTakeRound - 1) / kTakeRound;
-    int u[kTakeDeep];
+    const int pages = static_cast<int>(p.cache.pages), rounds = (pages + kRound - 1) / kRound;
+    int u[kDeep];
     auto read = [&](int round) {
-        const int first = round * kTakeRound + static_cast<int>(threadIdx.x) * kTakeDeep;
+        const int first = round * kRound + static_cast<int>(threadIdx.x) * kDeep;
 #pragma unroll
-        for (int i = 0; i < kTakeDeep; ++i) u[i] = first + i < pages ? p.uses[first + i] : 0;
+        for (int i = 0; i < kDeep; ++i) u[i] = first + i < pages ? p.uses[first + i] : 0;
         return first;
     };
     int mine = 0, total;
     for (int r = 0; r < rounds; ++r) {
         read(r);
 #pragma unroll
-        for (int i = 0; i < kTakeDeep; ++i) mine += u[i] > 0;
+        for (int i = 0; i < kDeep; ++i) mine += u[i] > 0;
     }
     block_scan(mine, s_sums, &total);
     int holes = 0, moved = 0;
     for (int r = 0; r < rounds; ++r) {
-        const int first = rounds == 1 ? static_cast<int>(threadIdx.x) * kTakeDeep : read(r);
+        const int first = rounds == 1 ? static_cast<int>(threadIdx.x) * kDeep : read(r);
         // Both at once: a round has 8192 of either at most.
         int both = 0, n;
 #pragma unroll
-        for (int i = 0; i < kTakeDeep; ++i) {
+        for (int i = 0; i < kDeep; ++i) {
             const bool used = u[i] > 0, in = first + i < pages;
             both += (in && first + i < total && !used ? 1 : 0) | (first + i >= total && used ? 1 << 16 : 0);
         }
         const int before = block_scan(both, s_sums, &n) - both;
         int hole = holes + (before & 0xFFFF), move = moved + (before >> 16);
 #pragma unroll
-        for (int i = 0; i < kTakeDeep; ++i) {
+        for (int i = 0; i < kDeep; ++i) {
             const int page = first + i;
             if (page < total) {
                 if (page < pages) {
@@ -400,16 +401,22 @@ __global__ void __launch_bounds__(kTakeThreads, 1) page_plan_kernel(const Compac
     }
 }
 
-template <int kLanes>
-__global__ void __launch_bounds__(kPageThreads) page_move_kernel(const CompactParams p) {
-    constexpr int kPass = kPageThreads / kLanes, kUnroll = 4, kRows = kPass * kUnroll;
+template <int kDeep>
+__global__ void __launch_bounds__(kTakeThreads, 1) page_plan_kernel(const CompactParams p) {
     griddep_wait();
     griddep_launch_dependents();
+    plan_moves<kDeep>(p);
+}
+
+// The pages that move and the lists, by block `block` of `blocks`.
+template <int kThreads, int kLanes>
+__device__ __forceinline__ void move_pages(const CompactParams &p, int block, int blocks) {
+    constexpr int kPass = kThreads / kLanes, kUnroll = 4, kRows = kPass * kUnroll;
     const int total = p.head[0], moved = p.head[1];
     const int rows = p.cache.page_size * p.cache.heads, chunks = (rows + kRows - 1) / kRows;
     const int piece = threadIdx.x % kLanes, in_pass = threadIdx.x / kLanes;
     const bool inside = piece * 16 < p.cache.row_bytes;
-    for (long long unit = blockIdx.x; unit < static_cast<long long>(moved) * chunks; unit += gridDim.x) {
+    for (long long unit = block; unit < static_cast<long long>(moved) * chunks; unit += blocks) {
         const int m = static_cast<int>(unit / chunks), r0 = static_cast<int>(unit - static_cast<long long>(m) * chunks) * kRows;
         const int src = p.above[m], dst = p.below[m];
         const long long from_page = src * p.cache.page_stride, to_page = dst * p.cache.page_stride;
@@ -434,7 +441,7 @@ __global__ void __launch_bounds__(kPageThreads) page_move_kernel(const CompactPa
                 __stcs(reinterpret_cast<uint4 *>(p.cache.v + to_page + o[u]), x[u][1]);
             }
         if (p.cache.k_scale)
-            for (int r = r0 + threadIdx.x; r < min(rows, r0 + kRows); r += kPageThreads) {
+            for (int r = r0 + threadIdx.x; r < min(rows, r0 + kRows); r += kThreads) {
                 int slot, head;
                 page_row(p.cache, r, p.slots_first, &slot, &head);
                 const long long a = kv_scale_offset(p.cache, src, slot, head), z = kv_scale_offset(p.cache, dst, slot, head);
@@ -445,16 +452,16 @@ __global__ void __launch_bounds__(kPageThreads) page_move_kernel(const CompactPa
             const int words = p.cache.heads * p.cache.dim / 8;         // 16 bytes each
             const uint4 *const a = reinterpret_cast<const uint4 *>(p.bounds.base) + static_cast<long long>(src) * words;
             uint4 *const z = reinterpret_cast<uint4 *>(p.bounds.base) + static_cast<long long>(dst) * words;
-            for (int i = threadIdx.x; i < words; i += kPageThreads) z[i] = a[i];
-            for (int i = threadIdx.x; i < p.cache.heads; i += kPageThreads)
+            for (int i = threadIdx.x; i < words; i += kThreads) z[i] = a[i];
+            for (int i = threadIdx.x; i < p.cache.heads; i += kThreads)
                 p.bounds.scale[static_cast<long long>(dst) * p.cache.heads + i] = p.bounds.scale[static_cast<long long>(src) * p.cache.heads + i];
         }
     }
     // The lists.
-    for (int b = blockIdx.x; b < p.table.batch; b += gridDim.x) {
+    for (int b = block; b < p.table.batch; b += blocks) {
         bool bad = false;
         const int count = kv_pages_of(kv_length(p.table.lengths[b], p.table.width, p.cache.page_size, &bad), p.cache.page_size);
-        for (int i = threadIdx.x; i < count; i += kPageThreads) {
+        for (int i = threadIdx.x; i < count; i += kThreads) {
             int page = p.table.pages[b * p.table.stride + i];
             if (page < 0 || page >= p.cache.pages) bad = true;
             else if (page >= total) {
@@ -466,6 +473,27 @@ __global__ void __launch_bounds__(kPageThreads) page_move_kernel(const CompactPa
         }
         if (bad) record_status(p.status, kStatusCache);
     }
+}
+
+template <int kLanes>
+__global__ void __launch_bounds__(kPageThreads) page_move_kernel(const CompactParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    move_pages<kPageThreads, kLanes>(p, blockIdx.x, gridDim.x);
+}
+
+// Both in one launch, for a small pool.
+template <int kLanes>
+__global__ void __launch_bounds__(kTakeThreads, 1) page_compact_few_kernel(const CompactParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int rank = static_cast<int>(cluster_ctarank());
+    if (rank == 0) {
+        if (p.cache.pages <= kTakeThreads) plan_moves<1>(p);
+        else plan_moves<kTakeDeep>(p);
+    }
+    cluster_sync();                                        // releases what the first block has written, and acquires it
+    move_pages<kTakeThreads, kLanes>(p, rank, kForkBlocks);
 }
 
 }  // namespace tgemm

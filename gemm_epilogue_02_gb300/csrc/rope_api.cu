@@ -84,8 +84,7 @@ tgemm_status check_common(const tgemm_qk_norm_rope_args *a, RopeParams *p, int *
             if (axis < 0 || axis >= a->axes) return TGEMM_ERR_INVALID_ARG;
             p->axis[i] = static_cast<unsigned char>(axis);
         }
-        if (a->axis_stride < 0 || a->axis_stride > (int64_t(1) << 40) || (a->axes > 1 && a->axis_stride < a->tokens))
-            return TGEMM_ERR_INVALID_ARG;
+        if (a->axis_stride < 0 || a->axis_stride > (int64_t(1) << 40)) return TGEMM_ERR_INVALID_ARG;      // 0: the axes share positions
         if (p->pairs > 0 && a->tokens > 0 && !a->positions) return TGEMM_ERR_INVALID_ARG;
     }
     const int weight = a->weight_f32 ? 4 : 2;

@@ -8,16 +8,18 @@ sizes into the calls' argument structures, as kv.py does.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
 from . import _binding as _b
-from .kv import _DT, _launch
+from .kv import _DT, _I32, _launch
 
 _forward, _backward = _b.QK_NORM_ROPE_ARGS.pack, _b.QK_NORM_ROPE_BACKWARD_ARGS.pack
-# pi * 2^188 (3.14159265358979323846264338327950288419716939937510582097494), rounded.
-_PI_188 = 314159265358979323846264338327950288419716939937510582097494 * 2 ** 188 // 10 ** 59
+# 2^192 / (2 pi), rounded down
+_PER_TURN = 2 ** 191 * 10 ** 75 // 3141592653589793238462643383279502884197169399375105820974944592307816406286
 _NO_ROWS = (0, 0, 0)
+_F32 = torch.float32
 
 
 class Rotary:
@@ -30,22 +32,24 @@ class Rotary:
 
     def __init__(self, frequencies, axes=None, interleaved: bool = False):
         rates = [float(f) for f in frequencies]
-        axes = [0] * len(rates) if axes is None else [int(a) for a in axes]
-        if len(axes) != len(rates) or any(a < 0 or a > 31 for a in axes):
-            raise ValueError("axes must name an axis, 0 to 31, for each frequency")
+        if axes is not None:
+            axes = [int(a) for a in axes]
+            if len(axes) != len(rates) or any(a < 0 or a > 31 for a in axes):
+                raise ValueError("axes must name an axis, 0 to 31, for each frequency")
         if not interleaved and len(rates) % 4:
             raise ValueError("pairs that are not interleaved must be a multiple of 4")
-        try:
-            ratios = [f.as_integer_ratio() for f in rates]
-        except (OverflowError, ValueError):
-            raise ValueError("frequencies must be finite") from None
-        # f / (2 pi) * 2^64, towards minus infinity
-        turns = [(n << 251) // (d * _PI_188) & 0xFFFFFFFFFFFFFFFF for n, d in ratios]
-        self.pairs, self.interleaved, self.axes = len(rates), bool(interleaved), max(axes, default=-1) + 1
+        if not all(abs(f) < 2.0 ** 64 for f in rates):
+            raise ValueError("frequencies must be finite and below 2^64")
+        # f = m 2^e, m a whole number below 2^53: f / (2 pi) * 2^64, rounded down and without its whole turns
+        turns = []
+        for f in rates:
+            m, e = math.frexp(f)
+            turns.append((int(m * 2.0 ** 53) * _PER_TURN >> 181 - e) & 0xFFFFFFFFFFFFFFFF)
+        self.pairs, self.interleaved, self.axes = len(rates), bool(interleaved), 1 if axes is None and rates else max(axes or (), default=-1) + 1
         self._turns = (ctypes.c_uint64 * max(1, len(rates)))(*turns)
-        self._axes = (ctypes.c_int32 * max(1, len(rates)))(*axes)
+        self._axes = None if axes is None else (ctypes.c_int32 * max(1, len(rates)))(*axes)
         c = _b.RotaryStruct()
-        c.turns, c.axes = ctypes.addressof(self._turns), ctypes.addressof(self._axes)
+        c.turns, c.axes = ctypes.addressof(self._turns), None if axes is None else ctypes.addressof(self._axes)
         c.pairs, c.interleaved = self.pairs, int(self.interleaved)
         self._struct = c
         self._address = ctypes.addressof(c)
@@ -62,7 +66,7 @@ def _refuse(Q, K, positions, rotary, eps, weights):
                           or K.stride(2) != 1):
         raise ValueError("K must be [tokens, k_heads, dim] of Q's tokens, dim and dtype with unit stride of dim")
     for w in weights:
-        if w is not None and (w.shape != Q.shape[2:] or w.stride(0) != 1 or w.dtype not in (Q.dtype, torch.float32)):
+        if w is not None and (w.shape != Q.shape[2:] or not w.is_contiguous() or w.dtype not in (Q.dtype, _F32)):
             raise ValueError("weights must be contiguous [dim] tensors, float32 or of Q's dtype")
     if eps is None and any(w is not None for w in weights):
         raise ValueError("weights go with the norm: eps must be a number")
@@ -77,57 +81,64 @@ def _refuse(Q, K, positions, rotary, eps, weights):
 
 
 def _common(Q, K, positions, rotary, q_weight, k_weight, eps, shift):
-    """(Q's shape, dtype and row arguments, K's shape and row arguments, the arguments after the rows).  Every attribute of
-    a tensor is read once; the library itself finds tensors that are not on its device."""
-    shape, dtype, (t, h, d) = Q.shape, Q.dtype, Q.stride() if Q.dim() == 3 else (0, 0, 0)
+    """(Q's shape, dtype and row arguments, K's shape and row arguments, the arguments after the rows).  Written out, as a
+    call's time is the host's where rows are few: every attribute of a tensor is read once, and it is left to the library
+    to find tensors that are not on its device."""
+    shape, dtype, stride = Q.shape, Q.dtype, Q.stride()
     code = _DT.get(dtype)
-    good = d == 1 and code is not None
-    tokens, q_heads, dim = shape if good else (0, 0, 0)
-    q, k, k_shape, k_heads = (Q.data_ptr(), t, h), _NO_ROWS, None, 0
-    if K is not None:
-        k_shape = K.shape
-        good = good and len(k_shape) == 3 and k_shape[0] == tokens and k_shape[2] == dim and K.dtype is dtype
-        if good:
-            k_heads = k_shape[1]
-            t, h, d = K.stride()
-            k = (K.data_ptr(), t, h)
-            good = d == 1
-    wide, w = None, [0, 0]
-    for i, x in enumerate((q_weight, k_weight)):
-        if x is not None and good:
-            kind = x.dtype
-            good = x.shape == shape[2:] and x.stride() == (1,) and (kind is dtype or kind is torch.float32) and wide in (None, kind) and (
-                eps is not None)
-            wide = kind
-            w[i] = x.data_ptr()
-    where = axis_stride = axes = plan = 0
-    if rotary is not None:
-        plan, axes = rotary._address, rotary.axes
-        good = good and 2 * rotary.pairs <= dim and positions is not None and positions.dtype is torch.int32
-        if good:
-            p = positions.shape
-            if len(p) == 1:
-                good = p[0] == tokens and axes <= 1 and positions.stride() == (1,)
-            else:
-                axis_stride, s = positions.stride() if len(p) == 2 else (0, 0)
-                good = s == 1 and p[1] == tokens and p[0] >= axes
-            where = positions.data_ptr()
-    elif eps is None:
+    if len(shape) != 3 or stride[2] != 1 or code is None:
+        _refuse(Q, K, positions, rotary, eps, (q_weight, k_weight))
+    tokens, q_heads, dim = shape
+    q = (Q.data_ptr(), stride[0], stride[1])
+    good = True
+    if K is None:
+        k, k_shape, k_heads = _NO_ROWS, None, 0
+    else:
+        k_shape, stride = K.shape, K.stride()
+        if len(k_shape) != 3:
+            _refuse(Q, K, positions, rotary, eps, (q_weight, k_weight))
+        k_tokens, k_heads, k_dim = k_shape
+        good = k_tokens == tokens and k_dim == dim and K.dtype is dtype and stride[2] == 1
+        k = (K.data_ptr(), stride[0], stride[1])
+    kind, qw, kw = None, 0, 0
+    if q_weight is not None:
+        kind = q_weight.dtype
+        good = good and q_weight.dim() == 1 and q_weight.numel() == dim and q_weight.is_contiguous() and eps is not None
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        good = good and k_weight.dim() == 1 and k_weight.numel() == dim and k_weight.is_contiguous() and eps is not None and (
+            kind is None or k_weight.dtype is kind)
+        kind = k_weight.dtype
+        kw = k_weight.data_ptr()
+    if kind is not None and kind is not dtype and kind is not _F32:
         good = False
+    if rotary is None:
+        where = axis_stride = axes = plan = 0
+        good = good and eps is not None
+    elif positions is None:
+        good = False
+    else:
+        plan, axes, stride, p = rotary._address, rotary.axes, positions.stride(), positions.shape
+        if len(p) == 2:
+            good = good and p[1] == tokens and p[0] >= axes and (stride[1] == 1 or tokens <= 1)
+        else:
+            good = good and len(p) == 1 and p[0] == tokens and axes <= 1 and (stride[0] == 1 or tokens <= 1)
+        good = good and positions.dtype is _I32 and 2 * rotary.pairs <= dim
+        where, axis_stride = positions.data_ptr(), stride[0]
     if not good:
         _refuse(Q, K, positions, rotary, eps, (q_weight, k_weight))
-    return shape, dtype, q, k_shape, k, (w[0], w[1], where, axis_stride, axes, tokens, q_heads, k_heads, dim, shift, plan,
-                                         wide is torch.float32, eps is not None, eps or 0.0, code)
+    return shape, dtype, q, k_shape, k, (qw, kw, where, axis_stride, axes, tokens, q_heads, k_heads, dim, shift, plan,
+                                         kind is _F32, eps is not None, eps or 0.0, code)
 
 
 def _rows(name, t, shape, dtype):
     """The row arguments of a tensor of that shape and dtype."""
-    if t is None or t.shape != shape or t.dtype is not dtype:
+    if t is None or t.dtype is not dtype or t.shape != shape:
         raise ValueError(_BAD_ROWS.format(name))
-    token, head, d = t.stride()
-    if d != 1:
+    stride = t.stride()
+    if stride[2] != 1:
         raise ValueError(_BAD_ROWS.format(name))
-    return t.data_ptr(), token, head
+    return t.data_ptr(), stride[0], stride[1]
 
 
 def qk_norm_rope(Q: torch.Tensor, K: torch.Tensor, positions: torch.Tensor, rotary: Rotary, Q_out: torch.Tensor,
@@ -174,7 +185,7 @@ def qk_norm_rope_backward(Q_out_grad: torch.Tensor, K_out_grad: torch.Tensor, Q:
     dw = [0, 0]
     for i, t in enumerate((q_weight_grad, k_weight_grad)):
         if t is not None:
-            if eps is None or t.dtype is not torch.float32 or t.shape != shape[2:] or t.stride() != (1,):
+            if eps is None or t.dtype is not _F32 or t.dim() != 1 or t.numel() != shape[2] or not t.is_contiguous():
                 raise ValueError("weights' gradients go with the norm and must be contiguous float32 [dim] tensors")
             dw[i] = t.data_ptr()
     space = room = 0

@@ -646,8 +646,9 @@ typedef struct {
  * (norm = 0: y = R(x), no weights), R turning pair i by the angle
  * (positions[axes[i], token] + shift) * frequency_i; rotary NULL: no rotation.
  * Weights have dim contiguous elements of `dtype`, or fp32 with weight_f32 = 1;
- * NULL: ones.  positions is int32 [axes, tokens], device, any values, axes at most 32; angles are
- * right to 2^-31 of a turn wherever they are.  All in fp32, rounded once.  dim is a
+ * NULL: ones.  positions is int32 [axes, tokens], device, any values (axis_stride 0: the axes
+ * share them), axes at most 32; position * frequency keeps 2^-31 of a turn
+ * whatever they are, the rest is fp32, rounded once.  dim is a
  * multiple of 8, at most 256.  q_heads or k_heads may be 0.  q_out and k_out may
  * be q and k themselves (the same strides), and may lie side by side with others
  * in one array; they overlap nothing else.

@@ -127,6 +127,16 @@ def test_shift_and_lengths(cuda_lib, shift):
     close(out[0], *forward64(q, w[0], 1e-6, angle, False), "bf16")
 
 
+def test_axes_that_share_positions(cuda_lib):
+    q, k, positions, w = case(9, 4, 2, 64, "fp16", seed=20)
+    f = frequencies(32)
+    one, three = ([torch.empty(t.shape, dtype=t.dtype, device="cuda") for t in (q, k)] for _ in range(2))
+    tg.qk_norm_rope(q, k, positions, tg.Rotary(f), *one, q_weight=w[0], k_weight=w[1])
+    tg.qk_norm_rope(q, k, positions.expand(3, -1), tg.Rotary(f, axes=[i % 3 for i in range(32)]), *three, q_weight=w[0], k_weight=w[1])
+    torch.cuda.synchronize()
+    assert torch.equal(one[0], three[0]) and torch.equal(one[1], three[1])
+
+
 @pytest.mark.parametrize("mode", ["norm_only", "rotation_only", "f32_weights", "no_weights"])
 def test_parts_of_it(cuda_lib, mode):
     tokens, dim, pairs = 50, 96, 48

@@ -11,7 +11,7 @@ import re
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gemm_epilogue_02_gb300", "csrc")
-ACCESS = re.compile(r"\bp\.(?!turns|axis\b|side\b|dbg_y)[\w.]+\s*\[|__ldc[gs]|__stcs|atomic|cp_async|record_status|kv_length\(|fork_length\(|fork_child|take_pages|cluster_sync|"
+ACCESS = re.compile(r"\bp\.(?!turns|axis\b|side\b|dbg_y)[\w.]+\s*\[|__ldc[gs]|__stcs|atomic|cp_async|record_status|kv_length\(|fork_length\(|fork_child|take_pages|plan_moves|move_pages|cluster_sync|"
                     r"rope_read|rope_write|rope_stage_weights\(|\*p\.in_use|\blist\[|\bto\[")
 
 
@@ -31,7 +31,7 @@ def kernels():
 
 def test_every_kernel_is_found():
     assert sorted(n for n, _ in kernels()) == [
-        "page_bounds_kernel", "page_choose_kernel", "page_fork_few_kernel", "page_fork_kernel", "page_free_kernel", "page_move_kernel",
+        "page_bounds_kernel", "page_choose_kernel", "page_compact_few_kernel", "page_fork_few_kernel", "page_fork_kernel", "page_free_kernel", "page_move_kernel",
         "page_plan_kernel", "page_take_kernel", "rope_backward_kernel", "rope_kernel"]
 
 

@@ -82,6 +82,7 @@ def test_valid_calls():
     assert backward(gqw=0, gkw=0, ws=0, wsb=0) in VALID
     assert backward(norm=0, qw=0, kw=0, gqw=0, gkw=0, q=0, k=0) in VALID       # a rotation alone does not read q and k
     assert forward(rotary=0, pos=0, axes=0, axis_stride=0) in VALID           # a norm alone
+    assert forward(Rotation(axes=[0, 1] * 16), axes=2, axis_stride=0) in VALID         # axes that share positions
 
 
 COMMON = [
@@ -90,7 +91,7 @@ COMMON = [
     (dict(norm=2), INVALID), (dict(f32=2), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
     (dict(norm=0), INVALID), (dict(shift=2 ** 31), INVALID), (dict(axes=0), INVALID), (dict(axes=33), INVALID),
     (dict(pos=0), INVALID), (dict(pos=AT["pos"] + 2), ALIGN), (dict(qw=AT["qw"] + 1), ALIGN), (dict(f32=1, kw=AT["kw"] + 2), ALIGN),
-    (dict(axes=2, axis_stride=TOKENS - 1), INVALID), (dict(axis_stride=-1), INVALID), (dict(qo=0), INVALID),
+    (dict(axes=2, axis_stride=2 ** 41), INVALID), (dict(axis_stride=-1), INVALID), (dict(qo=0), INVALID),
     (dict(qo=AT["qo"] + 8), ALIGN), (dict(qo_t=HQ * DIM + 4), ALIGN), (dict(qo_h=DIM - 8), INVALID), (dict(ko_h=-DIM), INVALID),
     (dict(qo=AT["q"] + 64), ALIAS), (dict(qo=AT["k"]), ALIAS), (dict(ko=AT["qo"]), ALIAS), (dict(qo=AT["pos"] - 1024), ALIAS),
     (dict(qo=AT["qw"]), ALIAS), (dict(qo=AT["q"], qo_t=HQ * DIM + 64), ALIAS), (dict(q_t=2 ** 62), INVALID),
@@ -132,7 +133,7 @@ def test_frequencies_become_turns():
     """f / (2 pi) * 2^64 modulo 2^64, to one unit."""
     getcontext().prec = 90
     pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
-    f = [10000.0 ** (-i / 64) for i in range(64)] + [0.0, -1.5, 7.0, 1e-300]
+    f = [10000.0 ** (-i / 64) for i in range(64)] + [0.0, -1.5, 7.0, 1e-300, 1.8e19, -12345678.9, 2.0 ** -60, 3e-19]
     for x, t in zip(f, tg.Rotary(f)._turns):
         want = int((Decimal(x) / (2 * pi) * Decimal(2) ** 64).to_integral_value(rounding="ROUND_FLOOR")) % 2 ** 64
         assert min((t - want) % 2 ** 64, (want - t) % 2 ** 64) <= 1
@@ -140,7 +141,7 @@ def test_frequencies_become_turns():
 
 @pytest.mark.parametrize("f,kw", [
     ([1.0] * 6, {}), ([1.0, float("nan"), 1.0, 1.0], {}), ([1.0, float("inf")], dict(interleaved=True)), ([1.0] * 4, dict(axes=[0, 1])),
-    ([1.0] * 4, dict(axes=[0, 0, 0, 32])), ([1.0] * 4, dict(axes=[0, 0, 0, -1])),
+    ([1.0] * 4, dict(axes=[0, 0, 0, 32])), ([1.0] * 4, dict(axes=[0, 0, 0, -1])), ([2.0 ** 64] * 4, {}),
 ])
 def test_rotary_refusals(f, kw):
     with pytest.raises(ValueError):
