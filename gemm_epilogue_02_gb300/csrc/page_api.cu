@@ -17,7 +17,7 @@ namespace tgemm {
 namespace {
 
 constexpr int kChooseMaxPages = 1 << 17;      // of a page list: eight blocks' keys then fit their shared memory
-constexpr int kChooseGather = 1 << 12;        // pages of a list whose keys a cluster's first block ranks alone
+constexpr int kChooseGather = 1 << 12;        // pages of a list whose keys a cluster's first block ranks alone (8193: 21.5 us so, 18 together)
 constexpr int kChooseMaxBytes = 224 * 1024;   // of a block's dynamic shared memory
 
 tgemm_status check_bounds(const tgemm_kv_page_bounds *b, const tgemm_kv_cache *c, KvBounds *view, Extent *e, Extent *es) {
@@ -93,10 +93,10 @@ cudaError_t launch_bounds(const RuntimeInfo &rt, const BoundsParams &p, cudaStre
     }
 }
 
-template <int kThreads, bool kBf16, int kChunks, int kStages>
+template <int kThreads, bool kBf16, int kChunks, int kStages, bool kFew>
 cudaError_t launch_choose_stages(const RuntimeInfo &rt, ChooseParams &p, int cluster, cudaStream_t s) {
     using Shape = ChooseShape<kThreads, kChunks, kStages>;
-    auto kernel = page_choose_kernel<kThreads, kBf16, kChunks, kStages>;
+    auto kernel = page_choose_kernel<kThreads, kBf16, kChunks, kStages, kFew>;
     static std::atomic<uint64_t> ready{0};      // bit per device
     const uint64_t bit = uint64_t(1) << rt.device;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
@@ -111,9 +111,10 @@ cudaError_t launch_choose_stages(const RuntimeInfo &rt, ChooseParams &p, int clu
 
 template <int kThreads, bool kBf16, int kChunks>
 cudaError_t launch_choose_shape(const RuntimeInfo &rt, ChooseParams &p, cudaStream_t s) {
-    // A block does 128 pages a microsecond, and a cluster's barriers cost it three: with lists of up to 512 pages a block
-    // alone is best, beyond them as many of a cluster as leave each an SM (1251 pages, 8 heads: one 16.1 us, two 14.1, four
-    // 11.6, eight 10.8; 251 pages: one 6.0, two 9.2; 128 lists of 2048: one 24, two 37).
+    // A cluster's barriers cost about 3 us, and a block scores 256 pages a microsecond where it has twice the warps: with lists
+    // of up to 512 pages a block alone is best, beyond them as many of a cluster as leave each an SM (1251 pages, 8 heads: one
+    // 16.1 us, two 14.1, four 11.6, eight 10.8 before the first block ranked alone, 8.2 since; 251 pages: one 6.0, two 9.2; 128
+    // lists of 2048: one 24, two 37).
     int cluster = 1;
     const int64_t lists = static_cast<int64_t>(p.table.batch) * p.cache.heads;
     if (p.table.width > 512)
@@ -122,10 +123,16 @@ cudaError_t launch_choose_shape(const RuntimeInfo &rt, ChooseParams &p, cudaStre
     p.cached = (p.table.width + cluster - 1) / cluster;
     p.gather = cluster > 1 && p.table.width <= kChooseGather;
     if (p.gather) p.cached = p.table.width;
+    // Where no SM has a second block, one of twice the warps (128 lists of 2048 pages: 23.2 -> 19.7 us; with 256 lists of up
+    // to 2049 it would be 32.9, two blocks an SM take 30.6).
+    if (lists * cluster <= rt.num_sms && p.table.width > 256 && p.group <= 8 &&
+        ChooseShape<2 * kThreads, kChunks, 3>::bytes(p.cached, p.group, p.cache.dim) <= kChooseMaxBytes)
+        return launch_choose_stages<2 * kThreads, kBf16, kChunks, 3, true>(rt, p, cluster, s);
     // Three stages let an SM have two blocks; queries of large groups over long lists leave room for two.
-    if (ChooseShape<kThreads, kChunks, 3>::bytes(p.cached, p.group, p.cache.dim) <= kChooseMaxBytes)
-        return launch_choose_stages<kThreads, kBf16, kChunks, 3>(rt, p, cluster, s);
-    return launch_choose_stages<kThreads, kBf16, kChunks, 2>(rt, p, cluster, s);
+    if (ChooseShape<kThreads, kChunks, 3>::bytes(p.cached, p.group, p.cache.dim) > kChooseMaxBytes)
+        return launch_choose_stages<kThreads, kBf16, kChunks, 2, false>(rt, p, cluster, s);
+    return p.group <= 8 ? launch_choose_stages<kThreads, kBf16, kChunks, 3, true>(rt, p, cluster, s)
+                        : launch_choose_stages<kThreads, kBf16, kChunks, 3, false>(rt, p, cluster, s);
 }
 
 template <bool kBf16>

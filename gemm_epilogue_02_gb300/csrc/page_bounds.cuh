@@ -407,18 +407,18 @@ struct ChooseShape {
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Four 8-bit whole numbers as fp16, 1152 more than they are: x + 128 put below 1024's bits.
+// Four 8-bit whole numbers as fp16, 1152 more than they are: x + 128 put below 1024's bits.  The first and third, then
+// the second and fourth.
 constexpr float kChooseBias = 1152.0f;
-__device__ __forceinline__ void widen_s8(uint32_t x, uint32_t &lo, uint32_t &hi) {
-    const uint32_t u = x ^ 0x80808080u, base = 0x64646464u;
-    lo = __byte_perm(u, base, 0x4140);
-    hi = __byte_perm(u, base, 0x4342);
+__device__ __forceinline__ void widen_s8(uint32_t x, uint32_t &even, uint32_t &odd) {
+    even = (x & 0x00FF00FFu) ^ 0x64806480u;
+    odd = ((x >> 8) & 0x00FF00FFu) ^ 0x64806480u;
 }
 
 // What there is to choose from: of `count` pages the first `first` and the last `recent` stay, and `best` of those between.
@@ -438,8 +438,9 @@ __host__ __device__ inline ChooseSpan choose_span(int n, int page_size, int keep
 
 // Grid: (cluster size, heads, batch), a cluster along x that shares a sequence
 // and key head.  kChunks: 64-byte pieces of a row of bounds.
-template <int kThreads, bool kBf16, int kChunks, int kStages>
-__global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChooseParams p) {
+// kFew: at most eight query heads, whose operands stay in registers.
+template <int kThreads, bool kBf16, int kChunks, int kStages, bool kFew>
+__global__ void __launch_bounds__(kThreads, kThreads * kChunks > 512 ? 1 : 2) page_choose_kernel(const ChooseParams p) {
     using Shape = ChooseShape<kThreads, kChunks, kStages>;
     constexpr int kWarps = kThreads / 32, kRow = choose_row(kChunks), kPitch = kChunks * 128 + 16;     // choose_pitch()
     extern __shared__ __align__(128) unsigned char choose_smem[];
@@ -484,10 +485,13 @@ __global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChoosePa
         const float s = kv_bounds_scale(top), up = kv_bounds_inverse(s);
 #pragma unroll
         for (int i = 0; i < kPer; i += 2) {
+            // (of four dims the second and third change places, as widen_s8() has them)
             const float y0 = rintf(x[i] * up), y1 = rintf(x[i + 1] * up);
-            const int at = h * pitch + 2 * (lane * kPer + i);
-            *reinterpret_cast<__half2 *>(positive + at) = __floats2half2_rn(fmaxf(y0, 0.0f), fmaxf(y1, 0.0f));
-            *reinterpret_cast<__half2 *>(negative + at) = __floats2half2_rn(fminf(y0, 0.0f), fminf(y1, 0.0f));
+            const int d = lane * kPer + i, at = h * pitch + 2 * (d & ~3) + (d & 2);
+            *reinterpret_cast<__half *>(positive + at) = __float2half_rn(fmaxf(y0, 0.0f));
+            *reinterpret_cast<__half *>(positive + at + 4) = __float2half_rn(fmaxf(y1, 0.0f));
+            *reinterpret_cast<__half *>(negative + at) = __float2half_rn(fminf(y0, 0.0f));
+            *reinterpret_cast<__half *>(negative + at + 4) = __float2half_rn(fminf(y1, 0.0f));
         }
         // Lanes of the same 64 dims: 32 / kChunks of them.
         float below = 0.0f, above = 0.0f;
@@ -519,9 +523,8 @@ __global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChoosePa
     // The blocks of a cluster go on together to every barrier, whatever length each of them has read.
     const int slice = min((span.middle + blocks - 1) / blocks, p.cached);      // (of a gathered list: p.cached for all)
     const int lo = span.first + min(span.middle, rank * slice), size = some ? min(span.middle, (rank + 1) * slice) - (lo - span.first) : 0;
-    // Lane i < 16 has page i of the warp's next 16; the ones after them are looked up a step ahead.
-    auto lookup = [&](int i0) { return lane < 16 && i0 + lane < size ? list[lo + i0 + lane] : -1; };
-    int next = lookup(warp * 16);
+    // The slice's page numbers wait where its keys go: each is read before its key is written.
+    for (int i = threadIdx.x; i < size; i += kThreads) keys[i] = static_cast<uint32_t>(list[lo + i]);
     // What stays whatever its score, and -1 past the pages kept.
     for (int i = rank * kThreads + threadIdx.x; i < p.keep; i += blocks * kThreads) {
         if (i >= span.keep) to[i] = -1;
@@ -532,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChoosePa
         griddep_launch_dependents();
         return;
     }
+    __syncthreads();
 
     // Scores: a warp has 16 pages at a time, whose bounds are copied to its ring kStages - 1 steps ahead.  A row is
     // both bounds of a page and head, 2 * dim bytes in one piece.
@@ -548,10 +552,11 @@ __global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChoosePa
             at_piece[c][w] = g * kRow + ((min(w * pieces / 2 + c * 4 + t4, 8 * kChunks - 1) ^ choose_swizzle(g)) << 4);
     int ahead = warp * 16;
     auto request = [&](int stage) {
-        const int page = next, i0 = ahead;
+        const int i0 = ahead;
         ahead += kWarps * 16;
-        next = lookup(ahead);
-        const bool there = lane < 16 && i0 + lane < size, valid = there && page >= 0 && page < p.cache.pages;
+        const bool there = lane < 16 && i0 + lane < size;
+        const int page = there ? static_cast<int>(keys[i0 + lane]) : -1;
+        const bool valid = page >= 0 && page < p.cache.pages;
         const unsigned ok = __ballot_sync(0xffffffffu, valid);
         if (ok != __ballot_sync(0xffffffffu, there) && lane == 0) record_status(p.status, kStatusCache);
         const uint32_t to = to_ring + stage * Shape::kStage;
@@ -570,6 +575,16 @@ __global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChoosePa
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) request(k);
     int stage = 0;
+    auto queries = [&](int h0, int half, uint4 (&q)[2 * kChunks]) {
+#pragma unroll
+        for (int k = 0; k < 2 * kChunks; ++k)
+            q[k] = *reinterpret_cast<const uint4 *>((k % 2 ? positive : negative) + (h0 + g) * pitch + k / 2 * 128 + t4 * 32 + half * 16);
+    };
+    uint4 kept_q[2][2 * kChunks];
+    if (kFew) {
+        queries(0, 0, kept_q[0]);
+        queries(0, 1, kept_q[1]);
+    }
     for (int i0 = warp * 16; i0 < size; i0 += kWarps * 16) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
@@ -581,31 +596,36 @@ __global__ void __launch_bounds__(kThreads, 2) page_choose_kernel(const ChoosePa
         const float scale[2] = {stage_scale[g], stage_scale[g + 8]};
         stage = stage + 1 == kStages ? 0 : stage + 1;
         float best[2] = {-INFINITY, -INFINITY};
-        for (int h0 = 0; h0 < heads8; h0 += 8) {
+        for (int h0 = 0; h0 < (kFew ? 8 : heads8); h0 += 8) {
+            // One chain of products for each bound of 64 dims, a step of each in turn.
             float acc[2 * kChunks][4];
+            uint4 xs[2 * kChunks], ys[2 * kChunks];
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
+            for (int k = 0; k < 2 * kChunks; ++k) {
+                const float2 bias = *reinterpret_cast<const float2 *>(s_bias + k * heads8 + h0 + 2 * t4);
+                acc[k][0] = acc[k][2] = bias.x;
+                acc[k][1] = acc[k][3] = bias.y;
+                // Past dim the queries are 0 and the bounds whatever the ring holds, as whole numbers.
+                const unsigned char *const at = at_hand + at_piece[k / 2][k % 2];
+                xs[k] = *reinterpret_cast<const uint4 *>(at);
+                ys[k] = *reinterpret_cast<const uint4 *>(at + 8 * kRow);
+            }
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const float2 bias = *reinterpret_cast<const float2 *>(s_bias + (2 * c + w) * heads8 + h0 + 2 * t4);
-                    float (&sum)[4] = acc[2 * c + w];
-                    sum[0] = sum[2] = bias.x;
-                    sum[1] = sum[3] = bias.y;
-                    const unsigned char *const queries = (w ? positive : negative) + (h0 + g) * pitch + c * 128 + t4 * 32;
-                    const uint4 q0 = *reinterpret_cast<const uint4 *>(queries), q1 = *reinterpret_cast<const uint4 *>(queries + 16);
-                    const uint32_t q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-                    // Past dim the queries are 0 and the bounds whatever the ring holds, as whole numbers.
-                    const unsigned char *const at = at_hand + at_piece[c][w];
-                    const uint4 xa = *reinterpret_cast<const uint4 *>(at), ya = *reinterpret_cast<const uint4 *>(at + 8 * kRow);
-                    const uint32_t x[4] = {xa.x, xa.y, xa.z, xa.w}, y[4] = {ya.x, ya.y, ya.z, ya.w};
+            for (int half = 0; half < 2; ++half) {
+                if (!kFew) queries(h0, half, kept_q[half]);
+                const uint4 (&q)[2 * kChunks] = kept_q[half];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < 2 * kChunks; ++k) {
+                        const uint32_t x = half ? (j ? xs[k].w : xs[k].z) : (j ? xs[k].y : xs[k].x);
+                        const uint32_t y = half ? (j ? ys[k].w : ys[k].z) : (j ? ys[k].y : ys[k].x);
                         uint32_t x0, x1, y0, y1;
-                        widen_s8(x[j], x0, x1);
-                        widen_s8(y[j], y0, y1);
-                        mma_f16(sum, x0, y0, x1, y1, q[2 * j], q[2 * j + 1]);
+                        widen_s8(x, x0, x1);
+                        widen_s8(y, y0, y1);
+                        mma_f16(acc[k], x0, y0, x1, y1, j ? q[k].z : q[k].x, j ? q[k].w : q[k].y);
                     }
-                }
+            }
 #pragma unroll
             for (int c = 1; c < 2 * kChunks; ++c)
 #pragma unroll
