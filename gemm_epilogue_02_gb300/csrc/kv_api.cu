@@ -198,7 +198,10 @@ int kv_debug_last_check() {
         cudaGetLastError();
         return 0;
     }
-    return static_cast<int>(v);
+    const int others[] = {static_cast<int>(v), page_debug_last_check(), rope_debug_last_check()};
+    for (const int id : others)
+        if (id != 0) return id;
+    return 0;
 }
 #endif
 

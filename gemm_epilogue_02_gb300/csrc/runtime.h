@@ -37,7 +37,7 @@ private:
 bool runtime_is_device_memory(const void *p, int device);
 
 #ifdef TGEMM_DEBUG
-// Debug build: reads and clears the first failed check of a translation unit's kernels.
+// Debug build: reads and clears the first failed check of a translation unit's kernels (kv_api.cu's: of all three).
 int kv_debug_last_check();
 int page_debug_last_check();
 int rope_debug_last_check();

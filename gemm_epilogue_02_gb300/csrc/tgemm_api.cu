@@ -1269,10 +1269,8 @@ extern "C" int tgemm_debug_last_check(void) {
         cudaGetLastError();
         return 0;
     }
-    const int others[] = {static_cast<int>(v), kv_debug_last_check(), page_debug_last_check(), rope_debug_last_check()};
-    for (const int id : others)
-        if (id != 0) return id;
-    return 0;
+    const int kv = kv_debug_last_check();
+    return v ? static_cast<int>(v) : kv;
 #else
     return -1;
 #endif
