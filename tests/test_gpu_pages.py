@@ -690,3 +690,25 @@ def test_debug_build_finds_nothing(cuda_lib):
         assert dbg.tgemm_last_device_status() == 0 and dbg.tgemm_debug_last_check() == 0
     finally:
         _binding._lib = release
+
+
+def test_example_runs(cuda_lib):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_samples.py")
+    spec = importlib.util.spec_from_file_location("decode_samples", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layer, used, status = example.main(steps=20)
+    assert status == 0
+    # Prompts of 300 and 77; 20 and 20 steps; one more after the compaction.  Two sequences that began again at the third's 320.
+    assert as_list(layer.lengths) == [341, 118, 341, 341, 341, 341, 118, 118]
+    uses, table, size = as_list(layer.uses), as_list(layer.table), 16
+    held = [0] * len(uses)
+    for row, n in zip(table, as_list(layer.lengths)):
+        for p in row[:-(-n // size)]:
+            held[p] += 1
+    assert uses == held
+    assert used == sum(u > 0 for u in held) - sum(n % size == 1 for n in as_list(layer.lengths))
+    # 300 positions are 18 full pages, 77 are 4: held by the prompt and its continuations alike.
+    assert all(table[b][:18] == table[0][:18] for b in (2, 3, 4, 5)) and all(table[b][:4] == table[1][:4] for b in (6, 7))
