@@ -36,6 +36,11 @@ tgemm_status check_bounds(const tgemm_kv_page_bounds *b, const tgemm_kv_cache *c
     return TGEMM_OK;
 }
 
+// Rows of a page, and pages, that the kernels count in 32 bits with room to step past them.
+bool countable_pool(const tgemm_kv_cache *c) {
+    return c->pages <= (1 << 30) && static_cast<int64_t>(c->page_size) * c->heads <= (1 << 30);
+}
+
 // Page counts that the kernels add up in 32 bits stay there.
 bool countable(int64_t batch, int64_t width) { return std::min<int64_t>(batch, 1024) * width <= INT32_MAX; }
 
@@ -128,9 +133,14 @@ cudaError_t launch_choose_shape(const RuntimeInfo &rt, ChooseParams &p, cudaStre
     if (lists * cluster <= rt.num_sms && p.table.width > 256 && p.group <= 8 &&
         ChooseShape<2 * kThreads, kChunks, 3>::bytes(p.cached, p.group, p.cache.dim) <= kChooseMaxBytes)
         return launch_choose_stages<2 * kThreads, kBf16, kChunks, 3, true>(rt, p, cluster, s);
-    // Three stages let an SM have two blocks; queries of large groups over long lists leave room for two.
-    if (ChooseShape<kThreads, kChunks, 3>::bytes(p.cached, p.group, p.cache.dim) > kChooseMaxBytes)
-        return launch_choose_stages<kThreads, kBf16, kChunks, 2, false>(rt, p, cluster, s);
+    // Three stages let an SM have two blocks; the longest lists of large groups 256 wide leave room for two.
+    if constexpr (kChunks > 2) {
+        if (ChooseShape<kThreads, kChunks, 3>::bytes(p.cached, p.group, p.cache.dim) > kChooseMaxBytes)
+            return launch_choose_stages<kThreads, kBf16, kChunks, 2, false>(rt, p, cluster, s);
+        static_assert(ChooseShape<kThreads, kChunks, 2>::bytes(kChooseMaxPages / 8, kChooseGroup, 64 * kChunks) <= kChooseMaxBytes, "fits");
+    } else {
+        static_assert(ChooseShape<kThreads, kChunks, 3>::bytes(kChooseMaxPages / 8, kChooseGroup, 64 * kChunks) <= kChooseMaxBytes, "fits");
+    }
     return p.group <= 8 ? launch_choose_stages<kThreads, kBf16, kChunks, 3, true>(rt, p, cluster, s)
                         : launch_choose_stages<kThreads, kBf16, kChunks, 3, false>(rt, p, cluster, s);
 }
@@ -253,6 +263,7 @@ tgemm_status check_pages(const tgemm_kv_cache *cache, int32_t *uses, int32_t *pa
     Extent ck, cv;
     tgemm_status st = check_cache(cache, &p->cache, &ck, &cv);
     if (st != TGEMM_OK) return st;
+    if (!countable_pool(cache)) return TGEMM_ERR_INVALID_ARG;
     if (!cache->e4m3) p->cache.k_scale = p->cache.v_scale = nullptr;      // the kernels go by them
     st = check_lists(pages, lengths, width, stride, batch, cache->page_size, &p->to, lists);
     if (st != TGEMM_OK) return st;
@@ -384,6 +395,7 @@ extern "C" tgemm_status tgemm_kv_compact(const tgemm_kv_compact_args *a, tgemm_s
     tgemm_status st = check_cache(a->cache, &p.cache, &ck, &cv);
     if (st != TGEMM_OK) return st;
     const tgemm_kv_cache *cache = a->cache;
+    if (!countable_pool(cache)) return TGEMM_ERR_INVALID_ARG;
     if (!cache->e4m3) p.cache.k_scale = p.cache.v_scale = nullptr;        // the kernels go by them
     if (a->bounds) {
         st = check_bounds(a->bounds, cache, &p.bounds, &eb, &es);

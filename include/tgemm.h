@@ -536,7 +536,7 @@ tgemm_status tgemm_attention_decode_lists(const tgemm_attention_decode_args *arg
  * lowest free ones, in the order of the sequences.  What cannot be done (no page
  * left, a list without room, a bad length, parent or page number) is recorded as
  * TGEMM_ERR_CACHE and left out.  The sums of 1024 sequences' list widths stay
- * below 2^31.
+ * below 2^31, pages and page_size * heads at most 2^30.
  */
 
 /*
@@ -646,12 +646,13 @@ typedef struct {
  * (norm = 0: y = R(x), no weights), R turning pair i by the angle
  * (positions[axes[i], token] + shift) * frequency_i; rotary NULL: no rotation.
  * Weights have dim contiguous elements of `dtype`, or fp32 with weight_f32 = 1;
- * NULL: ones.  positions is int32 [axes, tokens], device, any values (axis_stride 0: the axes
- * share them), axes at most 32; position * frequency keeps 2^-31 of a turn
- * whatever they are, the rest is fp32, rounded once.  dim is a
- * multiple of 8, at most 256.  q_heads or k_heads may be 0.  q_out and k_out may
- * be q and k themselves (the same strides), and may lie side by side with others
- * in one array; they overlap nothing else.
+ * NULL: ones.  positions is int32 [axes, tokens], device, any values
+ * (axis_stride 0: the axes share them), axes at most 32; position * frequency
+ * keeps 2^-31 of a turn whatever they are, the rest is fp32, rounded once (a row
+ * whose sum of squares passes fp32's range becomes zeros).  dim is a multiple of
+ * 8, at most 256.  q_heads or k_heads may be 0.  q_out and k_out may be q and k
+ * themselves (the same strides), and may lie side by side with others in one
+ * array; they overlap nothing else.
  */
 typedef struct {
     tgemm_rows q, k, q_out, k_out;
@@ -671,7 +672,8 @@ tgemm_status tgemm_qk_norm_rope(const tgemm_qk_norm_rope_args *args, tgemm_strea
  * k_grad, themselves), from those of what it wrote, q_grad and k_grad; and of the
  * weights, fp32 [dim], written, not added (NULL: not wanted; they need norm = 1
  * and the workspace).  Sums are fp32 in a fixed order: results are deterministic.
- * With norm = 0 q and k are not read.  workspace: device memory of
+ * With norm = 0 q and k are not read.  Rows whose sums pass fp32's range have
+ * gradients that are not finite.  workspace: device memory of
  * tgemm_qk_norm_rope_backward_workspace() bytes, 16-byte aligned, that held zeros
  * before its first use; the call leaves it fit for the next.  Calls that may
  * overlap on the GPU need one each.

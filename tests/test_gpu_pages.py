@@ -239,11 +239,14 @@ def test_extreme_queries_and_keys(cuda_lib):
     assert as_list(to_table)[0][0] == [int(f.table_host[0, i]) for i in lists[0][0]]
 
 
-@pytest.mark.parametrize("pages,batch", [(3000, 1), (9000, 2), (17000, 1), (600, 40)])
-def test_long_lists(cuda_lib, pages, batch):
-    """One block and clusters, more pages than one block has room for."""
+@pytest.mark.parametrize("pages,batch,dim,group", [
+    (3000, 1, 64, 3), (9000, 2, 64, 3), (17000, 1, 64, 3), (600, 40, 64, 3), (5000, 1, 128, 24), (700, 100, 128, 8), (4000, 2, 256, 8),
+    (131072, 1, 256, 64), (131072, 1, 64, 1),
+])
+def test_long_lists(cuda_lib, pages, batch, dim, group):
+    """One block and clusters, more pages than one block has room for, the longest list with the most heads."""
     g = torch.Generator().manual_seed(15)
-    heads, dim, group, keep = 2, 64, 3, 100
+    heads, keep = 2 if pages < 100000 else 1, 100
     cache = tg.PagedCache(*(torch.zeros(pages, 1, heads, dim, dtype=torch.float16, device="cuda") for _ in range(2)))
     bounds = tg.PageBounds(torch.randint(-127, 128, (pages, heads, 2, dim), dtype=torch.int8, generator=g).cuda(),
                            (2.0 ** torch.randint(-3, 1, (pages, heads), generator=g)).cuda())
@@ -260,10 +263,11 @@ def test_long_lists(cuda_lib, pages, batch):
         at = table[b, :n].long()
         lo, hi = bounds.bounds[at, :, 0].double(), bounds.bounds[at, :, 1].double()
         for h in range(heads):
-            z = q[b, h * group:(h + 1) * group].double()
-            # bounds of any order: the lower one counts where z < 0
-            s = (z[:, None] * torch.where(z[:, None] > 0, hi[None, :, h], lo[None, :, h])).sum(-1) * bounds.scale[at, h].double()
-            kept = choose(s.amax(0).tolist(), keep, 2, 3)
+            s = torch.full((n,), -float("inf"), dtype=torch.float64, device="cuda")
+            for z in q[b, h * group:(h + 1) * group].double():
+                # bounds of any order: the lower one counts where z < 0
+                s = torch.maximum(s, lo[:, h] @ z.clamp(max=0) + hi[:, h] @ z.clamp(min=0))
+            kept = choose((s * bounds.scale[at, h].double()).tolist(), keep, 2, 3)
             assert as_list(to_table[b, h]) == as_list(at[kept]) + [-1] * (keep - len(kept))
 
 

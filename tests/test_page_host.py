@@ -130,6 +130,16 @@ def test_lists_that_cannot_be_counted(f):
     assert f(c, width=2 ** 22, stride=2 ** 22, batch=512) == INVALID
 
 
+@pytest.mark.parametrize("f", [kv_grow, kv_free, kv_fork, kv_compact], ids=lambda f: f.__name__)
+@pytest.mark.parametrize("c", [
+    dict(page_size=1, page_stride=64, heads=1, slot_stride=64, pages=2 ** 30 + 1),
+    dict(page_size=2 ** 20, heads=2048, slot_stride=2048 * 64, page_stride=2 ** 37),
+])
+def test_pools_that_cannot_be_counted(f, c):
+    kw = dict(bounds=0) if f is kv_compact else {}
+    assert f(cache(**c), width=0, **kw) == INVALID
+
+
 @pytest.mark.parametrize("f", [kv_bounds, kv_select], ids=lambda f: f.__name__)
 @pytest.mark.parametrize("b,code", [
     (dict(bounds=0), INVALID), (dict(scale=0), INVALID), (dict(bounds=AT["bounds"] + 8), ALIGN), (dict(scale=AT["bscale"] + 2), ALIGN),
