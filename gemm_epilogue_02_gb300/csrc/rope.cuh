@@ -269,6 +269,28 @@ struct RopeAngles {
     }
 };
 
+// The rows turned (kBack: turned back): slot i of a lane's pairs by the angle whose
+// cosine and sine are c and s.  The first `turning` slots are pairs of the
+// rotation.  What is past them is kept as it is: a product with a sine of 0 would
+// carry an infinity or a NaN to the other element, and lose the sign of a zero.
+template <int V, bool kInterleaved, bool kBack>
+__device__ __forceinline__ void rope_turn(float2 (&a)[V / 2], float2 (&b)[V / 2], const float2 (&c)[V / 2], const float2 (&s)[V / 2],
+                                          int turning) {
+    if (turning <= 0) return;
+    auto turn = [&](auto whole) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 minus = make_float2(-s[i].x, -s[i].y), ta = kBack ? s[i] : minus, tb = kBack ? minus : s[i];
+            const float2 f = fma2(a[i], c[i], mul2(b[i], ta)), g = fma2(b[i], c[i], mul2(a[i], tb));
+            if (whole() || 2 * i < turning) a[i].x = f.x, b[i].x = g.x;
+            if (whole() || 2 * i + 1 < turning) a[i].y = f.y, b[i].y = g.y;
+        }
+    };
+    // Pairs that lie apart fill a lane; of those side by side one lane may have both kinds.
+    if (!kInterleaved || turning >= V) turn([] { return true; });
+    else turn([] { return false; });
+}
+
 // Work.  A pass is 32 / kLanes rows, of one token's queries or of its keys, for a
 // warp; the passes of all tokens in a row are cut into equal runs, one a warp.
 // N arrays of rows are followed together (addresses of the lane's row).
@@ -346,6 +368,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
     rope_units<V, kInterleaved>(l, p.dim, p.pairs, unit, is);
     RopeAngles<V, kLanes> angles;
     angles.init(p, l, row);
+    const int turning = p.pairs - l * V;    // of the lane's pairs: V or more, all
     const float inv_dim = 1.0f / static_cast<float>(p.dim);
     const int passes_q = (p.side[0].heads + kRows - 1) / kRows, passes = passes_q + (p.side[1].heads + kRows - 1) / kRows;
     const long long warps = static_cast<long long>(gridDim.x) * kWarps, warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -396,10 +419,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
         const float2 rr = make_float2(r, r);
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
-            const float2 f = mul2(mul2(a[i], rr), wa[i]), g = mul2(mul2(b[i], rr), wb[i]);
-            a[i] = fma2(f, c[i], mul2(g, make_float2(-s[i].x, -s[i].y)));
-            b[i] = fma2(g, c[i], mul2(f, s[i]));
+            a[i] = mul2(mul2(a[i], rr), wa[i]);
+            b[i] = mul2(mul2(b[i], rr), wb[i]);
         }
+        rope_turn<V, kInterleaved, false>(a, b, c, s, turning);
         const bool there = use.head < p.side[use.side].heads;
         const bool in[2] = {there && is[0], there && is[1]};
         if (there && TGEMM_CHECK(use.at[0] - p.side[use.side].y + 2 * p.dim <= p.dbg_y[use.side], kChkRope, p.status))
@@ -499,12 +522,8 @@ __global__ void __launch_bounds__(kRopeBackThreads, kRopeBackCtas) rope_backward
         rope_split2<kBf16, V, kInterleaved>(raw_g, a, b);
         rope_split2<kBf16, V, kInterleaved>(raw_x, x, y);
         request(raw_x, raw_g);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            const float2 f = fma2(a[i], c[i], mul2(b[i], s[i]));
-            b[i] = fma2(b[i], c[i], mul2(a[i], make_float2(-s[i].x, -s[i].y)));
-            a[i] = f;
-        }
+        // (from the thread's number each time: with one register more the kernel spills)
+        rope_turn<V, kInterleaved, true>(a, b, c, s, p.pairs - static_cast<int>(threadIdx.x) % kLanes * V);
         if (p.norm) {
             float2 sums = make_float2(0.0f, 0.0f), dots = make_float2(0.0f, 0.0f);
             {

@@ -304,3 +304,63 @@ def test_debug_build_finds_nothing(cuda_lib):
             _binding._lib = release
     assert dbg.tgemm_last_device_status() == 0 and dbg.tgemm_debug_last_check() == 0
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def odd_values(x, at, seed=0):
+    """x with infinities, NaN and zeros of both signs in some of the elements `at` of its rows."""
+    g = torch.Generator().manual_seed(seed)
+    y = x.clone()
+    for value in (float("inf"), float("-inf"), float("nan"), 0.0, -0.0):
+        where = torch.zeros(x.shape, dtype=torch.bool)
+        where[..., at] = torch.rand(x[..., at].shape, generator=g) < 0.1
+        y[where.to(x.device)] = value
+    return y
+
+
+def same_bits(a, b):
+    """Equal, signs of zeros included; NaN to NaN."""
+    return bool(((a.view(torch.int16) == b.view(torch.int16)) | (a.isnan() & b.isnan())).all())
+
+
+PARTS = [(128, 32, False), (128, 24, True), (96, 20, False), (8, 3, True), (256, 64, False), (72, 8, False), (64, 0, False), (112, 49, True)]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim,pairs,interleaved", PARTS)
+def test_elements_past_the_pairs_stay(cuda_lib, dim, pairs, interleaved, dtype):
+    """Infinities, NaN and the signs of zeros past the pairs stay where they are and touch nothing else, in both directions;
+    so do those of the pairs."""
+    q, k, positions, _ = case(23, 5, 2, dim, dtype, seed=30, far=900)
+    f = frequencies(pairs)
+    rotary, angle = tg.Rotary(f, interleaved=interleaved), angles64(positions, f, [0] * pairs)
+    past = list(range(2 * pairs, dim))
+    for where in (past, list(range(2 * pairs))):
+        x = [odd_values(t, where, seed=31) for t in (q, k)] if where else [q.clone(), k.clone()]
+        out, back = ([torch.empty_like(t) for t in x] for _ in range(2))
+        tg.qk_norm_rope(*x, positions, rotary, *out, eps=None)
+        tg.qk_norm_rope_backward(*x, x[0], x[1], positions, rotary, *back, eps=None)
+        torch.cuda.synchronize()
+        for t, y, z in zip(x, out, back):
+            assert same_bits(y[..., past], t[..., past]) and same_bits(z[..., past], t[..., past])
+            if where is past:
+                clean = t.double().cpu()
+                clean[..., past] = 0
+                for got, a in ((y, angle), (z, -angle)):
+                    want, bound = forward64(clean, None, None, a, interleaved)
+                    close(got[..., :2 * pairs], want[..., :2 * pairs], bound[..., :2 * pairs], dtype)
+
+
+@pytest.mark.parametrize("pairs,interleaved", [(32, False), (24, True), (0, False)])
+def test_infinity_past_the_pairs_with_the_norm(cuda_lib, pairs, interleaved):
+    """A row with an infinity has r = 0: the infinity becomes NaN, every other element 0."""
+    q, k, positions, w = case(6, 4, 2, 128, "bf16", seed=32, fused=False)
+    q[2, 1, 77], k[5, 0, 120] = float("inf"), float("-inf")
+    out = [torch.empty_like(t) for t in (q, k)]
+    rotary = tg.Rotary(frequencies(pairs), interleaved=interleaved) if pairs else None
+    tg.qk_norm_rope(q, k, positions, rotary, *out, q_weight=w[0], k_weight=w[1])
+    torch.cuda.synchronize()
+    for row, at in ((out[0][2, 1], 77), (out[1][5, 0], 120)):
+        assert row[at].isnan()
+        row[at] = 0
+        assert (row == 0).all()
+    assert out[0].isfinite().all() and out[1].isfinite().all()
