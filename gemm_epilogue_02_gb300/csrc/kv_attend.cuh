@@ -1158,7 +1158,7 @@ __global__ void __launch_bounds__(kSpreadThreads) kv_spread_kernel(const AttendP
         if (blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kStatusCache);
         n = p.weights.width;
     }
-    const int *list = p.table.pages + b * p.table.stride;
+    const int *list = p.table.pages + b * p.table.stride + head * p.table.head_stride;
     float *w = p.weights.base + b * p.weights.batch_stride + head * p.weights.head_stride;
     const long long row0 = static_cast<long long>(b) * p.cache.heads + head;
     const float *const scores = p.space.scores + row0 * p.positions * p.scored;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import gemm_epilogue_02_gb300 as tg
-from kv_helpers import E4M3, TDT, Filled, attend64, attend_bound, split_e4m3
+from kv_helpers import E4M3, TDT, Filled, attend64, attend_bound, score_error, split_e4m3
 from page_helpers import Pool, as_list, choose, int32, page_bounds, page_score
 
 pytestmark = pytest.mark.gpu
@@ -716,3 +716,37 @@ def test_example_runs(cuda_lib):
     assert used == sum(u > 0 for u in held) - sum(n % size == 1 for n in as_list(layer.lengths))
     # 300 positions are 18 full pages, 77 are 4: held by the prompt and its continuations alike.
     assert all(table[b][:18] == table[0][:18] for b in (2, 3, 4, 5)) and all(table[b][:4] == table[1][:4] for b in (6, 7))
+
+
+@pytest.mark.parametrize("group", [1, 4, 9])
+def test_weights_over_lists_that_differ(cuda_lib, group):
+    """A page that is not in the pool, in the list of one head: the weights of that head there stay, those of the others
+    grow by their attention, in the first head's list and in another's."""
+    n, heads, dim, page = 150, 3, 64, 16
+    f = Filled(tg, [n, n], heads, dim, page, "bf16", seed=40, extra=9)
+    q = torch.randn(2, heads * group, dim, device="cuda").bfloat16()
+    lists = f.table.unsqueeze(1).expand(-1, heads, -1).contiguous()
+    lists[0, 0, 2], lists[1, 1, 4], lists[1, 2, 0] = f.cache.pages, -1, 2 ** 30
+    gone = {(0, 0): 2, (1, 1): 4, (1, 2): 0}
+    o, w = torch.empty_like(q), torch.full((2, heads, n + 5), 2.0, device="cuda")
+    ws = tg.attention_decode_workspace(q, f.cache, lists, weights=True)
+    for round_ in range(2):                                       # the second finds the first one's scores in the workspace
+        tg.attention_decode(q, f.cache, lists, f.lengths, o, weights=w, workspace=ws)
+        assert tg.tgemm_last_device_status() == CACHE_ERROR
+        for b in range(2):
+            for h in range(heads):
+                bad = gone.get((b, h))
+                pos = torch.tensor([j for j in range(n) if j // page != bad])
+                rows = slice(h * group, (h + 1) * group)
+                o64, p, mag, reach, top = attend64(q[b, rows].cpu(), f.k64[b][:, h:h + 1], f.v64[b][:, h:h + 1], dim ** -0.5, keep=pos)
+                bound = attend_bound(o64, mag, reach, top, len(pos), dim, "bf16", "bf16", 0.0)
+                assert ((o[b, rows].double().cpu() - o64).abs() <= bound).all()
+                # a weight of p: its exponent's error and that of the sum below it, the sum's roundings, two exponentials and
+                # a division of 2^-22 each; then the group's sum and what is there, below group and 2 + 2 group
+                e = 2 * score_error(reach, dim, 0.0) + (n + 64) * 2.0 ** -24 + 2.0 ** -20
+                room = (p * e.unsqueeze(-1)).sum(0) + (group ** 2 + 2 * group + 2) * 2.0 ** -24
+                grown = w[b, h, :n].double().cpu() - 2
+                assert ((grown - (round_ + 1) * p.sum(0)).abs() <= (round_ + 1) * room).all(), (b, h)
+                if bad is not None:
+                    assert (w[b, h, bad * page:(bad + 1) * page] == 2).all()
+                assert (w[b, h, n:] == 2).all()
