@@ -524,6 +524,7 @@ __global__ void __launch_bounds__(kRopeBackThreads, kRopeBackCtas) rope_backward
         request(raw_x, raw_g);
         // (from the thread's number each time: with one register more the kernel spills)
         rope_turn<V, kInterleaved, true>(a, b, c, s, p.pairs - static_cast<int>(threadIdx.x) % kLanes * V);
+        const bool there = use.head < side.heads;
         if (p.norm) {
             float2 sums = make_float2(0.0f, 0.0f), dots = make_float2(0.0f, 0.0f);
             {
@@ -536,7 +537,8 @@ __global__ void __launch_bounds__(kRopeBackThreads, kRopeBackCtas) rope_backward
                 }
             }
             const float sum = rope_sum<kLanes>(sums.x + sums.y), dot = rope_sum<kLanes>(dots.x + dots.y);
-            const float r = rsqrtf(fmaf(sum, inv_dim, p.eps)), back = -r * r * dot * inv_dim;
+            // A row past the last head has no part in the weights' gradients, whatever eps is.
+            const float r = there ? rsqrtf(fmaf(sum, inv_dim, p.eps)) : 0.0f, back = -r * r * dot * inv_dim;
             const float2 rr = make_float2(r, r), bb = make_float2(back, back);
             float2 wa[V / 2], wb[V / 2];
             rope_weights(weights, l, wa, wb);
@@ -548,7 +550,6 @@ __global__ void __launch_bounds__(kRopeBackThreads, kRopeBackCtas) rope_backward
                 b[i] = mul2(rr, fma2(y[i], bb, mul2(b[i], wb[i])));
             }
         }
-        const bool there = use.head < side.heads;
         const bool in[2] = {there && is[0], there && is[1]};
         if (there && TGEMM_CHECK(use.at[0] - side.y + 2 * p.dim <= p.dbg_y[use.side], kChkRope, p.status))
             rope_write2<kBf16, V, kInterleaved>(use.at[0], a, b, unit, in);

@@ -364,3 +364,29 @@ def test_infinity_past_the_pairs_with_the_norm(cuda_lib, pairs, interleaved):
         row[at] = 0
         assert (row == 0).all()
     assert out[0].isfinite().all() and out[1].isfinite().all()
+
+
+@pytest.mark.parametrize("q_heads,k_heads,dim,pairs,interleaved", [
+    (6, 3, 128, 64, False), (4, 1, 64, 32, False), (1, 1, 96, 48, True), (3, 5, 72, 36, False), (7, 2, 256, 128, False), (1, 0, 32, 16, False),
+])
+def test_gradient_without_eps(cuda_lib, q_heads, k_heads, dim, pairs, interleaved):
+    """eps = 0, heads that do not fill the rows a warp has at a time: the weights' gradients are those of the rows there are."""
+    q, k, positions, w = case(37, q_heads, max(1, k_heads), dim, "bf16", seed=33)
+    if k_heads == 0:
+        k = None
+    f = frequencies(pairs)
+    rotary, angle = tg.Rotary(f, interleaved=interleaved), angles64(positions, f, [0] * pairs)
+    g = torch.Generator().manual_seed(34)
+    dq, dk = (None if t is None else torch.randn(t.shape, generator=g).to(t.dtype).cuda() for t in (q, k))
+    dqi, dki = (None if t is None else torch.empty(t.shape, dtype=t.dtype, device="cuda") for t in (q, k))
+    dw = [torch.empty(dim, device="cuda") for _ in range(2)]
+    tg.qk_norm_rope_backward(dq, dk, q, k, positions, rotary, dqi, dki, q_weight=w[0], k_weight=w[1], q_weight_grad=dw[0],
+                             k_weight_grad=dw[1], eps=0.0)
+    torch.cuda.synchronize()
+    for x, wi, dy, dx, dwi in ((q, w[0], dq, dqi, dw[0]), (k, w[1], dk, dki, dw[1])):
+        if x is None:
+            assert (dwi == 0).all()
+            continue
+        want, bound, want_w, bound_w = backward64(x, wi, dy, 0.0, angle, interleaved)
+        close(dx, want, bound, "bf16")
+        assert ((dwi.double().cpu() - want_w).abs() <= bound_w).all()
