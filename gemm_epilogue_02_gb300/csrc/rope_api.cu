@@ -4,7 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cmath>
+#include <cfloat>
 #include <cstring>
 
 #include "../../include/tgemm.h"
@@ -67,7 +67,7 @@ tgemm_status check_common(const tgemm_qk_norm_rope_args *a, RopeParams *p, int *
         a->dim < 8 || a->dim > 2 * kRopePairs || a->dim % 8 != 0 || !valid_dtype(a->dtype) || (a->norm != 0 && a->norm != 1) ||
         (a->weight_f32 != 0 && a->weight_f32 != 1) || a->shift < INT32_MIN || a->shift > INT32_MAX || a->axes < 0 || a->axes > 32)
         return TGEMM_ERR_INVALID_ARG;
-    if (a->norm ? !(a->eps >= 0.0) || !std::isfinite(a->eps) : (a->q_weight || a->k_weight)) return TGEMM_ERR_INVALID_ARG;
+    if (a->norm ? !(a->eps >= 0.0) || a->eps > FLT_MAX : (a->q_weight || a->k_weight)) return TGEMM_ERR_INVALID_ARG;
     if (!a->norm && !r) return TGEMM_ERR_INVALID_ARG;
     *v = 8;
     *interleaved = false;
@@ -98,7 +98,8 @@ tgemm_status check_common(const tgemm_qk_norm_rope_args *a, RopeParams *p, int *
     p->shift = static_cast<int>(a->shift);
     p->norm = static_cast<int>(a->norm);
     p->weight_f32 = static_cast<int>(a->weight_f32);
-    p->eps = static_cast<float>(a->eps);
+    // (an eps that fp32 rounds to 0 still keeps rows of zeros what they are)
+    p->eps = a->eps > 0.0 ? std::max(static_cast<float>(a->eps), FLT_TRUE_MIN) : 0.0f;
     return TGEMM_OK;
 }
 

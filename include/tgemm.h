@@ -649,7 +649,8 @@ typedef struct {
  * NULL: ones.  positions is int32 [axes, tokens], device, any values
  * (axis_stride 0: the axes share them), axes at most 32; position * frequency
  * keeps 2^-31 of a turn whatever they are, the rest is fp32, rounded once (a row
- * whose sum of squares passes fp32's range becomes zeros).  dim is a multiple of
+ * whose sum of squares passes fp32's range becomes zeros).  eps lies in fp32's
+ * range; with 0 a row whose mean square fp32 rounds to 0 is not finite.  dim is a multiple of
  * 8, at most 256.  q_heads or k_heads may be 0.  q_out and k_out may be q and k
  * themselves (the same strides), and may lie side by side with others in one
  * array; they overlap nothing else.

@@ -390,3 +390,21 @@ def test_gradient_without_eps(cuda_lib, q_heads, k_heads, dim, pairs, interleave
         want, bound, want_w, bound_w = backward64(x, wi, dy, 0.0, angle, interleaved)
         close(dx, want, bound, "bf16")
         assert ((dwi.double().cpu() - want_w).abs() <= bound_w).all()
+
+
+def test_smallest_eps(cuda_lib):
+    """An eps below fp32's numbers is not 0: a row of zeros stays one, and so does its gradient's part in the weights'."""
+    q, _, positions, w = case(9, 3, 1, 64, "bf16", seed=35, fused=False)
+    q[4, 1] = 0
+    f = frequencies(32)
+    rotary, angle = tg.Rotary(f), angles64(positions, f, [0] * 32)
+    out, dw = torch.empty_like(q), torch.empty(64, device="cuda")
+    tg.qk_norm_rope(q, None, positions, rotary, out, None, q_weight=w[0], eps=1e-60)
+    dy, dx = torch.randn(q.shape, device="cuda").bfloat16(), torch.empty_like(q)
+    dy[4, 1] = 0
+    tg.qk_norm_rope_backward(dy, None, q, None, positions, rotary, dx, None, q_weight=w[0], q_weight_grad=dw, eps=1e-60)
+    torch.cuda.synchronize()
+    close(out, *forward64(q, w[0], 1e-60, angle, False), "bf16")
+    want, bound, want_w, bound_w = backward64(q, w[0], dy, 1e-60, angle, False)
+    close(dx, want, bound, "bf16")
+    assert ((dw.double().cpu() - want_w).abs() <= bound_w).all()

@@ -186,3 +186,9 @@ def test_python_gradient_refusals(kw):
     with pytest.raises(ValueError):
         tg.qk_norm_rope_backward(d["Q_out"], d["K_out"], d["Q"], d["K"], d["positions"], d["rotary"], d["Q_out"], d["K_out"],
                                  q_weight=d["q_weight"], k_weight=d["k_weight"], **{n: x for n, x in kw.items() if not n.endswith("weight")})
+
+
+@pytest.mark.parametrize("eps,code", [(1e39, INVALID), (float("inf"), INVALID), (3.4e38, VALID), (1e-60, VALID), (0.0, VALID)])
+def test_range_of_eps(eps, code):
+    for call in (forward, backward):
+        assert call(eps=eps) == code if code == INVALID else call(eps=eps) in code and call(eps=eps) == call()
