@@ -538,14 +538,17 @@ __global__ void __launch_bounds__(kRopeBackThreads, kRopeBackCtas) rope_backward
             }
             const float sum = rope_sum<kLanes>(sums.x + sums.y), dot = rope_sum<kLanes>(dots.x + dots.y);
             // A row past the last head has no part in the weights' gradients, whatever eps is.
-            const float r = there ? rsqrtf(fmaf(sum, inv_dim, p.eps)) : 0.0f, back = -r * r * dot * inv_dim;
+            const float r = there ? rsqrtf(fmaf(sum, inv_dim, p.eps)) : 0.0f, back = -r * (dot * inv_dim);
             const float2 rr = make_float2(r, r), bb = make_float2(back, back);
             float2 wa[V / 2], wb[V / 2];
             rope_weights(weights, l, wa, wb);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
-                da[i] = fma2(a[i], mul2(x[i], rr), da[i]);
-                db[i] = fma2(b[i], mul2(y[i], rr), db[i]);
+                // (x r and r dot stay in fp32's range where r^2 does not)
+                x[i] = mul2(x[i], rr);
+                y[i] = mul2(y[i], rr);
+                da[i] = fma2(a[i], x[i], da[i]);
+                db[i] = fma2(b[i], y[i], db[i]);
                 a[i] = mul2(rr, fma2(x[i], bb, mul2(a[i], wa[i])));
                 b[i] = mul2(rr, fma2(y[i], bb, mul2(b[i], wb[i])));
             }
