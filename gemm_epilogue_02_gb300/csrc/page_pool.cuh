@@ -69,7 +69,7 @@ __device__ __forceinline__ int block_scan(int x, int *sums, int *total) {
 // Pages that n positions take.
 __host__ __device__ inline int kv_pages_of(int n, int page_size) { return n / page_size + (n % page_size > 0 ? 1 : 0); }
 
-// What a child takes over: its parent's length, or 0 (a bad parent, or a list without room for it).
+// A parent's length, cut to what its list holds (*bad); 0 for a bad parent, or where the child's list has no room for it.
 __host__ __device__ inline int fork_length(const int *lengths, int batch, int parent, int width, int page_size, int to_width, bool *bad) {
     if (parent == -1) return 0;
     if (parent < 0 || parent >= batch) {
@@ -82,6 +82,12 @@ __host__ __device__ inline int fork_length(const int *lengths, int batch, int pa
         return 0;
     }
     return n;
+}
+
+// What a child of `parent` takes over: its positions, or none where that cannot be done.
+__device__ __forceinline__ int fork_positions(const PagesParams &p, int parent, bool *bad) {
+    const int n = fork_length(p.table.lengths, p.table.batch, parent, p.table.width, p.cache.page_size, p.to.width, bad);
+    return *bad ? 0 : n;                   // (of a list that is not all its parent's, which entries are is not known)
 }
 
 // By one block of kTakeThreads.
@@ -102,7 +108,7 @@ __device__ __forceinline__ void take_pages(const PagesParams &p) {
         bool bad = false;
         if (b < p.to.batch) {
             if (kFork) {
-                n = fork_length(p.table.lengths, p.table.batch, p.parents[b], p.table.width, size, p.to.width, &bad);
+                n = fork_positions(p, p.parents[b], &bad);
                 first = n / size;
                 need = n % size > 0 ? 1 : 0;
             } else {
@@ -180,7 +186,7 @@ __device__ __forceinline__ void take_pages(const PagesParams &p) {
                 int f;
                 if (kFork) {
                     bool ignore = false;
-                    f = fork_length(p.table.lengths, p.table.batch, p.parents[b0 + lo], p.table.width, size, p.to.width, &ignore) / size;
+                    f = fork_positions(p, p.parents[b0 + lo], &ignore) / size;
                 } else {
                     bool ignore = false;
                     f = kv_pages_of(kv_length(p.to.lengths[b0 + lo], p.to.width, size, &ignore), size) + rank - s_end[lo];
@@ -233,7 +239,7 @@ __device__ __forceinline__ void fork_child(const PagesParams &p, int c, int chun
     constexpr int kPass = kThreads / kLanes, kUnroll = 4;
     const int size = p.cache.page_size, parent = p.parents[c];
     bool bad = false;
-    const int n = fork_length(p.table.lengths, p.table.batch, parent, p.table.width, size, p.to.width, &bad);
+    const int n = fork_positions(p, parent, &bad);
     const int full = n / size, rest = p.to.lengths[c] > full * size ? n - full * size : 0;
     if (n == 0) return;
     const int *const list = p.table.pages + parent * p.table.stride;

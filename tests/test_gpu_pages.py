@@ -750,3 +750,23 @@ def test_weights_over_lists_that_differ(cuda_lib, group):
                 if bad is not None:
                     assert (w[b, h, bad * page:(bad + 1) * page] == 2).all()
                 assert (w[b, h, n:] == 2).all()
+
+
+@pytest.mark.parametrize("children", [2, 40])
+def test_fork_leaves_bad_lengths_out(cuda_lib, children):
+    """A parent's length below 0 or past what its list holds: the child is empty, no count changes."""
+    for bad in (-1, 49, 2 ** 31 - 1):
+        h = Held([48, 20], 16, 60, seed=41, width=3)
+        h.d_lengths[0] = bad
+        parents = [0, 1] * (children // 2)
+        to, to_lengths = torch.full((children, 3), -9, dtype=torch.int32, device="cuda"), int32([5] * children)
+        want = h.images()
+        tg.kv_fork(h.cache, h.d_uses, h.d_table, h.d_lengths, int32(parents), to, to_lengths)
+        to_host, n_host = [[-9] * 3 for _ in range(children)], [0] * children
+        for a, z, rows in h.pool.fork(h.table, h.lengths, [-1 if p == 0 else p for p in parents], to_host, n_host):
+            for t in want:
+                t[z, :rows] = t[a, :rows]
+        torch.cuda.synchronize()
+        assert tg.tgemm_last_device_status() == CACHE_ERROR
+        assert as_list(h.d_uses) == h.pool.uses and as_list(to_lengths) == n_host and as_list(to) == to_host
+        assert all(torch.equal(a, b) for a, b in zip(h.images(), want))
