@@ -318,9 +318,10 @@ __global__ void __launch_bounds__(kPageThreads) page_free_kernel(const PagesPara
     const int b = blockIdx.x;
     if (threadIdx.x == 0) {
         bool bad = false;
-        s_n = kv_length(p.to.lengths[b], p.to.width, p.cache.page_size, &bad);
+        const int n = kv_length(p.to.lengths[b], p.to.width, p.cache.page_size, &bad);
+        s_n = bad ? 0 : n;                                 // which pages such a sequence holds is not known: it stays
         if (bad) record_status(p.status, kStatusCache);
-        p.to.lengths[b] = 0;
+        else p.to.lengths[b] = 0;
     }
     __syncthreads();
     const int count = kv_pages_of(s_n, p.cache.page_size);

@@ -574,7 +574,10 @@ typedef struct {
 } tgemm_kv_fork_args;
 tgemm_status tgemm_kv_fork(const tgemm_kv_fork_args *args, tgemm_stream_t stream);
 
-/* tgemm_kv_free — the sequences give their pages back: each is held once less, and lengths become 0. */
+/*
+ * tgemm_kv_free — the sequences give their pages back: each is held once less, and lengths become 0 (a length that
+ * the list cannot hold, and its sequence, stay as they are).
+ */
 typedef struct {
     const tgemm_kv_cache *cache;
     int32_t *uses;
@@ -593,7 +596,8 @@ tgemm_status tgemm_kv_free(const tgemm_kv_free_args *args, tgemm_stream_t stream
  *   in_use    int32 [1]: n; from page n on the pool is free
  * to_pages may be seq.pages (with its stride), to_uses may be uses.  workspace:
  * device memory of tgemm_kv_compact_workspace() bytes, 16-byte aligned; calls
- * that may overlap on the GPU need one each.
+ * that may overlap on the GPU need one each.  Of a length past what its list
+ * holds all of the list is translated, as pages move all the same.
  */
 typedef struct {
     const tgemm_kv_cache *cache;

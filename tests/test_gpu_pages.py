@@ -770,3 +770,17 @@ def test_fork_leaves_bad_lengths_out(cuda_lib, children):
         assert tg.tgemm_last_device_status() == CACHE_ERROR
         assert as_list(h.d_uses) == h.pool.uses and as_list(to_lengths) == n_host and as_list(to) == to_host
         assert all(torch.equal(a, b) for a, b in zip(h.images(), want))
+
+
+def test_free_leaves_bad_lengths_out(cuda_lib):
+    """A length below 0 or past what the list holds: no count changes, the sequence is as it was; the others are freed."""
+    for bad in (-1, 49, 2 ** 31 - 1):
+        h = Held([48, 20, 33], 16, 12, seed=42, width=3, shared=(0,))
+        h.d_lengths[0] = bad
+        tg.kv_free(h.cache, h.d_uses, h.d_table, h.d_lengths)
+        kept = h.lengths[0]
+        h.lengths[0] = 0                                         # the definition has nothing to free there
+        h.pool.free(h.table, h.lengths)
+        torch.cuda.synchronize()
+        assert tg.tgemm_last_device_status() == CACHE_ERROR
+        assert as_list(h.d_uses) == h.pool.uses and as_list(h.d_lengths) == [bad, 0, 0, 0] and kept == 48
