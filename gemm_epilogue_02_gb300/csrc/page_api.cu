@@ -257,6 +257,12 @@ extern "C" tgemm_status tgemm_kv_select(const tgemm_kv_select_args *a, tgemm_str
 // ---------------------------------------------------------------- pages
 namespace {
 
+bool overlaps_any(const Extent &x, std::initializer_list<Extent> others) {
+    for (const Extent &o : others)
+        if (overlaps(x, o)) return true;
+    return false;
+}
+
 // What fork, grow and free share: the cache, the counts and the lists that change.
 tgemm_status check_pages(const tgemm_kv_cache *cache, int32_t *uses, int32_t *pages, int32_t *lengths, int64_t width, int64_t stride,
                          int64_t batch, PagesParams *p, Extent *lists) {
@@ -324,6 +330,8 @@ extern "C" tgemm_status tgemm_kv_grow(const tgemm_kv_grow_args *a, tgemm_stream_
     if (st != TGEMM_OK) return st;
     if (a->batch == 0) return TGEMM_OK;
     if (!aligned4(a->tokens)) return TGEMM_ERR_ALIGNMENT;
+    const Extent et = {a->tokens, a->tokens ? a->batch * 4 : 0}, eu = {a->uses, static_cast<int64_t>(a->cache->pages) * 4};
+    if (overlaps_any(et, {eu, lists, {a->lengths, a->batch * 4}})) return TGEMM_ERR_ALIAS;
     RuntimeInfo rt;
     st = runtime_current(&rt);
     if (st != TGEMM_OK) return st;
@@ -348,6 +356,14 @@ extern "C" tgemm_status tgemm_kv_fork(const tgemm_kv_fork_args *a, tgemm_stream_
     if (!a->parents) return TGEMM_ERR_INVALID_ARG;
     if (!aligned4(a->parents)) return TGEMM_ERR_ALIGNMENT;
     if (cache->pages > 0 && cache->k == cache->v) return TGEMM_ERR_ALIAS;
+    // What is read besides the parents' rows is apart from what is written; the children's lists and lengths may be rows of
+    // the parents' arrays.
+    const Extent ck = {cache->k, p.cache.dbg_bytes}, cv = {cache->v, p.cache.dbg_bytes}, eu = {a->uses, static_cast<int64_t>(cache->pages) * 4};
+    const Extent en = {a->to_lengths, a->children * 4}, er = {a->parents, a->children * 4}, el = {a->seq.lengths, a->seq.batch * 4};
+    const Extent ep = {a->seq.pages, a->seq.batch > 0 ? ((a->seq.batch - 1) * a->seq.pages_stride + a->seq.pages_width) * 4 : 0};
+    if (overlaps_any(er, {eu, en, lists}) || overlaps_any(eu, {ep, el}) || overlaps(lists, el) || overlaps(en, ep)) return TGEMM_ERR_ALIAS;
+    for (const Extent &x : {er, ep, el})
+        if (cache_overlaps(cache, ck, cv, x)) return TGEMM_ERR_ALIAS;
     RuntimeInfo rt;
     st = runtime_current(&rt);
     if (st != TGEMM_OK) return st;

@@ -196,6 +196,18 @@ def test_no_structures():
         tg.tgemm_kv_compact_workspace(-1)
 
 
+@pytest.mark.parametrize("f,kw", [
+    (kv_fork, dict(parents=AT["uses"] + 64)), (kv_fork, dict(parents=AT["to"])), (kv_fork, dict(parents=AT["ton"] + 16)),
+    (kv_fork, dict(parents=AT["v"])), (kv_fork, dict(uses=AT["table"] + 128)), (kv_fork, dict(uses=AT["lengths"] - 124)),
+    (kv_fork, dict(to=AT["lengths"] - 8)), (kv_fork, dict(ton=AT["table"] + 252)), (kv_fork, dict(table=AT["k"] + 256)),
+    (kv_fork, dict(lengths=AT["v"])), (kv_fork, dict(c=cache(e4m3=1), parents=AT["ks"])),
+    (kv_grow, dict(tokens=AT["uses"] + 124)), (kv_grow, dict(tokens=AT["lengths"])), (kv_grow, dict(tokens=AT["table"] + 60)),
+], ids=lambda x: x.__name__ if callable(x) else "-".join(x))
+def test_what_is_read_is_not_written(f, kw):
+    """Parents, their lists and lengths, and the numbers of new tokens, against what the call writes."""
+    assert f(**kw) == ALIAS
+
+
 # ---------------------------------------------------------------- the functions as compiled for the host
 @pytest.fixture(scope="module")
 def host(tmp_path_factory):
