@@ -61,6 +61,12 @@ tgemm_status check_lists(int32_t *pages, int32_t *lengths, int64_t width, int64_
     return TGEMM_OK;
 }
 
+bool overlaps_any(const Extent &x, std::initializer_list<Extent> others) {
+    for (const Extent &o : others)
+        if (overlaps(x, o)) return true;
+    return false;
+}
+
 bool cache_overlaps(const tgemm_kv_cache *c, const Extent &k, const Extent &v, const Extent &x) {
     if (overlaps(x, k) || overlaps(x, v)) return true;
     if (!c->e4m3 || c->pages == 0) return false;
@@ -186,6 +192,10 @@ extern "C" tgemm_status tgemm_kv_bounds(const tgemm_kv_bounds_args *a, tgemm_str
     if (a->seq.batch == 0 || a->seq.pages_width == 0) return TGEMM_OK;
     if (!aligned4(a->starts)) return TGEMM_ERR_ALIGNMENT;
     if (cache_overlaps(cache, ck, cv, eb) || cache_overlaps(cache, ck, cv, es) || overlaps(eb, es)) return TGEMM_ERR_ALIAS;
+    const Extent ep = {a->seq.pages, ((a->seq.batch - 1) * a->seq.pages_stride + a->seq.pages_width) * 4};
+    const Extent el = {a->seq.lengths, a->seq.batch * 4}, et = {a->starts, a->starts ? (a->seq.batch + 1) * 4 : 0};
+    for (const Extent &x : {eb, es})
+        if (overlaps_any(x, {ep, el, et})) return TGEMM_ERR_ALIAS;
     RuntimeInfo rt;
     st = runtime_current(&rt);
     if (st != TGEMM_OK) return st;
@@ -256,12 +266,6 @@ extern "C" tgemm_status tgemm_kv_select(const tgemm_kv_select_args *a, tgemm_str
 
 // ---------------------------------------------------------------- pages
 namespace {
-
-bool overlaps_any(const Extent &x, std::initializer_list<Extent> others) {
-    for (const Extent &o : others)
-        if (overlaps(x, o)) return true;
-    return false;
-}
 
 // What fork, grow and free share: the cache, the counts and the lists that change.
 tgemm_status check_pages(const tgemm_kv_cache *cache, int32_t *uses, int32_t *pages, int32_t *lengths, int64_t width, int64_t stride,
@@ -436,6 +440,7 @@ extern "C" tgemm_status tgemm_kv_compact(const tgemm_kv_compact_args *a, tgemm_s
     const Extent all[] = {eu, etu, ei, ew, ep, etp, el};
     for (const Extent &x : all)
         if (cache_overlaps(cache, ck, cv, x) || (a->bounds && (overlaps(x, eb) || overlaps(x, es)))) return TGEMM_ERR_ALIAS;
+    if (a->bounds && (cache_overlaps(cache, ck, cv, eb) || cache_overlaps(cache, ck, cv, es) || overlaps(eb, es))) return TGEMM_ERR_ALIAS;
     // The counts and the lists may be replaced in place; otherwise what is written is apart from all else.
     const bool same_uses = a->uses == a->to_uses, same_lists = a->to_pages == a->seq.pages && a->to_stride == a->seq.pages_stride;
     if ((cache->pages > 0 && cache->k == cache->v) || (!same_uses && overlaps(eu, etu)) || (!same_lists && overlaps(ep, etp)))

@@ -208,6 +208,17 @@ def test_what_is_read_is_not_written(f, kw):
     assert f(**kw) == ALIAS
 
 
+@pytest.mark.parametrize("f,kw", [
+    (kv_bounds, dict(table=AT["bounds"] + 64)), (kv_bounds, dict(lengths=AT["bscale"] + 8)), (kv_bounds, dict(starts=AT["bscale"])),
+    (kv_bounds, dict(starts=AT["bounds"] - 32)), (kv_bounds, dict(table=AT["bscale"] + 508)),
+    (kv_compact, dict(bounds=bounds(bounds=AT["k"]))), (kv_compact, dict(bounds=bounds(scale=AT["v"] + 256))),
+    (kv_compact, dict(bounds=bounds(scale=AT["bounds"] + 4))), (kv_compact, dict(c=cache(e4m3=1), bounds=bounds(scale=AT["ks"]))),
+], ids=lambda x: x.__name__ if callable(x) else "-".join(x))
+def test_bounds_lie_apart(f, kw):
+    """Bounds against the lists that say which are written, and against the rows that move."""
+    assert f(**kw) == ALIAS
+
+
 # ---------------------------------------------------------------- the functions as compiled for the host
 @pytest.fixture(scope="module")
 def host(tmp_path_factory):
