@@ -50,6 +50,20 @@ inline bool extent(const int64_t *size, const int64_t *stride, int dims, int64_t
     return true;
 }
 
+// Whether rows of `width` elements in two dimensions share memory, with strides that extent() has found apart for each
+// dimension alone.
+inline bool rows_meet(const int64_t (&size)[2], const int64_t (&stride)[2], int64_t width) {
+    if (size[0] < 2 || size[1] < 2) return false;
+    const int a = size[0] <= size[1] ? 0 : 1, b = 1 - a, outer = stride[0] >= stride[1] ? 0 : 1;
+    if (stride[outer] - (size[1 - outer] - 1) * stride[1 - outer] >= width) return false;     // all of one between two of the other
+    // `e` steps along a against the steps along b that come nearest.
+    for (int64_t e = 1; e < size[a]; ++e) {
+        const int64_t to = e * stride[a], d = to / stride[b], rest = to - d * stride[b];
+        if ((d > 0 && d < size[b] && rest < width) || (d + 1 < size[b] && stride[b] - rest < width)) return true;
+    }
+    return false;
+}
+
 // Checks a cache's description and fills the kernels' view of it.
 inline tgemm_status check_cache(const tgemm_kv_cache *c, KvView *view, Extent *k, Extent *v) {
     if (!c) return TGEMM_ERR_INVALID_ARG;

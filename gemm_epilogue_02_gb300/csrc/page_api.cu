@@ -242,7 +242,7 @@ extern "C" tgemm_status tgemm_kv_select(const tgemm_kv_select_args *a, tgemm_str
     for (const Extent &x : {et, en})
         if (cache_overlaps(cache, ck, cv, x) || overlaps(x, eb) || overlaps(x, es) || overlaps(x, el) || overlaps(x, ep) || overlaps(x, eq))
             return TGEMM_ERR_ALIAS;
-    if (overlaps(et, en)) return TGEMM_ERR_ALIAS;
+    if (overlaps(et, en) || rows_meet(tsize, tstride, keep)) return TGEMM_ERR_ALIAS;
     RuntimeInfo rt;
     st = runtime_current(&rt);
     if (st != TGEMM_OK) return st;

@@ -31,6 +31,7 @@ tgemm_status check_rows(const tgemm_rows &r, int64_t tokens, int64_t heads, int6
     const int64_t inner_size[1] = {heads}, inner_stride[1] = {r.head_stride};
     if (!extent(size, stride, 2, dim, 2, written, &out->bytes) || !extent(inner_size, inner_stride, 1, dim, 2, written, &out->inner))
         return TGEMM_ERR_INVALID_ARG;
+    if (written && rows_meet(size, stride, dim)) return TGEMM_ERR_ALIAS;
     if (out->bytes > 0) {
         if (!r.data) return TGEMM_ERR_INVALID_ARG;
         if (!aligned16(r.data) || (tokens > 1 && r.token_stride % 8 != 0) || (heads > 1 && r.head_stride % 8 != 0))

@@ -219,6 +219,13 @@ def test_bounds_lie_apart(f, kw):
     assert f(**kw) == ALIAS
 
 
+@pytest.mark.parametrize("tob,toh,code", [(8, 4, ALIAS), (15, 4, ALIAS), (4, 32, VALID), (4, 31, ALIAS), (12, 8, ALIAS), (9, 4, ALIAS), (32, 4, VALID)])
+def test_lists_that_are_written_lie_apart(tob, toh, code):
+    """Lists of 4 of 4 heads and 8 sequences."""
+    got = kv_select(tob=tob, toh=toh)
+    assert got == code if code == ALIAS else got in code and got == kv_select()
+
+
 # ---------------------------------------------------------------- the functions as compiled for the host
 @pytest.fixture(scope="module")
 def host(tmp_path_factory):

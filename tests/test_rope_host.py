@@ -192,3 +192,18 @@ def test_python_gradient_refusals(kw):
 def test_range_of_eps(eps, code):
     for call in (forward, backward):
         assert call(eps=eps) == code if code == INVALID else call(eps=eps) in code and call(eps=eps) == call()
+
+
+@pytest.mark.parametrize("tokens,heads,t,h,code", [
+    (100, 8, 512, 64, VALID), (100, 8, 504, 64, ALIAS), (100, 8, 64, 6400, VALID), (100, 8, 64, 6392, ALIAS), (100, 8, 64, 64, ALIAS),
+    (2, 2, 64, 64, ALIAS), (1, 8, 64, 64, VALID), (100, 1, 64, 64, VALID), (100, 2, 192, 128, VALID), (100, 8, 128, 192, ALIAS),
+    (3, 2, 128, 192, VALID), (100, 2, 128, 200, ALIAS),
+])
+def test_rows_that_are_written_lie_apart(tokens, heads, t, h, code):
+    """Steps of t elements from token to token and h from head to head, rows of 64."""
+    kw = dict(tokens=tokens, hq=heads, q_t=heads * DIM, qo_t=t, qo_h=h)
+    offsets = sorted(i * t + j * h for i in range(tokens) for j in range(heads))
+    assert any(b - a < DIM for a, b in zip(offsets, offsets[1:])) == (code == ALIAS)
+    for call, more in ((forward, {}), (backward, dict(gq_t=heads * DIM))):
+        got = call(**kw, **more)
+        assert got == code if code == ALIAS else got in code and got == call()
