@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, kThreads * kChunks > 512 ? 1 : 2) pa
         if (bad && rank == 0) record_status(p.status, kStatusCache);
     }
     // The queries in whole numbers, one head a warp at a time.
+    bool far = false;                                            // a power above 2^100
     for (int h = warp; h < heads8; h += kWarps) {
         constexpr int kPer = 2 * kChunks;                        // dims lane * kPer ..
         float x[kPer], top = 0.0f;
@@ -511,8 +512,9 @@ __global__ void __launch_bounds__(kThreads, kThreads * kChunks > 512 ? 1 : 2) pa
             s_bias[(2 * c + 1) * heads8 + h] = -kChooseBias * above;
         }
         if (lane == 0) s_scale[h] = s;
+        far |= s > 0x1p100f;
     }
-    __syncthreads();
+    far = __syncthreads_or(far);
     const int n = s_n;
     const ChooseSpan span = choose_span(n, p.cache.page_size, p.keep, p.first, p.recent);
     const int *const list = p.table.pages + b * p.table.stride;
@@ -525,6 +527,14 @@ __global__ void __launch_bounds__(kThreads, kThreads * kChunks > 512 ? 1 : 2) pa
     const int lo = span.first + min(span.middle, rank * slice), size = some ? min(span.middle, (rank + 1) * slice) - (lo - span.first) : 0;
     // The slice's page numbers wait where its keys go: each is read before its key is written.
     for (int i = threadIdx.x; i < size; i += kThreads) keys[i] = static_cast<uint32_t>(list[lo + i]);
+    // The queries' powers at most 2^100, by a factor that all scores share: a sum times its query's power stays in fp32's
+    // range, and the page's power takes it out of there only with the score itself.
+    if (far && warp == 0) {
+        float top = 0.0f;
+        for (int h = lane; h < p.group; h += 32) top = fmaxf(top, s_scale[h]);
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+        for (int h = lane; h < p.group; h += 32) s_scale[h] *= 0x1p100f / top;
+    }
     // What stays whatever its score, and -1 past the pages kept.
     for (int i = rank * kThreads + threadIdx.x; i < p.keep; i += blocks * kThreads) {
         if (i >= span.keep) to[i] = -1;
@@ -636,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, kThreads * kChunks > 512 ? 1 : 2) pa
                 const float s = s_scale[h];
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    if (h < p.group) best[r] = fmaxf(best[r], acc[0][2 * r + i] * scale[r] * s);
+                    if (h < p.group) best[r] = fmaxf(best[r], acc[0][2 * r + i] * s * scale[r]);
             }
         }
 #pragma unroll

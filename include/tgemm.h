@@ -498,7 +498,7 @@ tgemm_status tgemm_kv_bounds(const tgemm_kv_bounds_args *args, tgemm_stream_t st
  * above (rounded to nearest even), a page's score is the largest over the head's
  * group of
  *     t s sum_d max(z_d lo_d, z_d hi_d)   (z_d lo_d for z_d < 0, z_d hi_d for z_d > 0)
- * in fp32, which is exact while it stays in fp32's range.  Written, for
+ * in fp32, which is exact from 2^-104 to the end of fp32's range.  Written, for
  * tgemm_attention_decode_lists:
  *   to_pages    int32 [batch, heads, keep]: page numbers in order of position, -1 past them
  *   to_lengths  int32 [batch]: positions on them

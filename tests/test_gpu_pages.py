@@ -784,3 +784,25 @@ def test_free_leaves_bad_lengths_out(cuda_lib):
         torch.cuda.synchronize()
         assert tg.tgemm_last_device_status() == CACHE_ERROR
         assert as_list(h.d_uses) == h.pool.uses and as_list(h.d_lengths) == [bad, 0, 0, 0] and kept == 48
+
+
+def test_scores_whose_factors_pass_fp32(cuda_lib):
+    """The sum times one power of two passes fp32's range, the score itself does not: the best pages all the same."""
+    f = Filled(tg, [160], 2, 128, 16, "bf16", seed=43)
+    f.k.copy_(torch.where(f.k > 0, 1.0, -1.0) * 2.0 ** 120)      # s = 2^114: a sum of 2^14 and more does not fit beside it
+    for i in range(10):
+        f.k[int(f.table_host[0, i])] *= 1 + i / 16
+    q = (torch.full((1, 4, 128), 2.0 ** -60, device="cuda")).bfloat16()
+    to_table, _, _ = select(f, q, 4, 0, 1)
+    lists, _ = selection(f, q, 4, 0, 1)
+    assert lists[0][0] == [6, 7, 8, 9]
+    assert as_list(to_table) == [[[int(f.table_host[0, i]) for i in lists[0][h]] for h in range(2)]]
+    # The other way round: a query at the end of the range, its group's others far below, and pages of 0 in between.
+    f.k.zero_()
+    f.k[int(f.table_host[0, 2])], f.k[int(f.table_host[0, 5])], f.k[int(f.table_host[0, 7])] = 2.0 ** -20, 2.0 ** -21, -2.0 ** -21
+    q = torch.full((1, 4, 128), 2.0 ** -70, device="cuda").bfloat16()
+    q[0, 1], q[0, 2] = 3e38, -3e38                               # of the two key heads
+    to_table, _, _ = select(f, q, 4, 0, 1)
+    lists, _ = selection(f, q, 4, 0, 1)
+    assert [sorted(x) for x in lists[0]] == [[0, 2, 5, 9], [2, 5, 7, 9]]        # (the least query decides where the largest is against)
+    assert as_list(to_table) == [[[int(f.table_host[0, i]) for i in lists[0][h]] for h in range(2)]]
