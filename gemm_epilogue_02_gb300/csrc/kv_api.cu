@@ -44,9 +44,9 @@ cudaError_t launch_append(const RuntimeInfo &rt, const AppendParams &p, cudaStre
     }
 }
 
-template <int kThreads>
+template <int kThreads, bool kAlone>
 cudaError_t launch_select_threads(const RuntimeInfo &rt, EvictParams &p, int64_t positions, int cluster, cudaStream_t s) {
-    auto kernel = kv_select_kernel<kThreads>;
+    auto kernel = kv_select_kernel<kThreads, kAlone>;
     const int64_t slice = (positions + cluster - 1) / cluster;
     p.cached = slice <= kSelectMaxCached ? static_cast<int>(slice) : 0;
     static std::atomic<uint64_t> ready{0};      // bit per device
@@ -64,10 +64,10 @@ cudaError_t launch_select_threads(const RuntimeInfo &rt, EvictParams &p, int64_t
 // positions: what a sequence can have at most.  Up to 4096 one block of 256
 // threads takes them; beyond, blocks of 1024 take 8192 each, up to eight blocks.
 cudaError_t launch_select(const RuntimeInfo &rt, EvictParams &p, int64_t positions, cudaStream_t s) {
-    if (positions <= 4096) return launch_select_threads<256>(rt, p, positions, 1, s);
+    if (positions <= 4096) return launch_select_threads<256, true>(rt, p, positions, 1, s);
     int cluster = 1;
     while (cluster < 8 && cluster * 8192 < positions) cluster *= 2;
-    return launch_select_threads<1024>(rt, p, positions, cluster, s);
+    return cluster == 1 ? launch_select_threads<1024, true>(rt, p, positions, 1, s) : launch_select_threads<1024, false>(rt, p, positions, cluster, s);
 }
 
 template <bool kE4m3, int kLanes>

@@ -33,15 +33,15 @@ struct EvictParams {
     unsigned int *status;
 };
 
-// Grid: (cluster size, heads, batch), a cluster along x.
-template <int kThreads>
+// Grid: (cluster size, heads, batch), a cluster along x.  kAlone: of one block.
+template <int kThreads, bool kAlone>
 __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParams p) {
     extern __shared__ uint32_t keys[];
     __shared__ RankShared<kThreads> sh;
     __shared__ int s_n;
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
-    const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int blocks = kAlone ? 1 : static_cast<int>(cluster.num_blocks()), rank = kAlone ? 0 : static_cast<int>(cluster.block_rank());
     const int head = blockIdx.y, b = blockIdx.z;
     kv_rank_clear(sh);
     griddep_wait();
@@ -85,12 +85,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const EvictParam
                 kept[j] = j;
                 to_w[j] = w[j];
             }
-        if (blocks == 1) return;
+        if (kAlone) return;
         // The blocks of a cluster go on together to every barrier, whatever length each of them has read.
     }
     __syncthreads();                             // the keys are there
 
-    kv_rank(
+    kv_rank<kAlone ? RankBy::kBlock : RankBy::kCluster>(
         sh, size, best, p.status, key_at,
         [&](int at, int i) {
             kept[at] = lo + i;

@@ -55,13 +55,17 @@ __device__ __forceinline__ void kv_rank_clear(RankShared<kThreads> &sh) {
 // This block has `size` keys, key_at(0) .. key_at(size - 1); put(at, i) is called for each of its keys i that is among the
 // `best`, at = 0 .. best - 1 its place among them.  Called by all threads of all blocks of a cluster (whatever their sizes),
 // after a barrier that follows kv_rank_clear().
-// kAlone: by one block, whether it has a cluster or not.
-template <bool kAlone = false, int kThreads, typename KeyAt, typename Put>
+// kBy: by what the launch decides, by one block (whether it has a cluster or not), or by a cluster of two or more.
+enum class RankBy { kLaunch, kBlock, kCluster };
+
+template <RankBy kBy = RankBy::kLaunch, int kThreads, typename KeyAt, typename Put>
 __device__ __forceinline__ void kv_rank(RankShared<kThreads> &sh, int size, int best, unsigned int *status, KeyAt key_at, Put put) {
     constexpr int kWarps = kThreads / 32;
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
-    const int blocks = kAlone ? 1 : static_cast<int>(cluster.num_blocks()), rank = kAlone ? 0 : static_cast<int>(cluster.block_rank());
+    const int blocks = kBy == RankBy::kBlock ? 1 : static_cast<int>(cluster.num_blocks());
+    const int rank = kBy == RankBy::kBlock ? 0 : static_cast<int>(cluster.block_rank());
+    const bool alone = kBy != RankBy::kCluster && blocks == 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t prefix = 0, counted = ~0u;          // the limit, and its bits that count
     int need = best;                             // rank of the limit among the keys with this prefix
@@ -75,7 +79,7 @@ __device__ __forceinline__ void kv_rank(RankShared<kThreads> &sh, int size, int 
             if ((key & mask) == prefix) atomicAdd(&sh.hist[pass][(key >> shift) & digit_mask], 1);
         }
         __syncthreads();
-        if (blocks == 1) {
+        if (alone) {
             // Thread t has the bins from kSelectBins - 1 - t * kPer down; the one in which the running sum from the
             // top reaches `need` has the limit's digit.  (The last pass leaves the upper bins empty.)
             constexpr int kPer = kSelectBins / kThreads;
@@ -143,7 +147,7 @@ __device__ __forceinline__ void kv_rank(RankShared<kThreads> &sh, int size, int 
         prefix |= static_cast<uint32_t>(sh.digit) << shift;
         need = sh.need;
         // All keys that share these bits stay: the others do not matter.  (Only where no other block waits.)
-        if (blocks == 1 && need == sh.count) {
+        if (alone && need == sh.count) {
             counted = ~0u << shift;
             break;
         }
@@ -170,7 +174,7 @@ __device__ __forceinline__ void kv_rank(RankShared<kThreads> &sh, int size, int 
     const int a = lane < kWarps ? sh.warp_sums[0][lane] : 0, e = lane < kWarps ? sh.warp_sums[1][lane] : 0;
     int at_larger = __reduce_add_sync(0xffffffffu, lane < warp ? a : 0);
     int at_equal = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0);
-    if (blocks > 1) {
+    if (!alone) {
         if (warp == 0) {
             const int x = __reduce_add_sync(0xffffffffu, a), y = __reduce_add_sync(0xffffffffu, e);
             if (lane == 0) {

@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, kThreads * kChunks > 512 ? 1 : 2) pa
         if (rank > 0) return;
         kv_rank_clear(sh);                       // in the ring's place
         __syncthreads();
-        kv_rank<true>(
+        kv_rank<RankBy::kBlock>(
             sh, some ? min(span.middle, p.cached) : 0, span.best, p.status, [&](int i) { return keys[i]; },
             [&](int at, int i) { to[span.first + at] = list[span.first + i]; });
         return;
