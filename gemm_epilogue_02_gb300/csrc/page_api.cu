@@ -287,15 +287,23 @@ tgemm_status check_pages(const tgemm_kv_cache *cache, int32_t *uses, int32_t *pa
     return TGEMM_OK;
 }
 
-// Bytes of the children's last pages up to which a cluster does all: beyond, two launches fill the GPU.
-constexpr int64_t kForkFew = 1 << 20;
-// The same for compaction: bytes of a pool (half of them move at most), and sequences.
-constexpr int64_t kCompactFew = 4 << 20, kCompactLists = 64;
+// Where there is little to do, a cluster does all in one launch, which saves 2 us of the host's time; beyond, two launches
+// fill the GPU.  Both sides below as called among others, and on the GPU alone.
+//
+// Fork: one child for each of the cluster's blocks, lists of up to 1024 pages, 1 MB of the children's last pages.  With
+// freeing, pages of 32 KB: 8 children, lists of 32 pages 10.6 us (two launches 12.4; on the GPU 8.0, 7.7), of 512 10.5
+// (12.4; 8.9, 9.4), of 2048 13.2 (13.1; 12.8, 12.1); 32 children 12.6 (12.3; 11.9, 8.1), 128 of 2 KB 29 (8 on the GPU).
+constexpr int64_t kForkFew = 1 << 20, kForkChildren = kForkBlocks, kForkList = 1024;
+// Compaction: pools of up to 160 pages and 4 MB (half of them move at most), 8 sequences.  Pages of 16 KB: a pool of 29 6.6 us
+// (two launches 8.4; on the GPU 5.0, 4.9), of 138 7.4 (8.5; 7.3, 4.9), of 413 15 (8.4; 15, 5.6); 16 sequences on 106 pages
+// 7.3 to 8.6 (8.5), 64 10.7 (8.4).
+constexpr int64_t kCompactFew = 4 << 20, kCompactPages = 160, kCompactLists = 8;
 
 template <int kLanes>
 cudaError_t launch_fork_lanes(const RuntimeInfo &rt, const PagesParams &p, cudaStream_t s) {
     const int64_t page_bytes = static_cast<int64_t>(p.cache.page_size) * p.cache.heads * p.cache.row_bytes * 2;
-    if (p.to.batch * page_bytes <= kForkFew) return launch(page_fork_few_kernel<kLanes>, dim3(kForkBlocks), kTakeThreads, 0, s, p, kForkBlocks);
+    if (p.to.batch <= kForkChildren && p.table.width <= kForkList && p.to.batch * page_bytes <= kForkFew)
+        return launch(page_fork_few_kernel<kLanes>, dim3(kForkBlocks), kTakeThreads, 0, s, p, kForkBlocks);
     const cudaError_t e = launch(page_take_kernel<true>, dim3(1), kTakeThreads, 0, s, p);
     if (e != cudaSuccess) return e;
     constexpr int kRows = kPageThreads / kLanes * 4;
@@ -309,7 +317,7 @@ cudaError_t launch_fork_lanes(const RuntimeInfo &rt, const PagesParams &p, cudaS
 template <int kLanes>
 cudaError_t launch_move_lanes(const RuntimeInfo &rt, const CompactParams &p, cudaStream_t s) {
     const int64_t page_bytes = static_cast<int64_t>(p.cache.page_size) * p.cache.heads * p.cache.row_bytes * 2;
-    if (p.cache.pages * page_bytes <= kCompactFew && p.table.batch <= kCompactLists)
+    if (p.cache.pages <= kCompactPages && p.cache.pages * page_bytes <= kCompactFew && p.table.batch <= kCompactLists)
         return launch(page_compact_few_kernel<kLanes>, dim3(kForkBlocks), kTakeThreads, 0, s, p, kForkBlocks);
     const cudaError_t e = p.cache.pages <= kTakeThreads ? launch(page_plan_kernel<1>, dim3(1), kTakeThreads, 0, s, p)
                                                         : launch(page_plan_kernel<kTakeDeep>, dim3(1), kTakeThreads, 0, s, p);

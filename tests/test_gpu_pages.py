@@ -806,3 +806,37 @@ def test_scores_whose_factors_pass_fp32(cuda_lib):
     lists, _ = selection(f, q, 4, 0, 1)
     assert [sorted(x) for x in lists[0]] == [[0, 2, 5, 9], [2, 5, 7, 9]]        # (the least query decides where the largest is against)
     assert as_list(to_table) == [[[int(f.table_host[0, i]) for i in lists[0][h]] for h in range(2)]]
+
+
+@pytest.mark.parametrize("children,list_pages", [(8, 5), (9, 5), (3, 1024), (3, 1025), (8, 1022), (33, 40), (1, 1400)])
+def test_forks_in_one_launch_and_in_two(cuda_lib, children, list_pages):
+    """Few children and short lists, and more than a cluster takes: the same pages, counts and rows."""
+    h = Held([(list_pages - 1) * 4 - 3, 4 * 4 + 1], 4, list_pages + 100, heads=1, seed=44, width=list_pages)
+    parents = [c % 2 for c in range(children)]
+    to, to_lengths = torch.full((children, list_pages), -9, dtype=torch.int32, device="cuda"), int32([0] * children)
+    want = h.images()
+    tg.kv_fork(h.cache, h.d_uses, h.d_table, h.d_lengths, int32(parents), to, to_lengths)
+    to_host, n_host = [[-9] * list_pages for _ in range(children)], [0] * children
+    for a, z, rows in h.pool.fork(h.table, h.lengths, parents, to_host, n_host):
+        for t in want:
+            t[z, :rows] = t[a, :rows]
+    h.check()
+    assert as_list(to) == to_host and as_list(to_lengths) == n_host
+    assert all(torch.equal(a, b) for a, b in zip(h.images(), want))
+    assert tg.tgemm_last_device_status() == 0
+
+
+@pytest.mark.parametrize("sequences,pages", [(8, 160), (8, 161), (9, 160), (1, 160), (30, 1024), (2, 1025)])
+def test_compactions_in_one_launch_and_in_two(cuda_lib, sequences, pages):
+    h = Held([(pages // 2 // sequences) * 4 - b % 4 for b in range(sequences)], 4, pages, heads=1, seed=45)
+    want = h.images()
+    to, to_uses, in_use = torch.full_like(h.d_table, -9), torch.full_like(h.d_uses, 77), int32([0])
+    tg.kv_compact(h.cache, h.d_uses, h.d_table, h.d_lengths, to, to_uses, in_use)
+    moves, n = h.pool.compact(h.table, h.lengths)
+    for a, z in moves.items():
+        for t in want:
+            t[z] = t[a]
+    h.check(table=to, uses=to_uses)
+    assert as_list(in_use) == [n] and moves
+    assert all(torch.equal(a, b) for a, b in zip(h.images(), want))
+    assert tg.tgemm_last_device_status() == 0
