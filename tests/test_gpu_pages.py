@@ -840,3 +840,123 @@ def test_compactions_in_one_launch_and_in_two(cuda_lib, sequences, pages):
     assert as_list(in_use) == [n] and moves
     assert all(torch.equal(a, b) for a, b in zip(h.images(), want))
     assert tg.tgemm_last_device_status() == 0
+
+
+WIDE_FORKS = [
+    # lengths, children, heads, dim, page, cache, layout: rows of all widths, more than a megabyte of last pages, more children
+    # than a block has threads
+    ([37, 50], 5, 2, 128, 16, "16", "pshd"), ([37, 50], 12, 3, 80, 16, "16", "phsd"), ([20, 31], 4, 1, 256, 24, "16", "pshd"),
+    ([37, 90], 6, 2, 256, 16, "e4m3", "phsd"), ([37, 90], 20, 2, 160, 16, "e4m3", "pshd"), ([100, 63, 130], 128, 8, 128, 64, "16", "pshd"),
+    ([100, 63, 130], 128, 8, 128, 64, "16", "phsd"), ([300, 200], 30, 8, 256, 128, "e4m3", "pshd"), ([61, 127], 40, 4, 112, 64, "16", "phsd"),
+    ([70, 33], 40, 4, 256, 32, "16", "phsd"), ([9, 3, 0, 8], 1200, 1, 64, 4, "16", "pshd"), ([2000], 1030, 2, 96, 8, "16", "phsd"),
+]
+
+
+@pytest.mark.parametrize("case", WIDE_FORKS, ids=lambda c: "-".join(map(str, c[1:])))
+def test_fork_of_all_rows(cuda_lib, case):
+    lengths, children, heads, dim, page, kind, layout = case
+    h = Held(lengths, page, sum(-(-n // page) for n in lengths) + children + 9, heads=heads, dim=dim, kind=kind, layout=layout, seed=50)
+    parents = [(7 * c) % (len(lengths) + 1) - 1 for c in range(children)]
+    to, to_lengths = torch.full((children, h.width), -9, dtype=torch.int32, device="cuda"), int32([0] * children)
+    want = h.images()
+    tg.kv_fork(h.cache, h.d_uses, h.d_table, h.d_lengths, int32(parents), to, to_lengths)
+    to_host, n_host = [[-9] * h.width for _ in range(children)], [0] * children
+    for a, z, rows in h.pool.fork(h.table, h.lengths, parents, to_host, n_host):
+        for t in want:
+            t[z, :rows] = t[a, :rows]
+    h.check()
+    assert as_list(to) == to_host and as_list(to_lengths) == n_host
+    assert all(torch.equal(a, b) for a, b in zip(h.images(), want))
+    tg.kv_free(h.cache, h.d_uses, to, to_lengths)
+    h.pool.free(to_host, n_host)
+    h.check()
+    assert tg.tgemm_last_device_status() == 0
+
+
+WIDE_COMPACTS = [
+    # lengths, heads, dim, page, pages, cache, layout
+    ([100, 300], 2, 128, 16, 60, "16", "pshd"), ([100, 300], 3, 80, 16, 60, "16", "phsd"), ([100, 30], 1, 256, 24, 20, "16", "phsd"),
+    ([100, 30], 2, 256, 16, 20, "e4m3", "pshd"), ([1000, 700], 8, 128, 64, 60, "16", "phsd"), ([900, 2000], 4, 112, 32, 300, "16", "pshd"),
+    ([900, 2000], 4, 256, 32, 300, "e4m3", "phsd"), ([3000] * 10, 2, 128, 16, 3000, "16", "pshd"), ([500] * 70, 1, 64, 64, 700, "16", "pshd"),
+    ([3000, 5], 2, 256, 16, 1024, "16", "pshd"),
+]
+
+
+@pytest.mark.parametrize("case", WIDE_COMPACTS, ids=lambda c: f"{len(c[0])}-" + "-".join(map(str, c[1:])))
+def test_compaction_of_all_rows(cuda_lib, case):
+    lengths, heads, dim, page, pages, kind, layout = case
+    h = Held(lengths, page, pages, heads=heads, dim=dim, kind=kind, layout=layout, seed=51)
+    bounds = tg.PageBounds(torch.randint(-127, 128, (pages, heads, 2, dim), dtype=torch.int8, generator=h.g).cuda(),
+                           torch.rand(pages, heads, generator=h.g).cuda())
+    want = h.images() + [bounds.bounds.cpu(), bounds.scale.cpu()]
+    to, to_uses, in_use = torch.full_like(h.d_table, -9), torch.full_like(h.d_uses, 77), int32([0])
+    tg.kv_compact(h.cache, h.d_uses, h.d_table, h.d_lengths, to, to_uses, in_use, bounds=bounds)
+    moves, n = h.pool.compact(h.table, h.lengths)
+    for a, z in moves.items():
+        for t in want:
+            t[z] = t[a]
+    h.check(table=to, uses=to_uses)
+    assert as_list(in_use) == [n] and moves
+    assert all(torch.equal(a, b) for a, b in zip(h.images() + [bounds.bounds.cpu(), bounds.scale.cpu()], want))
+    assert tg.tgemm_last_device_status() == 0
+
+
+@pytest.mark.parametrize("aside", [False, True])
+def test_serving_steps_queued(cuda_lib, aside):
+    """Steps of all calls, queued one after another with nothing that waits between them; what each has chosen and attended
+    to against what was appended until then."""
+    heads, group, dim, page, keep, slots, steps, pages = 2, 2, 64, 8, 5, 3, 25, 60
+    g = torch.Generator().manual_seed(60)
+    cache = tg.PagedCache(*(torch.zeros(pages, page, heads, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+    bounds = tg.PageBounds(torch.zeros(pages, heads, 2, dim, dtype=torch.int8, device="cuda"), torch.ones(pages, heads, device="cuda"))
+    uses, table = torch.zeros(pages, dtype=torch.int32, device="cuda"), torch.zeros(slots, 12, dtype=torch.int32, device="cuda")
+    lengths = torch.zeros(slots, dtype=torch.int32, device="cuda")
+    rotary = tg.Rotary([100.0 ** (-i / 32) for i in range(32)])
+    w = [(1 + 0.1 * torch.randn(dim, generator=g)).bfloat16().cuda() for _ in range(2)]
+    prompts = [50, 9, 23]
+    starts, counts = int32([0, 50, 59, 82]), int32(prompts)
+    positions = int32([i for n in prompts for i in range(n)])
+
+    def rows(n):
+        return [(torch.randn(n, m, dim, generator=g) * s).bfloat16().cuda() for m, s in ((heads * group, 2), (heads, 1), (heads, 1))]
+
+    inputs = [rows(sum(prompts))] + [rows(slots) for _ in range(steps)]
+    chosen = [torch.zeros(slots, heads, keep, dtype=torch.int32, device="cuda") for _ in range(steps)]
+    counted = [torch.zeros(slots, dtype=torch.int32, device="cuda") for _ in range(steps)]
+    out = [torch.full((slots, heads * group, dim), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(steps)]
+    ws = tg.attention_decode_workspace(out[0], cache, chosen[0])
+    stream = torch.cuda.Stream() if aside else None
+    torch.cuda.synchronize()
+    for i, (q, k, v) in enumerate(inputs):
+        tg.kv_grow(cache, uses, table, lengths, tokens=None if i else counts, stream=stream)
+        tg.qk_norm_rope(q, k, lengths if i else positions, rotary, q, k, q_weight=w[0], k_weight=w[1], shift=-1 if i else 0, stream=stream)
+        tg.kv_append(cache, k, v, table, lengths, starts=None if i else starts, stream=stream)
+        tg.kv_bounds(cache, bounds, table, lengths, starts=None if i else starts, stream=stream)
+        if i:
+            tg.kv_select(q, cache, bounds, table, lengths, chosen[i - 1], counted[i - 1], first=1, recent=2, stream=stream)
+            tg.attention_decode(q, cache, chosen[i - 1], counted[i - 1], out[i - 1], workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    assert tg.tgemm_last_device_status() == 0
+    lists = as_list(table)
+    ends = [sum(prompts[:b + 1]) for b in range(slots)]
+    kept = [[[t[b] if i else t[ends[b] - prompts[b]:ends[b]] for i, (_, *kv) in enumerate(inputs) for t in [kv[j]]] for j in range(2)]
+            for b in range(slots)]
+    for i in range(steps):
+        q = inputs[i + 1][0]
+        for b in range(slots):
+            n = prompts[b] + i + 1
+            k, v = (torch.cat([kept[b][j][0]] + [x.unsqueeze(0) for x in kept[b][j][1:i + 2]]).double().cpu() for j in range(2))
+            assert k.shape[0] == n
+            for h in range(heads):
+                queries = q[b, h * group:(h + 1) * group].double().cpu()
+                scores = [page_score(queries.numpy(), *page_bounds(k[p * page:(p + 1) * page, h].numpy())) if (p + 1) * page <= n else 0.0
+                          for p in range(-(-n // page))]
+                want = choose(scores, keep, 1, 2)
+                assert as_list(chosen[i])[b][h] == [lists[b][p] for p in want] + [-1] * (keep - len(want))
+                at = [p * page + s for p in want for s in range(page) if p * page + s < n]
+                assert int(counted[i][b]) == len(at)
+                p = torch.softmax(k[at, h] @ queries.T * dim ** -0.5, 0)
+                o = p.T @ v[at, h]
+                # bf16's half step of the output; weights off by 2^-16, their exponents by less than 2^-14
+                off = (out[i][b, h * group:(h + 1) * group].double().cpu() - o).abs()
+                assert off.max() <= 2.0 ** -8 * o.abs().max() + 2.0 ** -12 * v.abs().max()
