@@ -6,10 +6,11 @@
 // two makes every step exact: what the bounds are does not depend on how they
 // were computed.
 //
-// page_choose_kernel bounds the product of a query with any key of a page: q in
-// whole numbers of a power of two found in the same way, sum_d max(q_d lo_d, q_d
-// hi_d), times both powers; a page's score is the largest over the group's
-// heads.  The sum is that of q+ hi + q- lo (q+ = max(q, 0), q- = min(q, 0)), two
+// page_choose_kernel: with q the query in whole numbers, to nearest, of a power of
+// two found in the same way (8 bits of its largest element), sum_d max(q_d lo_d,
+// q_d hi_d) times both powers; a page's score is the largest over the group's
+// heads.  It bounds the product of any key of the page with the rounded query, the
+// query's own to within its rounding.  The sum is that of q+ hi + q- lo (q+ = max(q, 0), q- = min(q, 0)), two
 // products with pages as rows and heads as columns.  The whole numbers are widened
 // to fp16 for them (m16n8k16 takes 2.1 cycles of an SM, m16n8k32 of 8-bit whole
 // numbers 16.3) with 1152 added, which the accumulators of 64 dims each begin
@@ -384,7 +385,6 @@ struct ChooseParams {
     unsigned int *status;
 };
 
-constexpr int kChooseMaxCached = 32 * 1024;        // keys of a block's slice (128 KiB)
 constexpr int kChooseGroup = 64;                  // query heads of a key head, at most
 
 // Bytes of shared memory: keys, then the queries' two halves (fp16) with their scales.  Rows lie 16 bytes more than a

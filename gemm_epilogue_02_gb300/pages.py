@@ -68,7 +68,7 @@ def kv_select(Q: torch.Tensor, cache: PagedCache, bounds: PageBounds, page_table
     """Choose the pages that matter to each key head's queries: of a sequence's
     pages at most keep = to_page_table.shape[2] stay, the first `first`, the last
     `recent` and those between them whose bounds allow the largest product with
-    one of the head's queries.  Q is [batch, q_heads, dim].  Written are
+    one of the head's queries, as rounded to 8 bits of its largest element.  Q is [batch, q_heads, dim].  Written are
     to_page_table (int32 [batch, heads, keep], in order of position, -1 past them)
     and to_lengths (int32 [batch], the positions on them), for attention_decode()."""
     index = cache._index
