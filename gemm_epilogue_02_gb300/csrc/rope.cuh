@@ -28,6 +28,7 @@
 #include <cuda_fp16.h>
 
 #include "debug_checks.cuh"
+#include "fp32x2.cuh"
 #include "ptx.cuh"
 
 namespace tgemm {
@@ -203,24 +204,6 @@ __device__ __forceinline__ void rope_weights(const RopeWeights<V, kLanes> &from,
         a[2 * k] = make_float2(x.x, x.y), a[2 * k + 1] = make_float2(x.z, x.w);
         b[2 * k] = make_float2(y.x, y.y), b[2 * k + 1] = make_float2(y.z, y.w);
     }
-}
-
-// Two fp32 operations at once.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
 }
 
 template <int N>
