@@ -122,7 +122,7 @@ cudaError_t launch_choose_stages(const RuntimeInfo &rt, ChooseParams &p, int clu
 
 template <int kThreads, bool kBf16, int kChunks>
 cudaError_t launch_choose_shape(const RuntimeInfo &rt, ChooseParams &p, cudaStream_t s) {
-    // A cluster's barriers cost about 3 us, and a block scores 256 pages a microsecond where it has twice the warps: with lists
+    // A cluster's barriers cost about 3 us, and a block of 16 warps scores about 250 pages a microsecond where few run: with lists
     // of up to 512 pages a block alone is best, beyond them as many of a cluster as leave each an SM (1251 pages, 8 heads: one
     // 16.1 us, two 14.1, four 11.6, eight 10.8 before the first block ranked alone, 8.2 since; 251 pages: one 6.0, two 9.2; 128
     // lists of 2048: one 24, two 37).

@@ -158,8 +158,9 @@ __device__ __forceinline__ void bounds_scatter(T (&x)[N], int row, Min least) {
 // item of its own and goes through its rows one by one, so that what an item costs
 // besides its rows is shared by the groups; otherwise the groups share an item's
 // rows, which a long page wants that comes alone.  Neighbouring groups and warps
-// have neighbouring heads of a page.  With 16 bits the reading bounds it; widening
-// and scaling e4m3 costs more than that.
+// have neighbouring heads of a page.  With 16 bits the reading bounds it; with e4m3
+// a warp requests its rows, waits, and widens and scales them while none are on
+// their way (issue slots 62 % busy, DRAM 46 %).
 template <bool kBf16, bool kE4m3, int kLanes, int kUnroll, bool kAlone>
 __global__ void __launch_bounds__(kBoundsThreads, kE4m3 ? (kUnroll > 4 ? 2 : 3) : 4) page_bounds_kernel(const BoundsParams p) {
     constexpr int kWarps = kBoundsThreads / 32, kGroups = 32 / kLanes, kPer = kE4m3 ? 16 : 8;

@@ -18,7 +18,7 @@
 // once (400 MB moved within a pool of 1.6 GB: 134 us, 6.0 TB/s of both).  Where
 // there is little to copy, a launch costs more than it: a cluster of eight blocks
 // then plans and copies in one (8 children of two prompts, with freeing and growing:
-// 16 us as called, with a launch more 18.5; a pool of 140 pages compacted: 8.1, 9.5).
+// 15.5 us as called, with a launch more 18; a pool of 140 pages compacted: 7.9, 9.7).
 #pragma once
 #include "page_bounds.cuh"
 #include "kv_cache.cuh"

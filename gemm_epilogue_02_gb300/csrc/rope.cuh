@@ -9,6 +9,8 @@
 //
 //     dw = sum over rows of g x r,   dx = r (g w - x r^2 mean(g w x)).
 //
+// Elements past the pairs are passed through.
+//
 // Reading and writing each row once bounds it.  Angles: a frequency is given in
 // turns as a 64-bit fraction, so that position * frequency, which wraps at whole
 // turns by itself, keeps 2^-31 of a turn at any 32-bit position; the upper 32
@@ -21,7 +23,7 @@
 // query and 8 key heads, 128 wide (504 MB): 85 us, 5.9 TB/s; with two passes ahead
 // instead of three 87, with rows that move through registers 99, a token a warp and
 // its angles worked out by every lane 112.  The gradient of 16384 tokens (503 MB)
-// 90 us: one block of 12 warps an SM, two passes ahead (four blocks of 4 warps and
+// 91 us: one block of 12 warps an SM, two passes ahead (four blocks of 4 warps and
 // one pass 96; without a pass ahead 236, its registers leaving 8 warps).
 #pragma once
 #include <cuda_bf16.h>

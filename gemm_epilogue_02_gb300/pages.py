@@ -123,7 +123,8 @@ def kv_fork(cache: PagedCache, uses: torch.Tensor, page_table: torch.Tensor, len
 
 
 def kv_free(cache: PagedCache, uses: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor, stream=None) -> None:
-    """The sequences give their pages back: uses goes down by one on each, lengths become 0."""
+    """The sequences give their pages back: uses goes down by one on each, lengths
+    become 0 (a length that its list cannot hold stays, as does what it counts)."""
     index = cache._index
     pages, width, stride, batch = _table(page_table, index)
     length = _vector("lengths", lengths, batch, index)
