@@ -10,12 +10,13 @@
 // two found in the same way (8 bits of its largest element), sum_d max(q_d lo_d,
 // q_d hi_d) times both powers; a page's score is the largest over the group's
 // heads.  It bounds the product of any key of the page with the rounded query, the
-// query's own to within its rounding.  The sum is that of q+ hi + q- lo (q+ = max(q, 0), q- = min(q, 0)), two
-// products with pages as rows and heads as columns.  The whole numbers are widened
-// to fp16 for them (m16n8k16 takes 2.1 cycles of an SM, m16n8k32 of 8-bit whole
-// numbers 16.3) with 1152 added, which the accumulators of 64 dims each begin
-// without: what they hold stays below 2^24, so every sum is exact in fp32 in any
-// order, and the same pages are chosen however the work is split.
+// query's own to within its rounding.  The sum is that of q+ hi + q- lo (q+ =
+// max(q, 0), q- = min(q, 0)), two products with pages as rows and heads as columns.
+// The whole numbers are widened to fp16 for them (m16n8k16 takes 2.1 cycles of an
+// SM, m16n8k32 of 8-bit whole numbers 16.3) with 1152 added, which the accumulators
+// of 64 dims each begin without: what they hold stays below 2^24, so every sum is
+// exact in fp32 in any order, and the same pages are chosen however the work is
+// split.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
